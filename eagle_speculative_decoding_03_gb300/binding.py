@@ -23,7 +23,8 @@ FEAT_F, FEAT_FUSED = 1, 3
 FLAG_NO_GRAPH, FLAG_NO_PDL, FLAG_GEMM_TWO_CTA = 1, 2, 4
 MAX_DEPTH = 16
 KERNEL_KINDS = 14
-DEVERR_TIMEOUT, DEVERR_PREFIX, DEVERR_TOKEN, DEVERR_SELECT = 1, 2, 4, 8
+DEVERR_TIMEOUT, DEVERR_PREFIX, DEVERR_TOKEN, DEVERR_SELECT, DEVERR_PAGE = 1, 2, 4, 8, 16
+CACHE_BF16, CACHE_F4 = 1, 2
 
 
 class Config(C.Structure):
@@ -112,6 +113,31 @@ class DFlashOutputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("tokens", "logp", "lse", "hidden")]
 
 
+class KVCacheC(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("kind", "n_kv_heads", "head_dim", "page_size", "num_pages", "max_pages")] + \
+        [(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+        [("k_global", C.c_float), ("v_global", C.c_float), ("page_table", C.c_void_p)]
+
+
+class RopeC(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("theta", C.c_double),
+                ("inv_freq", C.POINTER(C.c_double)), ("amplitude", C.c_float)]
+
+
+class KVRows(C.Structure):
+    _fields_ = [("B", C.c_int32), ("N", C.c_int32), ("cu_rows", C.c_void_p), ("lens", C.c_void_p),
+                ("positions", C.c_void_p), ("dtype", C.c_int32), ("n_heads", C.c_int32)] + \
+        [(n, C.c_void_p) for n in ("k", "v", "q", "q_out")] + \
+        [(n, C.c_int64) for n in ("k_stride", "v_stride", "q_stride", "q_out_stride")]
+
+
+class KVAttention(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "N", "n_heads", "max_rows", "max_len", "mask_slots")] + \
+        [("cu_rows", C.c_void_p), ("lens", C.c_void_p), ("q", C.c_void_p), ("q_stride", C.c_int64),
+         ("mask", C.c_void_p), ("scale", C.c_float), ("out", C.c_void_p), ("out_stride", C.c_int64),
+         ("lse", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
 _lib = None
 
 
@@ -165,6 +191,19 @@ def load(path: str = LIB_PATH):
     lib.eagle_dflash_destroy.restype = None
     lib.eagle_speculative_accept.argtypes = [C.c_int32, C.c_int32, C.c_int32, P, P, P, P, P, P, P, P, P, P]
     lib.eagle_speculative_accept.restype = C.c_int
+    lib.eagle_rotary.argtypes = [C.c_int32, P, C.c_int64, C.c_int32, C.c_int32, C.c_int32, P, C.POINTER(RopeC), P,
+                                 C.c_int64, P]
+    lib.eagle_rotary.restype = C.c_int
+    lib.eagle_kv_append.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVRows), C.POINTER(RopeC), P, P]
+    lib.eagle_kv_append.restype = C.c_int
+    lib.eagle_kv_gather.argtypes = [C.POINTER(KVCacheC), C.c_int32, P, C.c_int32, P, P, P, P]
+    lib.eagle_kv_gather.restype = C.c_int
+    lib.eagle_kv_accept.argtypes = [C.POINTER(KVCacheC), C.c_int32, C.c_int32, C.c_int32, P, P, P, P, P, P]
+    lib.eagle_kv_accept.restype = C.c_int
+    lib.eagle_kv_attention_workspace.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVAttention)]
+    lib.eagle_kv_attention_workspace.restype = C.c_int64
+    lib.eagle_kv_attention.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVAttention), P, P]
+    lib.eagle_kv_attention.restype = C.c_int
     lib.eagle_draft_last_error.argtypes = []
     lib.eagle_draft_last_error.restype = C.c_char_p
     _lib = lib
@@ -498,3 +537,293 @@ class EagleDFlash:
         if st != EAGLE_OK:
             raise EagleError(st, load().eagle_draft_last_error().decode())
         return w.value
+
+
+# ------------------------------------------------------------- the caller's paged cache
+# These calls run on `stream`, or on torch's current stream where none is given; tensors they
+# allocate belong to that stream.  Tensors must be on the current device.
+
+def _bad(msg: str):
+    raise EagleError(EAGLE_ERR_INVALID_ARG, msg)
+
+
+def _tensor(t, name: str, dtypes, shape=None, contiguous: bool = True):
+    """A CUDA tensor of the current device with one of ``dtypes`` and ``shape`` (None: any size)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+        _bad(f"{name} must be a tensor of {dtypes}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
+        _bad(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        _bad(f"{name} must be on the current CUDA device")
+    return t
+
+
+def _rows(t, name: str, dtypes, heads=None, hd=None, n=None):
+    """Rows [N, H, hd] whose heads are contiguous; any row stride."""
+    _tensor(t, name, dtypes, (n, heads, hd), contiguous=False)
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        _bad(f"{name}: the heads of a row must be contiguous")
+    return t
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _on(stream):
+    import torch
+    return stream if stream is not None else torch.cuda.current_stream()
+
+
+def _dtype_of(t) -> int:
+    import torch
+    return DTYPE_BF16 if t.dtype == torch.bfloat16 else DTYPE_F32
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, linear: float = 1.0, banded: tuple | None = None,
+                     ramped: tuple | None = None) -> list:
+    """Inverse frequencies theta^(-2i/rot_dim), scaled for contexts longer than trained on.
+    ``linear``: all divided by the factor.  ``banded`` (factor, low, high, original): waves
+    longer than original/low positions are divided by the factor, those shorter than
+    original/high kept, a smooth blend between.  ``ramped`` (factor, fast, slow, original):
+    pairs that turn more than ``fast`` times within ``original`` positions are kept, those that
+    turn less than ``slow`` times divided by the factor, a linear ramp over the pair index
+    between."""
+    import math
+    if rot_dim < 2 or rot_dim % 2 or not theta > 0 or not linear > 0 or (banded and ramped):
+        _bad("rope_frequencies: bad arguments")
+    w = [theta ** (-2.0 * i / rot_dim) / linear for i in range(rot_dim // 2)]
+    if banded:
+        factor, low, high, original = banded
+        for i, f in enumerate(w):
+            turns = original * f / (2 * math.pi)             # turns within the original context
+            keep = min(1.0, max(0.0, (turns - low) / (high - low)))
+            w[i] = f * (keep + (1.0 - keep) / factor)
+    if ramped:
+        factor, fast, slow, original = ramped
+        index = lambda turns: rot_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
+        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rot_dim // 2 - 1)
+        for i, f in enumerate(w):
+            part = min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3)))
+            w[i] = f * (1.0 - part + part / factor)
+    return w
+
+
+class Rope:
+    """Rotary positions (eagle_rope_t): the first ``rot_dim`` dims in half-split or interleaved
+    pairs; ``inv_freq`` (rot_dim / 2 numbers, e.g. of rope_frequencies) replaces theta's powers."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, inv_freq=None,
+                 amplitude: float = 1.0):
+        self.rot_dim = int(rot_dim)
+        self._freq = None
+        if inv_freq is not None:
+            f = [float(x) for x in inv_freq]
+            if 2 * len(f) != self.rot_dim:
+                _bad("Rope: inv_freq must hold rot_dim / 2 numbers")
+            self._freq = (C.c_double * len(f))(*f)
+        self.c = RopeC(rot_dim=self.rot_dim, interleaved=1 if interleaved else 0, theta=float(theta),
+                       inv_freq=self._freq, amplitude=float(amplitude))
+
+
+def rotary(x, positions, rope: Rope, out=None, stream=None):
+    """x [N, H, hd] (float32 or bfloat16) rotated at int32 positions [N]; out may be x."""
+    import torch
+    _rows(x, "x", (torch.float32, torch.bfloat16))
+    N, H, hd = x.shape
+    _tensor(positions, "positions", torch.int32, (N,))
+    st = _on(stream)
+    if out is None:
+        with torch.cuda.stream(st):
+            out = torch.empty((N, H, hd), dtype=x.dtype, device=x.device)
+    _rows(out, "out", x.dtype, H, hd, N)
+    if N:
+        _check(load().eagle_rotary(_dtype_of(x), _ptr(x), _row_stride(x), N, H, hd, _ptr(positions), C.byref(rope.c),
+                                   _ptr(out), _row_stride(out), st.cuda_stream))
+    return out
+
+
+class KVCache:
+    """Paged keys and values of one layer (eagle_kv_cache_t) over the caller's tensors:
+    bf16 [pages, Hkv, page_size, hd], or uint8 codes [pages, Hkv, page_size, hd / 2] with uint8
+    (e4m3) scales [pages, Hkv, page_size, hd / 16]; page_table int32 [B, max_pages]."""
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None, k_global: float = 1.0, v_global: float = 1.0):
+        import torch
+        f4 = k.dtype == torch.uint8
+        _tensor(k, "k", (torch.bfloat16, torch.uint8), (None,) * 4)
+        _tensor(v, "v", k.dtype, tuple(k.shape))
+        _tensor(page_table, "page_table", torch.int32, (None, None))
+        P, H, ps, w = k.shape
+        hd = 2 * w if f4 else w
+        if f4:
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _tensor(t, name, torch.uint8, (P, H, ps, hd // 16))
+        elif k_scale is not None or v_scale is not None:
+            _bad("scales belong to a 4-bit cache")
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.kind, self.n_kv_heads, self.head_dim = (CACHE_F4 if f4 else CACHE_BF16), H, hd
+        self.err = torch.zeros((1,), dtype=torch.int32, device=k.device)
+        self.c = KVCacheC(kind=self.kind, n_kv_heads=H, head_dim=hd, page_size=ps, num_pages=P,
+                          max_pages=page_table.shape[1], k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale),
+                          v_scale=_ptr(v_scale), k_global=float(k_global), v_global=float(v_global),
+                          page_table=_ptr(page_table))
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, page_table, four_bit: bool = False,
+              k_global: float = 1.0, v_global: float = 1.0):
+        """A pool of zeros on page_table's device."""
+        import torch
+        def z(w, dt):
+            return torch.zeros((num_pages, n_kv_heads, page_size, w), dtype=dt, device=page_table.device)
+        if not four_bit:
+            return cls(z(head_dim, torch.bfloat16), z(head_dim, torch.bfloat16), page_table)
+        return cls(z(head_dim // 2, torch.uint8), z(head_dim // 2, torch.uint8), page_table,
+                   z(head_dim // 16, torch.uint8), z(head_dim // 16, torch.uint8), k_global, v_global)
+
+    def check(self) -> int:
+        """Synchronise; raise when a call on this cache recorded a device error, and clear it."""
+        import torch
+        torch.cuda.synchronize()
+        w = int(self.err.item())
+        if w:
+            self.err.zero_()
+            raise EagleError(EAGLE_ERR_DEVICE, f"device error word 0x{w:x}")
+        return w
+
+
+def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | None = None, q=None, q_out=None,
+              stream=None):
+    """Store a step's keys (rotated with a rope) and values [N, Hkv, hd] behind each request's
+    lens[b] keys; returns the rotated queries when q [N, Hq, hd] is given (q_out may be q)."""
+    import torch
+    H, hd = cache.n_kv_heads, cache.head_dim
+    _rows(k, "k", (torch.float32, torch.bfloat16), H, hd)
+    N = k.shape[0]
+    _rows(v, "v", k.dtype, H, hd, N)
+    _tensor(lens, "lens", torch.int32, (None,))
+    B = lens.shape[0]
+    _tensor(cu_rows, "cu_rows", torch.int32, (B + 1,))
+    if cache.page_table.shape[0] < B:
+        _bad("the page table has fewer rows than lens")
+    if rope is not None:
+        _tensor(positions, "positions", torch.int32, (N,))
+    st = _on(stream)
+    if q is not None:
+        _rows(q, "q", k.dtype, None, hd, N)
+        if q_out is None:
+            with torch.cuda.stream(st):   # rows of no request are not written
+                q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+        _rows(q_out, "q_out", q.dtype, q.shape[1], hd, N)
+    if N:
+        w = KVRows(B=B, N=N, cu_rows=_ptr(cu_rows), lens=_ptr(lens), positions=_ptr(positions), dtype=_dtype_of(k),
+                   n_heads=0 if q is None else q.shape[1], k=_ptr(k), v=_ptr(v), q=_ptr(q), q_out=_ptr(q_out),
+                   k_stride=_row_stride(k), v_stride=_row_stride(v), q_stride=0 if q is None else _row_stride(q),
+                   q_out_stride=0 if q is None else _row_stride(q_out))
+        _check(load().eagle_kv_append(C.byref(cache.c), C.byref(w), None if rope is None else C.byref(rope.c),
+                                      _ptr(cache.err), st.cuda_stream))
+    return None if q is None else q_out
+
+
+def kv_gather(cache: KVCache, cu_seqlens, total: int, k_out=None, v_out=None, stream=None):
+    """The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every request, packed bf16
+    [total, Hkv, hd]: the k_cache / v_cache of EagleDraft.tree and EagleVerify.verify."""
+    import torch
+    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (None,))
+    B = cu_seqlens.shape[0] - 1
+    if B < 1 or total < 0 or cache.page_table.shape[0] < B:
+        _bad("kv_gather: cu_seqlens needs 1 .. page_table rows requests, total must not be negative")
+    st = _on(stream)
+    shape = (int(total), cache.n_kv_heads, cache.head_dim)
+    with torch.cuda.stream(st):
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v_out is None else v_out
+    _tensor(k_out, "k_out", torch.bfloat16, shape)
+    _tensor(v_out, "v_out", torch.bfloat16, shape)
+    _check(load().eagle_kv_gather(C.byref(cache.c), B, _ptr(cu_seqlens), int(total), _ptr(k_out), _ptr(v_out),
+                                  _ptr(cache.err), st.cuda_stream))
+    return k_out, v_out
+
+
+def kv_accept(caches, lens, accept_len, accept_slots, new_lens=None, stream=None):
+    """Keep the accepted path of a verified tree (appended behind lens[b] keys in slot order) in
+    every cache of the list (one per layer, one shape and page table); returns the new lengths
+    lens + 1 + accept_len (new_lens may be lens)."""
+    import torch
+    caches = [caches] if isinstance(caches, KVCache) else list(caches)
+    if not caches:
+        _bad("kv_accept: no caches")
+    _tensor(accept_slots, "accept_slots", torch.int32, (None, None))
+    B, S = accept_slots.shape
+    _tensor(lens, "lens", torch.int32, (B,))
+    _tensor(accept_len, "accept_len", torch.int32, (B,))
+    if caches[0].page_table.shape[0] < B:
+        _bad("the page table has fewer rows than lens")
+    st = _on(stream)
+    if new_lens is None:
+        with torch.cuda.stream(st):
+            new_lens = torch.empty_like(lens)
+    _tensor(new_lens, "new_lens", torch.int32, (B,))
+    arr = (KVCacheC * len(caches))(*[c.c for c in caches])
+    _check(load().eagle_kv_accept(arr, len(caches), B, S, _ptr(lens), _ptr(accept_len), _ptr(accept_slots),
+                                  _ptr(new_lens), _ptr(caches[0].err), st.cuda_stream))
+    return new_lens
+
+
+def kv_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, mask=None, scale: float = 0.0, out=None,
+                 lse=False, workspace=None, stream=None):
+    """Attention of a step's rows (appended before) over the cache: bf16 q [N, Hq, hd]; row i of
+    request b sees the lens[b] keys before the step and the step's rows j by mask[b, i, j] (uint8
+    [B, S, S]) or j <= i.  max_rows / max_len bound one request's rows and keys.  Returns out,
+    or (out, lse [N, Hq]) with lse=True or a tensor.  ``workspace``: a uint8 tensor to keep
+    (at least kv_attention_workspace bytes); else one is taken from torch's allocator."""
+    import torch
+    _rows(q, "q", torch.bfloat16, None, cache.head_dim)
+    N, Hq, hd = q.shape
+    _tensor(lens, "lens", torch.int32, (None,))
+    B = lens.shape[0]
+    _tensor(cu_rows, "cu_rows", torch.int32, (B + 1,))
+    if cache.page_table.shape[0] < B:
+        _bad("the page table has fewer rows than lens")
+    S = 0
+    if mask is not None:
+        S = mask.shape[-1]
+        _tensor(mask, "mask", torch.uint8, (B, S, S))
+    st = _on(stream)
+    want_lse = lse is not None and lse is not False
+    a = KVAttention(B=B, N=N, n_heads=Hq, max_rows=int(max_rows), max_len=int(max_len), mask_slots=S,
+                    cu_rows=_ptr(cu_rows), lens=_ptr(lens), q=_ptr(q), q_stride=_row_stride(q), mask=_ptr(mask),
+                    scale=float(scale))
+    need = load().eagle_kv_attention_workspace(C.byref(cache.c), C.byref(a))
+    if need < 0:
+        _bad(load().eagle_draft_last_error().decode())
+    with torch.cuda.stream(st):
+        if out is None:
+            out = torch.empty((N, Hq, hd), dtype=torch.bfloat16, device=q.device)
+        if lse is True:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        if need and workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    _rows(out, "out", torch.bfloat16, Hq, hd, N)
+    a.out, a.out_stride = _ptr(out), _row_stride(out)
+    if want_lse:
+        _tensor(lse, "lse", torch.float32, (N, Hq))
+        a.lse = _ptr(lse)
+    if need:
+        _tensor(workspace, "workspace", torch.uint8, (None,))
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    if N:
+        _check(load().eagle_kv_attention(C.byref(cache.c), C.byref(a), _ptr(cache.err), st.cuda_stream))
+    return (out, lse) if want_lse else out
+
+
+def kv_attention_workspace(cache: KVCache, n_heads: int, N: int, B: int, max_rows: int, max_len: int) -> int:
+    """Bytes of workspace that kv_attention needs for these sizes."""
+    a = KVAttention(B=B, N=N, n_heads=n_heads, max_rows=max_rows, max_len=max_len)
+    need = load().eagle_kv_attention_workspace(C.byref(cache.c), C.byref(a))
+    if need < 0:
+        _bad(load().eagle_draft_last_error().decode())
+    return need

@@ -1,0 +1,593 @@
+// The caller's paged key / value cache: rotary positions, appending a step's rows, gathering
+// pages into the packed prefix, keeping an accepted path.  See include/eagle_draft.h.
+#include "kvcache.cuh"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+namespace eagle {
+
+eagle_status_t kv_fail(eagle_status_t st, const char* fmt, ...) {
+  char buf[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  set_last_error(buf);
+  return st;
+}
+
+static bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+eagle_status_t kv_pool(const eagle_kv_cache_t* c, const char* who, KvPool* out) {
+  if (!c) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null cache", who);
+  if (c->kind != EAGLE_CACHE_BF16 && c->kind != EAGLE_CACHE_F4)
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: unknown cache kind %d", who, c->kind);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128, not %d", who, c->head_dim);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64 or 128, not %d", who, c->page_size);
+  if (c->n_kv_heads < 1 || c->num_pages < 1 || c->max_pages < 1)
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: n_kv_heads, num_pages and max_pages must be at least 1", who);
+  if (static_cast<long long>(c->num_pages) * c->n_kv_heads >= (1ll << 31) / c->page_size)
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: num_pages * n_kv_heads * page_size must be below 2^31", who);
+  const bool f4 = c->kind == EAGLE_CACHE_F4;
+  if (!c->k || !c->v || !c->page_table || (f4 && (!c->k_scale || !c->v_scale)))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null cache pointer", who);
+  if (!aligned16(c->k) || !aligned16(c->v) || (f4 && (!aligned16(c->k_scale) || !aligned16(c->v_scale))))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: cache pointers must be 16-byte aligned", who);
+  if (f4 && !(c->k_global > 0.f && c->v_global > 0.f && std::isfinite(c->k_global) && std::isfinite(c->v_global)))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: k_global and v_global must be finite and positive", who);
+  out->k = c->k;
+  out->v = c->v;
+  out->ks = c->k_scale;
+  out->vs = c->v_scale;
+  out->kg = c->k_global;
+  out->vg = c->v_global;
+  out->table = c->page_table;
+  out->max_pages = c->max_pages;
+  out->num_pages = c->num_pages;
+  out->Hkv = c->n_kv_heads;
+  out->hd = c->head_dim;
+  out->ps_log = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  return EAGLE_OK;
+}
+
+namespace {
+
+constexpr int RT_THREADS = 256;
+constexpr int RT_WARPS = RT_THREADS / 32;
+constexpr int RT_MAX_PAIRS = 128;            // rot_dim <= 256
+
+// inv_freq as fractions of a turn in 64-bit fixed point: position * turn[i] mod 2^64 is the
+// angle's fraction of a turn, exact but for |position| 2^-65 turns.
+struct RopeTab {
+  unsigned long long turn[RT_MAX_PAIRS];
+  int pairs;                                 // rot_dim / 2 (0: no rotation)
+  int inter;
+  float amp;
+};
+
+struct RotArgs {
+  // source rows: queries (or eagle_rotary's x), keys, values
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  long long q_ld, k_ld, v_ld, qo_ld;         // row strides, elements
+  int Hq, Hk, Hv;                            // heads of each part (0: absent)
+  int N, hd;
+  const int* positions;
+  // append only
+  int B;
+  const int* cu;
+  const int* lens;
+  unsigned* err;
+  KvPool pool;
+  int rows_per_cta, slices;
+};
+
+EAGLE_DEV void load8(const float* p, float* x) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+EAGLE_DEV void load8(const __nv_bfloat16* p, float* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+EAGLE_DEV uint32_t pack2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+EAGLE_DEV void store8(float* p, const float* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+EAGLE_DEV uint4 pack8(const float* x) { return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])); }
+EAGLE_DEV void store8(__nv_bfloat16* p, const float* x) { *reinterpret_cast<uint4*>(p) = pack8(x); }
+
+// 8 dims of a cached row in 4 bits; the 16-dim group's other half is in lane ^ 1.  The values
+// are rounded to bf16 first, so the scale and the codes depend on the stored precision alone
+// and not on how the rotation was rounded.  Called by whole warps; `live` lanes store.
+EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, const float* x, float global, bool live, bool even) {
+  float y[8];
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] = bf16_to_f32(f32_to_bf16(x[e]));
+    if (y[e] != y[e]) y[e] = 0.f;            // NaN has no code: stored as 0
+    top = fmaxf(top, fabsf(y[e]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const uint32_t s = f32_to_e4m3(__fdiv_rn(top, 6.0f * global));
+  const float unit = e4m3_to_f32(s) * global;
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    // IEEE division: a value on a border between two codes divides to the border exactly
+    const float a = unit > 0.f ? __fdiv_rn(y[e], unit) : 0.f, b = unit > 0.f ? __fdiv_rn(y[e + 1], unit) : 0.f;
+    w |= e2m1x2(a, b) << (4 * e);
+  }
+  if (live) {
+    *reinterpret_cast<uint32_t*>(code) = w;
+    if (even) *scale = static_cast<uint8_t>(s);
+  }
+}
+
+// Rotates heads and (CACHE != 0) stores keys and values in their pages.  A lane holds 8
+// consecutive dims of one head: hd / 8 lanes per head, as many whole heads per warp as fit; a
+// half-layout pair's other dim comes from another lane of the head by a shuffle, so every load
+// of a head precedes its stores (in place is safe).  The CTA computes the cos / sin of its rows
+// once into shared memory; a warp keeps one row's in registers over all the heads it takes.
+// CACHE: 0 eagle_rotary, else eagle_cache_kind_t.
+template <typename T, int CACHE>
+__global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, const RopeTab rt) {
+  __shared__ float2 cs[RT_WARPS][RT_MAX_PAIRS];
+  __shared__ int s_page[RT_WARPS], s_tok[RT_WARPS], s_req[RT_WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = a.rows_per_cta, row0 = blockIdx.x * rows;
+  if (CACHE != 0 && tid < rows) {
+    const int n = row0 + tid;
+    const int b = n < a.N ? row_owner(a.cu, a.B, n) : -1;
+    int page = -1, t = 0;
+    if (b >= 0) {
+      t = __ldg(a.lens + b) + (n - __ldg(a.cu + b));
+      page = kv_page(a.pool, b, t, a.err);
+    }
+    s_req[tid] = b;
+    s_page[tid] = page;
+    s_tok[tid] = t;
+  }
+  for (int i = tid; i < rows * rt.pairs; i += RT_THREADS) {
+    const int r = i / rt.pairs, j = i - r * rt.pairs;
+    if (row0 + r < a.N) {
+      const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(__ldg(a.positions + row0 + r))) * rt.turn[j];
+      float s, c;
+      sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // half turns: 2^-31
+      cs[r][j] = make_float2(c * rt.amp, s * rt.amp);
+    }
+  }
+  __syncthreads();
+  const int wpr = RT_WARPS / rows;           // warps per row
+  const int r = warp / wpr, n = row0 + r;
+  if (n >= a.N) return;
+  if (CACHE != 0 && s_req[r] < 0) return;
+  const int lph = a.hd >> 3, hpw = 32 / lph; // lanes per head, heads per warp
+  const int sub = lane / lph, o = lane - sub * lph;
+  const bool in_warp = sub < hpw;
+  const int ro = rt.pairs >> 3;              // octets of one half of the rotated dims
+  const bool rot = o < 2 * ro;
+  // this lane's factors: y[e] = x[e] * c[e] + other[e] * s[e]
+  float c[8], s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    c[e] = 1.f;
+    s[e] = 0.f;
+    if (rot) {
+      const int j = rt.inter ? 4 * o + (e >> 1) : 8 * (o < ro ? o : o - ro) + e;
+      const float2 f = cs[r][j];
+      c[e] = f.x;
+      s[e] = (rt.inter ? (e & 1) == 0 : o < ro) ? -f.y : f.y;
+    }
+  }
+  const int other = rot && !rt.inter ? (o < ro ? lane + ro : lane - ro) : lane;
+  const int heads = a.Hq + a.Hk + a.Hv;
+  const int step = wpr * a.slices * hpw;
+#pragma unroll 2
+  for (int h0 = (blockIdx.y * wpr + warp % wpr) * hpw; h0 < heads; h0 += step) {
+    const int h = h0 + sub;
+    const bool live = in_warp && h < heads;
+    float x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
+    if (live) {
+      const T* src = is_q   ? static_cast<const T*>(a.q) + n * a.q_ld + static_cast<long long>(h) * a.hd
+                     : is_k ? static_cast<const T*>(a.k) + n * a.k_ld + static_cast<long long>(h - a.Hq) * a.hd
+                            : static_cast<const T*>(a.v) + n * a.v_ld + static_cast<long long>(h - a.Hq - a.Hk) * a.hd;
+      load8(src + 8 * o, x);
+    }
+    if (rt.inter) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], x[e ^ 1] * s[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = __shfl_sync(0xffffffffu, x[e], other);
+        y[e] = fmaf(x[e], c[e], z * s[e]);
+      }
+    }
+    if (!rot || (!is_q && !is_k)) {          // dims behind rot_dim, and values: as they are
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = x[e];
+    }
+    if (live && is_q) store8(static_cast<T*>(a.q_out) + n * a.qo_ld + static_cast<long long>(h) * a.hd + 8 * o, y);
+    if (CACHE != 0) {
+      const bool to = live && !is_q && s_page[r] >= 0;
+      const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hk;
+      const size_t row = to ? kv_row(a.pool, s_page[r], kvh, s_tok[r]) : 0;
+      if (CACHE == EAGLE_CACHE_BF16) {
+        if (to) store8(static_cast<__nv_bfloat16*>(is_k ? a.pool.k : a.pool.v) + row * a.hd + 8 * o, y);
+      } else {
+        store8_f4(static_cast<uint8_t*>(is_k ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
+                  static_cast<uint8_t*>(is_k ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), y,
+                  is_k ? a.pool.kg : a.pool.vg, to, (o & 1) == 0);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- gather
+constexpr int GA_THREADS = 256;
+constexpr int GA_TOKENS = 8;
+
+struct GatherArgs {
+  KvPool pool;
+  int B, total;
+  const int* cu;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  unsigned* err;
+};
+
+// A CTA writes GA_TOKENS packed rows of K and V, 16 bytes per thread and step, consecutive
+// threads consecutive bytes of the output; reads come in runs of one head's row.
+template <int CACHE>
+__global__ void __launch_bounds__(GA_THREADS) gather_kernel(const GatherArgs a) {
+  __shared__ int s_page[GA_TOKENS], s_tok[GA_TOKENS];
+  const int t0 = blockIdx.x * GA_TOKENS, tid = threadIdx.x;
+  if (tid < GA_TOKENS) {
+    const int n = t0 + tid;
+    const int b = n < a.total ? row_owner(a.cu, a.B, n) : -1;
+    int page = -2, t = 0;                    // -2: no request's row, left as it was
+    if (b >= 0) {
+      t = n - __ldg(a.cu + b);
+      page = kv_page(a.pool, b, t, a.err);   // -1: zeros
+    }
+    s_page[tid] = page;
+    s_tok[tid] = t;
+  }
+  __syncthreads();
+  const int oct = a.pool.hd >> 3, per = a.pool.Hkv * oct;   // octets per token
+  const int n_all = 2 * GA_TOKENS * per;
+#pragma unroll 4
+  for (int i = tid; i < n_all; i += GA_THREADS) {
+    const bool is_v = i >= GA_TOKENS * per;
+    const int r = is_v ? i - GA_TOKENS * per : i;
+    const int tk = r / per, rest = r - tk * per;
+    const int h = rest / oct, o = rest - h * oct;
+    const int page = s_page[tk];
+    if (page == -2) continue;
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (page >= 0) {
+      const size_t row = kv_row(a.pool, page, h, s_tok[tk]);
+      if (CACHE == EAGLE_CACHE_BF16) {
+        u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? a.pool.v : a.pool.k) + row * a.pool.hd) + o);
+      } else {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_v ? a.pool.v : a.pool.k) + row * (a.pool.hd >> 1)) + o);
+        const uint32_t sb = __ldg(static_cast<const uint8_t*>(is_v ? a.pool.vs : a.pool.ks) + row * (a.pool.hd >> 4) + (o >> 1));
+        const float unit = e4m3_to_f32(sb) * (is_v ? a.pool.vg : a.pool.kg);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = e2m1_to_f32(w >> (4 * e)) * unit;
+        u = pack8(x);
+      }
+    }
+    __nv_bfloat16* out = is_v ? a.v_out : a.k_out;
+    *reinterpret_cast<uint4*>(out + (static_cast<size_t>(t0 + tk) * per + rest) * 8) = u;
+  }
+}
+
+// ------------------------------------------------------------------------- accept
+constexpr int AK_MAX_CACHES = 64;
+
+struct AcceptCaches {
+  char* p[4 * AK_MAX_CACHES];                // k, v, k_scale, v_scale of every cache
+};
+struct KeepArgs {
+  KvPool pool;                               // caches[0]'s shape and table
+  int f4, B, S;
+  const int* lens;
+  const int* accept_len;
+  const int* slots;
+  int* new_lens;
+  unsigned* err;
+};
+
+// Moves count rows of `bytes` per (head, row) in units of U: a thread owns a column (head,
+// unit) and moves its units in path order, 8 reads in flight.  Slots ascend and slot j >= j + 1,
+// so a place written is never the source of a later move: only reads before writes matter, and
+// those are one thread's own.
+template <typename U>
+EAGLE_DEV void move_rows(const KvPool& c, char* base, int bytes, int count, const int* src_page, const int* src_tok,
+                         const int* dst_page, const int* dst_tok) {
+  const int units = bytes / static_cast<int>(sizeof(U));
+  for (int col = threadIdx.x; col < c.Hkv * units; col += blockDim.x) {
+    const int h = col / units, u = col - h * units;
+    for (int j0 = 0; j0 < count; j0 += 8) {
+      U x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j0 + e < count && src_page[j0 + e] >= 0)
+          x[e] = *(reinterpret_cast<const U*>(base + kv_row(c, src_page[j0 + e], h, src_tok[j0 + e]) * bytes) + u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j0 + e < count && src_page[j0 + e] >= 0 && dst_page[j0 + e] >= 0)
+          *(reinterpret_cast<U*>(base + kv_row(c, dst_page[j0 + e], h, dst_tok[j0 + e]) * bytes) + u) = x[e];
+    }
+  }
+}
+
+// One CTA per (request, cache, key / value).
+__global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __grid_constant__ AcceptCaches caches) {
+  __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_n;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int base = __ldg(a.lens + b);
+  if (tid == 0) {
+    // the path: ascending slots behind the root; anything else ends it
+    int n = min(max(__ldg(a.accept_len + b), 0), a.S - 1), prev = 0, j = 0;
+    if (__ldg(a.accept_len + b) != n) atomicOr(a.err, DEVERR_TOKEN);
+    for (; j < n; ++j) {
+      const int s = __ldg(a.slots + static_cast<size_t>(b) * a.S + j);
+      if (s <= prev || s >= a.S) {
+        atomicOr(a.err, DEVERR_TOKEN);
+        break;
+      }
+      prev = s;
+    }
+    s_n = j;
+  }
+  __syncthreads();
+  const int n = s_n;
+  if (tid < n) {
+    const int s = __ldg(a.slots + static_cast<size_t>(b) * a.S + tid);
+    src_tok[tid] = base + s;
+    dst_tok[tid] = base + 1 + tid;
+    src_page[tid] = s == tid + 1 ? -1 : kv_page(a.pool, b, base + s, a.err);   // (already in place)
+    dst_page[tid] = kv_page(a.pool, b, base + 1 + tid, a.err);
+  }
+  __syncthreads();
+  const int c = blockIdx.y, w = blockIdx.z;  // cache, 0 keys / 1 values
+  if (a.f4) {
+    move_rows<uint32_t>(a.pool, caches.p[4 * c + w], a.pool.hd >> 1, n, src_page, src_tok, dst_page, dst_tok);
+    move_rows<uint32_t>(a.pool, caches.p[4 * c + 2 + w], a.pool.hd >> 4, n, src_page, src_tok, dst_page, dst_tok);
+  } else {
+    move_rows<uint4>(a.pool, caches.p[4 * c + w], a.pool.hd * 2, n, src_page, src_tok, dst_page, dst_tok);
+  }
+}
+
+// The new lengths, after the moves (new_lens may be lens: every CTA of the moves reads lens).
+__global__ void keep_lens_kernel(const KeepArgs a) {
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= a.B) return;
+  const int n = min(max(__ldg(a.accept_len + b), 0), a.S - 1);
+  int prev = 0, j = 0;
+  for (; j < n; ++j) {
+    const int s = __ldg(a.slots + static_cast<size_t>(b) * a.S + j);
+    if (s <= prev || s >= a.S) break;
+    prev = s;
+  }
+  a.new_lens[b] = a.lens[b] + 1 + j;
+}
+
+eagle_status_t rope_table(const eagle_rope_t* r, int hd, const char* who, RopeTab* t) {
+  memset(t, 0, sizeof(*t));
+  if (!r) return EAGLE_OK;
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > hd || r->rot_dim > 2 * RT_MAX_PAIRS)
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: rot_dim must be a multiple of 16 up to head_dim, not %d", who, r->rot_dim);
+  if (r->interleaved != 0 && r->interleaved != 1) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", who);
+  if (!r->inv_freq && !(r->theta > 0.0 && std::isfinite(r->theta)))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: theta must be finite and positive", who);
+  if (!std::isfinite(r->amplitude)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: amplitude must be finite", who);
+  t->pairs = r->rot_dim / 2;
+  t->inter = r->interleaved;
+  t->amp = r->amplitude;
+  for (int i = 0; i < t->pairs; ++i) {
+    const double f = r->inv_freq ? r->inv_freq[i] : std::pow(r->theta, -2.0 * i / r->rot_dim);
+    if (!std::isfinite(f) || f < 0.0 || f > 1e6) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: inv_freq must lie in [0, 1e6]", who);
+    const double turns = f / 6.283185307179586476925286766559;
+    const double frac = turns - std::floor(turns);      // whole turns per position change nothing
+    t->turn[i] = static_cast<unsigned long long>(std::ldexp(frac, 64) < 18446744073709551616.0 ? std::ldexp(frac, 64) : 0.0);
+  }
+  return EAGLE_OK;
+}
+
+// Rows per CTA and head slices: many rows take 8 to a CTA (one warp per row, whose cos / sin
+// then serve all heads); few rows are spread over warps and CTAs so each warp has few heads.
+void rotate_shape(RotArgs* a) {
+  const int heads = a->Hq + a->Hk + a->Hv, hpw = 32 / (a->hd / 8);
+  const int iters = (heads + hpw - 1) / hpw;            // warp steps per row
+  const int sms = num_sms();
+  a->rows_per_cta = a->N >= 16 * sms ? 8 : a->N >= 4 * sms ? 4 : a->N >= 2 * sms ? 2 : 1;
+  const int wpr = RT_WARPS / a->rows_per_cta;
+  const long long ctas = (a->N + a->rows_per_cta - 1) / a->rows_per_cta;
+  const int most = std::max(1, (iters + wpr - 1) / wpr);
+  a->slices = static_cast<int>(std::min<long long>(most, std::max<long long>(1, 4ll * sms / std::max(1ll, ctas))));
+}
+
+template <int CACHE>
+eagle_status_t launch_rotate(RotArgs& a, const RopeTab& rt, int dtype, const char* who, cudaStream_t st) {
+  rotate_shape(&a);
+  const dim3 grid((a.N + a.rows_per_cta - 1) / a.rows_per_cta, a.slices);
+  if (dtype == EAGLE_DTYPE_BF16) rotate_kernel<__nv_bfloat16, CACHE><<<grid, RT_THREADS, 0, st>>>(a, rt);
+  else rotate_kernel<float, CACHE><<<grid, RT_THREADS, 0, st>>>(a, rt);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+}
+
+// a row array of the caller: 16-byte aligned base and row stride, rows that do not overlap
+bool bad_rows(const void* p, long long ld, int H, int hd, int dtype) {
+  const int es = dtype == EAGLE_DTYPE_BF16 ? 2 : 4;
+  return !aligned16(p) || ld < static_cast<long long>(H) * hd || (ld * es) % 16;
+}
+
+}  // namespace
+}  // namespace eagle
+
+using namespace eagle;
+
+extern "C" eagle_status_t eagle_rotary(int32_t dtype, const void* x, int64_t x_stride, int32_t N, int32_t H,
+                                       int32_t head_dim, const int32_t* positions, const eagle_rope_t* rope, void* out,
+                                       int64_t out_stride, void* stream) {
+  const char* who = "rotary";
+  if (!x || !positions || !rope || !out) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
+  if (dtype != EAGLE_DTYPE_F32 && dtype != EAGLE_DTYPE_BF16) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  if (N < 0 || H < 1) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need N >= 0 and H >= 1", who);
+  if (head_dim < 16 || head_dim > 256 || head_dim % 8)
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: head_dim must be a multiple of 8 in 16..256, not %d", who, head_dim);
+  if (bad_rows(x, x_stride, H, head_dim, dtype) || bad_rows(out, out_stride, H, head_dim, dtype))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
+  if (x == out && x_stride != out_stride) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: in place needs equal strides", who);
+  RopeTab rt;
+  const eagle_status_t r = rope_table(rope, head_dim, who, &rt);
+  if (r != EAGLE_OK) return r;
+  if (N == 0) return EAGLE_OK;
+  RotArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = x;
+  a.q_out = out;
+  a.q_ld = x_stride;
+  a.qo_ld = out_stride;
+  a.Hq = H;
+  a.N = N;
+  a.hd = head_dim;
+  a.positions = positions;
+  return launch_rotate<0>(a, rt, dtype, who, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" eagle_status_t eagle_kv_append(const eagle_kv_cache_t* cache, const eagle_kv_rows_t* w, const eagle_rope_t* rope,
+                                          uint32_t* err_word, void* stream) {
+  const char* who = "kv_append";
+  RotArgs a;
+  memset(&a, 0, sizeof(a));
+  eagle_status_t r = kv_pool(cache, who, &a.pool);
+  if (r != EAGLE_OK) return r;
+  if (!w || !err_word || !w->cu_rows || !w->lens || !w->k || !w->v || (rope && !w->positions) || (w->q && !w->q_out))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
+  if (w->dtype != EAGLE_DTYPE_F32 && w->dtype != EAGLE_DTYPE_BF16) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: unknown dtype", who);
+  if (w->B < 1 || w->N < 0 || (w->q && w->n_heads < 1)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need B >= 1, N >= 0, n_heads >= 1", who);
+  if (w->q && !rope) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: queries need a rope", who);
+  const int hd = cache->head_dim, Hkv = cache->n_kv_heads;
+  if (bad_rows(w->k, w->k_stride, Hkv, hd, w->dtype) || bad_rows(w->v, w->v_stride, Hkv, hd, w->dtype) ||
+      (w->q && (bad_rows(w->q, w->q_stride, w->n_heads, hd, w->dtype) || bad_rows(w->q_out, w->q_out_stride, w->n_heads, hd, w->dtype))))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
+  if (w->q && w->q == w->q_out && w->q_stride != w->q_out_stride)
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: in place needs equal strides", who);
+  RopeTab rt;
+  if ((r = rope_table(rope, hd, who, &rt)) != EAGLE_OK) return r;
+  if (w->N == 0) return EAGLE_OK;
+  a.q = w->q;
+  a.k = w->k;
+  a.v = w->v;
+  a.q_out = w->q_out;
+  a.q_ld = w->q_stride;
+  a.k_ld = w->k_stride;
+  a.v_ld = w->v_stride;
+  a.qo_ld = w->q_out_stride;
+  a.Hq = w->q ? w->n_heads : 0;
+  a.Hk = a.Hv = Hkv;
+  a.N = w->N;
+  a.hd = hd;
+  a.positions = w->positions;
+  a.B = w->B;
+  a.cu = w->cu_rows;
+  a.lens = w->lens;
+  a.err = err_word;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cache->kind == EAGLE_CACHE_BF16 ? launch_rotate<EAGLE_CACHE_BF16>(a, rt, w->dtype, who, st)
+                                         : launch_rotate<EAGLE_CACHE_F4>(a, rt, w->dtype, who, st);
+}
+
+extern "C" eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t B, const int32_t* cu_seqlens, int32_t total,
+                                          void* k_out, void* v_out, uint32_t* err_word, void* stream) {
+  const char* who = "kv_gather";
+  GatherArgs a;
+  const eagle_status_t r = kv_pool(cache, who, &a.pool);
+  if (r != EAGLE_OK) return r;
+  if (B < 1 || total < 0) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need B >= 1 and total >= 0", who);
+  if (total == 0) return EAGLE_OK;
+  if (!cu_seqlens || !k_out || !v_out || !err_word) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
+  if (!aligned16(k_out) || !aligned16(v_out)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: outputs must be 16-byte aligned", who);
+  a.B = B;
+  a.total = total;
+  a.cu = cu_seqlens;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.err = err_word;
+  const int grid = (total + GA_TOKENS - 1) / GA_TOKENS;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cache->kind == EAGLE_CACHE_BF16) gather_kernel<EAGLE_CACHE_BF16><<<grid, GA_THREADS, 0, st>>>(a);
+  else gather_kernel<EAGLE_CACHE_F4><<<grid, GA_THREADS, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+}
+
+extern "C" eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_t n_caches, int32_t B, int32_t S,
+                                          const int32_t* lens, const int32_t* accept_len, const int32_t* accept_slots,
+                                          int32_t* new_lens, uint32_t* err_word, void* stream) {
+  const char* who = "kv_accept";
+  if (!caches || n_caches < 1 || n_caches > AK_MAX_CACHES)
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need 1..%d caches", who, AK_MAX_CACHES);
+  if (!lens || !accept_len || !accept_slots || !new_lens || !err_word)
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
+  if (B < 1 || S < 1 || S > 64) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need B >= 1 and 1 <= S <= 64", who);
+  KeepArgs a;
+  AcceptCaches ac;
+  memset(&ac, 0, sizeof(ac));
+  for (int i = 0; i < n_caches; ++i) {
+    KvPool p;
+    const eagle_status_t r = kv_pool(caches + i, who, &p);
+    if (r != EAGLE_OK) return r;
+    const eagle_kv_cache_t &x = caches[i], &y = caches[0];
+    if (x.kind != y.kind || x.n_kv_heads != y.n_kv_heads || x.head_dim != y.head_dim || x.page_size != y.page_size ||
+        x.num_pages != y.num_pages || x.max_pages != y.max_pages || x.page_table != y.page_table)
+      return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: the caches must share one shape and page table", who);
+    if (i == 0) a.pool = p;
+    ac.p[4 * i] = static_cast<char*>(p.k);
+    ac.p[4 * i + 1] = static_cast<char*>(p.v);
+    ac.p[4 * i + 2] = static_cast<char*>(p.ks);
+    ac.p[4 * i + 3] = static_cast<char*>(p.vs);
+  }
+  a.f4 = caches[0].kind == EAGLE_CACHE_F4;
+  a.B = B;
+  a.S = S;
+  a.lens = lens;
+  a.accept_len = accept_len;
+  a.slots = accept_slots;
+  a.new_lens = new_lens;
+  a.err = err_word;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  keep_kernel<<<dim3(B, n_caches, 2), 256, 0, st>>>(a, ac);
+  keep_lens_kernel<<<(B + 127) / 128, 128, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+}

@@ -74,6 +74,8 @@ typedef enum { EAGLE_FEAT_F = 1, EAGLE_FEAT_FUSED = 3 } eagle_feat_kind_t;
 #define EAGLE_DEVERR_TOKEN       0x4u   /* a root token was outside [0, vocab) (treated as 0) */
 #define EAGLE_DEVERR_SELECT      0x8u   /* a row had fewer than k valid next-token candidates
                                            (non-finite logits); the missing children get token 0 */
+#define EAGLE_DEVERR_PAGE        0x10u  /* a key's place lies outside the page table, or its page
+                                           outside the pool (eagle_kv_* calls) */
 
 typedef struct {
   int32_t d;            /* hidden size; d % 128 == 0 for bf16 weights */
@@ -454,6 +456,140 @@ EAGLE_API eagle_status_t eagle_speculative_accept(int32_t B, int32_t S, int32_t 
                                                   const float* logits_draft, const uint64_t* seeds,
                                                   int32_t* accept_len, int32_t* accept_slots, int32_t* correction,
                                                   uint32_t* err_word, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The caller's key / value cache.  Drafting and verification read "the verified-prefix
+ * cache" ("Tree attention in one verification pass", aicassindra.com: one target pass, with
+ * a tree mask over cached keys); these calls make, grow, read and compact such a cache for
+ * models whose layers the caller runs: rotary positions, appending a step's rows, tree or
+ * causal attention over the pages, gathering pages into the packed prefix that
+ * eagle_draft_tree and eagle_verify_tree read, and keeping the accepted path of a verified tree.
+ *
+ * Pages: a pool of num_pages pages of page_size tokens; token t of request b sits in row
+ * t % page_size of page page_table[b][t / page_size].  Per page and KV head the rows are
+ * contiguous.  Requests may share pages that no call writes.
+ *   EAGLE_CACHE_BF16: k, v bf16 [num_pages][Hkv][page_size][hd].
+ *   EAGLE_CACHE_F4:   k, v e2m1 codes [num_pages][Hkv][page_size][hd / 2] (even dim in the low
+ *     nibble; bit 3 the sign, magnitudes 0 .5 1 1.5 2 3 4 6), k_scale, v_scale e4m3
+ *     [num_pages][Hkv][page_size][hd / 16].  A value is code * scale * k_global (v_global).
+ *     Appending takes the row's bf16 value (a rotated key is rounded to bf16 first) and stores
+ *     scale = e4m3(largest magnitude of the 16 dims / (6 global)), code = e2m1(value / (scale
+ *     global)), both rounded to nearest, ties to even, saturating; NaN is stored as 0, and a
+ *     group whose scale rounds to 0 as zeros.  0.5625 bytes per element instead of 2.
+ *
+ * All calls are stream-ordered, allocate nothing and keep no state: calls on one cache (or
+ * one workspace) must be ordered by the caller where they touch the same rows.  Device
+ * pointers except where marked; pointers of rows 16-byte aligned, strides in elements and
+ * multiples of 16 bytes.  Kernel-side problems set bits of *err_word (device, caller-owned):
+ * EAGLE_DEVERR_PAGE for a place outside the table or pool (the row is skipped, or read as
+ * zeros), EAGLE_DEVERR_PREFIX for lengths or row ranges outside the call's bounds (clamped),
+ * EAGLE_DEVERR_TOKEN for an accepted path that is not ascending slots of the tree.
+ * ------------------------------------------------------------------------------------ */
+typedef enum { EAGLE_CACHE_BF16 = 1, EAGLE_CACHE_F4 = 2 } eagle_cache_kind_t;
+
+typedef struct {
+  int32_t kind;               /* eagle_cache_kind_t */
+  int32_t n_kv_heads;         /* Hkv */
+  int32_t head_dim;           /* hd: 64 or 128 */
+  int32_t page_size;          /* tokens per page: 16, 32, 64 or 128 */
+  int32_t num_pages;          /* pages of the pool; num_pages * Hkv * page_size < 2^31 */
+  int32_t max_pages;          /* pages per request in the table (its row stride) */
+  void*   k;
+  void*   v;
+  void*   k_scale;            /* F4 only */
+  void*   v_scale;
+  float   k_global, v_global; /* F4 only: finite, > 0 */
+  const int32_t* page_table;  /* [B][max_pages] */
+} eagle_kv_cache_t;
+
+/* Rotary positions: the first rot_dim dims of a head are rotated in pairs by the angle
+ * position * inv_freq[i], scaled by `amplitude`; the others are copied.  Angles are formed
+ * as exact fractions of a turn (64-bit fixed point), so far positions lose nothing. */
+typedef struct {
+  int32_t rot_dim;            /* multiple of 16, <= head_dim */
+  int32_t interleaved;        /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+  double  theta;              /* inv_freq_i = theta^(-2i / rot_dim) where inv_freq is NULL */
+  const double* inv_freq;     /* HOST [rot_dim / 2] or NULL: scaled frequencies (long contexts) */
+  float   amplitude;          /* factor on cos and sin (1: plain rotation) */
+} eagle_rope_t;
+
+/* x [N][H][hd] (rows x_stride apart, heads contiguous) rotated at positions [N] into out;
+ * dtype EAGLE_DTYPE_F32 or _BF16, head_dim a multiple of 8 up to 256.  out may be x itself
+ * (same stride), and may not overlap it otherwise. */
+EAGLE_API eagle_status_t eagle_rotary(int32_t dtype, const void* x, int64_t x_stride, int32_t N, int32_t H,
+                                      int32_t head_dim, const int32_t* positions, const eagle_rope_t* rope,
+                                      void* out, int64_t out_stride, void* stream);
+
+/* The rows of one step: request b's rows are n = cu_rows[b] .. cu_rows[b + 1] - 1; row i of
+ * them becomes the request's key lens[b] + i.  Rows outside [cu_rows[0], cu_rows[B]) belong
+ * to no request: nothing of them is read or written.  No two rows may share a place. */
+typedef struct {
+  int32_t B, N;               /* requests, rows (the buffers' extent) */
+  const int32_t* cu_rows;     /* [B + 1] ascending, within [0, N] */
+  const int32_t* lens;        /* [B] keys each request held before these rows */
+  const int32_t* positions;   /* [N] rotary positions; needed only with a rope */
+  int32_t dtype;              /* of q, k, v, q_out: EAGLE_DTYPE_F32 or _BF16 */
+  int32_t n_heads;            /* query heads (only with q) */
+  const void* k;              /* [N][Hkv][hd], rows k_stride apart */
+  const void* v;              /* [N][Hkv][hd] */
+  const void* q;              /* [N][Hq][hd] or NULL: queries rotated in the same launch */
+  void*   q_out;              /* [N][Hq][hd]; may be q itself */
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+} eagle_kv_rows_t;
+
+/* Rotates the keys (and queries) and stores keys and values in their pages.  rope may be
+ * NULL: the keys are stored as they are (q must then be NULL). */
+EAGLE_API eagle_status_t eagle_kv_append(const eagle_kv_cache_t* cache, const eagle_kv_rows_t* rows,
+                                         const eagle_rope_t* rope, uint32_t* err_word, void* stream);
+
+/* The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every request as bf16
+ * [total][Hkv][hd] at rows cu_seqlens[b]..: the packed prefix of eagle_draft_tree and
+ * eagle_verify_tree.  `total` is the outputs' extent; rows outside the requests are left as
+ * they were. */
+EAGLE_API eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t B, const int32_t* cu_seqlens,
+                                         int32_t total, void* k_out, void* v_out, uint32_t* err_word, void* stream);
+
+/* After a verification: request b's tree of S slots was appended behind its lens[b] keys in
+ * slot order (root first).  Keeps the root and the accept_len[b] accepted slots
+ * accept_slots[b][..] (ascending, as eagle_verify_tree and eagle_speculative_accept write
+ * them): slot accept_slots[b][j] moves to key lens[b] + 1 + j in every one of the n_caches
+ * caches (HOST array, 1..64, e.g. one per layer; all of one shape, and of caches[0]'s page
+ * table), and new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens). */
+EAGLE_API eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_t n_caches, int32_t B, int32_t S,
+                                         const int32_t* lens, const int32_t* accept_len, const int32_t* accept_slots,
+                                         int32_t* new_lens, uint32_t* err_word, void* stream);
+
+/* Attention of a step's rows over the cache, after eagle_kv_append of the same rows: row i of
+ * request b sees the lens[b] keys before the step and, of the step's own R rows, the rows j with
+ * mask[b][i][j] != 0 (tree: the mask eagle_draft_tree emits) or, without a mask, j <= i
+ * (causal).  out = softmax(scale q k) v per query head; grouped heads as in
+ * eagle_draft_config_t.  A row that sees nothing, or only keys of score -infinity, gets zeros
+ * and lse -infinity; keys a row does not see have no influence on it whatever they hold.
+ * bf16 queries and outputs; scores, softmax and sums in fp32. */
+typedef struct {
+  int32_t B, N;               /* requests, rows */
+  int32_t n_heads;            /* Hq, a multiple of Hkv with Hq / Hkv <= 64 */
+  int32_t max_rows;           /* most rows of one request */
+  int32_t max_len;            /* most keys of one request, the step's own among them */
+  int32_t mask_slots;         /* S of the mask: each request has at most S rows, S <= 64 */
+  const int32_t* cu_rows;     /* [B + 1] as in eagle_kv_rows_t */
+  const int32_t* lens;        /* [B] */
+  const void* q;              /* bf16 [N][Hq][hd], rows q_stride apart */
+  int64_t q_stride;
+  const uint8_t* mask;        /* [B][S][S] or NULL: causal */
+  float   scale;              /* 0: 1 / sqrt(hd) */
+  void*   out;                /* bf16 [N][Hq][hd], rows out_stride apart */
+  int64_t out_stride;
+  float*  lse;                /* [N][Hq] log-sum-exp of the scaled scores, or NULL */
+  void*   workspace;          /* eagle_kv_attention_workspace bytes, 16-byte aligned (NULL if 0) */
+  int64_t workspace_bytes;
+} eagle_kv_attention_t;
+
+/* Bytes of workspace a call with these sizes needs (-1: invalid sizes).  Calls that may
+ * overlap on the GPU need a workspace each. */
+EAGLE_API int64_t eagle_kv_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args);
+EAGLE_API eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args,
+                                            uint32_t* err_word, void* stream);
 
 /* Thread-local description of the last error (never NULL). */
 EAGLE_API const char* eagle_draft_last_error(void);
