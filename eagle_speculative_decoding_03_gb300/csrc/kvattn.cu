@@ -1,98 +1,708 @@
 // Attention of a step's rows over the caller's paged key / value cache (bf16 or 4-bit), with
 // the tree mask of an emitted draft tree or causally.  See include/eagle_draft.h.
+//
+//   s = scale q k,  p = 2^(log2e (s - m)),  l = sum p,  out = (sum p v) / l
+//
+// All query heads of a KV group and all rows of a request share one pass over the keys: the
+// query vectors v = row * G + head of the group fill the 128 TMEM lanes of a tcgen05 tile (one
+// or two tiles per CTA), 128 keys to a step.  A CTA takes a range of the keys; the ranges of a
+// request meet in a combine kernel (fixed order, deterministic).
 #include "kvcache.cuh"
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 using namespace eagle;
 
 namespace {
 
 constexpr int KA_MAX_GROUP = 64;
+constexpr int KA_CH = 128;                 // keys per tile
+constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes)
+constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
+constexpr uint32_t KA_MISC = 2048;
+constexpr int KA_MAX_SLOTS = 14;
 
 struct KaArgs {
   KvPool pool;
-  int B, N, Hq, max_rows, max_len, S;
+  int B, N, Hq, G, max_rows, max_len, S;
+  int blocks;                              // query-vector blocks per request
+  int tiles_per_cta, splits;
   const int* cu;
   const int* lens;
   const __nv_bfloat16* q;
   long long q_ld;
   const unsigned char* mask;
-  float scale;
+  float scale_log2;                        // scale * log2(e)
   __nv_bfloat16* out;
   long long out_ld;
   float* lse;
+  float* part_o;                           // [splits][N][Hq][hd] unnormalised outputs (splits > 1)
+  float2* part_ml;                         // [splits][N][Hq] running maximum (log2 units) and sum
   unsigned* err;
 };
 
-// One warp per (row, query head): a lane holds hd / 32 dims; one pass over the visible keys
-// with the running maximum and sum.
-template <int HD, int CACHE>
-__global__ void __launch_bounds__(128) kv_attention_rows(const KaArgs a) {
+// Request b's rows and keys, clamped to what the call allows.
+struct Req {
+  int row0, R, ctx, len;
+};
+EAGLE_DEV Req request(const KaArgs& a, int b) {
+  Req r;
+  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), l = __ldg(a.lens + b);
+  r.row0 = min(max(c0, 0), a.N);
+  r.R = min(max(min(c1, a.N) - r.row0, 0), a.max_rows);
+  r.ctx = min(max(l, 0), max(a.max_len - r.R, 0));
+  if (r.row0 != c0 || r.R != c1 - c0 || r.ctx != l) atomicOr(a.err, DEVERR_PREFIX);
+  r.len = min(r.ctx + r.R, a.max_len);
+  return r;
+}
+
+// 128 bits of key visibility
+struct Bits {
+  unsigned long long lo, hi;
+};
+EAGLE_DEV Bits bits_below(int n) {         // bits [0, n)
+  Bits r;
+  r.lo = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+  r.hi = n >= 128 ? ~0ull : n <= 64 ? 0ull : (1ull << (n - 64)) - 1ull;
+  return r;
+}
+EAGLE_DEV Bits shift_up(unsigned long long m, int n) {   // m << n; n < 0: m >> -n
+  Bits r{0ull, 0ull};
+  if (n <= -64 || n >= 128) return r;
+  if (n < 0) r.lo = m >> -n;
+  else if (n == 0) r.lo = m;
+  else if (n < 64) { r.lo = m << n; r.hi = m >> (64 - n); }
+  else r.hi = m << (n - 64);
+  return r;
+}
+
+// byte offset of 16-byte chunk c (0-7) of row r in a 128-byte-swizzled block of 128-byte rows
+EAGLE_DEV uint32_t ka_sw(int r, int c) {
+  return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+EAGLE_DEV void st_smem16(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+// the larger of two, NaN if either is: a NaN score must reach the output
+EAGLE_DEV float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+EAGLE_DEV uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+EAGLE_DEV uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// byte B of w, two e2m1 codes -> fp16 pair (low nibble in the low half)
+template <int B>
+EAGLE_DEV uint32_t e2m1_pair(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t<4>;\n\tmov.b32 {t0, t1, t2, t3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t%2;\n\t}" : "=r"(r) : "r"(w), "n"(B));
+  return r;
+}
+EAGLE_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 16 consecutive dims of a cached row: 8 code bytes and their scale -> 16 fp16 values (exact:
+// a code has 2 significant bits and a scale 4; the range is 2^-10 .. 2688)
+EAGLE_DEV void dequant16(uint2 code, uint32_t scale, uint32_t* h) {
+  uint32_t s;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s) : "r"(scale * 0x101u));
+  h[0] = mul_f16x2(e2m1_pair<0>(code.x), s);
+  h[1] = mul_f16x2(e2m1_pair<1>(code.x), s);
+  h[2] = mul_f16x2(e2m1_pair<2>(code.x), s);
+  h[3] = mul_f16x2(e2m1_pair<3>(code.x), s);
+  h[4] = mul_f16x2(e2m1_pair<0>(code.y), s);
+  h[5] = mul_f16x2(e2m1_pair<1>(code.y), s);
+  h[6] = mul_f16x2(e2m1_pair<2>(code.y), s);
+  h[7] = mul_f16x2(e2m1_pair<3>(code.y), s);
+}
+
+// The tensor-core kernel.  HD 64 or 128; CACHE the cache kind; NB: query-vector tiles per CTA.
+//
+// Shared memory is a ring of entries, key tile and value tile in turn (128 rows of 128 bytes per
+// 64 dims, 128-byte swizzle).  bf16 pages come by TMA, one box per page and 64 dims; 4-bit pages
+// are read by converter warps, which write fp16 tiles.  Q is the A operand of S = Q K^T, in TMEM
+// (NB = 1) or shared memory (NB = 2, where S and O of two tiles take all 512 columns); P replaces
+// S in TMEM as the A operand of O += P V.  Work goes in units (key tile, query tile), S in
+// buffer unit & 1: one unit's QK^T and PV overlap another's softmax.
+//
+// A page that the keys end inside is loaded from a negative row, so that the copy reads zeros
+// and then the valid rows: memory behind the last key never enters a product (it may hold NaN,
+// and 0 * NaN would reach O).  The columns of that page are shifted by as much.
+//
+// P is rounded for the second product: fp16 (11 bits) with 4-bit caches; with bf16 values it
+// must be bf16, kept as hi + lo parts (two products) where one query tile leaves the kernel bound
+// by bytes, and rounded to 8 bits where two tiles make it bound by the tensor cores (an output
+// error of half a bf16 step's size).  l sums the unrounded p.
+__host__ __device__ constexpr int ka_threads(int cache, int nb) { return cache == EAGLE_CACHE_F4 ? 512 : 128 + 128 * nb; }
+__host__ __device__ constexpr uint32_t ka_entry(int hd) { return static_cast<uint32_t>(hd) * 2 * KA_CH; }
+
+template <int HD, int CACHE, int NB>
+__global__ void __launch_bounds__(ka_threads(CACHE, NB), 1)
+kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const KaArgs a, const int NS) {
+  constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
+  constexpr bool HILO = !F4 && NB == 1;
+  // fp16 p is held times 2^7 (below 2^15): its subnormal step is then 2^-31 of the largest p
+  constexpr float LIFT = F4 ? 7.f : 0.f;
+  constexpr int THREADS = ka_threads(CACHE, NB);
+  constexpr int CONV_WARP = 4 + 4 * NB, CONV = THREADS - 32 * CONV_WARP;   // converter threads (F4)
+  constexpr uint32_t ENTRY = ka_entry(HD), HALF = KA_CH * 128;
+  constexpr uint32_t T_O = 256, T_Q = 384;
+  extern __shared__ uint8_t ka_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ka_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring_u = smem_u32(sm);
+  const uint32_t q_u = ring_u + static_cast<uint32_t>(NS) * ENTRY;       // NB = 2: Q tiles
+  uint8_t* misc = sm + static_cast<uint32_t>(NS) * ENTRY + (NB == 2 ? 2 * ENTRY : 0);
+  const uint32_t misc_u = smem_u32(misc);
+  const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 240,
+                 bar_pe = misc_u + 256, bar_od = misc_u + 272, bar_fin = misc_u + 288;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 296);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 300);
+  unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [128] tree mask rows
+
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / a.blocks, blk0 = blockIdx.z - b * a.blocks;
+  const Req rq = request(a, b);
+  const int v0 = blk0 * KA_QV * NB;
+  const int qv = min(rq.R * a.G - v0, KA_QV * NB);
+  if (qv <= 0) return;
+  const int i_first = v0 / a.G, i_last = (v0 + qv - 1) / a.G;
+  // keys this block can see, and this CTA's tiles of them
+  const int seen = a.mask ? rq.len : min(rq.len, rq.ctx + i_last + 1);
+  const int all_tiles = (seen + KA_CH - 1) / KA_CH;
+  const int t_begin = split * a.tiles_per_cta;
+  if (t_begin * KA_CH >= rq.len) return;             // (not a range of this request at all)
+  const int T = max(0, min(all_tiles - t_begin, a.tiles_per_cta));
+  const int nb = NB == 2 && qv > KA_QV ? 2 : 1;
+  const int nq0 = min(4, (min(qv, KA_QV) + 31) / 32), nq1 = nb == 2 ? (qv - KA_QV + 31) / 32 : nq0;
+  const int U = T * nb;
+  const int mma_warp = 3;
+  const int ps = 1 << a.pool.ps_log;
+
+  if (tid == 0) {
+    for (int s = 0; s < KA_MAX_SLOTS; ++s) {
+      mbar_init(bar_kvf + 8 * s, F4 ? CONV / 32 : 1);
+      mbar_init(bar_kve + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_sf + 8 * i, 1);
+      mbar_init(bar_pf + 8 * i, i == 0 || nb == 1 ? nq0 : nq1);
+      mbar_init(bar_pe + 8 * i, 1);
+      mbar_init(bar_od + 8 * i, 1);
+    }
+    mbar_init(bar_fin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // tree mask rows of this block's rows as 64-bit words
+  if (a.mask) {
+    for (int i = i_first + warp; i <= i_last; i += THREADS / 32) {
+      const unsigned char* mrow = a.mask + (static_cast<size_t>(b) * a.S + i) * a.S;
+      const unsigned lo = __ballot_sync(0xffffffffu, lane < rq.R && __ldg(mrow + min(lane, a.S - 1)) != 0);
+      const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 < rq.R && __ldg(mrow + min(lane + 32, a.S - 1)) != 0);
+      if (lane == 0) rowbits[i - i_first] = lo | (static_cast<unsigned long long>(hi) << 32);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // the page that the request's keys end inside: its rows sit at the end of the box (bf16)
+  const int end_page = rq.len >> a.pool.ps_log, end_rows = F4 ? 0 : rq.len & (ps - 1);
+  auto box_row = [&](int pi) { return pi == end_page && end_rows ? end_rows - ps : 0; };
+
+  // queries: thread = vector; bf16 as they are, or fp16 scaled by a power of two so that the
+  // vector's largest magnitude lies in [2^14, 2^15) (8 significant bits always fit)
+  float row_scale = a.scale_log2 * (F4 ? a.pool.kg : 1.f);
+  if (warp >= 4 && warp < 4 + 4 * nb) {
+    const int g = (warp - 4) >> 2, lv = tid - 128 - 128 * g, v = v0 + KA_QV * g + lv;
+    const bool live = KA_QV * g + lv < qv;
+    const uint4* src = nullptr;
+    if (live) {
+      const int i = v / a.G;
+      src = reinterpret_cast<const uint4*>(a.q + (rq.row0 + i) * a.q_ld + static_cast<long long>(kvh * a.G + v - i * a.G) * HD);
+    }
+    float up = 1.f;
+    if (F4 && live) {
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int c = 0; c < HD / 8; ++c) {
+        const uint4 x = __ldg(src + c);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+      }
+      int ex = static_cast<int>(top >> 7);              // biased exponent of the largest magnitude
+      ex = ex == 255 ? 127 : max(ex, 30);               // (infinities and NaN pass; tiny vectors)
+      up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
+      row_scale *= __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < HD / 8; c0 += 4) {            // 32 dims: 16 packed columns
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 x = live ? __ldg(src + c0 + c) : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
+      }
+      if (F4) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+      }
+      if (NB == 1) {
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(w[e]);
+        tmem_st16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + T_Q + 4 * c0, f);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          st_smem16(q_u + g * ENTRY + ((c0 + c) >> 3) * HALF + ka_sw(lv, (c0 + c) & 7), w + 4 * c);
+      }
+    }
+    if (NB == 1) tmem_wait_st();
+    else fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (bf16)
+    if (!F4 && lane == 0) {
+      const uint64_t pol = policy_evict_first();
+      const int none = a.pool.num_pages * a.pool.Hkv;   // a block outside the map: zeros
+      const int per = KA_CH >> a.pool.ps_log;
+      for (int e = 0; e < 2 * T && ok; ++e) {
+        const int slot = e % NS;
+        if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, ((e / NS) & 1) ^ 1, a.err, abort_flag);
+        if (!ok) break;
+        const uint32_t dst = ring_u + slot * ENTRY, bar = bar_kvf + 8 * slot;
+        mbar_arrive_expect_tx(bar, ENTRY);
+        const int p0 = (t_begin + (e >> 1)) * per;
+        for (int p = 0; p < per; ++p) {
+          const int pi = p0 + p;
+          int blk = none;
+          if ((pi << a.pool.ps_log) < rq.len) {
+            const int page = kv_page(a.pool, b, pi << a.pool.ps_log, a.err);
+            if (page >= 0) blk = page * a.pool.Hkv + kvh;
+          }
+          const int r0 = box_row(pi);
+#pragma unroll
+          for (int h = 0; h < HD / 64; ++h)
+            tma_load_3d(dst + h * HALF + p * (ps * 128), e & 1 ? &tmv : &tmk, 64 * h, r0, blk, bar, pol);
+        }
+      }
+      if (!ok) {   // let copies already issued land before the CTA releases its shared memory
+        const long long t0 = clock64();
+        while (clock64() - t0 < 4000000) {
+        }
+      }
+    }
+  } else if (warp == mma_warp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_CH) : idesc_bf16_f32(128, KA_CH);
+      const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
+      for (int u = 0; u <= U && ok; ++u) {
+        if (u < U) {   // S = Q K^T of unit u, once P V of unit u - 2 (same buffer) is done
+          const int t = nb == 2 ? u >> 1 : u, g = nb == 2 ? u & 1 : 0, e = 2 * t, slot = e % NS;
+          if (g == 0) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
+          ok = ok && mbar_wait(bar_pe + 8 * (u & 1), ((u >> 1) & 1) ^ 1, a.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + (u & 1) * KA_CH;
+          const uint64_t dk = smem_desc_sw128(ring_u + slot * ENTRY);
+          const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
+#pragma unroll
+          for (int j = 0; j < HD / 16; ++j) {
+            const uint32_t ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
+            if (NB == 1) tc_mma_bf16_ta(d, tmem + T_Q + 8 * j, dk + ko, id1, j > 0 ? 1u : 0u);
+            else tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
+          }
+          tc_commit(bar_sf + 8 * (u & 1));
+          if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
+        }
+        if (u > 0) {   // O += P V of unit u - 1
+          const int w = u - 1, t = nb == 2 ? w >> 1 : w, g = nb == 2 ? w & 1 : 0, e = 2 * t + 1, slot = e % NS;
+          if (g == 0) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
+          ok = ok && mbar_wait(bar_pf + 8 * (w & 1), (w >> 1) & 1, a.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = smem_desc_sw128_mn(ring_u + slot * ENTRY, HALF, 1024);
+          const uint32_t tp = tmem + (w & 1) * KA_CH, tO = tmem + T_O + 128 * g;
+#pragma unroll
+          for (int j = 0; j < KA_CH / 16; ++j) {
+            const uint32_t first = (t > 0 || j > 0) ? 1u : 0u;
+            if (HILO) {   // keys [32 c, 32 c + 32): 16 hi columns at 32 c, 16 lo columns behind
+              const uint32_t pa = tp + 32 * (j >> 1) + 8 * (j & 1);
+              tc_mma_bf16_ta(tO, pa, dv + j * 128, id2, first);
+              tc_mma_bf16_ta(tO, pa + 16, dv + j * 128, id2, 1u);
+            } else {
+              tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, first);
+            }
+          }
+          tc_commit(bar_pe + 8 * (w & 1));
+          if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
+          tc_commit(bar_od + 8 * g);
+        }
+      }
+      if (!ok) {   // let MMAs already issued finish before TMEM is released
+        const long long t0 = clock64();
+        while (clock64() - t0 < 4000000) {
+        }
+      }
+      tc_commit(bar_fin);
+    }
+  } else if (warp >= CONV_WARP) {
+    if constexpr (F4) {
+    // ------------------------------ 4-bit pages -> fp16 tiles: 16 dims per thread and step,
+    // the next entry's codes in flight while this one is converted
+    constexpr int GR = HD / 16;                        // scale groups per row
+    constexpr int IT = KA_CH * GR / CONV;              // 16-dim groups per thread and entry
+    const int ct = tid - 32 * CONV_WARP, gidx = ct % GR, r0 = ct / GR;
+    constexpr int RSTEP = CONV / GR;
+    uint2 code[IT];
+    uint32_t scale[IT];
+    auto fetch = [&](int e) {
+      const uint8_t* cp = static_cast<const uint8_t*>(e & 1 ? a.pool.v : a.pool.k);
+      const uint8_t* sp = static_cast<const uint8_t*>(e & 1 ? a.pool.vs : a.pool.ks);
+      const int k0 = (t_begin + (e >> 1)) * KA_CH;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int t = k0 + r0 + i * RSTEP;
+        code[i] = make_uint2(0u, 0u);
+        scale[i] = 0u;
+        if (t < rq.len) {
+          const int page = kv_page(a.pool, b, t, a.err);
+          if (page >= 0) {
+            const size_t row = kv_row(a.pool, page, kvh, t);
+            code[i] = __ldg(reinterpret_cast<const uint2*>(cp + row * (HD / 2)) + gidx);
+            scale[i] = __ldg(sp + row * GR + gidx);
+          }
+        }
+      }
+    };
+    if (T > 0) fetch(0);
+    for (int e = 0; e < 2 * T; ++e) {
+      const int slot = e % NS;
+      if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, ((e / NS) & 1) ^ 1, a.err, abort_flag);
+      if (__any_sync(0xffffffffu, !ok)) break;
+      const uint32_t dst = ring_u + slot * ENTRY + (gidx >> 2) * HALF;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        uint32_t h[8];
+        dequant16(code[i], scale[i], h);
+        // (the two 64-dim halves share banks: the upper one stores its chunks in the other order)
+        const int r = r0 + i * RSTEP, c = 2 * (gidx & 3), sw = gidx >> 2;
+        uint32_t x[4], y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = sw ? h[4 + k] : h[k];
+          y[k] = sw ? h[k] : h[4 + k];
+        }
+        st_smem16(dst + ka_sw(r, c + sw), x);
+        st_smem16(dst + ka_sw(r, c + (sw ^ 1)), y);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_kvf + 8 * slot);
+      if (e + 1 < 2 * T) fetch(e + 1);
+    }
+    }
+  } else if (warp >= 4 && warp < 4 + 4 * nb) {
+    // ------------------------------------------------------------ softmax
+    const int g = (warp - 4) >> 2, lv = tid - 128 - 128 * g, v = v0 + KA_QV * g + lv;
+    const bool live = KA_QV * g + lv < qv;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int irow = live ? v / a.G : i_last;
+    const unsigned long long tree_bits = a.mask && live ? rowbits[irow - i_first] : 0ull;
+    const uint32_t tO = tmem + lane_base + T_O + 128 * g;
+    float m_run = -INFINITY, l_run = 0.f;              // raw scores' maximum; sum of p
+    if (((warp & 3)) < (g == 0 ? nq0 : nq1)) {
+      for (int t = 0; t < T; ++t) {
+        const int u = nb == 2 ? 2 * t + g : t;
+        ok = ok && mbar_wait_sleepy(bar_sf + 8 * (u & 1), (u >> 1) & 1, a.err, abort_flag);
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_base + (u & 1) * KA_CH;
+        const int k0 = (t_begin + t) * KA_CH;
+        // columns this vector sees; keys [k0, k0 + 128) but for the shifted last page
+        Bits vis{~0ull, ~0ull};
+        bool full = k0 + KA_CH <= rq.ctx;
+        if (!full) {
+          const int off = rq.ctx - k0;                 // column of the step's first own row
+          if (a.mask) {
+            const Bits own = shift_up(tree_bits, off);
+            vis = bits_below(off);
+            vis.lo |= own.lo;
+            vis.hi |= own.hi;
+          } else {
+            vis = bits_below(off + irow + 1);
+          }
+          if (end_rows) {
+            const int at = (end_page << a.pool.ps_log) - k0, sh = ps - end_rows;   // the page's first column
+            if (at >= 0 && at < KA_CH) {
+              const Bits below = bits_below(at);
+              // columns from `at` on move up by sh
+              Bits up;
+              const unsigned long long mlo = vis.lo & ~below.lo, mhi = vis.hi & ~below.hi;
+              if (sh < 64) {
+                up.lo = mlo << sh;
+                up.hi = (mhi << sh) | (mlo >> (64 - sh));
+              } else {
+                up.lo = 0ull;
+                up.hi = sh < 128 ? mlo << (sh - 64) : 0ull;
+              }
+              vis.lo = (vis.lo & below.lo) | up.lo;
+              vis.hi = (vis.hi & below.hi) | up.hi;
+            }
+          }
+          full = (vis.lo & vis.hi) == ~0ull;
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < KA_CH; c += 32) {
+          float s[32];
+          tmem_ld32(ts + c, s);
+          tmem_wait_ld();
+          if (!full) {
+            const uint32_t bits = static_cast<uint32_t>((c < 64 ? vis.lo : vis.hi) >> (c & 32));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? s[e] : -INFINITY;
+          }
+          float m4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = s[e];
+#pragma unroll
+          for (int e = 4; e < 32; ++e) m4[e & 3] = max_nan(m4[e & 3], s[e]);
+          mt = max_nan(mt, max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])));
+        }
+        float f = 1.f;
+        bool resc = false;
+        if (mt != -INFINITY) {
+          if (m_run == -INFINITY) {
+            m_run = mt;
+          } else if ((mt - m_run) * row_scale > KA_RESCALE) {
+            f = fast_exp2((m_run - mt) * row_scale);
+            m_run = mt;
+            resc = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+          // rows whose maximum rose: scale them in O once this tile's earlier P V are done
+          ok = ok && mbar_wait_sleepy(bar_od + 8 * g, (t - 1) & 1, a.err, abort_flag);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < HD; c0 += 32) {
+            float x[32];
+            tmem_ld32(tO + c0, x);
+            tmem_wait_ld();
+            uint32_t y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(x[e] * f);
+            tmem_st32(tO + c0, y);
+          }
+          tmem_wait_st();
+        }
+        l_run *= f;
+        const bool pw = live && ok && m_run != -INFINITY;
+        const float mb = m_run * row_scale - LIFT;
+        float p4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KA_CH; c += 32) {
+          float s[32];
+          tmem_ld32(ts + c, s);
+          tmem_wait_ld();
+          if (pw) {
+            const uint32_t bits = full ? 0xffffffffu : static_cast<uint32_t>((c < 64 ? vis.lo : vis.hi) >> (c & 32));
+            if (full) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = fast_exp2(fmaf(s[e], row_scale, -mb));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? fast_exp2(fmaf(s[e], row_scale, -mb)) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p4[e & 3] += s[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = 0.f;
+          }
+          if (HILO) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) split2_packed(s[2 * e], s[2 * e + 1], pk[e], pk[16 + e]);
+            tmem_st32(ts + c, pk);
+          } else {
+            float pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              pk[e] = __uint_as_float(F4 ? pack_f16(s[2 * e], s[2 * e + 1]) : pack_bf16(s[2 * e], s[2 * e + 1]));
+            tmem_st16(ts + c / 2, pk);   // over columns whose scores are read already
+          }
+        }
+        l_run += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_pf + 8 * (u & 1));
+      }
+      // ---- this CTA's result of vector v
+      if (T > 0) ok = mbar_wait_sleepy(bar_fin, 0, a.err, abort_flag) && ok;
+      tc_fence_after();
+      const int n = rq.row0 + irow, h = kvh * a.G + (v - irow * a.G);
+      const size_t at = static_cast<size_t>(n) * a.Hq + h;
+      // A non-finite V in a row that the step masks reaches every lane of its tile as 0 * NaN.
+      // Such sums are formed again from the visible keys alone.
+      bool again = false;
+      if (!F4 && T > 0 && (t_begin + T) * KA_CH > rq.ctx) {
+        bool bad = false;
+#pragma unroll 1
+        for (int c0 = 0; c0 < HD; c0 += 32) {
+          float x[32];
+          tmem_ld32(tO + c0, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) bad |= !(fabsf(x[e]) < INFINITY);
+        }
+        again = bad && live;
+      }
+      const float vg = F4 ? a.pool.vg : 1.f;
+      const float inv = l_run == 0.f ? 0.f : vg / l_run;
+      const bool none = l_run == 0.f;
+#pragma unroll 1
+      for (int c0 = 0; c0 < HD; c0 += 32) {
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = 0.f;
+        if (T > 0) {
+          tmem_ld32(tO + c0, x);
+          tmem_wait_ld();
+        }
+        if (again) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          const __nv_bfloat16* qp = a.q + n * a.q_ld + static_cast<long long>(h) * HD;
+          const int k_end = min(rq.len, (t_begin + T) * KA_CH);
+          for (int k = t_begin * KA_CH; k < k_end; ++k) {
+            const int j = k - rq.ctx;
+            if (j >= 0 && !(a.mask ? (tree_bits >> j) & 1ull : j <= irow)) continue;
+            const int page = kv_page(a.pool, b, k, a.err);
+            if (page < 0) continue;
+            const size_t row = kv_row(a.pool, page, kvh, k) * HD;
+            float s = 0.f;
+            for (int d = 0; d < HD; ++d)
+              s = fmaf(__bfloat162float(qp[d]), __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.k)[row + d]), s);
+            const float p = fast_exp2(fmaf(s, row_scale, -m_run * row_scale));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e] = fmaf(p, __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.v)[row + c0 + e]), x[e]);
+          }
+        }
+        if (!live) continue;
+        if (a.splits > 1) {
+          if (!none) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e] * vg, x[4 * e + 1] * vg, x[4 * e + 2] * vg, x[4 * e + 3] * vg);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + c0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = none ? 0u : pack_bf16(x[8 * e + 2 * k] * inv, x[8 * e + 2 * k + 1] * inv);
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (live) {
+        const float m2 = none ? -INFINITY : m_run * row_scale - LIFT;
+        if (a.splits > 1) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, l_run);
+        else if (a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(l_run)) * 0.6931471805599453f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Joins the key ranges of a request: one warp per (row, query head), HD / 32 dims per lane.
+template <int HD>
+__global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
   constexpr int E = HD / 32;
   const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int n = w / a.Hq, h = w - n * a.Hq;
   if (n >= a.N) return;
   const int b = row_owner(a.cu, a.B, n);
   if (b < 0) return;
-  const int i = n - __ldg(a.cu + b), R = __ldg(a.cu + b + 1) - __ldg(a.cu + b), ctx = __ldg(a.lens + b);
-  if (i >= a.max_rows || ctx < 0 || ctx + R > a.max_len) {
-    atomicOr(a.err, DEVERR_PREFIX);
-    return;
+  const Req rq = request(a, b);
+  if (n - rq.row0 >= rq.R || n < rq.row0) return;
+  const int used = min(a.splits, (rq.len + a.tiles_per_cta * KA_CH - 1) / (a.tiles_per_cta * KA_CH));
+  const size_t at = static_cast<size_t>(n) * a.Hq + h, step = static_cast<size_t>(a.N) * a.Hq;
+  float M = -INFINITY;
+  for (int s = lane; s < used; s += 32) M = fmaxf(M, a.part_ml[s * step + at].x);
+  M = warp_max(M);
+  float o[E], L = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < used; ++s) {
+    const float2 ml = a.part_ml[s * step + at];
+    if (ml.x == -INFINITY) continue;
+    const float f = M == INFINITY ? (ml.x == INFINITY ? 1.f : 0.f) : exp2f(ml.x - M);
+    L = fmaf(f, ml.y, L);
+    const float* p = a.part_o + (s * step + at) * HD + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e], o[e]);
   }
-  const int kvh = h / (a.Hq / a.pool.Hkv);
-  float q[E], o[E];
+  const bool none = L == 0.f;
+  const float inv = none ? 0.f : 1.f / L;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + lane * E);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[n * a.q_ld + static_cast<long long>(h) * HD + lane * E + e]) * a.scale;
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int t = 0; t < ctx + R; ++t) {
-    const int j = t - ctx;
-    if (j >= 0) {
-      const bool see = a.mask ? (j < a.S && i < a.S && a.mask[(static_cast<size_t>(b) * a.S + i) * a.S + j]) : j <= i;
-      if (!see) continue;
-    }
-    const int page = kv_page(a.pool, b, t, a.err);
-    float kx[E], vx[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = lane * E + e;
-      kx[e] = vx[e] = 0.f;
-      if (page < 0) continue;
-      const size_t row = kv_row(a.pool, page, kvh, t);
-      if (CACHE == EAGLE_CACHE_BF16) {
-        kx[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.k)[row * HD + d]);
-        vx[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.v)[row * HD + d]);
-      } else {
-        const int sh = 4 * (d & 1);
-        kx[e] = e2m1_to_f32((static_cast<const uint8_t*>(a.pool.k)[row * (HD / 2) + d / 2] >> sh) & 15) *
-                e4m3_to_f32(static_cast<const uint8_t*>(a.pool.ks)[row * (HD / 16) + d / 16]) * a.pool.kg;
-        vx[e] = e2m1_to_f32((static_cast<const uint8_t*>(a.pool.v)[row * (HD / 2) + d / 2] >> sh) & 15) *
-                e4m3_to_f32(static_cast<const uint8_t*>(a.pool.vs)[row * (HD / 16) + d / 16]) * a.pool.vg;
-      }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], kx[e], s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    if (mn == -INFINITY) {
-      if (s != s) l = s;
-      continue;
-    }
-    const float f = expf(m - mn), p = expf(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * vx[e];
-    m = mn;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[n * a.out_ld + static_cast<long long>(h) * HD + lane * E + e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
-  if (a.lse && lane == 0) a.lse[static_cast<size_t>(n) * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+  for (int e = 0; e < E; e += 2) dst[e / 2] = none ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[at] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// How a call is cut: query-vector tiles per CTA, blocks per request, key ranges.
+struct Plan {
+  int nb, blocks, tiles_per_cta, splits;
+};
+Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
+  Plan p;
+  const long long qv = static_cast<long long>(w->max_rows) * (w->n_heads / c->n_kv_heads);
+  p.nb = qv > KA_QV ? 2 : 1;
+  p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
+  const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
+  const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
+  const long long want = 4ll * num_sms();
+  long long per = std::max(1ll, (base * tiles + want - 1) / want);
+  if (base * tiles > num_sms()) per = std::max(per, std::min(8ll, (base * tiles + num_sms() - 1) / num_sms()));
+  per = std::min(per, tiles);
+  p.tiles_per_cta = static_cast<int>(per);
+  p.splits = static_cast<int>((tiles + per - 1) / per);
+  return p;
 }
 
 eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w, const char* who, KvPool* pool) {
@@ -109,18 +719,45 @@ eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t*
   return EAGLE_OK;
 }
 
+template <int HD, int CACHE, int NB>
+cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, cudaStream_t st) {
+  const void* fn = reinterpret_cast<const void*>(kv_attention_tc<HD, CACHE, NB>);
+  size_t cap = 0;
+  cudaError_t e = allow_max_smem(fn, &cap);
+  if (e != cudaSuccess) return e;
+  const size_t fixed = (NB == 2 ? 2 * ka_entry(HD) : 0) + KA_MISC + 1024;
+  const int ns = std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
+  const size_t smem = fixed + static_cast<size_t>(ns) * ka_entry(HD);
+  kv_attention_tc<HD, CACHE, NB><<<dim3(a.splits, a.pool.Hkv, a.B * a.blocks), ka_threads(CACHE, NB), smem, st>>>(tmk, tmv, a, ns);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, bool f4, int nb, cudaStream_t st) {
+  cudaError_t e;
+  if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
+  else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const long long warps = static_cast<long long>(a.N) * a.Hq;
+  kv_attention_combine<HD><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 extern "C" int64_t eagle_kv_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args) {
-  KvPool p;
-  if (check_args(cache, args, "kv_attention_workspace", &p) != EAGLE_OK) return -1;
-  return 0;
+  KvPool pool;
+  if (check_args(cache, args, "kv_attention_workspace", &pool) != EAGLE_OK) return -1;
+  const Plan p = plan(cache, args);
+  if (p.splits == 1) return 0;
+  return static_cast<int64_t>(p.splits) * args->N * args->n_heads * (4 * cache->head_dim + 8);
 }
 
 extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* w, uint32_t* err_word,
                                              void* stream) {
   const char* who = "kv_attention";
   KaArgs a;
+  memset(&a, 0, sizeof(a));
   const eagle_status_t r = check_args(cache, w, who, &a.pool);
   if (r != EAGLE_OK) return r;
   if (!err_word || !w->cu_rows || !w->lens || !w->q || !w->out) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
@@ -133,31 +770,40 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || reinterpret_cast<uintptr_t>(w->workspace) % 16))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
+  const Plan p = plan(cache, w);
+  const long long rows_heads = static_cast<long long>(w->N) * w->n_heads;
+  if (rows_heads > (1ll << 31) - 8 || cache->n_kv_heads > 65535 || static_cast<long long>(w->B) * p.blocks > 65535)
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: too many rows, heads or requests for one launch", who);
   a.B = w->B;
   a.N = w->N;
   a.Hq = w->n_heads;
+  a.G = w->n_heads / cache->n_kv_heads;
   a.max_rows = w->max_rows;
   a.max_len = w->max_len;
   a.S = w->mask_slots;
+  a.blocks = p.blocks;
+  a.tiles_per_cta = p.tiles_per_cta;
+  a.splits = p.splits;
   a.cu = w->cu_rows;
   a.lens = w->lens;
   a.q = static_cast<const __nv_bfloat16*>(w->q);
   a.q_ld = w->q_stride;
   a.mask = w->mask;
-  a.scale = w->scale > 0.f ? w->scale : 1.0f / std::sqrt(static_cast<float>(hd));
+  a.scale_log2 = (w->scale > 0.f ? w->scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f;
   a.out = static_cast<__nv_bfloat16*>(w->out);
   a.out_ld = w->out_stride;
   a.lse = w->lse;
+  a.part_o = static_cast<float*>(w->workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(p.splits) * w->N * w->n_heads * hd);
   a.err = err_word;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long ctas = (static_cast<long long>(w->N) * w->n_heads + 3) / 4;
-  if (ctas > 0x7fffffff) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: too many rows", who);
-  const dim3 grid(static_cast<unsigned>(ctas));
-  const bool bf = cache->kind == EAGLE_CACHE_BF16;
-  if (hd == 64 && bf) kv_attention_rows<64, EAGLE_CACHE_BF16><<<grid, 128, 0, st>>>(a);
-  else if (hd == 64) kv_attention_rows<64, EAGLE_CACHE_F4><<<grid, 128, 0, st>>>(a);
-  else if (bf) kv_attention_rows<128, EAGLE_CACHE_BF16><<<grid, 128, 0, st>>>(a);
-  else kv_attention_rows<128, EAGLE_CACHE_F4><<<grid, 128, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const bool f4 = cache->kind == EAGLE_CACHE_F4;
+  CUtensorMap tmk, tmv;
+  memset(&tmk, 0, sizeof(tmk));
+  memset(&tmv, 0, sizeof(tmv));
+  const long long blocks = static_cast<long long>(cache->num_pages) * cache->n_kv_heads;
+  if (!f4 && (!make_page_map(&tmk, cache->k, hd, cache->page_size, blocks) || !make_page_map(&tmv, cache->v, hd, cache->page_size, blocks)))
+    return kv_fail(EAGLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  const cudaError_t e = hd == 64 ? launch_all<64>(tmk, tmv, a, f4, p.nb, st) : launch_all<128>(tmk, tmv, a, f4, p.nb, st);
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }

@@ -1,0 +1,259 @@
+"""GPU parity of eagle_kv_attention (bf16 and 4-bit pages; tree masks and causal rows) against
+the float64 oracle, on pools whose every unused row holds NaN.
+
+Bound, per output: the products are exact in fp32 up to the accumulation, so a score is off by
+at most eps_s = (hd + 4) 2^-24 qk (qk the largest sum |q k| scale) plus the exponent's own rounding
+(2^-22 relative in 2^x, and its argument's 2^-23 |s| twice); p keeps 8 significant bits at least in
+the second product (relative 2^-8), sums add (hd + 128) 2^-24 relative.  So out is off by at most
+(2^-8 + 2 (eps_s + eps_e)) sum p |v| / sum p, and its bf16 rounding 2^-8 |out| on top.  With a
+4-bit cache p is an fp16 number held times 2^7 or more where it is largest: below fp16's normal
+range its rounding is absolute, half a step of 2^-24, which is 2^-32 of the largest p per key, or
+2^-32 sum |v| of the output (a key that takes all and whose value is a zero code leaves no
+relative bound).  The
+log-sum-exp is off by eps_s + eps_e + 2^-23 |lse|."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from eagle_speculative_decoding_03_gb300 import binding as eb
+from oracle import kv_oracle as K
+from kv_util import cu, dev, make_cache, see_matrix, tree_masks
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from eagle_speculative_decoding_03_gb300 import build
+    build.build()
+    return eb.load()
+
+
+def check(out, lse, ref, hd):
+    o, l, mag, qk, vsum = ref
+    eps_s = (hd + 4) * 2.0 ** -24 * qk
+    eps_e = 2.0 ** -21 + 2.0 ** -21 * qk
+    tol = (2.0 ** -8 + 2 * (eps_s + eps_e)[..., None] + (hd + 128) * 2.0 ** -24) * mag + 2.0 ** -8 * np.abs(o) + 2.0 ** -32 * vsum + 1e-30
+    bad = ~(np.abs(out - o) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4], float(np.nanmax(np.abs(out - o) / tol)))
+    some = np.isfinite(l)
+    assert (lse[~some] == -np.inf).all()
+    dl = np.abs(lse[some] - l[some])
+    tl = (eps_s + eps_e)[some] + 2.0 ** -21 * (1 + np.abs(l[some]))
+    assert (dl <= tl).all(), float((dl / tl).max())
+
+
+def run(rng, kind, hd, ps, Hkv, G, ctx, rows, tree=False, S=None, scale=0.0, mask=None, pad=0, max_len=None, qscale=1.0):
+    keys = [c + r for c, r in zip(ctx, rows)]
+    cache, held = make_cache(rng, kind, hd, ps, Hkv, keys)
+    N = sum(rows) + pad
+    q = K.bf16(qscale * rng.standard_normal((N, Hkv * G, hd)))
+    if tree and mask is None:
+        mask = tree_masks(rng, len(ctx), S or max(max(rows), 1), rows)
+    out = torch.full((N, Hkv * G, hd), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, Hkv * G), 7.0, device="cuda")
+    eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu(rows)), dev(np.array(ctx, np.int32)), max_rows=max(max(rows), 1),
+                    max_len=max_len or max(max(keys), 1), mask=None if mask is None else dev(mask), scale=scale, out=out, lse=lse)
+    assert cache.check() == 0
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    at = 0
+    for b, (c, r) in enumerate(zip(ctx, rows)):
+        if r:
+            ref = K.attention(q[at:at + r], held[b][0], held[b][1], see_matrix(c, r, None if mask is None else mask[b]),
+                              scale or hd ** -0.5)
+            check(o[at:at + r], l[at:at + r], ref, hd)
+        at += r
+    assert (o[at:] == 7.0).all() and (l[at:] == 7.0).all()   # rows of no request
+    return cache, out
+
+
+KINDS = ["bf16", "f4"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hd,ps,Hkv,G,ctx,rows", [
+    (128, 64, 2, 4, [0], [1]),                       # the first token
+    (128, 16, 1, 1, [1, 0, 15, 16, 17], [1, 1, 1, 1, 1]),
+    (128, 64, 2, 4, [127, 128, 129, 0, 255], [1, 1, 1, 1, 1]),
+    (64, 32, 3, 5, [40, 300, 63], [1, 1, 1]),        # odd group, odd head count
+    (128, 128, 1, 8, [1000, 37], [1, 1]),            # a page larger than what is left of it
+    (64, 128, 2, 64, [200], [1]),                    # the largest group
+    (128, 32, 2, 7, [5000, 3, 0], [1, 1, 0]),        # several key ranges; a request without rows
+])
+def test_single_tokens(kind, hd, ps, Hkv, G, ctx, rows):
+    run(np.random.default_rng(hd + ps + G), kind, hd, ps, Hkv, G, ctx, rows)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hd,ps,Hkv,G,ctx,rows,S", [
+    (128, 64, 2, 4, [100, 0, 64], [7, 1, 12], 12),
+    (128, 16, 1, 4, [333], [61], 64),                # 244 vectors: two query tiles
+    (128, 128, 2, 8, [120, 127], [61, 13], 61),      # the tree crosses a tile; two blocks of vectors
+    (64, 32, 2, 3, [31, 97], [64, 33], 64),
+    (128, 64, 1, 1, [2000], [40], 40),
+])
+def test_tree_rows(kind, hd, ps, Hkv, G, ctx, rows, S):
+    run(np.random.default_rng(S + ps), kind, hd, ps, Hkv, G, ctx, rows, tree=True, S=S, pad=3)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hd,ps,Hkv,G,ctx,rows", [
+    (128, 64, 2, 4, [0], [130]),                     # a prompt on its own
+    (128, 16, 1, 3, [70, 0, 5], [200, 17, 90]),
+    (64, 32, 1, 2, [129, 257], [150, 64]),
+    (128, 128, 1, 8, [900], [77]),
+])
+def test_causal_chunks(kind, hd, ps, Hkv, G, ctx, rows):
+    run(np.random.default_rng(ctx[0] + 7), kind, hd, ps, Hkv, G, ctx, rows)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("ctx", [0, 50])
+def test_rows_that_see_nothing(kind, ctx):
+    """Mask rows of zeros: without a context zeros and -inf, with one the context alone."""
+    rng = np.random.default_rng(3)
+    mask = np.zeros((1, 9, 9), np.uint8)
+    mask[0, 4, :3] = 1
+    run(rng, kind, 128, 16, 2, 4, [ctx], [9], mask=mask)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_sharp_and_scaled_scores(kind):
+    """Scores of hundreds (one key takes all), a given scale, a bound larger than the lengths."""
+    run(np.random.default_rng(4), kind, 128, 32, 2, 4, [700, 10], [3, 2], qscale=40.0, max_len=4096)
+    run(np.random.default_rng(5), kind, 64, 32, 2, 4, [700, 10], [3, 2], scale=0.01)
+    run(np.random.default_rng(6), kind, 128, 32, 1, 4, [300], [2], qscale=1e-18)
+
+
+def test_non_finite_values_in_masked_keys():
+    """Infinite and NaN keys and values of rows that a row's mask hides do not reach it; a row
+    that sees them gets what the sums give."""
+    rng = np.random.default_rng(8)
+    ctx, R, S = 70, 6, 6
+    cache, held = make_cache(rng, "bf16", 128, 16, 1, [ctx + R])
+    mask = np.eye(S, dtype=np.uint8)[None]
+    k, v = (x.clone() for x in (cache.k, cache.v))
+    tab = cache.page_table.cpu().numpy()
+    def put(t, i, val):
+        pg, r = int(tab[0, (ctx + i) // 16]), (ctx + i) % 16
+        t[pg, 0, r, 5] = val
+    put(cache.v, 1, float("nan"))
+    put(cache.v, 2, float("inf"))
+    put(cache.k, 3, float("nan"))
+    q = K.bf16(rng.standard_normal((R, 4, 128)))
+    out, lse = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu([R])), dev(np.array([ctx], np.int32)), max_rows=R,
+                               max_len=ctx + R, mask=dev(mask), lse=True)
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    ref = K.attention(q, held[0][0], held[0][1], see_matrix(ctx, R, mask[0]), 128 ** -0.5)
+    for i in (0, 4, 5):
+        check(o[i:i + 1], l[i:i + 1], tuple(x[i:i + 1] for x in ref), 128)
+    assert np.isnan(o[1, :, 5]).all() and np.isfinite(np.delete(o[1], 5, 1)).all()
+    assert np.isinf(o[2, :, 5]).all() and np.isfinite(np.delete(o[2], 5, 1)).all()
+    assert np.isnan(o[3]).all() and np.isnan(l[3]).all()
+    # a NaN query: its own row only
+    cache.k.copy_(k)
+    cache.v.copy_(v)
+    qn = q.copy()
+    qn[2, 1, 7] = np.nan
+    out = eb.kv_attention(cache, dev(qn, torch.bfloat16), dev(cu([R])), dev(np.array([ctx], np.int32)), max_rows=R,
+                          max_len=ctx + R, mask=dev(mask)).double().cpu().numpy()
+    assert np.isnan(out[2, 1]).all() and np.isfinite(np.delete(out.reshape(R * 4, 128), 2 * 4 + 1, 0)).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_strided_rows_graph_and_streams(kind):
+    """q and out as slices of wider rows; the same call replayed from a CUDA graph after the cache
+    and the lengths changed, and run on another stream: bit-equal results."""
+    rng = np.random.default_rng(9)
+    ctx, rows, H, G = [400, 90], [5, 3], 2, 4
+    cache, held = make_cache(rng, kind, 128, 64, H, [c + r for c, r in zip(ctx, rows)], room=[1000, 1000])
+    wide = torch.randn(8, H * G * 128 + 256, device="cuda").to(torch.bfloat16)
+    q = wide[:, 128:128 + H * G * 128].unflatten(1, (H * G, 128))
+    outw = torch.zeros(8, H * G * 128 + 64, dtype=torch.bfloat16, device="cuda")
+    out = outw[:, :H * G * 128].unflatten(1, (H * G, 128))
+    c, n = dev(cu(rows)), dev(np.array(ctx, np.int32))
+    need = eb.kv_attention_workspace(cache, H * G, 8, 2, 5, 1000)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    call = lambda **kw: eb.kv_attention(cache, q, c, n, max_rows=5, max_len=1000, workspace=ws, **kw)  # noqa: E731
+    plain = call().clone()
+    call(out=out)
+    assert torch.equal(out, plain) and (outw[:, H * G * 128:] == 0).all()
+    at = 0
+    qd = q.double().cpu().numpy()
+    for b, r in enumerate(rows):
+        ref = K.attention(qd[at:at + r], held[b][0], held[b][1], see_matrix(ctx[b], r), 128 ** -0.5)
+        assert np.abs(plain[at:at + r].double().cpu().numpy() - ref[0]).max() < 0.05
+        at += r
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(stream=side)
+    side.synchronize()
+    assert torch.equal(got, plain)
+    with torch.cuda.stream(side):
+        got = call()
+    side.synchronize()
+    assert torch.equal(got, plain)
+    gout = torch.zeros_like(plain)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out=gout)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(gout, plain)
+    n -= 37                                    # the graph reads the lengths of the day
+    want = call().clone()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(gout, want) and not torch.equal(want, plain)
+    assert cache.check() == 0
+
+
+def test_bad_pages_and_lengths_are_reported():
+    rng = np.random.default_rng(10)
+    cache, _ = make_cache(rng, "bf16", 128, 16, 1, [40, 40])
+    q = torch.randn(2, 4, 128, device="cuda").to(torch.bfloat16)
+    good = cache.page_table.clone()
+    args = (dev(cu([1, 1])), dev(np.array([39, 39], np.int32)))
+    want = eb.kv_attention(cache, q, *args, max_rows=1, max_len=40)
+    assert cache.check() == 0
+    cache.page_table[0, 1] = cache.k.shape[0]
+    got = eb.kv_attention(cache, q, *args, max_rows=1, max_len=40)
+    with pytest.raises(eb.EagleError) as e:
+        cache.check()
+    assert e.value.status == eb.EAGLE_ERR_DEVICE and "0x10" in str(e.value)
+    assert torch.equal(got[1], want[1])        # the other request is whole
+    cache.page_table.copy_(good)
+    eb.kv_attention(cache, q, args[0], dev(np.array([39, 80], np.int32)), max_rows=1, max_len=40)
+    with pytest.raises(eb.EagleError) as e:
+        cache.check()
+    assert "0x2" in str(e.value)
+    assert cache.check() == 0
+
+
+def test_pool_of_more_than_2_31_elements():
+    """Pages whose offsets pass 32 bits."""
+    ps, hd, H = 64, 128, 2
+    P = 2 ** 31 // (ps * hd * H) + 600
+    rng = np.random.default_rng(11)
+    for kind in KINDS:
+        w, dt = (hd, torch.bfloat16) if kind == "bf16" else (hd // 2, torch.uint8)
+        PP = P if kind == "bf16" else 2 * P
+        k = torch.zeros(PP, H, ps, w, dtype=dt, device="cuda")
+        v = torch.zeros_like(k)
+        small, held = make_cache(rng, kind, hd, ps, H, [500])
+        n = small.k.shape[0]
+        table = small.page_table + (PP - n)
+        k[PP - n:], v[PP - n:] = small.k, small.v
+        sc = []
+        if kind == "f4":
+            for s in (small.k_scale, small.v_scale):
+                t = torch.zeros(PP, H, ps, hd // 16, dtype=torch.uint8, device="cuda")
+                t[PP - n:] = s
+                sc.append(t)
+        cache = eb.KVCache(k, v, table.contiguous(), *sc, **({} if kind == "bf16" else {"k_global": 1.0, "v_global": 0.5}))
+        q = torch.randn(1, 8, hd, device="cuda").to(torch.bfloat16)
+        args = (q, dev(cu([1])), dev(np.array([499], np.int32)))
+        assert torch.equal(eb.kv_attention(cache, *args, max_rows=1, max_len=500),
+                           eb.kv_attention(small, *args, max_rows=1, max_len=500))
+        assert cache.check() == 0
+        del k, v, sc, cache
