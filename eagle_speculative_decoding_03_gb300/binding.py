@@ -198,7 +198,7 @@ def load(path: str = LIB_PATH):
     lib.eagle_kv_append.restype = C.c_int
     lib.eagle_kv_gather.argtypes = [C.POINTER(KVCacheC), C.c_int32, P, C.c_int32, P, P, P, P]
     lib.eagle_kv_gather.restype = C.c_int
-    lib.eagle_kv_accept.argtypes = [C.POINTER(KVCacheC), C.c_int32, C.c_int32, C.c_int32, P, P, P, P, P, P]
+    lib.eagle_kv_accept.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, P, P, P, P, P, P]
     lib.eagle_kv_accept.restype = C.c_int
     lib.eagle_kv_attention_workspace.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVAttention)]
     lib.eagle_kv_attention_workspace.restype = C.c_int64
@@ -541,46 +541,60 @@ class EagleDFlash:
 
 # ------------------------------------------------------------- the caller's paged cache
 # These calls run on `stream`, or on torch's current stream where none is given; tensors they
-# allocate belong to that stream.  Tensors must be on the current device.
+# allocate belong to that stream.  Tensors must be on the current device.  (The checks take a
+# fast path first: a single-token step's calls are as short as their host time.)
 
 def _bad(msg: str):
     raise EagleError(EAGLE_ERR_INVALID_ARG, msg)
 
 
-def _tensor(t, name: str, dtypes, shape=None, contiguous: bool = True):
-    """A CUDA tensor of the current device with one of ``dtypes`` and ``shape`` (None: any size)."""
+def _here(stream):
+    """(current device, raw handle of the call's stream)"""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
-        _bad(f"{name} must be a tensor of {dtypes}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
+    dev = torch.cuda.current_device()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+
+
+def _tensor(t, name: str, dtype, shape, dev: int, contiguous: bool = True):
+    """A tensor of device ``dev`` with this dtype and shape (None: any size)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        _bad(f"{name} must be a {dtype} tensor")
+    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
         _bad(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         _bad(f"{name} must be contiguous")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         _bad(f"{name} must be on the current CUDA device")
-    return t
 
 
-def _rows(t, name: str, dtypes, heads=None, hd=None, n=None):
-    """Rows [N, H, hd] whose heads are contiguous; any row stride."""
-    _tensor(t, name, dtypes, (n, heads, hd), contiguous=False)
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+def _rows(t, name: str, dtype, shape, dev: int) -> int:
+    """Rows [N, H, hd] whose heads are contiguous: the row stride in elements."""
+    _tensor(t, name, dtype, shape, dev, contiguous=False)
+    n, h, d = t.shape
+    s = t.stride()
+    if n and ((s[2] != 1 and d > 1) or (h > 1 and s[1] != d)):
         _bad(f"{name}: the heads of a row must be contiguous")
-    return t
+    return s[0] if n > 1 else h * d
 
 
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _on(stream):
+def _new(like, shape, dtype, stream):
+    """An uninitialised tensor that belongs to ``stream`` (None: the current one)."""
     import torch
-    return stream if stream is not None else torch.cuda.current_stream()
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _dtype_of(t) -> int:
+def _float_kind(t, name: str) -> int:
     import torch
-    return DTYPE_BF16 if t.dtype == torch.bfloat16 else DTYPE_F32
+    d = getattr(t, "dtype", None)
+    if d is torch.bfloat16:
+        return DTYPE_BF16
+    if d is torch.float32:
+        return DTYPE_F32
+    _bad(f"{name} must be a float32 or bfloat16 tensor")
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, linear: float = 1.0, banded: tuple | None = None,
@@ -627,22 +641,24 @@ class Rope:
             self._freq = (C.c_double * len(f))(*f)
         self.c = RopeC(rot_dim=self.rot_dim, interleaved=1 if interleaved else 0, theta=float(theta),
                        inv_freq=self._freq, amplitude=float(amplitude))
+        self.ref = C.byref(self.c)
 
 
 def rotary(x, positions, rope: Rope, out=None, stream=None):
     """x [N, H, hd] (float32 or bfloat16) rotated at int32 positions [N]; out may be x."""
     import torch
-    _rows(x, "x", (torch.float32, torch.bfloat16))
+    dev, st = _here(stream)
+    kind = _float_kind(x, "x")
+    ld = _rows(x, "x", x.dtype, (None, None, None), dev)
     N, H, hd = x.shape
-    _tensor(positions, "positions", torch.int32, (N,))
-    st = _on(stream)
+    _tensor(positions, "positions", torch.int32, (N,), dev)
     if out is None:
-        with torch.cuda.stream(st):
-            out = torch.empty((N, H, hd), dtype=x.dtype, device=x.device)
-    _rows(out, "out", x.dtype, H, hd, N)
+        out = _new(x, (N, H, hd), x.dtype, stream)
+        old = H * hd
+    else:
+        old = _rows(out, "out", x.dtype, (N, H, hd), dev)
     if N:
-        _check(load().eagle_rotary(_dtype_of(x), _ptr(x), _row_stride(x), N, H, hd, _ptr(positions), C.byref(rope.c),
-                                   _ptr(out), _row_stride(out), st.cuda_stream))
+        _check(load().eagle_rotary(kind, x.data_ptr(), ld, N, H, hd, positions.data_ptr(), rope.ref, out.data_ptr(), old, st))
     return out
 
 
@@ -653,15 +669,16 @@ class KVCache:
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None, k_global: float = 1.0, v_global: float = 1.0):
         import torch
-        f4 = k.dtype == torch.uint8
-        _tensor(k, "k", (torch.bfloat16, torch.uint8), (None,) * 4)
-        _tensor(v, "v", k.dtype, tuple(k.shape))
-        _tensor(page_table, "page_table", torch.int32, (None, None))
+        dev = torch.cuda.current_device()
+        f4 = getattr(k, "dtype", None) == torch.uint8
+        _tensor(k, "k", torch.uint8 if f4 else torch.bfloat16, (None,) * 4, dev)
+        _tensor(v, "v", k.dtype, tuple(k.shape), dev)
+        _tensor(page_table, "page_table", torch.int32, (None, None), dev)
         P, H, ps, w = k.shape
         hd = 2 * w if f4 else w
         if f4:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                _tensor(t, name, torch.uint8, (P, H, ps, hd // 16))
+                _tensor(t, name, torch.uint8, (P, H, ps, hd // 16), dev)
         elif k_scale is not None or v_scale is not None:
             _bad("scales belong to a 4-bit cache")
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
@@ -671,6 +688,7 @@ class KVCache:
                           max_pages=page_table.shape[1], k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale),
                           v_scale=_ptr(v_scale), k_global=float(k_global), v_global=float(v_global),
                           page_table=_ptr(page_table))
+        self.ref, self.err_ptr, self.max_requests = C.byref(self.c), self.err.data_ptr(), page_table.shape[0]
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, page_table, four_bit: bool = False,
@@ -700,51 +718,60 @@ def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | 
     """Store a step's keys (rotated with a rope) and values [N, Hkv, hd] behind each request's
     lens[b] keys; returns the rotated queries when q [N, Hq, hd] is given (q_out may be q)."""
     import torch
+    dev, st = _here(stream)
     H, hd = cache.n_kv_heads, cache.head_dim
-    _rows(k, "k", (torch.float32, torch.bfloat16), H, hd)
+    kind = _float_kind(k, "k")
+    k_ld = _rows(k, "k", k.dtype, (None, H, hd), dev)
     N = k.shape[0]
-    _rows(v, "v", k.dtype, H, hd, N)
-    _tensor(lens, "lens", torch.int32, (None,))
-    B = lens.shape[0]
-    _tensor(cu_rows, "cu_rows", torch.int32, (B + 1,))
-    if cache.page_table.shape[0] < B:
-        _bad("the page table has fewer rows than lens")
+    v_ld = _rows(v, "v", k.dtype, (N, H, hd), dev)
+    B = _requests(cache, cu_rows, lens, dev)
     if rope is not None:
-        _tensor(positions, "positions", torch.int32, (N,))
-    st = _on(stream)
+        _tensor(positions, "positions", torch.int32, (N,), dev)
+    Hq = q_ld = qo_ld = 0
     if q is not None:
-        _rows(q, "q", k.dtype, None, hd, N)
-        if q_out is None:
-            with torch.cuda.stream(st):   # rows of no request are not written
-                q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-        _rows(q_out, "q_out", q.dtype, q.shape[1], hd, N)
+        q_ld = _rows(q, "q", k.dtype, (N, None, hd), dev)
+        Hq = q.shape[1]
+        if q_out is None:   # (rows of no request are not written)
+            q_out, qo_ld = _new(q, (N, Hq, hd), k.dtype, stream), Hq * hd
+        else:
+            qo_ld = _rows(q_out, "q_out", k.dtype, (N, Hq, hd), dev)
     if N:
-        w = KVRows(B=B, N=N, cu_rows=_ptr(cu_rows), lens=_ptr(lens), positions=_ptr(positions), dtype=_dtype_of(k),
-                   n_heads=0 if q is None else q.shape[1], k=_ptr(k), v=_ptr(v), q=_ptr(q), q_out=_ptr(q_out),
-                   k_stride=_row_stride(k), v_stride=_row_stride(v), q_stride=0 if q is None else _row_stride(q),
-                   q_out_stride=0 if q is None else _row_stride(q_out))
-        _check(load().eagle_kv_append(C.byref(cache.c), C.byref(w), None if rope is None else C.byref(rope.c),
-                                      _ptr(cache.err), st.cuda_stream))
-    return None if q is None else q_out
+        w = KVRows(B, N, cu_rows.data_ptr(), lens.data_ptr(), None if rope is None else positions.data_ptr(), kind, Hq,
+                   k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out) if Hq else None, k_ld, v_ld, q_ld, qo_ld)
+        _check(load().eagle_kv_append(cache.ref, C.byref(w), None if rope is None else rope.ref, cache.err_ptr, st))
+    return q_out if Hq else None
+
+
+def _requests(cache: KVCache, cu_rows, lens, dev: int) -> int:
+    import torch
+    _tensor(lens, "lens", torch.int32, (None,), dev)
+    B = lens.shape[0]
+    _tensor(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
+    if cache.max_requests < B:
+        _bad("the page table has fewer rows than lens")
+    return B
 
 
 def kv_gather(cache: KVCache, cu_seqlens, total: int, k_out=None, v_out=None, stream=None):
     """The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every request, packed bf16
     [total, Hkv, hd]: the k_cache / v_cache of EagleDraft.tree and EagleVerify.verify."""
     import torch
-    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (None,))
-    B = cu_seqlens.shape[0] - 1
-    if B < 1 or total < 0 or cache.page_table.shape[0] < B:
+    dev, st = _here(stream)
+    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
+    B, total = cu_seqlens.shape[0] - 1, int(total)
+    if B < 1 or total < 0 or cache.max_requests < B:
         _bad("kv_gather: cu_seqlens needs 1 .. page_table rows requests, total must not be negative")
-    st = _on(stream)
-    shape = (int(total), cache.n_kv_heads, cache.head_dim)
-    with torch.cuda.stream(st):
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v_out is None else v_out
-    _tensor(k_out, "k_out", torch.bfloat16, shape)
-    _tensor(v_out, "v_out", torch.bfloat16, shape)
-    _check(load().eagle_kv_gather(C.byref(cache.c), B, _ptr(cu_seqlens), int(total), _ptr(k_out), _ptr(v_out),
-                                  _ptr(cache.err), st.cuda_stream))
+    shape = (total, cache.n_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = _new(cache.k, shape, torch.bfloat16, stream)
+    else:
+        _tensor(k_out, "k_out", torch.bfloat16, shape, dev)
+    if v_out is None:
+        v_out = _new(cache.k, shape, torch.bfloat16, stream)
+    else:
+        _tensor(v_out, "v_out", torch.bfloat16, shape, dev)
+    _check(load().eagle_kv_gather(cache.ref, B, cu_seqlens.data_ptr(), total, k_out.data_ptr(), v_out.data_ptr(),
+                                  cache.err_ptr, st))
     return k_out, v_out
 
 
@@ -753,23 +780,24 @@ def kv_accept(caches, lens, accept_len, accept_slots, new_lens=None, stream=None
     every cache of the list (one per layer, one shape and page table); returns the new lengths
     lens + 1 + accept_len (new_lens may be lens)."""
     import torch
+    dev, st = _here(stream)
     caches = [caches] if isinstance(caches, KVCache) else list(caches)
     if not caches:
         _bad("kv_accept: no caches")
-    _tensor(accept_slots, "accept_slots", torch.int32, (None, None))
+    _tensor(accept_slots, "accept_slots", torch.int32, (None, None), dev)
     B, S = accept_slots.shape
-    _tensor(lens, "lens", torch.int32, (B,))
-    _tensor(accept_len, "accept_len", torch.int32, (B,))
-    if caches[0].page_table.shape[0] < B:
+    _tensor(lens, "lens", torch.int32, (B,), dev)
+    _tensor(accept_len, "accept_len", torch.int32, (B,), dev)
+    if caches[0].max_requests < B:
         _bad("the page table has fewer rows than lens")
-    st = _on(stream)
     if new_lens is None:
-        with torch.cuda.stream(st):
-            new_lens = torch.empty_like(lens)
-    _tensor(new_lens, "new_lens", torch.int32, (B,))
-    arr = (KVCacheC * len(caches))(*[c.c for c in caches])
-    _check(load().eagle_kv_accept(arr, len(caches), B, S, _ptr(lens), _ptr(accept_len), _ptr(accept_slots),
-                                  _ptr(new_lens), _ptr(caches[0].err), st.cuda_stream))
+        new_lens = _new(lens, (B,), torch.int32, stream)
+    else:
+        _tensor(new_lens, "new_lens", torch.int32, (B,), dev)
+    n = len(caches)
+    arr = C.byref(caches[0].c) if n == 1 else (KVCacheC * n)(*[c.c for c in caches])
+    _check(load().eagle_kv_accept(arr, n, B, S, lens.data_ptr(), accept_len.data_ptr(), accept_slots.data_ptr(),
+                                  new_lens.data_ptr(), caches[0].err_ptr, st))
     return new_lens
 
 
@@ -781,43 +809,40 @@ def kv_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, 
     or (out, lse [N, Hq]) with lse=True or a tensor.  ``workspace``: a uint8 tensor to keep
     (at least kv_attention_workspace bytes); else one is taken from torch's allocator."""
     import torch
-    _rows(q, "q", torch.bfloat16, None, cache.head_dim)
+    dev, st = _here(stream)
+    q_ld = _rows(q, "q", torch.bfloat16, (None, None, cache.head_dim), dev)
     N, Hq, hd = q.shape
-    _tensor(lens, "lens", torch.int32, (None,))
-    B = lens.shape[0]
-    _tensor(cu_rows, "cu_rows", torch.int32, (B + 1,))
-    if cache.page_table.shape[0] < B:
-        _bad("the page table has fewer rows than lens")
+    B = _requests(cache, cu_rows, lens, dev)
     S = 0
     if mask is not None:
         S = mask.shape[-1]
-        _tensor(mask, "mask", torch.uint8, (B, S, S))
-    st = _on(stream)
-    want_lse = lse is not None and lse is not False
-    a = KVAttention(B=B, N=N, n_heads=Hq, max_rows=int(max_rows), max_len=int(max_len), mask_slots=S,
-                    cu_rows=_ptr(cu_rows), lens=_ptr(lens), q=_ptr(q), q_stride=_row_stride(q), mask=_ptr(mask),
-                    scale=float(scale))
-    need = load().eagle_kv_attention_workspace(C.byref(cache.c), C.byref(a))
+        _tensor(mask, "mask", torch.uint8, (B, S, S), dev)
+    if out is None:
+        out, out_ld = _new(q, (N, Hq, hd), torch.bfloat16, stream), Hq * hd
+    else:
+        out_ld = _rows(out, "out", torch.bfloat16, (N, Hq, hd), dev)
+    if lse is True:
+        lse = _new(q, (N, Hq), torch.float32, stream)
+    elif lse is False:
+        lse = None
+    elif lse is not None:
+        _tensor(lse, "lse", torch.float32, (N, Hq), dev)
+    a = KVAttention(B, N, Hq, int(max_rows), int(max_len), S, cu_rows.data_ptr(), lens.data_ptr(), q.data_ptr(), q_ld,
+                    _ptr(mask), float(scale), out.data_ptr(), out_ld, _ptr(lse))
+    ref = C.byref(a)
+    lib = load()
+    need = lib.eagle_kv_attention_workspace(cache.ref, ref)
     if need < 0:
-        _bad(load().eagle_draft_last_error().decode())
-    with torch.cuda.stream(st):
-        if out is None:
-            out = torch.empty((N, Hq, hd), dtype=torch.bfloat16, device=q.device)
-        if lse is True:
-            lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
-        if need and workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    _rows(out, "out", torch.bfloat16, Hq, hd, N)
-    a.out, a.out_stride = _ptr(out), _row_stride(out)
-    if want_lse:
-        _tensor(lse, "lse", torch.float32, (N, Hq))
-        a.lse = _ptr(lse)
+        _bad(lib.eagle_draft_last_error().decode())
     if need:
-        _tensor(workspace, "workspace", torch.uint8, (None,))
-        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+        if workspace is None:
+            workspace = _new(q, (need,), torch.uint8, stream)
+        else:
+            _tensor(workspace, "workspace", torch.uint8, (None,), dev)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     if N:
-        _check(load().eagle_kv_attention(C.byref(cache.c), C.byref(a), _ptr(cache.err), st.cuda_stream))
-    return (out, lse) if want_lse else out
+        _check(lib.eagle_kv_attention(cache.ref, ref, cache.err_ptr, st))
+    return out if lse is None else (out, lse)
 
 
 def kv_attention_workspace(cache: KVCache, n_heads: int, N: int, B: int, max_rows: int, max_len: int) -> int:

@@ -10,7 +10,9 @@
 #include "kvcache.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 using namespace eagle;
@@ -23,6 +25,7 @@ constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes
 constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
 constexpr uint32_t KA_MISC = 2048;
 constexpr int KA_MAX_SLOTS = 14;
+constexpr int KA_FIXED = 6;               // a CTA's fixed cost in tiles
 
 struct KaArgs {
   KvPool pool;
@@ -91,6 +94,22 @@ EAGLE_DEV float max_nan(float x, float y) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
+EAGLE_DEV float max3_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+// (x, y) * (a, a) + (b, b) and (x, y) + (z, w), two fp32 lanes an instruction
+EAGLE_DEV void fma2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+EAGLE_DEV void add2(float& x, float& y, float z, float w) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(z), "f"(w));
+}
 EAGLE_DEV uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -127,6 +146,11 @@ EAGLE_DEV void dequant16(uint2 code, uint32_t scale, uint32_t* h) {
   h[6] = mul_f16x2(e2m1_pair<2>(code.y), s);
   h[7] = mul_f16x2(e2m1_pair<3>(code.y), s);
 }
+
+template <int R>
+EAGLE_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // The tensor-core kernel.  HD 64 or 128; CACHE the cache kind; NB: query-vector tiles per CTA.
 //
@@ -284,10 +308,15 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   __syncthreads();
   tc_fence_after();
 
+  // Registers move from the control and converter warps to the softmax warps, whose threads hold
+  // a row of 128 scores (each role's branch opens with its share; the shares stay within what the
+  // launch gave the CTA).
+  constexpr bool MOVE = THREADS > 256;
   bool ok = true;
-  if (warp == 0) {
+  if (warp < 4) {
+    if constexpr (MOVE) set_regs_down<40>();
     // ------------------------------------------------------------ TMA producer (bf16)
-    if (!F4 && lane == 0) {
+    if (warp == 0 && !F4 && lane == 0) {
       const uint64_t pol = policy_evict_first();
       const int none = a.pool.num_pages * a.pool.Hkv;   // a block outside the map: zeros
       const int per = KA_CH >> a.pool.ps_log;
@@ -317,9 +346,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         }
       }
     }
-  } else if (warp == mma_warp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (warp == mma_warp && lane == 0) {
       const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_CH) : idesc_bf16_f32(128, KA_CH);
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
       for (int u = 0; u <= U && ok; ++u) {
@@ -374,6 +402,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
+    set_regs_down<NB == 2 ? 88 : 128>();
     // ------------------------------ 4-bit pages -> fp16 tiles: 16 dims per thread and step,
     // the next entry's codes in flight while this one is converted
     constexpr int GR = HD / 16;                        // scale groups per row
@@ -428,7 +457,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       if (e + 1 < 2 * T) fetch(e + 1);
     }
     }
-  } else if (warp >= 4 && warp < 4 + 4 * nb) {
+  } else {
+    if constexpr (MOVE) set_regs_up<F4 ? 192 : 224>();
     // ------------------------------------------------------------ softmax
     const int g = (warp - 4) >> 2, lv = tid - 128 - 128 * g, v = v0 + KA_QV * g + lv;
     const bool live = KA_QV * g + lv < qv;
@@ -437,10 +467,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const unsigned long long tree_bits = a.mask && live ? rowbits[irow - i_first] : 0ull;
     const uint32_t tO = tmem + lane_base + T_O + 128 * g;
     float m_run = -INFINITY, l_run = 0.f;              // raw scores' maximum; sum of p
-    if (((warp & 3)) < (g == 0 ? nq0 : nq1)) {
+    if (g < nb && (warp & 3) < (g == 0 ? nq0 : nq1)) {
       for (int t = 0; t < T; ++t) {
         const int u = nb == 2 ? 2 * t + g : t;
-        ok = ok && mbar_wait_sleepy(bar_sf + 8 * (u & 1), (u >> 1) & 1, a.err, abort_flag);
+        ok = ok && mbar_wait(bar_sf + 8 * (u & 1), (u >> 1) & 1, a.err, abort_flag);
         tc_fence_after();
         const uint32_t ts = tmem + lane_base + (u & 1) * KA_CH;
         const int k0 = (t_begin + t) * KA_CH;
@@ -477,24 +507,25 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           }
           full = (vis.lo & vis.hi) == ~0ull;
         }
-        float mt = -INFINITY;
+        // the row's 128 scores stay in registers from the maximum to the probabilities
+        float s[KA_CH];
 #pragma unroll
-        for (int c = 0; c < KA_CH; c += 32) {
-          float s[32];
-          tmem_ld32(ts + c, s);
-          tmem_wait_ld();
-          if (!full) {
-            const uint32_t bits = static_cast<uint32_t>((c < 64 ? vis.lo : vis.hi) >> (c & 32));
+        for (int c = 0; c < KA_CH; c += 32) tmem_ld32(ts + c, s + c);
+        tmem_wait_ld();
+        if (!full) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? s[e] : -INFINITY;
-          }
-          float m4[4];
+          for (int e = 0; e < 64; ++e) s[e] = (vis.lo >> e) & 1ull ? s[e] : -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = s[e];
-#pragma unroll
-          for (int e = 4; e < 32; ++e) m4[e & 3] = max_nan(m4[e & 3], s[e]);
-          mt = max_nan(mt, max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])));
+          for (int e = 0; e < 64; ++e) s[64 + e] = (vis.hi >> e) & 1ull ? s[64 + e] : -INFINITY;
         }
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = max_nan(s[e], s[e + 8]);
+#pragma unroll
+        for (int e = 16; e < KA_CH; e += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m8[k] = max3_nan(m8[k], s[e + k], s[e + 8 + k]);
+        const float mt = max_nan(max3_nan(max3_nan(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3_nan(m8[5], m8[6], m8[7]));
         float f = 1.f;
         bool resc = false;
         if (mt != -INFINITY) {
@@ -523,43 +554,33 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           tmem_wait_st();
         }
         l_run *= f;
-        const bool pw = live && ok && m_run != -INFINITY;
-        const float mb = m_run * row_scale - LIFT;
-        float p4[4] = {0.f, 0.f, 0.f, 0.f};
+        // a row without a key so far takes the maximum as 0: every score is -inf, every p is 0
+        // (lanes past the last vector hold scores of 0 and are never read)
+        const float mb = (m_run == -INFINITY ? 0.f : m_run * row_scale) - LIFT;
+        float p8[8] = {};
 #pragma unroll
         for (int c = 0; c < KA_CH; c += 32) {
-          float s[32];
-          tmem_ld32(ts + c, s);
-          tmem_wait_ld();
-          if (pw) {
-            const uint32_t bits = full ? 0xffffffffu : static_cast<uint32_t>((c < 64 ? vis.lo : vis.hi) >> (c & 32));
-            if (full) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] = fast_exp2(fmaf(s[e], row_scale, -mb));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? fast_exp2(fmaf(s[e], row_scale, -mb)) : 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) p4[e & 3] += s[e];
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = 0.f;
+          for (int e = c; e < c + 32; e += 2) {
+            fma2(s[e], s[e + 1], row_scale, -mb);
+            s[e] = fast_exp2(s[e]);
+            s[e + 1] = fast_exp2(s[e + 1]);
+            add2(p8[e & 7], p8[(e & 7) + 1], s[e], s[e + 1]);
           }
           if (HILO) {
             uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) split2_packed(s[2 * e], s[2 * e + 1], pk[e], pk[16 + e]);
+            for (int e = 0; e < 16; ++e) split2_packed(s[c + 2 * e], s[c + 2 * e + 1], pk[e], pk[16 + e]);
             tmem_st32(ts + c, pk);
           } else {
             float pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              pk[e] = __uint_as_float(F4 ? pack_f16(s[2 * e], s[2 * e + 1]) : pack_bf16(s[2 * e], s[2 * e + 1]));
-            tmem_st16(ts + c / 2, pk);   // over columns whose scores are read already
+              pk[e] = __uint_as_float(F4 ? pack_f16(s[c + 2 * e], s[c + 2 * e + 1]) : pack_bf16(s[c + 2 * e], s[c + 2 * e + 1]));
+            tmem_st16(ts + c / 2, pk);
           }
         }
-        l_run += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+        l_run += ((p8[0] + p8[1]) + (p8[2] + p8[3])) + ((p8[4] + p8[5]) + (p8[6] + p8[7]));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -696,9 +717,19 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
   const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
-  const long long want = 4ll * num_sms();
-  long long per = std::max(1ll, (base * tiles + want - 1) / want);
-  if (base * tiles > num_sms()) per = std::max(per, std::min(8ll, (base * tiles + num_sms() - 1) / num_sms()));
+  // key ranges: the split whose waves of CTAs (one per SM) take least, a CTA costing its tiles
+  // and as much again as KA_FIXED tiles for its start, its result and the joining of the ranges
+  const long long sms = num_sms();
+  long long per = tiles, best = -1;
+  for (long long n = 1; n <= tiles && n <= 4096; ++n) {
+    const long long t = (tiles + n - 1) / n;
+    const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + KA_FIXED);
+    if (best < 0 || cost < best) {
+      best = cost;
+      per = t;
+    }
+  }
+  if (const char* ov = getenv("EAGLE_KV_TILES")) per = std::max(1, atoi(ov));
   per = std::min(per, tiles);
   p.tiles_per_cta = static_cast<int>(per);
   p.splits = static_cast<int>((tiles + per - 1) / per);
@@ -721,10 +752,16 @@ eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t*
 
 template <int HD, int CACHE, int NB>
 cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, cudaStream_t st) {
-  const void* fn = reinterpret_cast<const void*>(kv_attention_tc<HD, CACHE, NB>);
-  size_t cap = 0;
-  cudaError_t e = allow_max_smem(fn, &cap);
+  static std::atomic<size_t> granted[64];   // shared memory per device, set on its first call
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  size_t cap = dev < 64 ? granted[dev].load() : 0;
+  if (!cap) {
+    e = allow_max_smem(reinterpret_cast<const void*>(kv_attention_tc<HD, CACHE, NB>), &cap);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) granted[dev].store(cap);
+  }
   const size_t fixed = (NB == 2 ? 2 * ka_entry(HD) : 0) + KA_MISC + 1024;
   const int ns = std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
   const size_t smem = fixed + static_cast<size_t>(ns) * ka_entry(HD);
