@@ -147,6 +147,12 @@ EAGLE_DEV void dequant16(uint2 code, uint32_t scale, uint32_t* h) {
   h[7] = mul_f16x2(e2m1_pair<3>(code.y), s);
 }
 
+// one thread of a converged warp, the same one every time
+EAGLE_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 template <int R>
 EAGLE_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -347,7 +353,9 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       }
     }
     // ------------------------------------------------------------ MMA issuer
-    if (warp == mma_warp && lane == 0) {
+    // The whole warp walks the units, so that the descriptors stay in uniform registers; one
+    // elected thread issues.  (A loop inside `lane == 0` spent 130 cycles on each instruction.)
+    if (warp == mma_warp) {
       const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_CH) : idesc_bf16_f32(128, KA_CH);
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
       for (int u = 0; u <= U && ok; ++u) {
@@ -355,42 +363,50 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           const int t = nb == 2 ? u >> 1 : u, g = nb == 2 ? u & 1 : 0, e = 2 * t, slot = e % NS;
           if (g == 0) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
           ok = ok && mbar_wait(bar_pe + 8 * (u & 1), ((u >> 1) & 1) ^ 1, a.err, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + (u & 1) * KA_CH;
           const uint64_t dk = smem_desc_sw128(ring_u + slot * ENTRY);
           const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < HD / 16; ++j) {
-            const uint32_t ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
-            if (NB == 1) tc_mma_bf16_ta(d, tmem + T_Q + 8 * j, dk + ko, id1, j > 0 ? 1u : 0u);
-            else tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
+            for (int j = 0; j < HD / 16; ++j) {
+              const uint32_t ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
+              if (NB == 1) tc_mma_bf16_ta(d, tmem + T_Q + 8 * j, dk + ko, id1, j > 0 ? 1u : 0u);
+              else tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
+            }
+            tc_commit(bar_sf + 8 * (u & 1));
+            if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
           }
-          tc_commit(bar_sf + 8 * (u & 1));
-          if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
+          __syncwarp();
         }
         if (u > 0) {   // O += P V of unit u - 1
           const int w = u - 1, t = nb == 2 ? w >> 1 : w, g = nb == 2 ? w & 1 : 0, e = 2 * t + 1, slot = e % NS;
           if (g == 0) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
           ok = ok && mbar_wait(bar_pf + 8 * (w & 1), (w >> 1) & 1, a.err, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dv = smem_desc_sw128_mn(ring_u + slot * ENTRY, HALF, 1024);
           const uint32_t tp = tmem + (w & 1) * KA_CH, tO = tmem + T_O + 128 * g;
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < KA_CH / 16; ++j) {
-            const uint32_t first = (t > 0 || j > 0) ? 1u : 0u;
-            if (HILO) {   // keys [32 c, 32 c + 32): 16 hi columns at 32 c, 16 lo columns behind
-              const uint32_t pa = tp + 32 * (j >> 1) + 8 * (j & 1);
-              tc_mma_bf16_ta(tO, pa, dv + j * 128, id2, first);
-              tc_mma_bf16_ta(tO, pa + 16, dv + j * 128, id2, 1u);
-            } else {
-              tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, first);
+            for (int j = 0; j < KA_CH / 16; ++j) {
+              const uint32_t first = (t > 0 || j > 0) ? 1u : 0u;
+              if (HILO) {   // keys [32 c, 32 c + 32): 16 hi columns at 32 c, 16 lo columns behind
+                const uint32_t pa = tp + 32 * (j >> 1) + 8 * (j & 1);
+                tc_mma_bf16_ta(tO, pa, dv + j * 128, id2, first);
+                tc_mma_bf16_ta(tO, pa + 16, dv + j * 128, id2, 1u);
+              } else {
+                tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, first);
+              }
             }
+            tc_commit(bar_pe + 8 * (w & 1));
+            if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
+            tc_commit(bar_od + 8 * g);
           }
-          tc_commit(bar_pe + 8 * (w & 1));
-          if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
-          tc_commit(bar_od + 8 * g);
+          __syncwarp();
         }
       }
       if (!ok) {   // let MMAs already issued finish before TMEM is released
@@ -398,7 +414,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         while (clock64() - t0 < 4000000) {
         }
       }
-      tc_commit(bar_fin);
+      __syncwarp();
+      if (elect_one()) tc_commit(bar_fin);
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
