@@ -20,7 +20,8 @@ using namespace eagle;
 namespace {
 
 constexpr int KA_MAX_GROUP = 64;
-constexpr int KA_CH = 128;                 // keys per tile
+constexpr int KA_CH = 128;                 // keys per tile (a ring entry)
+constexpr int KA_H = 64;                   // keys per unit of work (half a tile)
 constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes)
 constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
 constexpr uint32_t KA_MISC = 2048;
@@ -147,6 +148,9 @@ EAGLE_DEV void dequant16(uint2 code, uint32_t scale, uint32_t* h) {
   h[7] = mul_f16x2(e2m1_pair<3>(code.y), s);
 }
 
+// a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
+// registers (the operands of tcgen05.mma)
+EAGLE_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // one thread of a converged warp, the same one every time
 EAGLE_DEV bool elect_one() {
   uint32_t r;
@@ -164,8 +168,10 @@ EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;
 // 64 dims, 128-byte swizzle).  bf16 pages come by TMA, one box per page and 64 dims; 4-bit pages
 // are read by converter warps, which write fp16 tiles.  Q is the A operand of S = Q K^T, in TMEM
 // (NB = 1) or shared memory (NB = 2, where S and O of two tiles take all 512 columns); P replaces
-// S in TMEM as the A operand of O += P V.  Work goes in units (key tile, query tile), S in
-// buffer unit & 1: one unit's QK^T and PV overlap another's softmax.
+// S in TMEM as the A operand of O += P V.  Work goes in units of 64 keys, two S buffers per query
+// tile: a unit's QK^T runs while the unit before it is in the softmax, so the softmax warps find
+// their scores ready.  (One 128-key buffer per query tile, whose QK^T had to wait for the
+// softmax and the P V of the same buffer, took 4160 cycles per 128 keys and two query tiles.)
 //
 // A page that the keys end inside is loaded from a negative row, so that the copy reads zeros
 // and then the valid rows: memory behind the last key never enters a product (it may hold NaN,
@@ -191,19 +197,23 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   constexpr uint32_t T_O = 256, T_Q = 384;
   extern __shared__ uint8_t ka_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ka_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ring_u = smem_u32(sm);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const uint32_t ring_u = uniform(smem_u32(sm));
   const uint32_t q_u = ring_u + static_cast<uint32_t>(NS) * ENTRY;       // NB = 2: Q tiles
   uint8_t* misc = sm + static_cast<uint32_t>(NS) * ENTRY + (NB == 2 ? 2 * ENTRY : 0);
   const uint32_t misc_u = smem_u32(misc);
-  const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 240,
-                 bar_pe = misc_u + 256, bar_od = misc_u + 272, bar_fin = misc_u + 288;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 296);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 300);
+  const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 256,
+                 bar_pe = misc_u + 288, bar_fin = misc_u + 336;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 344);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 348);
   unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [128] tree mask rows
 
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / a.blocks, blk0 = blockIdx.z - b * a.blocks;
-  const Req rq = request(a, b);
+  Req rq = request(a, b);
+  rq.row0 = uniform(rq.row0);
+  rq.R = uniform(rq.R);
+  rq.ctx = uniform(rq.ctx);
+  rq.len = uniform(rq.len);
   const int v0 = blk0 * KA_QV * NB;
   const int qv = min(rq.R * a.G - v0, KA_QV * NB);
   if (qv <= 0) return;
@@ -216,20 +226,23 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   const int T = max(0, min(all_tiles - t_begin, a.tiles_per_cta));
   const int nb = NB == 2 && qv > KA_QV ? 2 : 1;
   const int nq0 = min(4, (min(qv, KA_QV) + 31) / 32), nq1 = nb == 2 ? (qv - KA_QV + 31) / 32 : nq0;
-  const int U = T * nb;
   const int mma_warp = 3;
   const int ps = 1 << a.pool.ps_log;
+  // the page that the request's keys end inside: its rows sit at the end of the box (bf16)
+  const int end_page = rq.len >> a.pool.ps_log, end_rows = F4 ? 0 : rq.len & (ps - 1);
+  // units of 64 columns (none when this range lies behind what the block sees)
+  const int columns = end_rows && (end_page << a.pool.ps_log) < seen ? (end_page + 1) << a.pool.ps_log : seen;
+  const int W = min(2 * T, (columns - t_begin * KA_CH + KA_H - 1) / KA_H);
 
   if (tid == 0) {
     for (int s = 0; s < KA_MAX_SLOTS; ++s) {
       mbar_init(bar_kvf + 8 * s, F4 ? CONV / 32 : 1);
       mbar_init(bar_kve + 8 * s, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {              // query tile i >> 1, buffer i & 1
       mbar_init(bar_sf + 8 * i, 1);
-      mbar_init(bar_pf + 8 * i, i == 0 || nb == 1 ? nq0 : nq1);
+      mbar_init(bar_pf + 8 * i, i < 2 ? nq0 : nq1);
       mbar_init(bar_pe + 8 * i, 1);
-      mbar_init(bar_od + 8 * i, 1);
     }
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
@@ -251,10 +264,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
-  // the page that the request's keys end inside: its rows sit at the end of the box (bf16)
-  const int end_page = rq.len >> a.pool.ps_log, end_rows = F4 ? 0 : rq.len & (ps - 1);
   auto box_row = [&](int pi) { return pi == end_page && end_rows ? end_rows - ps : 0; };
 
   // queries: thread = vector; bf16 as they are, or fp16 scaled by a power of two so that the
@@ -317,7 +328,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   // Registers move from the control and converter warps to the softmax warps, whose threads hold
   // a row of 128 scores (each role's branch opens with its share; the shares stay within what the
   // launch gave the CTA).
-  constexpr bool MOVE = THREADS > 256;
+  constexpr bool MOVE = THREADS > 384;
   bool ok = true;
   if (warp < 4) {
     if constexpr (MOVE) set_regs_down<40>();
@@ -356,18 +367,19 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     // The whole warp walks the units, so that the descriptors stay in uniform registers; one
     // elected thread issues.  (A loop inside `lane == 0` spent 130 cycles on each instruction.)
     if (warp == mma_warp) {
-      const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_CH) : idesc_bf16_f32(128, KA_CH);
+      const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_H) : idesc_bf16_f32(128, KA_H);
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
-      for (int u = 0; u <= U && ok; ++u) {
-        if (u < U) {   // S = Q K^T of unit u, once P V of unit u - 2 (same buffer) is done
-          const int t = nb == 2 ? u >> 1 : u, g = nb == 2 ? u & 1 : 0, e = 2 * t, slot = e % NS;
-          if (g == 0) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
-          ok = ok && mbar_wait(bar_pe + 8 * (u & 1), ((u >> 1) & 1) ^ 1, a.err, abort_flag);
+      for (int w = 0; w <= W && ok; ++w) {
+        for (int g = 0; g < nb && ok && w < W; ++g) {
+          // S = Q K^T of unit w, once P V of unit w - 2 (same buffer) is done
+          const int e = w & ~1, slot = e % NS, buf = 2 * g + (w & 1);
+          if (g == 0 && !(w & 1)) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
+          ok = ok && mbar_wait(bar_pe + 8 * buf, ((w >> 1) & 1) ^ 1, a.err, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tmem + (u & 1) * KA_CH;
-          const uint64_t dk = smem_desc_sw128(ring_u + slot * ENTRY);
+          const uint32_t d = tmem + buf * KA_H;
+          const uint64_t dk = smem_desc_sw128(ring_u + slot * ENTRY + (w & 1) * (KA_H * 128));
           const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
           if (elect_one()) {
 #pragma unroll
@@ -376,24 +388,25 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
               if (NB == 1) tc_mma_bf16_ta(d, tmem + T_Q + 8 * j, dk + ko, id1, j > 0 ? 1u : 0u);
               else tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
             }
-            tc_commit(bar_sf + 8 * (u & 1));
-            if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
+            tc_commit(bar_sf + 8 * buf);
+            if (g == nb - 1 && ((w & 1) || w == W - 1)) tc_commit(bar_kve + 8 * slot);
           }
           __syncwarp();
         }
-        if (u > 0) {   // O += P V of unit u - 1
-          const int w = u - 1, t = nb == 2 ? w >> 1 : w, g = nb == 2 ? w & 1 : 0, e = 2 * t + 1, slot = e % NS;
-          if (g == 0) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
-          ok = ok && mbar_wait(bar_pf + 8 * (w & 1), (w >> 1) & 1, a.err, abort_flag);
+        const int x = w - 1;   // O += P V of unit x
+        for (int g = 0; g < nb && ok && x >= 0; ++g) {
+          const int e = x | 1, slot = e % NS, buf = 2 * g + (x & 1);
+          if (g == 0 && !(x & 1)) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
+          ok = ok && mbar_wait(bar_pf + 8 * buf, (x >> 1) & 1, a.err, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dv = smem_desc_sw128_mn(ring_u + slot * ENTRY, HALF, 1024);
-          const uint32_t tp = tmem + (w & 1) * KA_CH, tO = tmem + T_O + 128 * g;
+          const uint64_t dv = smem_desc_sw128_mn(ring_u + slot * ENTRY + (x & 1) * (KA_H * 128), HALF, 1024);
+          const uint32_t tp = tmem + buf * KA_H, tO = tmem + T_O + 128 * g;
           if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < KA_CH / 16; ++j) {
-              const uint32_t first = (t > 0 || j > 0) ? 1u : 0u;
+            for (int j = 0; j < KA_H / 16; ++j) {
+              const uint32_t first = (x > 0 || j > 0) ? 1u : 0u;
               if (HILO) {   // keys [32 c, 32 c + 32): 16 hi columns at 32 c, 16 lo columns behind
                 const uint32_t pa = tp + 32 * (j >> 1) + 8 * (j & 1);
                 tc_mma_bf16_ta(tO, pa, dv + j * 128, id2, first);
@@ -402,9 +415,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, first);
               }
             }
-            tc_commit(bar_pe + 8 * (w & 1));
-            if (g == nb - 1) tc_commit(bar_kve + 8 * slot);
-            tc_commit(bar_od + 8 * g);
+            tc_commit(bar_pe + 8 * buf);
+            if (g == nb - 1 && ((x & 1) || x == W - 1)) tc_commit(bar_kve + 8 * slot);
           }
           __syncwarp();
         }
@@ -419,7 +431,6 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
-    set_regs_down<NB == 2 ? 88 : 128>();
     // ------------------------------ 4-bit pages -> fp16 tiles: 16 dims per thread and step,
     // the next entry's codes in flight while this one is converted
     constexpr int GR = HD / 16;                        // scale groups per row
@@ -475,7 +486,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
     }
   } else {
-    if constexpr (MOVE) set_regs_up<F4 ? 192 : 224>();
+    if constexpr (MOVE) set_regs_up<152>();
     // ------------------------------------------------------------ softmax
     const int g = (warp - 4) >> 2, lv = tid - 128 - 128 * g, v = v0 + KA_QV * g + lv;
     const bool live = KA_QV * g + lv < qv;
@@ -485,61 +496,50 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const uint32_t tO = tmem + lane_base + T_O + 128 * g;
     float m_run = -INFINITY, l_run = 0.f;              // raw scores' maximum; sum of p
     if (g < nb && (warp & 3) < (g == 0 ? nq0 : nq1)) {
-      for (int t = 0; t < T; ++t) {
-        const int u = nb == 2 ? 2 * t + g : t;
-        ok = ok && mbar_wait(bar_sf + 8 * (u & 1), (u >> 1) & 1, a.err, abort_flag);
+      for (int w = 0; w < W; ++w) {
+        const int buf = 2 * g + (w & 1);
+        ok = ok && mbar_wait(bar_sf + 8 * buf, (w >> 1) & 1, a.err, abort_flag);
         tc_fence_after();
-        const uint32_t ts = tmem + lane_base + (u & 1) * KA_CH;
-        const int k0 = (t_begin + t) * KA_CH;
-        // columns this vector sees; keys [k0, k0 + 128) but for the shifted last page
-        Bits vis{~0ull, ~0ull};
-        bool full = k0 + KA_CH <= rq.ctx;
-        if (!full) {
-          const int off = rq.ctx - k0;                 // column of the step's first own row
+        const uint32_t ts = tmem + lane_base + buf * KA_H;
+        // the row's scores stay in registers from the maximum to the probabilities
+        float s[KA_H];
+        tmem_ld32(ts, s);
+        tmem_ld32(ts + 32, s + 32);
+        // columns this vector sees; keys k0, k0 + 1, ... but for the shifted last page
+        const int k0 = t_begin * KA_CH + w * KA_H;
+        const int kt = k0 & ~(KA_CH - 1), off = rq.ctx - kt;   // the tile; its column of the first own row
+        unsigned long long vis = ~0ull;
+        if (off < KA_CH) {
+          Bits seen_cols;
           if (a.mask) {
             const Bits own = shift_up(tree_bits, off);
-            vis = bits_below(off);
-            vis.lo |= own.lo;
-            vis.hi |= own.hi;
+            seen_cols = bits_below(off);
+            seen_cols.lo |= own.lo;
+            seen_cols.hi |= own.hi;
           } else {
-            vis = bits_below(off + irow + 1);
+            seen_cols = bits_below(off + irow + 1);
           }
-          if (end_rows) {
-            const int at = (end_page << a.pool.ps_log) - k0, sh = ps - end_rows;   // the page's first column
-            if (at >= 0 && at < KA_CH) {
-              const Bits below = bits_below(at);
-              // columns from `at` on move up by sh
-              Bits up;
-              const unsigned long long mlo = vis.lo & ~below.lo, mhi = vis.hi & ~below.hi;
-              if (sh < 64) {
-                up.lo = mlo << sh;
-                up.hi = (mhi << sh) | (mlo >> (64 - sh));
-              } else {
-                up.lo = 0ull;
-                up.hi = sh < 128 ? mlo << (sh - 64) : 0ull;
-              }
-              vis.lo = (vis.lo & below.lo) | up.lo;
-              vis.hi = (vis.hi & below.hi) | up.hi;
-            }
+          const int at = (end_page << a.pool.ps_log) - kt, sh = ps - end_rows;   // the last page's first column
+          if (end_rows && at >= 0 && at < KA_CH) {   // columns from `at` on move up by sh (1 .. 127)
+            const Bits below = bits_below(at);
+            const unsigned long long mlo = seen_cols.lo & ~below.lo, mhi = seen_cols.hi & ~below.hi;
+            const unsigned long long ulo = sh < 64 ? mlo << sh : 0ull;
+            const unsigned long long uhi = sh < 64 ? (mhi << sh) | (mlo >> (64 - sh)) : mlo << (sh - 64);
+            seen_cols.lo = (seen_cols.lo & below.lo) | ulo;
+            seen_cols.hi = (seen_cols.hi & below.hi) | uhi;
           }
-          full = (vis.lo & vis.hi) == ~0ull;
+          vis = w & 1 ? seen_cols.hi : seen_cols.lo;
         }
-        // the row's 128 scores stay in registers from the maximum to the probabilities
-        float s[KA_CH];
-#pragma unroll
-        for (int c = 0; c < KA_CH; c += 32) tmem_ld32(ts + c, s + c);
         tmem_wait_ld();
-        if (!full) {
+        if (vis != ~0ull) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) s[e] = (vis.lo >> e) & 1ull ? s[e] : -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) s[64 + e] = (vis.hi >> e) & 1ull ? s[64 + e] : -INFINITY;
+          for (int e = 0; e < KA_H; ++e) s[e] = (vis >> e) & 1ull ? s[e] : -INFINITY;
         }
         float m8[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) m8[e] = max_nan(s[e], s[e + 8]);
 #pragma unroll
-        for (int e = 16; e < KA_CH; e += 16)
+        for (int e = 16; e < KA_H; e += 16)
 #pragma unroll
           for (int k = 0; k < 8; ++k) m8[k] = max3_nan(m8[k], s[e + k], s[e + 8 + k]);
         const float mt = max_nan(max3_nan(max3_nan(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3_nan(m8[5], m8[6], m8[7]));
@@ -555,8 +555,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           }
         }
         if (__any_sync(0xffffffffu, resc)) {
-          // rows whose maximum rose: scale them in O once this tile's earlier P V are done
-          ok = ok && mbar_wait_sleepy(bar_od + 8 * g, (t - 1) & 1, a.err, abort_flag);
+          // rows whose maximum rose: scale them in O once the earlier P V are done
+          ok = ok && mbar_wait(bar_pe + 8 * (buf ^ 1), ((w - 1) >> 1) & 1, a.err, abort_flag);
           tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < HD; c0 += 32) {
@@ -576,7 +576,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const float mb = (m_run == -INFINITY ? 0.f : m_run * row_scale) - LIFT;
         float p8[8] = {};
 #pragma unroll
-        for (int c = 0; c < KA_CH; c += 32) {
+        for (int c = 0; c < KA_H; c += 32) {
 #pragma unroll
           for (int e = c; e < c + 32; e += 2) {
             fma2(s[e], s[e + 1], row_scale, -mb);
@@ -601,7 +601,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_pf + 8 * (u & 1));
+        if (lane == 0) mbar_arrive(bar_pf + 8 * buf);
       }
       // ---- this CTA's result of vector v
       if (T > 0) ok = mbar_wait_sleepy(bar_fin, 0, a.err, abort_flag) && ok;
