@@ -151,6 +151,18 @@ EAGLE_DEV void dequant16(uint2 code, uint32_t scale, uint32_t* h) {
 // a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
 // registers (the operands of tcgen05.mma)
 EAGLE_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// A place in the ring of NS entries: slot and the parity of its turn.  (Stepped, not computed: a
+// division by NS costs the MMA warp as much as it takes to issue a unit.)
+struct RingPos {
+  int slot, turn;
+  EAGLE_DEV void step(int n, int NS) {
+    slot += n;
+    if (slot >= NS) {
+      slot -= NS;
+      turn ^= 1;
+    }
+  }
+};
 // one thread of a converged warp, the same one every time
 EAGLE_DEV bool elect_one() {
   uint32_t r;
@@ -224,27 +236,26 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   const int t_begin = split * a.tiles_per_cta;
   if (t_begin * KA_CH >= rq.len) return;             // (not a range of this request at all)
   const int T = max(0, min(all_tiles - t_begin, a.tiles_per_cta));
-  const int nb = NB == 2 && qv > KA_QV ? 2 : 1;
+  const int nb = uniform(NB == 2 && qv > KA_QV ? 2 : 1);
   const int nq0 = min(4, (min(qv, KA_QV) + 31) / 32), nq1 = nb == 2 ? (qv - KA_QV + 31) / 32 : nq0;
-  const int mma_warp = 3;
   const int ps = 1 << a.pool.ps_log;
   // the page that the request's keys end inside: its rows sit at the end of the box (bf16)
   const int end_page = rq.len >> a.pool.ps_log, end_rows = F4 ? 0 : rq.len & (ps - 1);
   // units of 64 columns (none when this range lies behind what the block sees)
   const int columns = end_rows && (end_page << a.pool.ps_log) < seen ? (end_page + 1) << a.pool.ps_log : seen;
-  const int W = min(2 * T, (columns - t_begin * KA_CH + KA_H - 1) / KA_H);
+  const int W = uniform(min(2 * T, (columns - t_begin * KA_CH + KA_H - 1) / KA_H));
 
   if (tid == 0) {
     for (int s = 0; s < KA_MAX_SLOTS; ++s) {
       mbar_init(bar_kvf + 8 * s, F4 ? CONV / 32 : 1);
-      mbar_init(bar_kve + 8 * s, 1);
+      mbar_init(bar_kve + 8 * s, nb);
     }
     for (int i = 0; i < 4; ++i) {              // query tile i >> 1, buffer i & 1
       mbar_init(bar_sf + 8 * i, 1);
       mbar_init(bar_pf + 8 * i, i < 2 ? nq0 : nq1);
       mbar_init(bar_pe + 8 * i, 1);
     }
-    mbar_init(bar_fin, 1);
+    mbar_init(bar_fin, nb);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -337,9 +348,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       const uint64_t pol = policy_evict_first();
       const int none = a.pool.num_pages * a.pool.Hkv;   // a block outside the map: zeros
       const int per = KA_CH >> a.pool.ps_log;
-      for (int e = 0; e < 2 * T && ok; ++e) {
-        const int slot = e % NS;
-        if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, ((e / NS) & 1) ^ 1, a.err, abort_flag);
+      RingPos rp{0, 0};
+      for (int e = 0; e < 2 * T && ok; ++e, rp.step(1, NS)) {
+        const int slot = rp.slot;
+        if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
         if (!ok) break;
         const uint32_t dst = ring_u + slot * ENTRY, bar = bar_kvf + 8 * slot;
         mbar_arrive_expect_tx(bar, ENTRY);
@@ -364,61 +376,62 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       }
     }
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks the units, so that the descriptors stay in uniform registers; one
-    // elected thread issues.  (A loop inside `lane == 0` spent 130 cycles on each instruction.)
-    if (warp == mma_warp) {
+    // One thread per query tile walks the units and issues; nothing in the loop divides or votes,
+    // since every hundred cycles here are a hundred of the tensor cores' idle time.  (One thread
+    // for both tiles: 1.26 us per 64 keys.)
+    if (warp >= 2 && warp - 2 < nb && elect_one()) {
+      const int g = warp - 2;
       const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_H) : idesc_bf16_f32(128, KA_H);
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
+      const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
+      const uint32_t tO = tmem + T_O + 128 * g;
+      RingPos kp{0, 0}, vp{1, 0};            // the key tile of unit w, the value tile of unit w - 1
       for (int w = 0; w <= W && ok; ++w) {
-        for (int g = 0; g < nb && ok && w < W; ++g) {
+        if (w < W) {
           // S = Q K^T of unit w, once P V of unit w - 2 (same buffer) is done
-          const int e = w & ~1, slot = e % NS, buf = 2 * g + (w & 1);
-          if (g == 0 && !(w & 1)) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
+          const int buf = 2 * g + (w & 1);
+          if (!(w & 1)) ok = mbar_wait(bar_kvf + 8 * kp.slot, kp.turn, a.err, abort_flag);
           ok = ok && mbar_wait(bar_pe + 8 * buf, ((w >> 1) & 1) ^ 1, a.err, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + buf * KA_H;
-          const uint64_t dk = smem_desc_sw128(ring_u + slot * ENTRY + (w & 1) * (KA_H * 128));
-          const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
-          if (elect_one()) {
+          const uint64_t dk = smem_desc_sw128(ring_u + kp.slot * ENTRY + (w & 1) * (KA_H * 128));
 #pragma unroll
-            for (int j = 0; j < HD / 16; ++j) {
-              const uint32_t ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
-              if (NB == 1) tc_mma_bf16_ta(d, tmem + T_Q + 8 * j, dk + ko, id1, j > 0 ? 1u : 0u);
-              else tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
-            }
-            tc_commit(bar_sf + 8 * buf);
-            if (g == nb - 1 && ((w & 1) || w == W - 1)) tc_commit(bar_kve + 8 * slot);
+          for (int j = 0; j < HD / 16; ++j) {
+            const uint32_t ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
+            if (NB == 1) tc_mma_bf16_ta(d, tmem + T_Q + 8 * j, dk + ko, id1, j > 0 ? 1u : 0u);
+            else tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
           }
-          __syncwarp();
+          tc_commit(bar_sf + 8 * buf);
+          if ((w & 1) || w == W - 1) {
+            tc_commit(bar_kve + 8 * kp.slot);
+            kp.step(2, NS);
+          }
         }
-        const int x = w - 1;   // O += P V of unit x
-        for (int g = 0; g < nb && ok && x >= 0; ++g) {
-          const int e = x | 1, slot = e % NS, buf = 2 * g + (x & 1);
-          if (g == 0 && !(x & 1)) ok = mbar_wait(bar_kvf + 8 * slot, (e / NS) & 1, a.err, abort_flag);
+        if (w > 0) {   // O += P V of unit x
+          const int x = w - 1, buf = 2 * g + (x & 1);
+          if (!(x & 1)) ok = mbar_wait(bar_kvf + 8 * vp.slot, vp.turn, a.err, abort_flag);
           ok = ok && mbar_wait(bar_pf + 8 * buf, (x >> 1) & 1, a.err, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dv = smem_desc_sw128_mn(ring_u + slot * ENTRY + (x & 1) * (KA_H * 128), HALF, 1024);
-          const uint32_t tp = tmem + buf * KA_H, tO = tmem + T_O + 128 * g;
-          if (elect_one()) {
+          const uint64_t dv = smem_desc_sw128_mn(ring_u + vp.slot * ENTRY + (x & 1) * (KA_H * 128), HALF, 1024);
+          const uint32_t tp = tmem + buf * KA_H;
 #pragma unroll
-            for (int j = 0; j < KA_H / 16; ++j) {
-              const uint32_t first = (x > 0 || j > 0) ? 1u : 0u;
-              if (HILO) {   // keys [32 c, 32 c + 32): 16 hi columns at 32 c, 16 lo columns behind
-                const uint32_t pa = tp + 32 * (j >> 1) + 8 * (j & 1);
-                tc_mma_bf16_ta(tO, pa, dv + j * 128, id2, first);
-                tc_mma_bf16_ta(tO, pa + 16, dv + j * 128, id2, 1u);
-              } else {
-                tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, first);
-              }
+          for (int j = 0; j < KA_H / 16; ++j) {
+            const uint32_t first = (x > 0 || j > 0) ? 1u : 0u;
+            if (HILO) {   // keys [32 c, 32 c + 32): 16 hi columns at 32 c, 16 lo columns behind
+              const uint32_t pa = tp + 32 * (j >> 1) + 8 * (j & 1);
+              tc_mma_bf16_ta(tO, pa, dv + j * 128, id2, first);
+              tc_mma_bf16_ta(tO, pa + 16, dv + j * 128, id2, 1u);
+            } else {
+              tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, first);
             }
-            tc_commit(bar_pe + 8 * buf);
-            if (g == nb - 1 && ((x & 1) || x == W - 1)) tc_commit(bar_kve + 8 * slot);
           }
-          __syncwarp();
+          tc_commit(bar_pe + 8 * buf);
+          if ((x & 1) || x == W - 1) {
+            tc_commit(bar_kve + 8 * vp.slot);
+            vp.step(2, NS);
+          }
         }
       }
       if (!ok) {   // let MMAs already issued finish before TMEM is released
@@ -426,8 +439,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         while (clock64() - t0 < 4000000) {
         }
       }
-      __syncwarp();
-      if (elect_one()) tc_commit(bar_fin);
+      tc_commit(bar_fin);
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
@@ -459,9 +471,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       }
     };
     if (T > 0) fetch(0);
-    for (int e = 0; e < 2 * T; ++e) {
-      const int slot = e % NS;
-      if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, ((e / NS) & 1) ^ 1, a.err, abort_flag);
+    RingPos rp{0, 0};
+    for (int e = 0; e < 2 * T; ++e, rp.step(1, NS)) {
+      const int slot = rp.slot;
+      if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
       if (__any_sync(0xffffffffu, !ok)) break;
       const uint32_t dst = ring_u + slot * ENTRY + (gidx >> 2) * HALF;
 #pragma unroll
