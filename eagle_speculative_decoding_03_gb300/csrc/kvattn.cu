@@ -111,6 +111,12 @@ EAGLE_DEV void add2(float& x, float& y, float z, float w) {
       "mov.b64 {%0, %1}, p;\n\t}"
       : "+f"(x), "+f"(y) : "f"(z), "f"(w));
 }
+// `bytes` (a multiple of 16) of global memory into shared memory, completing on `bar`
+EAGLE_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
 EAGLE_DEV uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -178,7 +184,7 @@ EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;
 //
 // Shared memory is a ring of entries, key tile and value tile in turn (128 rows of 128 bytes per
 // 64 dims, 128-byte swizzle).  bf16 pages come by TMA, one box per page and 64 dims; 4-bit pages
-// are read by converter warps, which write fp16 tiles.  Q is the A operand of S = Q K^T, in TMEM
+// by bulk copies into a ring of raw tiles, which converter warps turn into fp16 tiles.  Q is the A operand of S = Q K^T, in TMEM
 // (NB = 1) or shared memory (NB = 2, where S and O of two tiles take all 512 columns); P replaces
 // S in TMEM as the A operand of O += P V.  Work goes in units of 64 keys, two S buffers per query
 // tile: a unit's QK^T runs while the unit before it is in the softmax, so the softmax warps find
@@ -195,6 +201,9 @@ EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;
 // error of half a bf16 step's size).  l sums the unrounded p.
 __host__ __device__ constexpr int ka_threads(int cache, int nb) { return cache == EAGLE_CACHE_F4 ? 512 : 128 + 128 * nb; }
 __host__ __device__ constexpr uint32_t ka_entry(int hd) { return static_cast<uint32_t>(hd) * 2 * KA_CH; }
+// 4-bit caches: a ring of raw tiles (128 rows of codes, then their scales) behind the entries
+constexpr int KA_RAW = 7;
+__host__ __device__ constexpr uint32_t ka_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_CH + hd / 16 * KA_CH; }
 
 template <int HD, int CACHE, int NB>
 __global__ void __launch_bounds__(ka_threads(CACHE, NB), 1)
@@ -205,19 +214,22 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   constexpr float LIFT = F4 ? 7.f : 0.f;
   constexpr int THREADS = ka_threads(CACHE, NB);
   constexpr int CONV_WARP = 4 + 4 * NB, CONV = THREADS - 32 * CONV_WARP;   // converter threads (F4)
-  constexpr uint32_t ENTRY = ka_entry(HD), HALF = KA_CH * 128;
+  constexpr uint32_t ENTRY = ka_entry(HD), HALF = KA_CH * 128, RAW = ka_raw_bytes(HD), RAW_SCALES = HD / 2 * KA_CH;
   constexpr uint32_t T_O = 256, T_Q = 384;
   extern __shared__ uint8_t ka_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ka_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t ring_u = uniform(smem_u32(sm));
   const uint32_t q_u = ring_u + static_cast<uint32_t>(NS) * ENTRY;       // NB = 2: Q tiles
-  uint8_t* misc = sm + static_cast<uint32_t>(NS) * ENTRY + (NB == 2 ? 2 * ENTRY : 0);
+  uint8_t* raw = sm + static_cast<uint32_t>(NS) * ENTRY + (NB == 2 ? 2 * ENTRY : 0);   // F4: raw tiles
+  uint8_t* misc = raw + (F4 ? KA_RAW * RAW : 0);
   const uint32_t misc_u = smem_u32(misc);
   const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 256,
                  bar_pe = misc_u + 288, bar_fin = misc_u + 336;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 344);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 348);
+  const uint32_t bar_rf = misc_u + 352, bar_re = misc_u + 408;            // raw tiles full / free
+  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 464);   // pages each holds (bits)
   unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [128] tree mask rows
 
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / a.blocks, blk0 = blockIdx.z - b * a.blocks;
@@ -256,6 +268,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       mbar_init(bar_pe + 8 * i, 1);
     }
     mbar_init(bar_fin, nb);
+    for (int s = 0; F4 && s < KA_RAW; ++s) {
+      mbar_init(bar_rf + 8 * s, 1);
+      mbar_init(bar_re + 8 * s, F4 ? CONV / 32 : 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -343,30 +359,47 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   bool ok = true;
   if (warp < 4) {
     if constexpr (MOVE) set_regs_down<40>();
-    // ------------------------------------------------------------ TMA producer (bf16)
-    if (warp == 0 && !F4 && lane == 0) {
+    // ------------------------------------------------------------ producer: lane = page of the tile
+    if (warp == 0) {
       const uint64_t pol = policy_evict_first();
-      const int none = a.pool.num_pages * a.pool.Hkv;   // a block outside the map: zeros
       const int per = KA_CH >> a.pool.ps_log;
       RingPos rp{0, 0};
-      for (int e = 0; e < 2 * T && ok; ++e, rp.step(1, NS)) {
+      const int slots = F4 ? KA_RAW : NS;
+      int page = -1;
+      for (int e = 0; e < 2 * T; ++e, rp.step(1, slots)) {
         const int slot = rp.slot;
-        if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
+        const int pi = (t_begin + (e >> 1)) * per + lane;
+        if (!(e & 1)) {   // the tile's keys and values are in the same pages
+          page = -1;
+          if (lane < per && (pi << a.pool.ps_log) < rq.len) page = kv_page(a.pool, b, pi << a.pool.ps_log, a.err);
+        }
+        const uint32_t bar = (F4 ? bar_rf : bar_kvf) + 8 * slot;
+        if (e >= slots) ok = mbar_wait_sleepy((F4 ? bar_re : bar_kve) + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t dst = ring_u + slot * ENTRY, bar = bar_kvf + 8 * slot;
-        mbar_arrive_expect_tx(bar, ENTRY);
-        const int p0 = (t_begin + (e >> 1)) * per;
-        for (int p = 0; p < per; ++p) {
-          const int pi = p0 + p;
-          int blk = none;
-          if ((pi << a.pool.ps_log) < rq.len) {
-            const int page = kv_page(a.pool, b, pi << a.pool.ps_log, a.err);
-            if (page >= 0) blk = page * a.pool.Hkv + kvh;
+        if (F4) {
+          const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+          const uint32_t codes = static_cast<uint32_t>(ps) * (HD / 2), scales = static_cast<uint32_t>(ps) * (HD / 16);
+          if (lane == 0) {
+            raw_pages[slot] = have;
+            mbar_arrive_expect_tx(bar, __popc(have) * (codes + scales));
           }
-          const int r0 = box_row(pi);
+          __syncwarp();
+          if (page >= 0) {
+            const size_t row = kv_row(a.pool, page, kvh, 0);
+            const uint32_t dst = smem_u32(raw + slot * RAW);
+            bulk_load(dst + lane * codes, static_cast<const uint8_t*>(e & 1 ? a.pool.v : a.pool.k) + row * (HD / 2), codes, bar);
+            bulk_load(dst + RAW_SCALES + lane * scales, static_cast<const uint8_t*>(e & 1 ? a.pool.vs : a.pool.ks) + row * (HD / 16), scales, bar);
+          }
+        } else {
+          if (lane == 0) mbar_arrive_expect_tx(bar, ENTRY);
+          __syncwarp();
+          if (lane < per) {   // (a page that is not there reads as zeros: a block outside the map)
+            const int blk = page >= 0 ? page * a.pool.Hkv + kvh : a.pool.num_pages * a.pool.Hkv;
+            const uint32_t dst = ring_u + slot * ENTRY + lane * (ps * 128);
 #pragma unroll
-          for (int h = 0; h < HD / 64; ++h)
-            tma_load_3d(dst + h * HALF + p * (ps * 128), e & 1 ? &tmv : &tmk, 64 * h, r0, blk, bar, pol);
+            for (int h = 0; h < HD / 64; ++h) tma_load_3d(dst + h * HALF, e & 1 ? &tmv : &tmk, 64 * h, box_row(pi), blk, bar, pol);
+          }
         }
       }
       if (!ok) {   // let copies already issued land before the CTA releases its shared memory
@@ -443,46 +476,41 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
-    // ------------------------------ 4-bit pages -> fp16 tiles: 16 dims per thread and step,
-    // the next entry's codes in flight while this one is converted
+    // ------------------------------ raw tiles -> fp16 tiles: 16 dims per thread and step
     constexpr int GR = HD / 16;                        // scale groups per row
     constexpr int IT = KA_CH * GR / CONV;              // 16-dim groups per thread and entry
-    const int ct = tid - 32 * CONV_WARP, gidx = ct % GR, r0 = ct / GR;
     constexpr int RSTEP = CONV / GR;
-    uint2 code[IT];
-    uint32_t scale[IT];
-    auto fetch = [&](int e) {
-      const uint8_t* cp = static_cast<const uint8_t*>(e & 1 ? a.pool.v : a.pool.k);
-      const uint8_t* sp = static_cast<const uint8_t*>(e & 1 ? a.pool.vs : a.pool.ks);
+    const int ct = tid - 32 * CONV_WARP, gidx = ct % GR, r0 = ct / GR;
+    const int sw = gidx >> 2;   // (the two 64-dim halves share banks: the upper one stores its chunks in the other order)
+    RingPos rp{0, 0}, wp{0, 0};
+    for (int e = 0; e < 2 * T; ++e, rp.step(1, NS), wp.step(1, KA_RAW)) {
+      ok = mbar_wait_sleepy(bar_rf + 8 * wp.slot, wp.turn, a.err, abort_flag);
+      const uint8_t* src = raw + wp.slot * RAW;
+      const uint32_t have = raw_pages[wp.slot];
       const int k0 = (t_begin + (e >> 1)) * KA_CH;
+      uint2 code[IT];
+      uint32_t scale[IT];
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        const int t = k0 + r0 + i * RSTEP;
-        code[i] = make_uint2(0u, 0u);
-        scale[i] = 0u;
-        if (t < rq.len) {
-          const int page = kv_page(a.pool, b, t, a.err);
-          if (page >= 0) {
-            const size_t row = kv_row(a.pool, page, kvh, t);
-            code[i] = __ldg(reinterpret_cast<const uint2*>(cp + row * (HD / 2)) + gidx);
-            scale[i] = __ldg(sp + row * GR + gidx);
-          }
+        const int r = r0 + i * RSTEP;
+        code[i] = reinterpret_cast<const uint2*>(src + r * (HD / 2))[gidx];
+        scale[i] = src[RAW_SCALES + r * GR + gidx];
+        // rows behind the last key, and of pages that are not there: zeros
+        if (k0 + r >= rq.len || !((have >> (r >> a.pool.ps_log)) & 1u)) {
+          code[i] = make_uint2(0u, 0u);
+          scale[i] = 0u;
         }
       }
-    };
-    if (T > 0) fetch(0);
-    RingPos rp{0, 0};
-    for (int e = 0; e < 2 * T; ++e, rp.step(1, NS)) {
-      const int slot = rp.slot;
-      if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_re + 8 * wp.slot);
+      if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag) && ok;
       if (__any_sync(0xffffffffu, !ok)) break;
-      const uint32_t dst = ring_u + slot * ENTRY + (gidx >> 2) * HALF;
+      const uint32_t dst = ring_u + rp.slot * ENTRY + sw * HALF;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         uint32_t h[8];
         dequant16(code[i], scale[i], h);
-        // (the two 64-dim halves share banks: the upper one stores its chunks in the other order)
-        const int r = r0 + i * RSTEP, c = 2 * (gidx & 3), sw = gidx >> 2;
+        const int r = r0 + i * RSTEP, c = 2 * (gidx & 3);
         uint32_t x[4], y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -494,8 +522,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_kvf + 8 * slot);
-      if (e + 1 < 2 * T) fetch(e + 1);
+      if (lane == 0) mbar_arrive(bar_kvf + 8 * rp.slot);
     }
     }
   } else {
@@ -792,7 +819,7 @@ cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaAr
     if (e != cudaSuccess) return e;
     if (dev < 64) granted[dev].store(cap);
   }
-  const size_t fixed = (NB == 2 ? 2 * ka_entry(HD) : 0) + KA_MISC + 1024;
+  const size_t fixed = (NB == 2 ? 2 * ka_entry(HD) : 0) + (CACHE == EAGLE_CACHE_F4 ? KA_RAW * ka_raw_bytes(HD) : 0) + KA_MISC + 1024;
   const int ns = std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
   const size_t smem = fixed + static_cast<size_t>(ns) * ka_entry(HD);
   kv_attention_tc<HD, CACHE, NB><<<dim3(a.splits, a.pool.Hkv, a.B * a.blocks), ka_threads(CACHE, NB), smem, st>>>(tmk, tmv, a, ns);
