@@ -27,6 +27,7 @@ constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum ma
 constexpr uint32_t KA_MISC = 2048;
 constexpr int KA_MAX_SLOTS = 14;
 constexpr int KA_FIXED = 6;               // a CTA's fixed cost in tiles
+constexpr int KS_FIXED = 2;               // the same for the kernel for few query vectors
 
 struct KaArgs {
   KvPool pool;
@@ -726,6 +727,325 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------------ few query vectors, 4 bits
+// Up to 8 query vectors per KV head (a token of each of 8 grouped heads).  The tensor-core kernel
+// above spends 128 rows of MMA and a trip of every key through shared memory on them; here the
+// 4-bit keys go from global memory to registers to mma.sync fragments:
+//   S^T [16 keys x 8 vectors] = K Q^T        A = keys, B = queries
+//   O^T [16 dims x 8 vectors] += V^T P^T     A = values, B = P (an 8 x 8 transpose of S^T's tile)
+// Any order of the dims serves S as long as Q has the same, and any order serves O, so a lane takes
+// the dims that lie together in memory: lane (g, c) = (lane / 4, lane % 4) holds keys g and g + 8,
+// dims [c hd / 4, (c + 1) hd / 4) of K, and of keys 2c, 2c + 1, 2c + 8, 2c + 9 dims
+// [g hd / 8, (g + 1) hd / 8) of V.  A value pair of two keys is one byte of two codes (two bit
+// operations on four pairs), one conversion and one product with the pair of scales.
+// Each of the CTA's 4 warps walks 32-key steps; the next step's keys load while this step's
+// values are in use, and the other way round.  Bound by bytes (144 per key and head of 128) as
+// long as about 230 instructions per 16 keys keep up: 3.6 cycles per key and SM, of 6.1.
+constexpr int KS_WARPS = 4;
+constexpr int KS_KEYS = 32;
+constexpr int KS_QV = 8;
+
+EAGLE_DEV void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+EAGLE_DEV uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// two e4m3 bytes (low half of x) -> fp16 pair
+EAGLE_DEV uint32_t e4m3_pair(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+template <int W>
+EAGLE_DEV void load_words(uint32_t* d, const uint8_t* p) {
+  if constexpr (W == 4) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+  } else if constexpr (W == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    d[0] = x.x; d[1] = x.y;
+  } else {
+    d[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const KaArgs a) {
+  constexpr int KW = HD / 32, VW = HD / 64, ST = HD / 16;      // words of a lane's K row, V row; 16-dim steps
+  __shared__ float s_o[KS_WARPS][HD][KS_QV];
+  __shared__ float s_m[KS_WARPS][KS_QV], s_l[KS_WARPS][KS_QV];
+  __shared__ unsigned long long s_bits[KS_QV];
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const Req rq = request(a, b);
+  const int qv = rq.R * a.G;
+  const int kb = split * a.tiles_per_cta * KA_CH;
+  if (qv <= 0 || kb >= rq.len) return;
+  const int ke = min(rq.len, kb + a.tiles_per_cta * KA_CH);
+  const uint8_t* const kc = static_cast<const uint8_t*>(a.pool.k);
+  const uint8_t* const vc = static_cast<const uint8_t*>(a.pool.v);
+  const uint8_t* const ksc = static_cast<const uint8_t*>(a.pool.ks);
+  const uint8_t* const vsc = static_cast<const uint8_t*>(a.pool.vs);
+  if (a.mask) {                              // the step's visibility per query vector
+    for (int v = warp; v < qv; v += KS_WARPS) {
+      const unsigned char* mrow = a.mask + (static_cast<size_t>(b) * a.S + v / a.G) * a.S;
+      const unsigned lo = __ballot_sync(0xffffffffu, lane < rq.R && __ldg(mrow + min(lane, a.S - 1)) != 0);
+      if (lane == 0) s_bits[v] = lo;         // (at most 8 rows)
+    }
+    __syncthreads();
+  }
+
+  // this lane's part of query vector g as fp16, scaled by a power of two (as in the kernel above)
+  uint32_t q[ST][2];
+  float up_scale = 0.f;
+  {
+    const bool live = g < qv;
+    const int i = g / a.G;
+    const uint2* src = reinterpret_cast<const uint2*>(a.q + (rq.row0 + (live ? i : 0)) * a.q_ld +
+                                                      static_cast<long long>(kvh * a.G + (live ? g - i * a.G : 0)) * HD + c * (HD / 4));
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      const uint2 x = live ? __ldg(src + s) : make_uint2(0u, 0u);
+      q[s][0] = x.x;
+      q[s][1] = x.y;
+      top = max(max(top, max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu)), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    int ex = static_cast<int>(top >> 7);
+    ex = ex == 255 ? 127 : max(ex, 30);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
+    up_scale = a.scale_log2 * a.pool.kg * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        q[s][h] = pack_f16(__uint_as_float(q[s][h] << 16) * up, __uint_as_float(q[s][h] & 0xFFFF0000u) * up);
+  }
+  // score factors of vectors 2c and 2c + 1 (the columns this lane holds of S^T)
+  const float sc0 = __shfl_sync(0xffffffffu, up_scale, 8 * c), sc1 = __shfl_sync(0xffffffffu, up_scale, 8 * c + 4);
+
+  float o[ST][4];
+#pragma unroll
+  for (int j = 0; j < ST; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // log2 units; sums over this lane's keys
+
+  uint32_t kw[2][2][KW], kss[2][2], vw[2][4][VW], vss[2][4];
+  auto page_rows = [&](int k0, long long* row) {   // first pool row of each 16-key group, -1: none
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      const int t = k0 + 16 * gr;
+      row[gr] = -1;
+      if (t < ke) {
+        const int page = kv_page(a.pool, b, t, a.err);
+        if (page >= 0) row[gr] = static_cast<long long>(kv_row(a.pool, page, kvh, t));
+      }
+    }
+  };
+  auto load_k = [&](int k0, const long long* row) {
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = g + 8 * h;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) kw[gr][h][w] = 0u;
+        kss[gr][h] = 0u;
+        if (row[gr] >= 0 && k0 + 16 * gr + r < ke) {
+          load_words<KW>(kw[gr][h], kc + (row[gr] + r) * (HD / 2) + c * (KW * 4));
+          const uint8_t* sp = ksc + (row[gr] + r) * (HD / 16) + c * (HD / 64);
+          kss[gr][h] = HD == 128 ? __ldg(reinterpret_cast<const unsigned short*>(sp)) : __ldg(sp);
+        }
+      }
+  };
+  auto load_v = [&](int k0, const long long* row) {
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int w = 0; w < VW; ++w) vw[gr][i][w] = 0u;
+        vss[gr][i] = 0u;
+        if (row[gr] >= 0 && k0 + 16 * gr + r < ke) {
+          load_words<VW>(vw[gr][i], vc + (row[gr] + r) * (HD / 2) + g * (VW * 4));
+          vss[gr][i] = __ldg(vsc + (row[gr] + r) * (HD / 16) + (g * HD) / 128);
+        }
+      }
+  };
+
+  int k0 = kb + warp * KS_KEYS;
+  constexpr int STEP = KS_WARPS * KS_KEYS;
+  long long row[2], row_next[2];
+  page_rows(k0, row);
+  if (k0 < ke) {
+    load_k(k0, row);
+    load_v(k0, row);
+  }
+  page_rows(k0 + STEP, row_next);
+  for (; k0 < ke; k0 += STEP) {
+    // ---- scores of 32 keys: s[gr] = {key g: vectors 2c, 2c + 1; key g + 8: the same}
+    float s[2][4];
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[gr][e] = 0.f;
+      uint32_t sk[2][2];                     // scale pairs per key and 16-dim group
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = e4m3_pair(kss[gr][h]);
+        sk[h][0] = __byte_perm(x, x, 0x1010);
+        sk[h][1] = HD == 128 ? __byte_perm(x, x, 0x3232) : sk[h][0];
+      }
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {         // 8 dims a word: two 16-dim steps of 4 dims a lane
+        const uint32_t x = kw[gr][0][w], y = kw[gr][1][w], sx = sk[0][w / 2], sy = sk[1][w / 2];
+        mma_f16(s[gr], mul_f16x2(e2m1_pair<0>(x), sx), mul_f16x2(e2m1_pair<0>(y), sy), mul_f16x2(e2m1_pair<1>(x), sx),
+                mul_f16x2(e2m1_pair<1>(y), sy), q[2 * w][0], q[2 * w][1]);
+        mma_f16(s[gr], mul_f16x2(e2m1_pair<2>(x), sx), mul_f16x2(e2m1_pair<2>(y), sy), mul_f16x2(e2m1_pair<3>(x), sx),
+                mul_f16x2(e2m1_pair<3>(y), sy), q[2 * w + 1][0], q[2 * w + 1][1]);
+      }
+    }
+    const int kn = k0 + STEP;
+    if (kn < ke) load_k(kn, row_next);
+    // ---- softmax in log2 units
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      s[gr][0] *= sc0;
+      s[gr][1] *= sc1;
+      s[gr][2] *= sc0;
+      s[gr][3] *= sc1;
+    }
+    if (k0 + KS_KEYS > rq.ctx || k0 + KS_KEYS > ke) {   // the step's own rows, or past the range
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = k0 + 16 * gr + g + 8 * (e >> 1), v = 2 * c + (e & 1), j = key - rq.ctx;
+          bool see = key < ke;
+          if (j >= 0) see = see && v < qv && (a.mask ? (s_bits[v] >> j) & 1ull : j <= v / a.G);
+          if (!see) s[gr][e] = -INFINITY;
+        }
+    }
+    const float t0 = max_nan(max3_nan(s[0][0], s[0][2], s[1][0]), s[1][2]), t1 = max_nan(max3_nan(s[0][1], s[0][3], s[1][1]), s[1][3]);
+    // the running maximum moves only when some score exceeds it by more than KA_RESCALE
+    if (__any_sync(0xffffffffu, !(t0 <= m0 + KA_RESCALE) || !(t1 <= m1 + KA_RESCALE))) {
+      float n0 = max_nan(t0, m0), n1 = max_nan(t1, m1);
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        n0 = max_nan(n0, __shfl_xor_sync(0xffffffffu, n0, d));
+        n1 = max_nan(n1, __shfl_xor_sync(0xffffffffu, n1, d));
+      }
+      const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int j = 0; j < ST; ++j) {
+        o[j][0] *= f0;
+        o[j][1] *= f1;
+        o[j][2] *= f0;
+        o[j][3] *= f1;
+      }
+    }
+    // p times 2^7 in fp16 (as above); a vector that sees nothing yet: maximum 0, every p 0
+    const float b0 = (m0 == -INFINITY ? 0.f : m0) - 7.f, b1 = (m1 == -INFINITY ? 0.f : m1) - 7.f;
+    uint32_t pb[2][2];
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = fast_exp2(s[gr][2 * h] - b0), p1 = fast_exp2(s[gr][2 * h + 1] - b1);
+        l0 += p0;
+        l1 += p1;
+        pb[gr][h] = transpose8x8(pack_f16(p0, p1));   // keys 2c, 2c + 1 (+ 8 h) of vector g
+      }
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int gr = 0; gr < 2; ++gr) {
+      const uint32_t sa = e4m3_pair(vss[gr][0] | (vss[gr][1] << 8)), sb = e4m3_pair(vss[gr][2] | (vss[gr][3] << 8));
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {         // 8 dims a word: 4 tiles of 2 dims a lane
+        const uint32_t x0 = vw[gr][0][w], x1 = vw[gr][1][w], y0 = vw[gr][2][w], y1 = vw[gr][3][w];
+        const uint32_t xe = (x0 & 0x0F0F0F0Fu) | ((x1 << 4) & 0xF0F0F0F0u), xo = ((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u);
+        const uint32_t ye = (y0 & 0x0F0F0F0Fu) | ((y1 << 4) & 0xF0F0F0F0u), yo = ((y0 >> 4) & 0x0F0F0F0Fu) | (y1 & 0xF0F0F0F0u);
+        mma_f16(o[4 * w], mul_f16x2(e2m1_pair<0>(xe), sa), mul_f16x2(e2m1_pair<0>(xo), sa), mul_f16x2(e2m1_pair<0>(ye), sb),
+                mul_f16x2(e2m1_pair<0>(yo), sb), pb[gr][0], pb[gr][1]);
+        mma_f16(o[4 * w + 1], mul_f16x2(e2m1_pair<1>(xe), sa), mul_f16x2(e2m1_pair<1>(xo), sa), mul_f16x2(e2m1_pair<1>(ye), sb),
+                mul_f16x2(e2m1_pair<1>(yo), sb), pb[gr][0], pb[gr][1]);
+        mma_f16(o[4 * w + 2], mul_f16x2(e2m1_pair<2>(xe), sa), mul_f16x2(e2m1_pair<2>(xo), sa), mul_f16x2(e2m1_pair<2>(ye), sb),
+                mul_f16x2(e2m1_pair<2>(yo), sb), pb[gr][0], pb[gr][1]);
+        mma_f16(o[4 * w + 3], mul_f16x2(e2m1_pair<3>(xe), sa), mul_f16x2(e2m1_pair<3>(xo), sa), mul_f16x2(e2m1_pair<3>(ye), sb),
+                mul_f16x2(e2m1_pair<3>(yo), sb), pb[gr][0], pb[gr][1]);
+      }
+    }
+    if (kn < ke) {
+      load_v(kn, row_next);
+      page_rows(kn + STEP, row_next);
+    }
+  }
+  // ---- the four warps' states, in warp order
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+  }
+  if (g == 0) {
+    s_m[warp][2 * c] = m0;
+    s_m[warp][2 * c + 1] = m1;
+    s_l[warp][2 * c] = l0;
+    s_l[warp][2 * c + 1] = l1;
+  }
+#pragma unroll
+  for (int j = 0; j < ST; ++j) {             // tile j of a lane: dims g hd / 8 + 2 j and + 1
+    const int d = g * (HD / 8) + 2 * j;
+    s_o[warp][d][2 * c] = o[j][0];
+    s_o[warp][d][2 * c + 1] = o[j][1];
+    s_o[warp][d + 1][2 * c] = o[j][2];
+    s_o[warp][d + 1][2 * c + 1] = o[j][3];
+  }
+  __syncthreads();
+  for (int x = tid; x < qv * (HD / 2); x += 32 * KS_WARPS) {
+    const int v = x / (HD / 2), d = 2 * (x - v * (HD / 2));
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < KS_WARPS; ++w) M = max_nan(M, s_m[w][v]);
+    float L = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < KS_WARPS; ++w) {
+      if (s_m[w][v] == -INFINITY) continue;
+      const float f = fast_exp2(s_m[w][v] - M);
+      L = fmaf(f, s_l[w][v], L);
+      y0 = fmaf(f, s_o[w][d][v], y0);
+      y1 = fmaf(f, s_o[w][d + 1][v], y1);
+    }
+    const int i = v / a.G;
+    const size_t at = static_cast<size_t>(rq.row0 + i) * a.Hq + kvh * a.G + (v - i * a.G);
+    const bool none = L == 0.f;
+    const float m2 = none ? -INFINITY : M - 7.f;
+    if (a.splits > 1) {
+      if (!none)
+        *reinterpret_cast<float2*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + d) =
+            make_float2(y0 * a.pool.vg, y1 * a.pool.vg);
+      if (d == 0) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, L);
+    } else {
+      const float inv = none ? 0.f : a.pool.vg / L;
+      *reinterpret_cast<uint32_t*>(a.out + (rq.row0 + i) * a.out_ld + static_cast<long long>(kvh * a.G + v - i * a.G) * HD + d) =
+          none ? 0u : pack_bf16(y0 * inv, y1 * inv);
+      if (d == 0 && a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(L)) * 0.6931471805599453f;
+    }
+  }
+}
+
 // Joins the key ranges of a request: one warp per (row, query head), HD / 32 dims per lane.
 template <int HD>
 __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
@@ -765,22 +1085,24 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
 
 // How a call is cut: query-vector tiles per CTA, blocks per request, key ranges.
 struct Plan {
+  bool step;                               // the kernel for few vectors of a 4-bit cache
   int nb, blocks, tiles_per_cta, splits;
 };
 Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   Plan p;
   const long long qv = static_cast<long long>(w->max_rows) * (w->n_heads / c->n_kv_heads);
+  p.step = c->kind == EAGLE_CACHE_F4 && qv <= KS_QV;
   p.nb = qv > KA_QV ? 2 : 1;
   p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
   const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
   // key ranges: the split whose waves of CTAs (one per SM) take least, a CTA costing its tiles
   // and as much again as KA_FIXED tiles for its start, its result and the joining of the ranges
-  const long long sms = num_sms();
+  const long long sms = num_sms() * (p.step ? 4 : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
   long long per = tiles, best = -1;
   for (long long n = 1; n <= tiles && n <= 4096; ++n) {
     const long long t = (tiles + n - 1) / n;
-    const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + KA_FIXED);
+    const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + fixed);
     if (best < 0 || cost < best) {
       best = cost;
       per = t;
@@ -827,9 +1149,13 @@ cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaAr
 }
 
 template <int HD>
-cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, bool f4, int nb, cudaStream_t st) {
+cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, bool f4, const Plan& p, cudaStream_t st) {
   cudaError_t e;
-  if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
+  const int nb = p.nb;
+  if (p.step) {
+    kv_attention_step_f4<HD><<<dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS, 0, st>>>(a);
+    e = cudaGetLastError();
+  } else if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
   else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
   if (e != cudaSuccess || a.splits == 1) return e;
   const long long warps = static_cast<long long>(a.N) * a.Hq;
@@ -898,6 +1224,6 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   const long long blocks = static_cast<long long>(cache->num_pages) * cache->n_kv_heads;
   if (!f4 && (!make_page_map(&tmk, cache->k, hd, cache->page_size, blocks) || !make_page_map(&tmv, cache->v, hd, cache->page_size, blocks)))
     return kv_fail(EAGLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  const cudaError_t e = hd == 64 ? launch_all<64>(tmk, tmv, a, f4, p.nb, st) : launch_all<128>(tmk, tmv, a, f4, p.nb, st);
+  const cudaError_t e = hd == 64 ? launch_all<64>(tmk, tmv, a, f4, p, st) : launch_all<128>(tmk, tmv, a, f4, p, st);
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }
