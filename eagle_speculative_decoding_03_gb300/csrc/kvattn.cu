@@ -839,52 +839,77 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // log2 units; sums over this lane's keys
 
   uint32_t kw[2][2][KW], kss[2][2], vw[2][4][VW], vss[2][4];
-  auto page_rows = [&](int k0, long long* row) {   // first pool row of each 16-key group, -1: none
+  // first pool row of each 16-key group of the step at k0; -1: no such page
+  auto page_rows = [&](int k0, int* row) {
 #pragma unroll
     for (int gr = 0; gr < 2; ++gr) {
       const int t = k0 + 16 * gr;
       row[gr] = -1;
       if (t < ke) {
         const int page = kv_page(a.pool, b, t, a.err);
-        if (page >= 0) row[gr] = static_cast<long long>(kv_row(a.pool, page, kvh, t));
+        if (page >= 0) row[gr] = static_cast<int>(kv_row(a.pool, page, kvh, t));   // (below 2^31)
       }
     }
   };
-  auto load_k = [&](int k0, const long long* row) {
+  // (a step whose keys are all there loads without a test)
+  auto load_k = [&](int k0, const int* row) {
+    const uint8_t *cp[2], *sp[2];
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
+    for (int gr = 0; gr < 2; ++gr) {
+      const size_t r = static_cast<size_t>(max(row[gr], 0)) + g;
+      cp[gr] = kc + r * (HD / 2) + c * (KW * 4);
+      sp[gr] = ksc + r * (HD / 16) + c * (HD / 64);
+    }
+    auto get = [&](int gr, int h) {
+      load_words<KW>(kw[gr][h], cp[gr] + 8 * h * (HD / 2));
+      const uint8_t* s1 = sp[gr] + 8 * h * (HD / 16);
+      kss[gr][h] = HD == 128 ? __ldg(reinterpret_cast<const unsigned short*>(s1)) : __ldg(s1);
+    };
+    if (k0 + KS_KEYS <= ke && (row[0] | row[1]) >= 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g + 8 * h;
+      for (int x = 0; x < 4; ++x) get(x >> 1, x & 1);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int gr = x >> 1, h = x & 1;
 #pragma unroll
         for (int w = 0; w < KW; ++w) kw[gr][h][w] = 0u;
         kss[gr][h] = 0u;
-        if (row[gr] >= 0 && k0 + 16 * gr + r < ke) {
-          load_words<KW>(kw[gr][h], kc + (row[gr] + r) * (HD / 2) + c * (KW * 4));
-          const uint8_t* sp = ksc + (row[gr] + r) * (HD / 16) + c * (HD / 64);
-          kss[gr][h] = HD == 128 ? __ldg(reinterpret_cast<const unsigned short*>(sp)) : __ldg(sp);
-        }
+        if (row[gr] >= 0 && k0 + 16 * gr + g + 8 * h < ke) get(gr, h);
       }
+    }
   };
-  auto load_v = [&](int k0, const long long* row) {
+  auto load_v = [&](int k0, const int* row) {
+    const uint8_t *cp[2], *sp[2];
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr)
+    for (int gr = 0; gr < 2; ++gr) {
+      const size_t r = static_cast<size_t>(max(row[gr], 0)) + 2 * c;
+      cp[gr] = vc + r * (HD / 2) + g * (VW * 4);
+      sp[gr] = vsc + r * (HD / 16) + (g * HD) / 128;
+    }
+    auto get = [&](int gr, int i) {
+      const int d = (i & 1) + 8 * (i >> 1);
+      load_words<VW>(vw[gr][i], cp[gr] + d * (HD / 2));
+      vss[gr][i] = __ldg(sp[gr] + d * (HD / 16));
+    };
+    if (k0 + KS_KEYS <= ke && (row[0] | row[1]) >= 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+      for (int x = 0; x < 8; ++x) get(x >> 2, x & 3);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int gr = x >> 2, i = x & 3;
 #pragma unroll
         for (int w = 0; w < VW; ++w) vw[gr][i][w] = 0u;
         vss[gr][i] = 0u;
-        if (row[gr] >= 0 && k0 + 16 * gr + r < ke) {
-          load_words<VW>(vw[gr][i], vc + (row[gr] + r) * (HD / 2) + g * (VW * 4));
-          vss[gr][i] = __ldg(vsc + (row[gr] + r) * (HD / 16) + (g * HD) / 128);
-        }
+        if (row[gr] >= 0 && k0 + 16 * gr + 2 * c + (i & 1) + 8 * (i >> 1) < ke) get(gr, i);
       }
+    }
   };
 
   int k0 = kb + warp * KS_KEYS;
   constexpr int STEP = KS_WARPS * KS_KEYS;
-  long long row[2], row_next[2];
+  int row[2], row_next[2];
   page_rows(k0, row);
   if (k0 < ke) {
     load_k(k0, row);
