@@ -729,21 +729,25 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 
 // ------------------------------------------------------------------ few query vectors, 4 bits
 // Up to 8 query vectors per KV head (a token of each of 8 grouped heads).  The tensor-core kernel
-// above spends 128 rows of MMA and a trip of every key through shared memory on them; here the
-// 4-bit keys go from global memory to registers to mma.sync fragments:
+// above spends 128 rows of MMA and a decoded copy of every key in shared memory on them; here the
+// 4-bit keys go from their raw tiles to registers and mma.sync fragments:
 //   S^T [16 keys x 8 vectors] = K Q^T        A = keys, B = queries
 //   O^T [16 dims x 8 vectors] += V^T P^T     A = values, B = P (an 8 x 8 transpose of S^T's tile)
 // Any order of the dims serves S as long as Q has the same, and any order serves O, so a lane takes
-// the dims that lie together in memory: lane (g, c) = (lane / 4, lane % 4) holds keys g and g + 8,
-// dims [c hd / 4, (c + 1) hd / 4) of K, and of keys 2c, 2c + 1, 2c + 8, 2c + 9 dims
-// [g hd / 8, (g + 1) hd / 8) of V.  A value pair of two keys is one byte of two codes (two bit
-// operations on four pairs), one conversion and one product with the pair of scales.
-// Each of the CTA's 4 warps walks 32-key steps; the next step's keys load while this step's
-// values are in use, and the other way round.  Bound by bytes (144 per key and head of 128) as
-// long as about 230 instructions per 16 keys keep up: 3.6 cycles per key and SM, of 6.1.
+// the dims that lie together in memory: lane (g, c) = (lane / 4, lane % 4) holds dims
+// [c hd / 4, (c + 1) hd / 4) of two keys of K, and dims [g hd / 8, (g + 1) hd / 8) of four keys of
+// V.  A value pair of two keys is one byte of two codes (two bit operations on four pairs), one
+// conversion and one product with the pair of scales.
+// One warp copies raw tiles of 128 keys (18 KB at hd 128: codes and scales of K and V) into a ring
+// by bulk copies; four warps take 32 keys of a tile each.  Bound by bytes (144 per key and head of
+// 128) as long as the instructions keep up; loading the fragments straight from global memory
+// left too few bytes in flight (176 us at 32 requests of 17,000 keys on average, 8 heads).
 constexpr int KS_WARPS = 4;
-constexpr int KS_KEYS = 32;
+constexpr int KS_KEYS = 32;                // keys of a warp's step
 constexpr int KS_QV = 8;
+constexpr int KS_CTAS = 3;                 // per SM
+constexpr int KS_STAGES = 4;
+__host__ __device__ constexpr uint32_t ks_stage(int hd) { return 2 * ka_raw_bytes(hd); }
 
 EAGLE_DEV void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -764,22 +768,27 @@ EAGLE_DEV uint32_t e4m3_pair(uint32_t x) {
 template <int W>
 EAGLE_DEV void load_words(uint32_t* d, const uint8_t* p) {
   if constexpr (W == 4) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
     d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
   } else if constexpr (W == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
     d[0] = x.x; d[1] = x.y;
   } else {
-    d[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    d[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
 
 template <int HD>
-__global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const KaArgs a) {
+__global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step_f4(const KaArgs a) {
   constexpr int KW = HD / 32, VW = HD / 64, ST = HD / 16;      // words of a lane's K row, V row; 16-dim steps
-  __shared__ float s_o[KS_WARPS][HD][KS_QV];
+  constexpr uint32_t RAW = ka_raw_bytes(HD), SCALES = HD / 2 * KA_CH;   // a tensor's part of a stage; its scales
+  extern __shared__ __align__(128) uint8_t ks_raw[];           // [KS_STAGES][K | V][codes | scales]
+  __shared__ __align__(8) uint64_t s_full[KS_STAGES], s_free[KS_STAGES];
+  __shared__ uint32_t s_pages[KS_STAGES];
+  __shared__ int s_abort;
   __shared__ float s_m[KS_WARPS][KS_QV], s_l[KS_WARPS][KS_QV];
   __shared__ unsigned long long s_bits[KS_QV];
+  float (*s_o)[HD][KS_QV] = reinterpret_cast<float (*)[HD][KS_QV]>(ks_raw);   // (after the last tile)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const Req rq = request(a, b);
@@ -787,19 +796,65 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
   const int kb = split * a.tiles_per_cta * KA_CH;
   if (qv <= 0 || kb >= rq.len) return;
   const int ke = min(rq.len, kb + a.tiles_per_cta * KA_CH);
-  const uint8_t* const kc = static_cast<const uint8_t*>(a.pool.k);
-  const uint8_t* const vc = static_cast<const uint8_t*>(a.pool.v);
-  const uint8_t* const ksc = static_cast<const uint8_t*>(a.pool.ks);
-  const uint8_t* const vsc = static_cast<const uint8_t*>(a.pool.vs);
+  const int tiles = (ke - kb + KA_CH - 1) / KA_CH;
+  if (tid == 0) {
+    for (int i = 0; i < KS_STAGES; ++i) {
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(s_free + i), KS_WARPS);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
   if (a.mask) {                              // the step's visibility per query vector
-    for (int v = warp; v < qv; v += KS_WARPS) {
+    for (int v = warp; v < qv; v += KS_WARPS + 1) {
       const unsigned char* mrow = a.mask + (static_cast<size_t>(b) * a.S + v / a.G) * a.S;
       const unsigned lo = __ballot_sync(0xffffffffu, lane < rq.R && __ldg(mrow + min(lane, a.S - 1)) != 0);
       if (lane == 0) s_bits[v] = lo;         // (at most 8 rows)
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  bool ok = true;
+  if (warp == KS_WARPS) {
+    // ------------------------------------------------------------ producer: lane = page of the tile
+    const int ps = 1 << a.pool.ps_log, per = KA_CH >> a.pool.ps_log;
+    const uint32_t codes = static_cast<uint32_t>(ps) * (HD / 2), scales = static_cast<uint32_t>(ps) * (HD / 16);
+    RingPos rp{0, 0};
+    for (int t = 0; t < tiles; ++t, rp.step(1, KS_STAGES)) {
+      const int k = kb + t * KA_CH + (lane << a.pool.ps_log);
+      int page = -1;
+      if (lane < per && k < ke) page = kv_page(a.pool, b, k, a.err);
+      if (t >= KS_STAGES) ok = mbar_wait_sleepy(smem_u32(s_free + rp.slot), rp.turn ^ 1, a.err, &s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0), bar = smem_u32(s_full + rp.slot);
+      if (lane == 0) {
+        s_pages[rp.slot] = have;
+        mbar_arrive_expect_tx(bar, __popc(have) * 2 * (codes + scales));
+      }
+      __syncwarp();
+      if (page >= 0) {
+        const size_t row = kv_row(a.pool, page, kvh, 0);
+        const uint32_t dst = smem_u32(ks_raw) + rp.slot * ks_stage(HD) + lane * codes, dss = smem_u32(ks_raw) + rp.slot * ks_stage(HD) + SCALES + lane * scales;
+        bulk_load(dst, static_cast<const uint8_t*>(a.pool.k) + row * (HD / 2), codes, bar);
+        bulk_load(dss, static_cast<const uint8_t*>(a.pool.ks) + row * (HD / 16), scales, bar);
+        bulk_load(dst + RAW, static_cast<const uint8_t*>(a.pool.v) + row * (HD / 2), codes, bar);
+        bulk_load(dss + RAW, static_cast<const uint8_t*>(a.pool.vs) + row * (HD / 16), scales, bar);
+      }
+    }
+    if (!ok) {   // let copies already issued land before the CTA releases its shared memory
+      const long long t0 = clock64();
+      while (clock64() - t0 < 4000000) {
+      }
+    }
   }
 
+  float o[ST][4];
+#pragma unroll
+  for (int j = 0; j < ST; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // log2 units; sums over this lane's keys
+  if (warp < KS_WARPS) {
   // this lane's part of query vector g as fp16, scaled by a power of two (as in the kernel above)
   uint32_t q[ST][2];
   float up_scale = 0.f;
@@ -831,92 +886,57 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
   // score factors of vectors 2c and 2c + 1 (the columns this lane holds of S^T)
   const float sc0 = __shfl_sync(0xffffffffu, up_scale, 8 * c), sc1 = __shfl_sync(0xffffffffu, up_scale, 8 * c + 4);
 
-  float o[ST][4];
-#pragma unroll
-  for (int j = 0; j < ST; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // log2 units; sums over this lane's keys
-
-  uint32_t kw[2][2][KW], kss[2][2], vw[2][4][VW], vss[2][4];
-  // first pool row of each 16-key group of the step at k0; -1: no such page
-  auto page_rows = [&](int k0, int* row) {
-#pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-      const int t = k0 + 16 * gr;
-      row[gr] = -1;
-      if (t < ke) {
-        const int page = kv_page(a.pool, b, t, a.err);
-        if (page >= 0) row[gr] = static_cast<int>(kv_row(a.pool, page, kvh, t));   // (below 2^31)
-      }
-    }
-  };
-  // (a step whose keys are all there loads without a test)
-  auto load_k = [&](int k0, const int* row) {
-    const uint8_t *cp[2], *sp[2];
+  // Which key of a 16-key group is row k of the fragments: an order in which neighbouring rows of K
+  // and the four rows of a V load fall on different banks as far as 64-byte rows can.
+  const int kr = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;        // row g of K (and + 8)
+  const int vr0 = c, vr1 = 4 + (c ^ 1);                        // rows 2c, 2c + 1 of V (and + 8)
+  RingPos rp{0, 0};
+  for (int t = 0; t < tiles; ++t, rp.step(1, KS_STAGES)) {
+    const int k0 = kb + t * KA_CH + warp * KS_KEYS;
+    ok = ok && mbar_wait(smem_u32(s_full + rp.slot), rp.turn, a.err, &s_abort);
+    const uint8_t* st = ks_raw + rp.slot * ks_stage(HD);
+    uint32_t kw[2][2][KW], kss[2][2], vw[2][4][VW], vss[2][4];
 #pragma unroll
     for (int gr = 0; gr < 2; ++gr) {
-      const size_t r = static_cast<size_t>(max(row[gr], 0)) + g;
-      cp[gr] = kc + r * (HD / 2) + c * (KW * 4);
-      sp[gr] = ksc + r * (HD / 16) + c * (HD / 64);
-    }
-    auto get = [&](int gr, int h) {
-      load_words<KW>(kw[gr][h], cp[gr] + 8 * h * (HD / 2));
-      const uint8_t* s1 = sp[gr] + 8 * h * (HD / 16);
-      kss[gr][h] = HD == 128 ? __ldg(reinterpret_cast<const unsigned short*>(s1)) : __ldg(s1);
-    };
-    if (k0 + KS_KEYS <= ke && (row[0] | row[1]) >= 0) {
+      const int base = warp * KS_KEYS + 16 * gr;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) get(x >> 1, x & 1);
-    } else {
+      for (int h = 0; h < 2; ++h) {
+        const int r = base + kr + 8 * h;
+        load_words<KW>(kw[gr][h], st + r * (HD / 2) + c * (KW * 4));
+        const uint8_t* sp = st + SCALES + r * (HD / 16) + c * (HD / 64);
+        kss[gr][h] = HD == 128 ? *reinterpret_cast<const unsigned short*>(sp) : *sp;
+      }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int gr = x >> 1, h = x & 1;
-#pragma unroll
-        for (int w = 0; w < KW; ++w) kw[gr][h][w] = 0u;
-        kss[gr][h] = 0u;
-        if (row[gr] >= 0 && k0 + 16 * gr + g + 8 * h < ke) get(gr, h);
+      for (int i = 0; i < 4; ++i) {
+        const int r = base + ((i & 1) ? vr1 : vr0) + 8 * (i >> 1);
+        load_words<VW>(vw[gr][i], st + RAW + r * (HD / 2) + g * (VW * 4));
+        vss[gr][i] = st[RAW + SCALES + r * (HD / 16) + (g * HD) / 128];
       }
     }
-  };
-  auto load_v = [&](int k0, const int* row) {
-    const uint8_t *cp[2], *sp[2];
+    // rows behind the last key, and of pages that are not there: zeros
+    const uint32_t have = s_pages[rp.slot];
+    if (k0 + KS_KEYS > ke || have != (1u << (KA_CH >> a.pool.ps_log)) - 1u) {
 #pragma unroll
-    for (int gr = 0; gr < 2; ++gr) {
-      const size_t r = static_cast<size_t>(max(row[gr], 0)) + 2 * c;
-      cp[gr] = vc + r * (HD / 2) + g * (VW * 4);
-      sp[gr] = vsc + r * (HD / 16) + (g * HD) / 128;
-    }
-    auto get = [&](int gr, int i) {
-      const int d = (i & 1) + 8 * (i >> 1);
-      load_words<VW>(vw[gr][i], cp[gr] + d * (HD / 2));
-      vss[gr][i] = __ldg(sp[gr] + d * (HD / 16));
-    };
-    if (k0 + KS_KEYS <= ke && (row[0] | row[1]) >= 0) {
+      for (int gr = 0; gr < 2; ++gr) {
+        const bool page = (have >> ((warp * KS_KEYS + 16 * gr) >> a.pool.ps_log)) & 1u;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) get(x >> 2, x & 3);
-    } else {
+        for (int h = 0; h < 2; ++h)
+          if (!page || k0 + 16 * gr + kr + 8 * h >= ke) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int gr = x >> 2, i = x & 3;
+            for (int w = 0; w < KW; ++w) kw[gr][h][w] = 0u;
+            kss[gr][h] = 0u;
+          }
 #pragma unroll
-        for (int w = 0; w < VW; ++w) vw[gr][i][w] = 0u;
-        vss[gr][i] = 0u;
-        if (row[gr] >= 0 && k0 + 16 * gr + 2 * c + (i & 1) + 8 * (i >> 1) < ke) get(gr, i);
+        for (int i = 0; i < 4; ++i)
+          if (!page || k0 + 16 * gr + ((i & 1) ? vr1 : vr0) + 8 * (i >> 1) >= ke) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vw[gr][i][w] = 0u;
+            vss[gr][i] = 0u;
+          }
       }
     }
-  };
-
-  int k0 = kb + warp * KS_KEYS;
-  constexpr int STEP = KS_WARPS * KS_KEYS;
-  int row[2], row_next[2];
-  page_rows(k0, row);
-  if (k0 < ke) {
-    load_k(k0, row);
-    load_v(k0, row);
-  }
-  page_rows(k0 + STEP, row_next);
-  for (; k0 < ke; k0 += STEP) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(s_free + rp.slot));
     // ---- scores of 32 keys: s[gr] = {key g: vectors 2c, 2c + 1; key g + 8: the same}
     float s[2][4];
 #pragma unroll
@@ -939,8 +959,6 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
                 mul_f16x2(e2m1_pair<3>(y), sy), q[2 * w + 1][0], q[2 * w + 1][1]);
       }
     }
-    const int kn = k0 + STEP;
-    if (kn < ke) load_k(kn, row_next);
     // ---- softmax in log2 units
 #pragma unroll
     for (int gr = 0; gr < 2; ++gr) {
@@ -954,7 +972,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
       for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = k0 + 16 * gr + g + 8 * (e >> 1), v = 2 * c + (e & 1), j = key - rq.ctx;
+          const int key = k0 + 16 * gr + kr + 8 * (e >> 1), v = 2 * c + (e & 1), j = key - rq.ctx;
           bool see = key < ke;
           if (j >= 0) see = see && v < qv && (a.mask ? (s_bits[v] >> j) & 1ull : j <= v / a.G);
           if (!see) s[gr][e] = -INFINITY;
@@ -1013,12 +1031,11 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
                 mul_f16x2(e2m1_pair<3>(yo), sb), pb[gr][0], pb[gr][1]);
       }
     }
-    if (kn < ke) {
-      load_v(kn, row_next);
-      page_rows(kn + STEP, row_next);
-    }
   }
+  }
+  __syncthreads();                           // every tile is read: the ring takes the states
   // ---- the four warps' states, in warp order
+  if (warp < KS_WARPS) {
 #pragma unroll
   for (int d = 4; d < 32; d <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -1038,8 +1055,9 @@ __global__ void __launch_bounds__(32 * KS_WARPS, 4) kv_attention_step_f4(const K
     s_o[warp][d + 1][2 * c] = o[j][2];
     s_o[warp][d + 1][2 * c + 1] = o[j][3];
   }
+  }
   __syncthreads();
-  for (int x = tid; x < qv * (HD / 2); x += 32 * KS_WARPS) {
+  for (int x = tid; x < qv * (HD / 2); x += 32 * KS_WARPS + 32) {
     const int v = x / (HD / 2), d = 2 * (x - v * (HD / 2));
     float M = -INFINITY;
 #pragma unroll
@@ -1123,7 +1141,7 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
   // key ranges: the split whose waves of CTAs (one per SM) take least, a CTA costing its tiles
   // and as much again as KA_FIXED tiles for its start, its result and the joining of the ranges
-  const long long sms = num_sms() * (p.step ? 4 : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
+  const long long sms = num_sms() * (p.step ? KS_CTAS : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
   long long per = tiles, best = -1;
   for (long long n = 1; n <= tiles && n <= 4096; ++n) {
     const long long t = (tiles + n - 1) / n;
@@ -1174,12 +1192,27 @@ cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaAr
 }
 
 template <int HD>
+cudaError_t launch_step(const KaArgs& a, cudaStream_t st) {
+  constexpr size_t smem = static_cast<size_t>(KS_STAGES) * ks_stage(HD);
+  static std::atomic<int> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load()) {
+    e = cudaFuncSetAttribute(kv_attention_step_f4<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(1);
+  }
+  kv_attention_step_f4<HD><<<dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS + 32, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int HD>
 cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, bool f4, const Plan& p, cudaStream_t st) {
   cudaError_t e;
   const int nb = p.nb;
   if (p.step) {
-    kv_attention_step_f4<HD><<<dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS, 0, st>>>(a);
-    e = cudaGetLastError();
+    e = launch_step<HD>(a, st);
   } else if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
   else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
   if (e != cudaSuccess || a.splits == 1) return e;
