@@ -1141,7 +1141,7 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
   // key ranges: the split whose waves of CTAs (one per SM) take least, a CTA costing its tiles
   // and as much again as KA_FIXED tiles for its start, its result and the joining of the ranges
-  const long long sms = num_sms() * (p.step ? KS_CTAS : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
+  const long long sms = std::max(1, num_sms()) * (p.step ? KS_CTAS : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
   long long per = tiles, best = -1;
   for (long long n = 1; n <= tiles && n <= 4096; ++n) {
     const long long t = (tiles + n - 1) / n;

@@ -426,7 +426,7 @@ eagle_status_t rope_table(const eagle_rope_t* r, int hd, const char* who, RopeTa
 void rotate_shape(RotArgs* a) {
   const int heads = a->Hq + a->Hk + a->Hv, hpw = 32 / (a->hd / 8);
   const int iters = (heads + hpw - 1) / hpw;            // warp steps per row
-  const int sms = num_sms();
+  const int sms = std::max(1, num_sms());
   a->rows_per_cta = a->N >= 16 * sms ? 8 : a->N >= 4 * sms ? 4 : a->N >= 2 * sms ? 2 : 1;
   const int wpr = RT_WARPS / a->rows_per_cta;
   const long long ctas = (a->N + a->rows_per_cta - 1) / a->rows_per_cta;

@@ -1,0 +1,344 @@
+"""GPU parity of the paged cache's calls (eagle_rotary, eagle_kv_append, eagle_kv_gather,
+eagle_kv_accept) against the float64 oracle, and a run of all of them around a drafted tree.
+
+Rotation bound: with u = 2^-24, an angle is off by at most pi u (the fraction of a half turn rounded
+to fp32), cos and sin by 2 u more, their product with the amplitude by u; y = x c + z s then rounds
+twice.  Together less than 8 u (|x| + |z|) amplitude, and half a step of the output's type."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from eagle_speculative_decoding_03_gb300 import binding as eb, configs, synth
+from oracle import kv_oracle as K
+from kv_util import cu, dev, make_cache, pack_codes, pages, see_matrix
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from eagle_speculative_decoding_03_gb300 import build
+    build.build()
+    return eb.load()
+
+
+def partner(x, rot, inter):
+    z = np.zeros_like(x)
+    i = np.arange(rot)
+    j = i ^ 1 if inter else (i + rot // 2) % rot
+    z[..., i] = x[..., j]
+    return np.abs(z)
+
+
+def check_rotation(y, x, pos, w, inter, amp, half_step):
+    ref = K.rotary(x, pos, w, inter, amp)
+    tol = 8 * U * (np.abs(x) + partner(x, 2 * len(w), inter)) * max(abs(amp), 1) + half_step * np.abs(ref) + 1e-37
+    assert (np.abs(y - ref) <= tol).all(), float((np.abs(y - ref) / tol).max())
+    assert (y[..., 2 * len(w):] == x[..., 2 * len(w):]).all()     # the rest of the head is copied
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,H,hd,rot,inter,far", [
+    (1, 1, 128, 128, False, 5), (3, 5, 64, 32, True, 4000), (7, 3, 96, 48, False, 10 ** 6), (2, 40, 128, 16, True, 2 ** 31 - 1),
+    (700, 9, 128, 128, True, 10 ** 5), (2500, 2, 256, 112, False, 100), (333, 4, 80, 80, False, 32000), (5, 2, 16, 16, False, 9),
+    (1301, 6, 40, 32, True, 50000)])
+def test_rotary(dtype, N, H, hd, rot, inter, far):
+    rng = np.random.default_rng(N + hd)
+    x = K.bf16(rng.standard_normal((N, H, hd))) if dtype == "bf16" else rng.standard_normal((N, H, hd)).astype(np.float32).astype(np.float64)
+    pos = rng.integers(0, far, N, endpoint=True)
+    pos[0] = far
+    t = dev(x, torch.bfloat16 if dtype == "bf16" else torch.float32)
+    rope = eb.Rope(rot, theta=5e5, interleaved=inter)
+    w = 5e5 ** (-np.arange(0, rot, 2) / rot)
+    y = eb.rotary(t, dev(pos.astype(np.int32)), rope)
+    check_rotation(y.double().cpu().numpy(), x, pos, w, inter, 1.0, 2.0 ** -8 if dtype == "bf16" else U)
+    eb.rotary(t, dev(pos.astype(np.int32)), rope, out=t)          # in place: the same
+    assert torch.equal(t, y)
+
+
+def test_rotary_scaled_frequencies_amplitude_and_strides():
+    rng = np.random.default_rng(1)
+    w = eb.rope_frequencies(64, 1e4, banded=(8.0, 1.0, 4.0, 8192))
+    wide = torch.randn(50, 700, device="cuda")
+    x = wide[:, 60:60 + 5 * 128].unflatten(1, (5, 128))
+    pos = rng.integers(-100, 200000, 50)                           # a negative position turns back
+    rope = eb.Rope(64, inv_freq=w, amplitude=1.25)
+    outw = torch.zeros(50, 1280, device="cuda")
+    y = eb.rotary(x, dev(pos.astype(np.int32)), rope, out=outw[:, 640:].unflatten(1, (5, 128)))
+    check_rotation(y.double().cpu().numpy(), x.double().cpu().numpy(), pos, np.array(w), False, 1.25, U)
+    assert (outw[:, :640] == 0).all()
+    assert eb.rotary(x[:0], dev(pos[:0].astype(np.int32)), rope).shape == (0, 5, 128)
+
+
+def held_rows(cache, table, b, n, ps):
+    """Request b's first n rows of every pool tensor, on the host."""
+    t = np.arange(n)
+    pg, r = table[b, t // ps], t % ps
+    out = []
+    for x in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        out.append(None if x is None else x.float().cpu().numpy()[pg, :, r] if x.dtype == torch.bfloat16 else x.cpu().numpy()[pg, :, r])
+    return out
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,ps,Hkv,Hq,lens,rows,rot,inter", [
+    (128, 16, 2, 8, [0], [1], 128, False), (128, 64, 3, 9, [15, 0, 63, 64], [2, 1, 0, 70], 64, True),
+    (64, 32, 8, 8, [31, 5, 100] * 12, [1] * 36, 64, False), (64, 128, 1, 5, [200, 0], [300, 129], 48, False),
+    (128, 16, 4, 0, [7, 8, 9], [61, 61, 61], 128, False)])
+def test_append(kind, dtype, hd, ps, Hkv, Hq, lens, rows, rot, inter):
+    """Rotated keys and values land in their pages, queries come back rotated, nothing else of
+    the pool or of the rows behind the last request changes."""
+    rng = np.random.default_rng(ps + hd + len(lens))
+    tt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    N, pad = sum(rows), 3
+    room = [a + r for a, r in zip(lens, rows)]
+    table, P = pages(rng, room, ps)
+    f4 = kind == "f4"
+    cache = eb.KVCache.empty(P, ps, Hkv, hd, dev(table), four_bit=f4, k_global=1.0, v_global=0.25)
+    for x in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        if x is not None:
+            x.fill_(3)
+    qkv = torch.randn(N + pad, (Hq + 2 * Hkv) * hd, device="cuda").to(tt)
+    if f4:
+        qkv[0, -hd:-hd + 16] = 0                                   # a group of zeros
+        qkv[0, -16:] = 1e5                                         # one past the largest value
+    q, k, v = (x.unflatten(1, (-1, hd)) for x in (qkv[:, :Hq * hd] if Hq else qkv[:, :hd], qkv[:, Hq * hd:(Hq + Hkv) * hd],
+                                                  qkv[:, (Hq + Hkv) * hd:]))
+    pos = dev(np.concatenate([np.arange(a, a + r) for a, r in zip(lens, rows)] + [np.zeros(pad)]).astype(np.int32))
+    rope = eb.Rope(rot, theta=1e4, interleaved=inter)
+    q_out = torch.full((N + pad, max(Hq, 1), hd), 7.0, dtype=tt, device="cuda")
+    eb.kv_append(cache, k, v, dev(cu(rows)), dev(np.array(lens, np.int32)), positions=pos, rope=rope, q=q if Hq else None,
+                 q_out=q_out if Hq else None)
+    assert cache.check() == 0
+    if Hq:
+        want = eb.rotary(q, pos, rope)
+        assert torch.equal(q_out[:N], want[:N]) and (q_out[N:] == 7.0).all()
+        check_rotation(want.double().cpu().numpy(), q.double().cpu().numpy(), pos.cpu().numpy(), 1e4 ** (-np.arange(0, rot, 2) / rot),
+                       inter, 1.0, 2.0 ** -8 if dtype == "bf16" else U)
+    # the stored keys: the rotation (checked above on its own) rounded to bf16
+    rk = eb.rotary(k, pos, rope).to(torch.bfloat16).double().cpu().numpy()
+    rv = v.to(torch.bfloat16).double().cpu().numpy()
+    at = 0
+    untouched = np.ones((P, ps), bool)
+    for b, (a, r) in enumerate(zip(lens, rows)):
+        got = held_rows(cache, table, b, a + r, ps)
+        for i, x in ((0, rk[at:at + r]), (1, rv[at:at + r])):
+            if not f4:
+                assert (got[i][a:] == x).all()
+            else:
+                code, sc, _ = K.quantise(x, 1.0 if i == 0 else 0.25)
+                assert (got[i][a:] == pack_codes(code)).all() and (got[2 + i][a:] == sc).all()
+        t = np.arange(a, a + r)
+        untouched[table[b, t // ps], t % ps] = False
+        at += r
+    for x in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        if x is not None:
+            assert (x.float().cpu().numpy().transpose(0, 2, 1, 3)[untouched] == 3).all()
+
+
+def test_append_without_rope_and_with_special_values():
+    rng = np.random.default_rng(5)
+    table, P = pages(rng, [40], 16)
+    x = torch.randn(40, 2, 128, device="cuda")
+    cache = eb.KVCache.empty(P, 16, 2, 128, dev(table))
+    x[3, 0, 4], x[3, 1, 5], x[4, 0, 6] = float("nan"), float("inf"), -float("inf")
+    args = (dev(cu([40])), dev(np.array([0], np.int32)))
+    assert eb.kv_append(cache, x, x, *args) is None
+    got = held_rows(cache, table, 0, 40, 16)
+    assert np.array_equal(got[0], x.to(torch.bfloat16).float().cpu().numpy(), equal_nan=True) and np.array_equal(got[0], got[1], equal_nan=True)
+    c4 = eb.KVCache.empty(P, 16, 2, 128, dev(table), four_bit=True)
+    eb.kv_append(c4, x, x, *args)
+    k, v = eb.kv_gather(c4, dev(cu([40])), 40)
+    assert torch.equal(k, v) and torch.isfinite(k).all()
+    assert k[3, 0, 4] == 0 and k[3, 1, 5] == 2688 and k[4, 0, 6] == -2688    # NaN -> 0, infinities saturate
+
+
+def test_append_reports_places_outside_the_table():
+    rng = np.random.default_rng(6)
+    table, P = pages(rng, [32, 32], 16)
+    cache = eb.KVCache.empty(P, 16, 1, 64, dev(table))
+    x = torch.randn(4, 1, 64, device="cuda").to(torch.bfloat16)
+    eb.kv_append(cache, x, x, dev(cu([2, 2])), dev(np.array([31, 3], np.int32)))   # key 32 has no page
+    with pytest.raises(eb.EagleError) as e:
+        cache.check()
+    assert "0x10" in str(e.value) and cache.check() == 0
+    assert (held_rows(cache, table, 0, 32, 16)[0][31] == x[0].float().cpu().numpy()).all()
+    assert (held_rows(cache, table, 1, 5, 16)[0][3:] == x[2:].float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+@pytest.mark.parametrize("hd,ps,Hkv,keys", [(128, 16, 2, [1]), (64, 32, 3, [0, 33, 64, 7, 0]), (128, 64, 8, [300, 1, 129]),
+                                           (64, 128, 1, [127, 128, 129])])
+def test_gather(kind, hd, ps, Hkv, keys):
+    rng = np.random.default_rng(hd + ps)
+    cache, held = make_cache(rng, kind, hd, ps, Hkv, keys)
+    total = sum(keys)
+    k = torch.full((total + 5, Hkv, hd), 9.0, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    eb.kv_gather(cache, dev(cu(keys)), total + 5, k_out=k, v_out=v)
+    assert cache.check() == 0
+    for got, i in ((k, 0), (v, 1)):
+        got = got.double().cpu().numpy()
+        assert (got[:total] == np.concatenate([h[i] for h in held])).all() and (got[total:] == 9.0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+@pytest.mark.parametrize("hd,ps,Hkv,layers", [(128, 16, 2, 1), (64, 32, 3, 5), (128, 64, 1, 64)])
+def test_accept(kind, hd, ps, Hkv, layers):
+    rng = np.random.default_rng(layers)
+    S, lens = 24, [0, 30, 61, 5, 17]
+    B = len(lens)
+    acc = np.array([0, 1, S - 1, 9, 5], np.int32)
+    slots = np.full((B, S), -1, np.int32)
+    for b in range(B):
+        slots[b, :acc[b]] = np.sort(rng.choice(np.arange(1, S), acc[b], replace=False))
+    slots[4, :5] = [1, 2, 3, 4, 5]                                  # nothing to move
+    room = [n + S for n in lens]
+    made = [make_cache(np.random.default_rng(7), kind, hd, ps, Hkv, room) for _ in range(layers)]
+    table = made[0][0].page_table                                   # (one shape, one table)
+    caches = []
+    for i, (c, _) in enumerate(made):
+        sc = () if kind == "bf16" else (c.k_scale, c.v_scale, 1.0, 0.5)
+        caches.append(eb.KVCache(c.k, c.v.roll(i, 0).contiguous() if i else c.v, table, *sc))
+    before = [eb.kv_gather(c, dev(cu(room)), sum(room)) for c in caches]
+    lens_t = dev(np.array(lens, np.int32))
+    new = eb.kv_accept(caches, lens_t, dev(acc), dev(slots))
+    for c in caches:
+        assert c.check() == 0
+    assert new.cpu().tolist() == [n + 1 + a for n, a in zip(lens, acc)]
+    at = cu(room)
+    for c, old in zip(caches, before):
+        got = eb.kv_gather(c, dev(cu(room)), sum(room))
+        for x, y in zip(got, old):
+            x, y = x.view(torch.int16).cpu().numpy(), y.view(torch.int16).cpu().numpy()   # bits: poisoned rows are NaN
+            for b in range(B):
+                o = at[b]
+                want = y[o:at[b + 1]].copy()
+                want[lens[b] + 1:lens[b] + 1 + acc[b]] = y[o + lens[b] + slots[b, :acc[b]]]
+                assert (x[o:at[b + 1]] == want).all()
+    same = eb.kv_accept(caches, lens_t, dev(np.zeros(B, np.int32)), dev(slots), new_lens=lens_t)   # in place
+    assert same is lens_t and lens_t.cpu().tolist() == [n + 1 for n in lens]
+
+
+def test_accept_refuses_paths_that_do_not_ascend():
+    rng = np.random.default_rng(8)
+    cache, held = make_cache(rng, "bf16", 64, 16, 1, [30, 30, 30])
+    slots = np.full((3, 8), -1, np.int32)
+    slots[0, :3] = [2, 5, 5]
+    slots[1, :3] = [1, 9, 3]
+    slots[2, :2] = [3, 6]
+    new = eb.kv_accept([cache], dev(np.array([20, 20, 20], np.int32)), dev(np.array([3, 3, 2], np.int32)), dev(slots))
+    with pytest.raises(eb.EagleError) as e:
+        cache.check()
+    assert "0x4" in str(e.value)
+    assert new.cpu().tolist() == [23, 22, 23]                        # each path ends before the bad slot
+    k, _ = eb.kv_gather(cache, dev(cu([30] * 3)), 90)
+    k = k.double().cpu().numpy()
+    assert (k[21] == held[0][0][22]).all() and (k[22] == held[0][0][25]).all() and (k[60 + 22] == held[2][0][26]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+def test_a_round_of_drafting_and_verification(kind):
+    """A prefix appended to pages, gathered for the draft; its tree appended layer by layer and
+    attended with the tree's mask; the accepted path kept in every layer; the next prefix gathered.
+    The whole round runs on one stream without reading anything back."""
+    cfg = configs.get("small_dyn")
+    W, I = synth.make_weights(cfg), synth.make_inputs(cfg)
+    B, H, hd, ps = cfg.B, cfg.n_kv_heads, cfg.head_dim, 32
+    n = np.diff(I["cu_seqlens"])
+    S = cfg.kept_per_request() + 1
+    rng = np.random.default_rng(11)
+    table, P = pages(rng, [int(x) + S for x in n], ps)
+    shared = dev(table)                                              # the layers' one page table
+    layers = [eb.KVCache.empty(P, ps, H, hd, shared, four_bit=kind == "f4") for _ in range(2)]
+    dI = eb.device_inputs(I)
+    cus, zero = dI["cu_seqlens"], torch.zeros(B, dtype=torch.int32, device="cuda")
+    kk, vv = (dI[x].view(torch.bfloat16).view(-1, H, hd) for x in ("k_cache", "v_cache"))
+    for c in layers:
+        eb.kv_append(c, kk, vv, cus, zero)                            # (already rotated)
+    k, v = eb.kv_gather(layers[0], cus, int(n.sum()))
+    if kind == "bf16":
+        assert torch.equal(k, kk) and torch.equal(v, vv)
+    dI["k_cache"], dI["v_cache"] = k.view(torch.int16), v.view(torch.int16)
+    d = eb.EagleDraft(cfg, eb.device_weights(W))
+    tree = d.tree(dI)
+    lens = (cus[1:] - cus[:-1]).contiguous()
+    cr = torch.arange(B + 1, dtype=torch.int32, device="cuda") * S
+    rope = eb.Rope(hd, theta=cfg.rope_theta)
+    pos = tree["positions"].reshape(-1)
+    qkv = [torch.randn(B * S, (cfg.n_heads + 2 * H) * hd, device="cuda").to(torch.bfloat16) for _ in layers]
+    outs = []
+    for c, x in zip(layers, qkv):
+        q, k1, v1 = (y.unflatten(1, (-1, hd)) for y in x.split([cfg.n_heads * hd, H * hd, H * hd], 1))
+        qr = eb.kv_append(c, k1, v1, cr, lens, positions=pos, rope=rope, q=q)
+        outs.append((qr, eb.kv_attention(c, qr, cr, lens, max_rows=S, max_len=int(n.max()) + S, mask=tree["mask"])))
+    # a path of the tree: the greedy walk down the first children
+    acc, slots = torch.zeros(B, dtype=torch.int32), torch.full((B, S), -1, dtype=torch.int32)
+    par = tree["parents"].cpu()
+    for b in range(B):
+        u = 0
+        while True:
+            kids = [i for i in range(1, S) if par[b, i] == u]
+            if not kids:
+                break
+            u = kids[-1]
+            slots[b, acc[b]] = u
+            acc[b] += 1
+    assert int(acc.min()) >= 1
+    before = [eb.kv_gather(c, dev(cu([int(x) + S for x in n])), int(n.sum()) + B * S) for c in layers]
+    new = eb.kv_accept(layers, lens, acc.cuda(), slots.cuda())
+    for c in layers:
+        assert c.check() == 0
+    d.check()
+    nl = new.cpu().numpy()
+    assert (nl == n + 1 + acc.numpy()).all()
+    at = cu([int(x) + S for x in n])
+    for c, (bk, bv), (qr, o) in zip(layers, before, outs):
+        k, v = eb.kv_gather(c, dev(cu(nl)), int(nl.sum()))
+        to = cu(nl)
+        for b in range(B):
+            path = [0] + slots[b, :acc[b]].tolist()
+            idx = at[b] + np.concatenate([np.arange(n[b]), n[b] + np.array(path)])
+            assert torch.equal(k[to[b]:to[b + 1]], bk[idx]) and torch.equal(v[to[b]:to[b + 1]], bv[idx])
+            K64, V64 = (x[at[b]:at[b] + n[b] + S].double().cpu().numpy() for x in (bk, bv))
+            m = tree["mask"][b].cpu().numpy()
+            ref, _, mag, qk, vs = K.attention(qr[b * S:(b + 1) * S].double().cpu().numpy(), K64, V64, see_matrix(int(n[b]), S, m), hd ** -0.5)
+            got = o[b * S:(b + 1) * S].double().cpu().numpy()
+            # (the attention's own test derives this bound)
+            tol = (2.0 ** -8 + 2 * ((hd + 4) * U * qk + 2.0 ** -21 * (1 + qk))[..., None] + (hd + 128) * U) * mag + 2.0 ** -8 * np.abs(ref) \
+                + 2.0 ** -32 * vs + 1e-30
+            assert (np.abs(got - ref) <= tol).all()
+    d.close()
+
+
+def test_bindings_refuse_what_the_kernels_cannot_take():
+    rng = np.random.default_rng(12)
+    cache, _ = make_cache(rng, "bf16", 128, 16, 2, [20])
+    x = torch.randn(1, 2, 128, device="cuda").to(torch.bfloat16)
+    q = torch.randn(1, 4, 128, device="cuda").to(torch.bfloat16)
+    c1, n1 = dev(cu([1])), dev(np.array([19], np.int32))
+    bad = [lambda: eb.kv_append(cache, x.half(), x.half(), c1, n1), lambda: eb.kv_append(cache, x, x.float(), c1, n1),
+           lambda: eb.kv_append(cache, x[:, :1], x, c1, n1), lambda: eb.kv_append(cache, x, x, c1.long(), n1),
+           lambda: eb.kv_append(cache, x.transpose(0, 1), x, c1, n1), lambda: eb.kv_append(cache, x, x, c1, n1, q=q),
+           lambda: eb.kv_append(cache, x, x, c1, n1, rope=eb.Rope(128)), lambda: eb.kv_append(cache, x.cpu(), x, c1, n1),
+           lambda: eb.kv_append(cache, x[..., ::2], x, c1, n1),
+           lambda: eb.kv_append(cache, x, x, dev(cu([1, 0])), dev(np.array([1, 1], np.int32))),
+           lambda: eb.kv_attention(cache, q.float(), c1, n1, 1, 20), lambda: eb.kv_attention(cache, q[:, :3], c1, n1, 1, 20),
+           lambda: eb.kv_attention(cache, q, c1, n1, 1, 20, mask=torch.ones(1, 1, 1, device="cuda")),
+           lambda: eb.kv_attention(cache, q, c1, n1, 0, 20), lambda: eb.kv_attention(cache, q, c1, n1, 1, 20, out=q.float()),
+           lambda: eb.kv_attention(cache, q, c1, n1, 1, 5000, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: eb.kv_gather(cache, dev(cu([1, 1, 1])), 3), lambda: eb.kv_gather(cache, c1, -1),
+           lambda: eb.kv_gather(cache, c1, 1, k_out=torch.empty(2, 2, 128, dtype=torch.bfloat16, device="cuda")),
+           lambda: eb.kv_accept([], n1, n1, n1[None]), lambda: eb.kv_accept(cache, n1, n1.long(), n1[None]),
+           lambda: eb.rotary(q.half(), n1, eb.Rope(128)), lambda: eb.rotary(q, n1.cpu(), eb.Rope(128)),
+           lambda: eb.rotary(q, dev(np.zeros(2, np.int32)), eb.Rope(128)), lambda: eb.Rope(128, inv_freq=[1.0]),
+           lambda: eb.KVCache(cache.k, cache.v, cache.page_table.long()), lambda: eb.KVCache(cache.k, cache.v[:1], cache.page_table),
+           lambda: eb.KVCache(cache.k, cache.v, cache.page_table, k_scale=cache.k), lambda: eb.KVCache(cache.k.cpu(), cache.v, cache.page_table)]
+    for i, f in enumerate(bad):
+        with pytest.raises(eb.EagleError):
+            f()
+            raise AssertionError(f"case {i} was taken")
+    assert cache.check() == 0
