@@ -548,51 +548,69 @@ def _bad(msg: str):
     raise EagleError(EAGLE_ERR_INVALID_ARG, msg)
 
 
+_torch = None
+
+
 def _here(stream):
-    """(current device, raw handle of the call's stream)"""
-    import torch
-    dev = torch.cuda.current_device()
-    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    """(torch, current device, raw handle of the call's stream)"""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    dev = _torch.cuda.current_device()
+    return _torch, dev, (_torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def _tensor(t, name: str, dtype, shape, dev: int, contiguous: bool = True):
-    """A tensor of device ``dev`` with this dtype and shape (None: any size)."""
+    """Refuses all but a tensor of device ``dev`` with this dtype and shape (None: any size)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and (not contiguous or t.is_contiguous()):
+            s = t.shape
+            if s == shape or (len(s) == len(shape) and all([w is None or w == n for w, n in zip(shape, s)])):
+                return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         _bad(f"{name} must be a {dtype} tensor")
-    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
-        _bad(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        _bad(f"{name} must be contiguous")
     if t.get_device() != dev:
         _bad(f"{name} must be on the current CUDA device")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        _bad(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
+    _bad(f"{name} must be contiguous")
+
+
+def _ints(t, name: str, n, dev: int) -> int:
+    """A contiguous int32 vector (of n numbers, if n is given): its length."""
+    if not (isinstance(t, _torch.Tensor) and t.dtype is _torch.int32 and t.dim() == 1 and t.get_device() == dev and t.is_contiguous()
+            and (n is None or t.numel() == n)):
+        _tensor(t, name, _torch.int32, (n,), dev)
+    return t.numel()
 
 
 def _rows(t, name: str, dtype, shape, dev: int) -> int:
     """Rows [N, H, hd] whose heads are contiguous: the row stride in elements."""
     _tensor(t, name, dtype, shape, dev, contiguous=False)
     n, h, d = t.shape
-    s = t.stride()
-    if n and ((s[2] != 1 and d > 1) or (h > 1 and s[1] != d)):
+    s0, s1, s2 = t.stride()
+    if n and ((s2 != 1 and d > 1) or (h > 1 and s1 != d)):
         _bad(f"{name}: the heads of a row must be contiguous")
-    return s[0] if n > 1 else h * d
+    return s0 if n > 1 else h * d
 
 
 def _new(like, shape, dtype, stream):
     """An uninitialised tensor that belongs to ``stream`` (None: the current one)."""
-    import torch
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
+        return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
+    with _torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
 
 def _float_kind(t, name: str) -> int:
-    import torch
     d = getattr(t, "dtype", None)
-    if d is torch.bfloat16:
+    if d is _torch.bfloat16:
         return DTYPE_BF16
-    if d is torch.float32:
+    if d is _torch.float32:
         return DTYPE_F32
     _bad(f"{name} must be a float32 or bfloat16 tensor")
 
@@ -650,12 +668,11 @@ class Rope:
 
 def rotary(x, positions, rope: Rope, out=None, stream=None):
     """x [N, H, hd] (float32 or bfloat16) rotated at int32 positions [N]; out may be x."""
-    import torch
-    dev, st = _here(stream)
+    torch, dev, st = _here(stream)
     kind = _float_kind(x, "x")
     ld = _rows(x, "x", x.dtype, (None, None, None), dev)
     N, H, hd = x.shape
-    _tensor(positions, "positions", torch.int32, (N,), dev)
+    _ints(positions, "positions", N, dev)
     if out is None:
         out = _new(x, (N, H, hd), x.dtype, stream)
         old = H * hd
@@ -672,8 +689,7 @@ class KVCache:
     (e4m3) scales [pages, Hkv, page_size, hd / 16]; page_table int32 [B, max_pages]."""
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None, k_global: float = 1.0, v_global: float = 1.0):
-        import torch
-        dev = torch.cuda.current_device()
+        torch, dev, _ = _here(None)
         f4 = getattr(k, "dtype", None) == torch.uint8
         _tensor(k, "k", torch.uint8 if f4 else torch.bfloat16, (None,) * 4, dev)
         _tensor(v, "v", k.dtype, tuple(k.shape), dev)
@@ -721,8 +737,7 @@ def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | 
               stream=None):
     """Store a step's keys (rotated with a rope) and values [N, Hkv, hd] behind each request's
     lens[b] keys; returns the rotated queries when q [N, Hq, hd] is given (q_out may be q)."""
-    import torch
-    dev, st = _here(stream)
+    torch, dev, st = _here(stream)
     H, hd = cache.n_kv_heads, cache.head_dim
     kind = _float_kind(k, "k")
     k_ld = _rows(k, "k", k.dtype, (None, H, hd), dev)
@@ -730,7 +745,7 @@ def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | 
     v_ld = _rows(v, "v", k.dtype, (N, H, hd), dev)
     B = _requests(cache, cu_rows, lens, dev)
     if rope is not None:
-        _tensor(positions, "positions", torch.int32, (N,), dev)
+        _ints(positions, "positions", N, dev)
     Hq = q_ld = qo_ld = 0
     if q is not None:
         q_ld = _rows(q, "q", k.dtype, (N, None, hd), dev)
@@ -747,10 +762,8 @@ def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | 
 
 
 def _requests(cache: KVCache, cu_rows, lens, dev: int) -> int:
-    import torch
-    _tensor(lens, "lens", torch.int32, (None,), dev)
-    B = lens.shape[0]
-    _tensor(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
+    B = _ints(lens, "lens", None, dev)
+    _ints(cu_rows, "cu_rows", B + 1, dev)
     if cache.max_requests < B:
         _bad("the page table has fewer rows than lens")
     return B
@@ -759,10 +772,8 @@ def _requests(cache: KVCache, cu_rows, lens, dev: int) -> int:
 def kv_gather(cache: KVCache, cu_seqlens, total: int, k_out=None, v_out=None, stream=None):
     """The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every request, packed bf16
     [total, Hkv, hd]: the k_cache / v_cache of EagleDraft.tree and EagleVerify.verify."""
-    import torch
-    dev, st = _here(stream)
-    _tensor(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
-    B, total = cu_seqlens.shape[0] - 1, int(total)
+    torch, dev, st = _here(stream)
+    B, total = _ints(cu_seqlens, "cu_seqlens", None, dev) - 1, int(total)
     if B < 1 or total < 0 or cache.max_requests < B:
         _bad("kv_gather: cu_seqlens needs 1 .. page_table rows requests, total must not be negative")
     shape = (total, cache.n_kv_heads, cache.head_dim)
@@ -783,21 +794,20 @@ def kv_accept(caches, lens, accept_len, accept_slots, new_lens=None, stream=None
     """Keep the accepted path of a verified tree (appended behind lens[b] keys in slot order) in
     every cache of the list (one per layer, one shape and page table); returns the new lengths
     lens + 1 + accept_len (new_lens may be lens)."""
-    import torch
-    dev, st = _here(stream)
+    torch, dev, st = _here(stream)
     caches = [caches] if isinstance(caches, KVCache) else list(caches)
     if not caches:
         _bad("kv_accept: no caches")
     _tensor(accept_slots, "accept_slots", torch.int32, (None, None), dev)
     B, S = accept_slots.shape
-    _tensor(lens, "lens", torch.int32, (B,), dev)
-    _tensor(accept_len, "accept_len", torch.int32, (B,), dev)
+    _ints(lens, "lens", B, dev)
+    _ints(accept_len, "accept_len", B, dev)
     if caches[0].max_requests < B:
         _bad("the page table has fewer rows than lens")
     if new_lens is None:
         new_lens = _new(lens, (B,), torch.int32, stream)
     else:
-        _tensor(new_lens, "new_lens", torch.int32, (B,), dev)
+        _ints(new_lens, "new_lens", B, dev)
     n = len(caches)
     arr = C.byref(caches[0].c) if n == 1 else (KVCacheC * n)(*[c.c for c in caches])
     _check(load().eagle_kv_accept(arr, n, B, S, lens.data_ptr(), accept_len.data_ptr(), accept_slots.data_ptr(),
@@ -812,8 +822,7 @@ def kv_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, 
     [B, S, S]) or j <= i.  max_rows / max_len bound one request's rows and keys.  Returns out,
     or (out, lse [N, Hq]) with lse=True or a tensor.  ``workspace``: a uint8 tensor to keep
     (at least kv_attention_workspace bytes); else one is taken from torch's allocator."""
-    import torch
-    dev, st = _here(stream)
+    torch, dev, st = _here(stream)
     q_ld = _rows(q, "q", torch.bfloat16, (None, None, cache.head_dim), dev)
     N, Hq, hd = q.shape
     B = _requests(cache, cu_rows, lens, dev)

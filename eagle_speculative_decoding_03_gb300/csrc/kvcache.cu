@@ -90,17 +90,33 @@ struct RotArgs {
   int rows_per_cta, slices;
 };
 
-EAGLE_DEV void load8(const float* p, float* x) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// 8 consecutive values of a row as loaded: two 16-byte words of floats or one of bf16
+template <typename T>
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+EAGLE_DEV Raw8<T> load_raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    r.w[4 * i] = u.x;
+    r.w[4 * i + 1] = u.y;
+    r.w[4 * i + 2] = u.z;
+    r.w[4 * i + 3] = u.w;
+  }
+  return r;
 }
-EAGLE_DEV void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+EAGLE_DEV void unpack8(const Raw8<float>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
+}
+EAGLE_DEV void unpack8(const Raw8<__nv_bfloat16>& r, float* x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    x[2 * i] = __uint_as_float(r.w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
   }
 }
 EAGLE_DEV uint32_t pack2(float a, float b) {
@@ -130,13 +146,15 @@ EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, const float* x, float gl
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   const uint32_t s = f32_to_e4m3(__fdiv_rn(top, 6.0f * global));
   const float unit = e4m3_to_f32(s) * global;
+  // value / unit as a product with the reciprocal, off by less than 2^-20 up to 6; rounded to
+  // multiples of 2^-18 (adding and taking away 48), so that a value on a border between two codes,
+  // whose quotient is a multiple of 1/4, is on it exactly (a bf16 value over a 4-bit scale that is
+  // not on the border is 2^-11 or more away; an IEEE division each took half the kernel's time)
+  const float inv = unit > 0.f ? __fdiv_rn(1.0f, unit) : 0.f;
+  auto ratio = [&](float v) { return copysignf(__fadd_rn(__fmaf_rn(fabsf(v), inv, 48.f), -48.f), v); };
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    // IEEE division: a value on a border between two codes divides to the border exactly
-    const float a = unit > 0.f ? __fdiv_rn(y[e], unit) : 0.f, b = unit > 0.f ? __fdiv_rn(y[e + 1], unit) : 0.f;
-    w |= e2m1x2(a, b) << (4 * e);
-  }
+  for (int e = 0; e < 8; e += 2) w |= e2m1x2(ratio(y[e]), ratio(y[e + 1])) << (4 * e);
   if (live) {
     *reinterpret_cast<uint32_t*>(code) = w;
     if (even) *scale = static_cast<uint8_t>(s);
@@ -202,29 +220,26 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
   const int other = rot && !rt.inter ? (o < ro ? lane + ro : lane - ro) : lane;
   const int heads = a.Hq + a.Hk + a.Hv;
   const int step = wpr * a.slices * hpw;
-#pragma unroll 2
-  for (int h0 = (blockIdx.y * wpr + warp % wpr) * hpw; h0 < heads; h0 += step) {
-    const int h = h0 + sub;
-    const bool live = in_warp && h < heads;
+  auto source = [&](int h) {
+    return (h < a.Hq            ? static_cast<const T*>(a.q) + n * a.q_ld + static_cast<long long>(h) * a.hd
+            : h < a.Hq + a.Hk ? static_cast<const T*>(a.k) + n * a.k_ld + static_cast<long long>(h - a.Hq) * a.hd
+                              : static_cast<const T*>(a.v) + n * a.v_ld + static_cast<long long>(h - a.Hq - a.Hk) * a.hd) + 8 * o;
+  };
+  auto turn = [&](int h, bool live, const Raw8<T>& raw) {
     float x[8], y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    unpack8(raw, x);
     const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
-    if (live) {
-      const T* src = is_q   ? static_cast<const T*>(a.q) + n * a.q_ld + static_cast<long long>(h) * a.hd
-                     : is_k ? static_cast<const T*>(a.k) + n * a.k_ld + static_cast<long long>(h - a.Hq) * a.hd
-                            : static_cast<const T*>(a.v) + n * a.v_ld + static_cast<long long>(h - a.Hq - a.Hk) * a.hd;
-      load8(src + 8 * o, x);
-    }
     if (rt.inter) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], x[e ^ 1] * s[e]);
     } else {
+      Raw8<T> oth;
+      float z[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float z = __shfl_sync(0xffffffffu, x[e], other);
-        y[e] = fmaf(x[e], c[e], z * s[e]);
-      }
+      for (int e = 0; e < static_cast<int>(2 * sizeof(T)); ++e) oth.w[e] = __shfl_sync(0xffffffffu, raw.w[e], other);
+      unpack8(oth, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], z[e] * s[e]);
     }
     if (!rot || (!is_q && !is_k)) {          // dims behind rot_dim, and values: as they are
 #pragma unroll
@@ -237,32 +252,53 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
       const size_t row = to ? kv_row(a.pool, s_page[r], kvh, s_tok[r]) : 0;
       if (CACHE == EAGLE_CACHE_BF16) {
         if (to) store8(static_cast<__nv_bfloat16*>(is_k ? a.pool.k : a.pool.v) + row * a.hd + 8 * o, y);
-      } else {
+      } else if (__any_sync(0xffffffffu, to)) {
         store8_f4(static_cast<uint8_t*>(is_k ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
                   static_cast<uint8_t*>(is_k ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), y,
                   is_k ? a.pool.kg : a.pool.vg, to, (o & 1) == 0);
       }
     }
+  };
+  // HB heads of a warp in flight: their loads before the first store (which might alias them)
+  constexpr int HB = 4;
+  for (int h0 = (blockIdx.y * wpr + warp % wpr) * hpw; h0 < heads; h0 += HB * step) {
+    Raw8<T> raw[HB];
+    bool live[HB];
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      const int h = h0 + i * step + sub;
+      live[i] = in_warp && h < heads;
+#pragma unroll
+      for (int e = 0; e < static_cast<int>(2 * sizeof(T)); ++e) raw[i].w[e] = 0u;
+      if (live[i]) raw[i] = load_raw8(source(h));
+    }
+#pragma unroll
+    for (int i = 0; i < HB; ++i)
+      if (h0 + i * step < heads) turn(h0 + i * step + sub, live[i], raw[i]);
   }
 }
 
 // ------------------------------------------------------------------------- gather
 constexpr int GA_THREADS = 256;
-constexpr int GA_TOKENS = 8;
+constexpr int GA_TOKENS = 16;
+constexpr int GA_STEPS = 4;
 
 struct GatherArgs {
   KvPool pool;
   int B, total;
+  unsigned by_heads;                         // ceil(2^32 / Hkv): j / Hkv by a product, exact for j < 16 Hkv, Hkv < 2^14; 0 for one head
   const int* cu;
   __nv_bfloat16* k_out;
   __nv_bfloat16* v_out;
   unsigned* err;
 };
 
-// A CTA writes GA_TOKENS packed rows of K and V, 16 bytes per thread and step, consecutive
-// threads consecutive bytes of the output; reads come in runs of one head's row.
-template <int CACHE>
+// A CTA writes GA_TOKENS packed rows of K (blockIdx.y = 0) or V, 16 bytes per thread and step,
+// consecutive threads consecutive bytes of the output; reads come in runs of one head's row.
+// Loads of GA_STEPS steps are issued before the first store.
+template <int HD, int CACHE>
 __global__ void __launch_bounds__(GA_THREADS) gather_kernel(const GatherArgs a) {
+  constexpr int OCT = HD / 8, ROWS = GA_THREADS / OCT;     // rows (token, head) a step covers
   __shared__ int s_page[GA_TOKENS], s_tok[GA_TOKENS];
   const int t0 = blockIdx.x * GA_TOKENS, tid = threadIdx.x;
   if (tid < GA_TOKENS) {
@@ -277,33 +313,53 @@ __global__ void __launch_bounds__(GA_THREADS) gather_kernel(const GatherArgs a) 
     s_tok[tid] = t;
   }
   __syncthreads();
-  const int oct = a.pool.hd >> 3, per = a.pool.Hkv * oct;   // octets per token
-  const int n_all = 2 * GA_TOKENS * per;
-#pragma unroll 4
-  for (int i = tid; i < n_all; i += GA_THREADS) {
-    const bool is_v = i >= GA_TOKENS * per;
-    const int r = is_v ? i - GA_TOKENS * per : i;
-    const int tk = r / per, rest = r - tk * per;
-    const int h = rest / oct, o = rest - h * oct;
-    const int page = s_page[tk];
-    if (page == -2) continue;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (page >= 0) {
-      const size_t row = kv_row(a.pool, page, h, s_tok[tk]);
-      if (CACHE == EAGLE_CACHE_BF16) {
-        u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? a.pool.v : a.pool.k) + row * a.pool.hd) + o);
-      } else {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_v ? a.pool.v : a.pool.k) + row * (a.pool.hd >> 1)) + o);
-        const uint32_t sb = __ldg(static_cast<const uint8_t*>(is_v ? a.pool.vs : a.pool.ks) + row * (a.pool.hd >> 4) + (o >> 1));
-        const float unit = e4m3_to_f32(sb) * (is_v ? a.pool.vg : a.pool.kg);
-        float x[8];
+  const bool is_v = blockIdx.y != 0;
+  const uint8_t* pool = static_cast<const uint8_t*>(is_v ? a.pool.v : a.pool.k);
+  const uint8_t* scales = static_cast<const uint8_t*>(is_v ? a.pool.vs : a.pool.ks);
+  const float global = is_v ? a.pool.vg : a.pool.kg;
+  __nv_bfloat16* const out = is_v ? a.v_out : a.k_out;
+  const int o = tid % OCT, n_rows = GA_TOKENS * a.pool.Hkv;
+  for (int j0 = tid / OCT; j0 < n_rows; j0 += GA_STEPS * ROWS) {
+    uint4 u[GA_STEPS];
+    uint32_t sb[GA_STEPS];
+    int page[GA_STEPS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = e2m1_to_f32(w >> (4 * e)) * unit;
-        u = pack8(x);
+    for (int i = 0; i < GA_STEPS; ++i) {
+      const int j = j0 + i * ROWS;
+      u[i] = make_uint4(0u, 0u, 0u, 0u);
+      sb[i] = 0u;
+      page[i] = -2;
+      if (j < n_rows) {
+        const int tk = a.by_heads ? __umulhi(j, a.by_heads) : j, h = j - tk * a.pool.Hkv;
+        page[i] = s_page[tk];
+        if (page[i] >= 0) {
+          const size_t row = kv_row(a.pool, page[i], h, s_tok[tk]);
+          if (CACHE == EAGLE_CACHE_BF16) {
+            u[i] = __ldg(reinterpret_cast<const uint4*>(pool + row * (HD * 2)) + o);
+          } else {
+            u[i].x = __ldg(reinterpret_cast<const uint32_t*>(pool + row * (HD / 2)) + o);
+            sb[i] = __ldg(scales + row * (HD / 16) + (o >> 1));
+          }
+        }
       }
     }
-    __nv_bfloat16* out = is_v ? a.v_out : a.k_out;
-    *reinterpret_cast<uint4*>(out + (static_cast<size_t>(t0 + tk) * per + rest) * 8) = u;
+#pragma unroll
+    for (int i = 0; i < GA_STEPS; ++i) {
+      if (page[i] == -2) continue;
+      if (CACHE == EAGLE_CACHE_F4) {
+        const uint32_t w = u[i].x;
+        const float unit = e4m3_to_f32(sb[i]) * global;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = e2m1_pair_f32(w >> (8 * e));
+          x[2 * e] = f.x * unit;
+          x[2 * e + 1] = f.y * unit;
+        }
+        u[i] = pack8(x);
+      }
+      *reinterpret_cast<uint4*>(out + (static_cast<size_t>(t0) * a.pool.Hkv + j0 + i * ROWS) * HD + 8 * o) = u[i];
+    }
   }
 }
 
@@ -349,32 +405,37 @@ EAGLE_DEV void move_rows(const KvPool& c, char* base, int bytes, int count, cons
 
 // One CTA per (request, cache, key / value).
 __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __grid_constant__ AcceptCaches caches) {
-  __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_n;
+  __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_end[2];
   const int b = blockIdx.x, tid = threadIdx.x;
   const int base = __ldg(a.lens + b);
-  if (tid == 0) {
-    // the path: ascending slots behind the root; anything else ends it
-    int n = min(max(__ldg(a.accept_len + b), 0), a.S - 1), prev = 0, j = 0;
-    if (__ldg(a.accept_len + b) != n) atomicOr(a.err, DEVERR_TOKEN);
-    for (; j < n; ++j) {
-      const int s = __ldg(a.slots + static_cast<size_t>(b) * a.S + j);
-      if (s <= prev || s >= a.S) {
-        atomicOr(a.err, DEVERR_TOKEN);
-        break;
-      }
-      prev = s;
-    }
-    s_n = j;
+  // the path: ascending slots behind the root; anything else ends it
+  const int want = __ldg(a.accept_len + b);
+  int n = min(max(want, 0), a.S - 1);
+  bool wrong = false;
+  int s = 0;
+  if (tid < 64) {
+    s = tid < n ? __ldg(a.slots + static_cast<size_t>(b) * a.S + tid) : 0;
+    src_tok[tid] = s;
+    s_end[tid >> 5] = 64;
   }
   __syncthreads();
-  const int n = s_n;
+  if (tid < 64) {
+    wrong = tid < n && (s <= (tid ? src_tok[tid - 1] : 0) || s >= a.S);
+    const unsigned bits = __ballot_sync(0xffffffffu, wrong);
+    if ((tid & 31) == 0 && bits) s_end[tid >> 5] = tid + __ffs(bits) - 1;
+  }
+  __syncthreads();
+  const int end = min(s_end[0], s_end[1]);
+  if (tid == 0 && (want != n || end < n)) atomicOr(a.err, DEVERR_TOKEN);
+  n = min(n, end);
   if (tid < n) {
-    const int s = __ldg(a.slots + static_cast<size_t>(b) * a.S + tid);
     src_tok[tid] = base + s;
     dst_tok[tid] = base + 1 + tid;
     src_page[tid] = s == tid + 1 ? -1 : kv_page(a.pool, b, base + s, a.err);   // (already in place)
     dst_page[tid] = kv_page(a.pool, b, base + 1 + tid, a.err);
   }
+  // new_lens apart from lens: written here; in place, after every CTA has read lens
+  if (tid == 0 && a.new_lens != a.lens && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + 1 + n;
   __syncthreads();
   const int c = blockIdx.y, w = blockIdx.z;  // cache, 0 keys / 1 values
   if (a.f4) {
@@ -385,7 +446,7 @@ __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __gri
   }
 }
 
-// The new lengths, after the moves (new_lens may be lens: every CTA of the moves reads lens).
+// The new lengths in place of the old (every CTA of the moves reads those).
 __global__ void keep_lens_kernel(const KeepArgs a) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= a.B) return;
@@ -540,13 +601,18 @@ extern "C" eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t
   a.B = B;
   a.total = total;
   a.cu = cu_seqlens;
+  if (cache->n_kv_heads >= 1 << 14) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: more than 16383 heads", who);
+  a.by_heads = cache->n_kv_heads > 1 ? static_cast<unsigned>(((1ull << 32) + cache->n_kv_heads - 1) / cache->n_kv_heads) : 0u;
   a.k_out = static_cast<__nv_bfloat16*>(k_out);
   a.v_out = static_cast<__nv_bfloat16*>(v_out);
   a.err = err_word;
-  const int grid = (total + GA_TOKENS - 1) / GA_TOKENS;
+  const dim3 grid((total + GA_TOKENS - 1) / GA_TOKENS, 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->kind == EAGLE_CACHE_BF16) gather_kernel<EAGLE_CACHE_BF16><<<grid, GA_THREADS, 0, st>>>(a);
-  else gather_kernel<EAGLE_CACHE_F4><<<grid, GA_THREADS, 0, st>>>(a);
+  const bool bf = cache->kind == EAGLE_CACHE_BF16;
+  if (cache->head_dim == 64 && bf) gather_kernel<64, EAGLE_CACHE_BF16><<<grid, GA_THREADS, 0, st>>>(a);
+  else if (cache->head_dim == 64) gather_kernel<64, EAGLE_CACHE_F4><<<grid, GA_THREADS, 0, st>>>(a);
+  else if (bf) gather_kernel<128, EAGLE_CACHE_BF16><<<grid, GA_THREADS, 0, st>>>(a);
+  else gather_kernel<128, EAGLE_CACHE_F4><<<grid, GA_THREADS, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }
@@ -587,7 +653,7 @@ extern "C" eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_
   a.err = err_word;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   keep_kernel<<<dim3(B, n_caches, 2), 256, 0, st>>>(a, ac);
-  keep_lens_kernel<<<(B + 127) / 128, 128, 0, st>>>(a);
+  if (new_lens == lens) keep_lens_kernel<<<(B + 127) / 128, 128, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }

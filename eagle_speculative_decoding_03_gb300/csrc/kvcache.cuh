@@ -65,11 +65,11 @@ EAGLE_DEV uint32_t f32_to_e4m3(float x) {
 EAGLE_DEV float e4m3_to_f32(uint32_t b) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
 }
-// The value of an e2m1 code: sign and 3 magnitude bits at the top of an fp16's exponent and
-// mantissa stand for value * 2^-14 (its subnormals included), so one shift and one product decode.
-EAGLE_DEV float e2m1_to_f32(uint32_t n) {
-  const uint16_t h = static_cast<uint16_t>(((n & 8u) << 12) | ((n & 7u) << 9));
-  return __half2float(__ushort_as_half(h)) * 16384.0f;
+// The values of the two e2m1 codes in the low byte of w (low nibble first).
+EAGLE_DEV float2 e2m1_pair_f32(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 t<4>;\n\tmov.b32 {t0, t1, t2, t3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t0;\n\t}" : "=r"(h) : "r"(w));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
 // Checks a cache struct and fills the kernels' view; `who` names the entry point in messages.
