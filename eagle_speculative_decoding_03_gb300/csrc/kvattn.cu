@@ -26,7 +26,7 @@ constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes
 constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
 constexpr uint32_t KA_MISC = 2048;
 constexpr int KA_MAX_SLOTS = 14;
-constexpr int KA_FIXED = 6;               // a CTA's fixed cost in tiles
+constexpr int KA_FIXED = 12;              // a CTA's fixed cost in tiles
 constexpr int KS_FIXED = 2;               // the same for the kernel for few query vectors
 
 struct KaArgs {
@@ -103,14 +103,14 @@ EAGLE_DEV float max3_nan(float x, float y, float z) {
 }
 // (x, y) * (a, a) + (b, b) and (x, y) + (z, w), two fp32 lanes an instruction
 EAGLE_DEV void fma2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
-      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+  const float2 r = __ffma2_rn(make_float2(x, y), make_float2(a, a), make_float2(b, b));
+  x = r.x;
+  y = r.y;
 }
 EAGLE_DEV void add2(float& x, float& y, float z, float w) {
-  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
-      "mov.b64 {%0, %1}, p;\n\t}"
-      : "+f"(x), "+f"(y) : "f"(z), "f"(w));
+  const float2 r = __fadd2_rn(make_float2(x, y), make_float2(z, w));
+  x = r.x;
+  y = r.y;
 }
 // `bytes` (a multiple of 16) of global memory into shared memory, completing on `bar`
 EAGLE_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -140,19 +140,18 @@ EAGLE_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 16 consecutive dims of a cached row: 8 code bytes and their scale -> 16 fp16 values (exact:
+// 8 consecutive dims of a cached row: 4 code bytes and the pair of their scale -> 8 fp16 values (exact:
 // a code has 2 significant bits and a scale 4; the range is 2^-10 .. 2688)
-EAGLE_DEV void dequant16(uint2 code, uint32_t scale, uint32_t* h) {
+EAGLE_DEV uint32_t scale_pair(uint32_t scale) {
   uint32_t s;
   asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s) : "r"(scale * 0x101u));
-  h[0] = mul_f16x2(e2m1_pair<0>(code.x), s);
-  h[1] = mul_f16x2(e2m1_pair<1>(code.x), s);
-  h[2] = mul_f16x2(e2m1_pair<2>(code.x), s);
-  h[3] = mul_f16x2(e2m1_pair<3>(code.x), s);
-  h[4] = mul_f16x2(e2m1_pair<0>(code.y), s);
-  h[5] = mul_f16x2(e2m1_pair<1>(code.y), s);
-  h[6] = mul_f16x2(e2m1_pair<2>(code.y), s);
-  h[7] = mul_f16x2(e2m1_pair<3>(code.y), s);
+  return s;
+}
+EAGLE_DEV void dequant8(uint32_t code, uint32_t s, uint32_t* h) {
+  h[0] = mul_f16x2(e2m1_pair<0>(code), s);
+  h[1] = mul_f16x2(e2m1_pair<1>(code), s);
+  h[2] = mul_f16x2(e2m1_pair<2>(code), s);
+  h[3] = mul_f16x2(e2m1_pair<3>(code), s);
 }
 
 // a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
@@ -200,10 +199,14 @@ EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;
 // must be bf16, kept as hi + lo parts (two products) where one query tile leaves the kernel bound
 // by bytes, and rounded to 8 bits where two tiles make it bound by the tensor cores (an output
 // error of half a bf16 step's size).  l sums the unrounded p.
-__host__ __device__ constexpr int ka_threads(int cache, int nb) { return cache == EAGLE_CACHE_F4 ? 512 : 128 + 128 * nb; }
+__host__ __device__ constexpr int ka_threads(int cache, int nb) { return 128 + 128 * nb + (cache == EAGLE_CACHE_F4 ? 256 : 0); }
+// registers per thread of the 4-bit kernel's roles after they moved (the launch checks their sum)
+constexpr int KA_REG_CTRL = 40;
+__host__ __device__ constexpr int ka_reg_softmax(int nb) { return nb == 2 ? 136 : 152; }
+__host__ __device__ constexpr int ka_reg_conv(int nb) { return nb == 2 ? 80 : 128; }
 __host__ __device__ constexpr uint32_t ka_entry(int hd) { return static_cast<uint32_t>(hd) * 2 * KA_CH; }
 // 4-bit caches: a ring of raw tiles (128 rows of codes, then their scales) behind the entries
-constexpr int KA_RAW = 7;
+constexpr int KA_RAW = 3;
 __host__ __device__ constexpr uint32_t ka_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_CH + hd / 16 * KA_CH; }
 
 template <int HD, int CACHE, int NB>
@@ -226,7 +229,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   uint8_t* misc = raw + (F4 ? KA_RAW * RAW : 0);
   const uint32_t misc_u = smem_u32(misc);
   const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 256,
-                 bar_pe = misc_u + 288, bar_fin = misc_u + 336;
+                 bar_pe = misc_u + 288, bar_q = misc_u + 320, bar_fin = misc_u + 336;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 344);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 348);
   const uint32_t bar_rf = misc_u + 352, bar_re = misc_u + 408;            // raw tiles full / free
@@ -234,6 +237,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [128] tree mask rows
 
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / a.blocks, blk0 = blockIdx.z - b * a.blocks;
+  pdl_trigger();                             // (the combine kernel may start and wait)
   Req rq = request(a, b);
   rq.row0 = uniform(rq.row0);
   rq.R = uniform(rq.R);
@@ -269,6 +273,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       mbar_init(bar_pe + 8 * i, 1);
     }
     mbar_init(bar_fin, nb);
+    mbar_init(bar_q, 4 * nb);
     for (int s = 0; F4 && s < KA_RAW; ++s) {
       mbar_init(bar_rf + 8 * s, 1);
       mbar_init(bar_re + 8 * s, F4 ? CONV / 32 : 1);
@@ -348,18 +353,17 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
     if (NB == 1) tmem_wait_st();
     else fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_q);       // (the producer's copies are under way meanwhile)
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-
   // Registers move from the control and converter warps to the softmax warps, whose threads hold
   // a row of 128 scores (each role's branch opens with its share; the shares stay within what the
   // launch gave the CTA).
-  constexpr bool MOVE = THREADS > 384;
+  constexpr bool MOVE = F4;
   bool ok = true;
   if (warp < 4) {
-    if constexpr (MOVE) set_regs_down<40>();
+    if constexpr (MOVE) set_regs_down<KA_REG_CTRL>();
     // ------------------------------------------------------------ producer: lane = page of the tile
     if (warp == 0) {
       const uint64_t pol = policy_evict_first();
@@ -419,6 +423,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
       const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
       const uint32_t tO = tmem + T_O + 128 * g;
+      ok = mbar_wait(bar_q, 0, a.err, abort_flag);
+      tc_fence_after();
       RingPos kp{0, 0}, vp{1, 0};            // the key tile of unit w, the value tile of unit w - 1
       for (int w = 0; w <= W && ok; ++w) {
         if (w < W) {
@@ -477,10 +483,12 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
+    set_regs_down<ka_reg_conv(NB)>();
     // ------------------------------ raw tiles -> fp16 tiles: 16 dims per thread and step
     constexpr int GR = HD / 16;                        // scale groups per row
     constexpr int IT = KA_CH * GR / CONV;              // 16-dim groups per thread and entry
     constexpr int RSTEP = CONV / GR;
+    static_assert(RSTEP % 8 == 0, "the swizzle repeats every 8 rows");
     const int ct = tid - 32 * CONV_WARP, gidx = ct % GR, r0 = ct / GR;
     const int sw = gidx >> 2;   // (the two 64-dim halves share banks: the upper one stores its chunks in the other order)
     RingPos rp{0, 0}, wp{0, 0};
@@ -496,30 +504,32 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const int r = r0 + i * RSTEP;
         code[i] = reinterpret_cast<const uint2*>(src + r * (HD / 2))[gidx];
         scale[i] = src[RAW_SCALES + r * GR + gidx];
-        // rows behind the last key, and of pages that are not there: zeros
-        if (k0 + r >= rq.len || !((have >> (r >> a.pool.ps_log)) & 1u)) {
-          code[i] = make_uint2(0u, 0u);
-          scale[i] = 0u;
+      }
+      if (k0 + KA_CH > rq.len || have != (1u << (KA_CH >> a.pool.ps_log)) - 1u) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {       // rows behind the last key, and of pages that are not there: zeros
+          const int r = r0 + i * RSTEP;
+          if (k0 + r >= rq.len || !((have >> (r >> a.pool.ps_log)) & 1u)) {
+            code[i] = make_uint2(0u, 0u);
+            scale[i] = 0u;
+          }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_re + 8 * wp.slot);
       if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag) && ok;
       if (__any_sync(0xffffffffu, !ok)) break;
-      const uint32_t dst = ring_u + rp.slot * ENTRY + sw * HALF;
+      // (rows r0 + i RSTEP share their place in the swizzle: RSTEP is a multiple of 8)
+      const uint32_t dst = ring_u + rp.slot * ENTRY + sw * HALF, c = 2 * (gidx & 3);
+      const uint32_t d0 = dst + ka_sw(r0, c + sw), d1 = dst + ka_sw(r0, c + (sw ^ 1));
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
-        uint32_t h[8];
-        dequant16(code[i], scale[i], h);
-        const int r = r0 + i * RSTEP, c = 2 * (gidx & 3);
-        uint32_t x[4], y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[k] = sw ? h[4 + k] : h[k];
-          y[k] = sw ? h[k] : h[4 + k];
-        }
-        st_smem16(dst + ka_sw(r, c + sw), x);
-        st_smem16(dst + ka_sw(r, c + (sw ^ 1)), y);
+        const uint32_t s = scale_pair(scale[i]);
+        uint32_t h[4];
+        dequant8(sw ? code[i].y : code[i].x, s, h);
+        st_smem16(d0 + i * (RSTEP * 128), h);
+        dequant8(sw ? code[i].x : code[i].y, s, h);
+        st_smem16(d1 + i * (RSTEP * 128), h);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -527,7 +537,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
     }
   } else {
-    if constexpr (MOVE) set_regs_up<152>();
+    if constexpr (MOVE) set_regs_up<ka_reg_softmax(NB)>();
     // ------------------------------------------------------------ softmax
     const int g = (warp - 4) >> 2, lv = tid - 128 - 128 * g, v = v0 + KA_QV * g + lv;
     const bool live = KA_QV * g + lv < qv;
@@ -791,6 +801,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   float (*s_o)[HD][KS_QV] = reinterpret_cast<float (*)[HD][KS_QV]>(ks_raw);   // (after the last tile)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  pdl_trigger();
   const Req rq = request(a, b);
   const int qv = rq.R * a.G;
   const int kb = split * a.tiles_per_cta * KA_CH;
@@ -1093,6 +1104,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
 template <int HD>
 __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
   constexpr int E = HD / 32;
+  pdl_wait();                                // the ranges' results
   const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int n = w / a.Hq, h = w - n * a.Hq;
   if (n >= a.N) return;
@@ -1140,12 +1152,12 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
   // key ranges: the split whose waves of CTAs (one per SM) take least, a CTA costing its tiles
-  // and as much again as KA_FIXED tiles for its start, its result and the joining of the ranges
+  // and `fixed` more for its start and its result, and four ranges a tile's time where they join
   const long long sms = std::max(1, num_sms()) * (p.step ? KS_CTAS : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
   long long per = tiles, best = -1;
   for (long long n = 1; n <= tiles && n <= 4096; ++n) {
     const long long t = (tiles + n - 1) / n;
-    const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + fixed);
+    const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + fixed) + n / 4;
     if (best < 0 || cost < best) {
       best = cost;
       per = t;
@@ -1182,6 +1194,13 @@ cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaAr
   if (!cap) {
     e = allow_max_smem(reinterpret_cast<const void*>(kv_attention_tc<HD, CACHE, NB>), &cap);
     if (e != cudaSuccess) return e;
+    if (CACHE == EAGLE_CACHE_F4) {   // the roles' registers must fit what the launch gives, or they would wait for ever
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kv_attention_tc<HD, CACHE, NB>);
+      if (e != cudaSuccess) return e;
+      const int need = 128 * KA_REG_CTRL + 128 * NB * ka_reg_softmax(NB) + 256 * ka_reg_conv(NB);
+      if (fa.numRegs / 8 * 8 * ka_threads(CACHE, NB) < need || fa.numRegs < ka_reg_conv(NB)) return cudaErrorInvalidConfiguration;
+    }
     if (dev < 64) granted[dev].store(cap);
   }
   const size_t fixed = (NB == 2 ? 2 * ka_entry(HD) : 0) + (CACHE == EAGLE_CACHE_F4 ? KA_RAW * ka_raw_bytes(HD) : 0) + KA_MISC + 1024;
@@ -1217,8 +1236,17 @@ cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
   else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
   if (e != cudaSuccess || a.splits == 1) return e;
   const long long warps = static_cast<long long>(a.N) * a.Hq;
-  kv_attention_combine<HD><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
-  return cudaGetLastError();
+  // (starts while the ranges still run and waits for them: their results, and nothing before)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.blockDim = dim3(128);
+  return cudaLaunchKernelEx(&cfg, kv_attention_combine<HD>, a);
 }
 
 }  // namespace
