@@ -601,9 +601,9 @@ def _rows(t, name: str, dtype, shape, dev: int) -> int:
 def _new(like, shape, dtype, stream):
     """An uninitialised tensor that belongs to ``stream`` (None: the current one)."""
     if stream is None:
-        return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
+        return _torch.empty(shape, dtype=dtype, device=like.device)
     with _torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return _torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _float_kind(t, name: str) -> int:
@@ -655,12 +655,11 @@ class Rope:
     def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, inv_freq=None,
                  amplitude: float = 1.0):
         self.rot_dim = int(rot_dim)
-        self._freq = None
-        if inv_freq is not None:
-            f = [float(x) for x in inv_freq]
-            if 2 * len(f) != self.rot_dim:
-                _bad("Rope: inv_freq must hold rot_dim / 2 numbers")
-            self._freq = (C.c_double * len(f))(*f)
+        # (the powers of theta are taken once here rather than in every call)
+        f = rope_frequencies(self.rot_dim, theta) if inv_freq is None else [float(x) for x in inv_freq]
+        if 2 * len(f) != self.rot_dim:
+            _bad("Rope: inv_freq must hold rot_dim / 2 numbers")
+        self._freq = (C.c_double * len(f))(*f)
         self.c = RopeC(rot_dim=self.rot_dim, interleaved=1 if interleaved else 0, theta=float(theta),
                        inv_freq=self._freq, amplitude=float(amplitude))
         self.ref = C.byref(self.c)

@@ -12,7 +12,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 
 using namespace eagle;
@@ -56,10 +55,10 @@ EAGLE_DEV Req request(const KaArgs& a, int b) {
   Req r;
   const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), l = __ldg(a.lens + b);
   r.row0 = min(max(c0, 0), a.N);
-  r.R = min(max(min(c1, a.N) - r.row0, 0), a.max_rows);
-  r.ctx = min(max(l, 0), max(a.max_len - r.R, 0));
+  r.R = min(max(min(c1, a.N) - r.row0, 0), min(a.max_rows, a.max_len));
+  r.ctx = min(max(l, 0), a.max_len - r.R);
   if (r.row0 != c0 || r.R != c1 - c0 || r.ctx != l) atomicOr(a.err, DEVERR_PREFIX);
-  r.len = min(r.ctx + r.R, a.max_len);
+  r.len = r.ctx + r.R;
   return r;
 }
 
@@ -1155,7 +1154,8 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   // and `fixed` more for its start and its result, and four ranges a tile's time where they join
   const long long sms = std::max(1, num_sms()) * (p.step ? KS_CTAS : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
   long long per = tiles, best = -1;
-  for (long long n = 1; n <= tiles && n <= 4096; ++n) {
+  const long long most = std::min(tiles, 8 * sms / base + 1);   // (beyond 8 waves more ranges only cost)
+  for (long long n = 1; n <= most; ++n) {
     const long long t = (tiles + n - 1) / n;
     const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + fixed) + n / 4;
     if (best < 0 || cost < best) {
@@ -1163,8 +1163,6 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
       per = t;
     }
   }
-  if (const char* ov = getenv("EAGLE_KV_TILES")) per = std::max(1, atoi(ov));
-  per = std::min(per, tiles);
   p.tiles_per_cta = static_cast<int>(per);
   p.splits = static_cast<int>((tiles + per - 1) / per);
   return p;
@@ -1176,6 +1174,7 @@ eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t*
   if (!w) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null arguments", who);
   if (w->B < 1 || w->N < 0 || w->max_rows < 1 || w->max_len < 1)
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need B, max_rows, max_len >= 1 and N >= 0", who);
+  if (w->max_len > 1 << 30) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: max_len must be at most 2^30", who);
   if (w->n_heads < 1 || w->n_heads % c->n_kv_heads || w->n_heads / c->n_kv_heads > KA_MAX_GROUP)
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: n_heads must be 1..%d times n_kv_heads", who, KA_MAX_GROUP);
   if (w->mask && (w->mask_slots < 1 || w->mask_slots > 64 || w->max_rows > w->mask_slots))

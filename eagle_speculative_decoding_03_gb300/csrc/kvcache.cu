@@ -606,7 +606,7 @@ extern "C" eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t
   a.k_out = static_cast<__nv_bfloat16*>(k_out);
   a.v_out = static_cast<__nv_bfloat16*>(v_out);
   a.err = err_word;
-  const dim3 grid((total + GA_TOKENS - 1) / GA_TOKENS, 2);
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(total) + GA_TOKENS - 1) / GA_TOKENS), 2);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->kind == EAGLE_CACHE_BF16;
   if (cache->head_dim == 64 && bf) gather_kernel<64, EAGLE_CACHE_BF16><<<grid, GA_THREADS, 0, st>>>(a);
