@@ -482,13 +482,14 @@ eagle_status_t rope_table(const eagle_rope_t* r, int hd, const char* who, RopeTa
   return EAGLE_OK;
 }
 
-// Rows per CTA and head slices: many rows take 8 to a CTA (one warp per row, whose cos / sin
-// then serve all heads); few rows are spread over warps and CTAs so each warp has few heads.
+// Rows per CTA and head slices: the more rows, the fewer warps share one, and the more heads its
+// cos / sin serve; few rows are spread over warps and CTAs so that each warp has few heads.  (At
+// 8,000 rows 4 to a CTA take 64 us of append_prompt_f4 where 8 take 66.)
 void rotate_shape(RotArgs* a) {
   const int heads = a->Hq + a->Hk + a->Hv, hpw = 32 / (a->hd / 8);
   const int iters = (heads + hpw - 1) / hpw;            // warp steps per row
   const int sms = std::max(1, num_sms());
-  a->rows_per_cta = a->N >= 16 * sms ? 8 : a->N >= 4 * sms ? 4 : a->N >= 2 * sms ? 2 : 1;
+  a->rows_per_cta = a->N >= 128 * sms ? 8 : a->N >= 4 * sms ? 4 : a->N >= 2 * sms ? 2 : 1;
   const int wpr = RT_WARPS / a->rows_per_cta;
   const long long ctas = (a->N + a->rows_per_cta - 1) / a->rows_per_cta;
   const int most = std::max(1, (iters + wpr - 1) / wpr);
