@@ -187,8 +187,10 @@ EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;
 // (NB = 1) or shared memory (NB = 2, where S and O of two tiles take all 512 columns); P replaces
 // S in TMEM as the A operand of O += P V.  Work goes in units of 64 keys, two S buffers per query
 // tile: a unit's QK^T runs while the unit before it is in the softmax, so the softmax warps find
-// their scores ready.  (One 128-key buffer per query tile, whose QK^T had to wait for the
-// softmax and the P V of the same buffer, took 4160 cycles per 128 keys and two query tiles.)
+// their scores ready: 1650 cycles a unit and two query tiles, of which the tensor cores need 1280
+// (48 for each of 16 QK^T instructions, whose operands both come from shared memory, 64 for each
+// of 8 of P V).  One 128-key buffer per query tile, whose QK^T had to wait for the softmax and the
+// P V of the same buffer, took 2080; two threads per vector instead of one, 1800.
 //
 // A page that the keys end inside is loaded from a negative row, so that the copy reads zeros
 // and then the valid rows: memory behind the last key never enters a product (it may hold NaN,
@@ -705,14 +707,13 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
               x[e] = fmaf(p, __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.v)[row + c0 + e]), x[e]);
           }
         }
-        if (!live) continue;
-        if (a.splits > 1) {
+        if (live && a.splits > 1) {
           if (!none) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e] * vg, x[4 * e + 1] * vg, x[4 * e + 2] * vg, x[4 * e + 3] * vg);
           }
-        } else {
+        } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + c0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -723,6 +724,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        __syncwarp();                        // (the next TMEM load is the whole warp's)
       }
       if (live) {
         const float m2 = none ? -INFINITY : m_run * row_scale - LIFT;
