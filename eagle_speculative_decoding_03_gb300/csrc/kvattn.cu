@@ -752,7 +752,9 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 // One warp copies raw tiles of 128 keys (18 KB at hd 128: codes and scales of K and V) into a ring
 // by bulk copies; four warps take 32 keys of a tile each.  Bound by bytes (144 per key and head of
 // 128) as long as the instructions keep up; loading the fragments straight from global memory
-// left too few bytes in flight (176 us at 32 requests of 17,000 keys on average, 8 heads).
+// left too few bytes in flight (176 us at 32 requests of 14,700 keys on average, 8 heads; 131 now:
+// 62% of the measured bandwidth, bound by issue: 0.59 of the cycles).  Eight warps of 16 keys took
+// 152 us, with 3 CTAs per SM 197.
 constexpr int KS_WARPS = 4;
 constexpr int KS_KEYS = 32;                // keys of a warp's step
 constexpr int KS_QV = 8;
