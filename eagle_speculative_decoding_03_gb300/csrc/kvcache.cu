@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <type_traits>
 
 namespace eagle {
 
@@ -218,63 +219,77 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
     }
   }
   const int other = rot && !rt.inter ? (o < ro ? lane + ro : lane - ro) : lane;
-  const int heads = a.Hq + a.Hk + a.Hv;
-  const int step = wpr * a.slices * hpw;
-  auto source = [&](int h) {
-    return (h < a.Hq            ? static_cast<const T*>(a.q) + n * a.q_ld + static_cast<long long>(h) * a.hd
-            : h < a.Hq + a.Hk ? static_cast<const T*>(a.k) + n * a.k_ld + static_cast<long long>(h - a.Hq) * a.hd
-                              : static_cast<const T*>(a.v) + n * a.v_ld + static_cast<long long>(h - a.Hq - a.Hk) * a.hd) + 8 * o;
-  };
-  auto turn = [&](int h, bool live, const Raw8<T>& raw) {
-    float x[8], y[8];
-    unpack8(raw, x);
-    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
-    if (rt.inter) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], x[e ^ 1] * s[e]);
+  const bool whole = 2 * rt.pairs == a.hd;   // every dim is rotated
+  const int page = CACHE != 0 ? s_page[r] : -1;
+  const size_t row0_of = CACHE != 0 && page >= 0 ? kv_row(a.pool, page, 0, s_tok[r]) : 0;   // head 0's pool row
+  const int head_rows = CACHE != 0 ? 1 << a.pool.ps_log : 0;                                // from head to head
+  // PART 0: rotated to q_out; 1: rotated to the keys' pages; 2: as they are to the values' pages
+  auto put = [&](auto part, int h, bool live, const Raw8<T>& raw) {
+    constexpr int PART = decltype(part)::value;
+    float y[8];
+    if constexpr (PART == 2) {
+      unpack8(raw, y);
     } else {
-      Raw8<T> oth;
-      float z[8];
+      float x[8];
+      unpack8(raw, x);
+      if (rt.inter) {
 #pragma unroll
-      for (int e = 0; e < static_cast<int>(2 * sizeof(T)); ++e) oth.w[e] = __shfl_sync(0xffffffffu, raw.w[e], other);
-      unpack8(oth, z);
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], x[e ^ 1] * s[e]);
+      } else {
+        Raw8<T> oth;
+        float z[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], z[e] * s[e]);
-    }
-    if (!rot || (!is_q && !is_k)) {          // dims behind rot_dim, and values: as they are
+        for (int e = 0; e < static_cast<int>(2 * sizeof(T)); ++e) oth.w[e] = __shfl_sync(0xffffffffu, raw.w[e], other);
+        unpack8(oth, z);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[e];
-    }
-    if (live && is_q) store8(static_cast<T*>(a.q_out) + n * a.qo_ld + static_cast<long long>(h) * a.hd + 8 * o, y);
-    if (CACHE != 0) {
-      const bool to = live && !is_q && s_page[r] >= 0;
-      const int kvh = is_k ? h - a.Hq : h - a.Hq - a.Hk;
-      const size_t row = to ? kv_row(a.pool, s_page[r], kvh, s_tok[r]) : 0;
-      if (CACHE == EAGLE_CACHE_BF16) {
-        if (to) store8(static_cast<__nv_bfloat16*>(is_k ? a.pool.k : a.pool.v) + row * a.hd + 8 * o, y);
-      } else if (__any_sync(0xffffffffu, to)) {
-        store8_f4(static_cast<uint8_t*>(is_k ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
-                  static_cast<uint8_t*>(is_k ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), y,
-                  is_k ? a.pool.kg : a.pool.vg, to, (o & 1) == 0);
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], z[e] * s[e]);
+      }
+      if (!whole && !rot) {                  // dims behind rot_dim: as they are
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e];
       }
     }
-  };
-  // HB heads of a warp in flight: their loads before the first store (which might alias them)
-  constexpr int HB = 4;
-  for (int h0 = (blockIdx.y * wpr + warp % wpr) * hpw; h0 < heads; h0 += HB * step) {
-    Raw8<T> raw[HB];
-    bool live[HB];
-#pragma unroll
-    for (int i = 0; i < HB; ++i) {
-      const int h = h0 + i * step + sub;
-      live[i] = in_warp && h < heads;
-#pragma unroll
-      for (int e = 0; e < static_cast<int>(2 * sizeof(T)); ++e) raw[i].w[e] = 0u;
-      if (live[i]) raw[i] = load_raw8(source(h));
+    if constexpr (PART == 0) {
+      if (live) store8(static_cast<T*>(a.q_out) + n * a.qo_ld + (h * a.hd + 8 * o), y);
+    } else if constexpr (CACHE == EAGLE_CACHE_BF16) {
+      if (live && page >= 0)
+        store8(static_cast<__nv_bfloat16*>(PART == 1 ? a.pool.k : a.pool.v) + (row0_of + static_cast<size_t>(h) * head_rows) * a.hd + 8 * o, y);
+    } else if constexpr (CACHE == EAGLE_CACHE_F4) {
+      const size_t row = row0_of + static_cast<size_t>(h) * head_rows;
+      store8_f4(static_cast<uint8_t*>(PART == 1 ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
+                static_cast<uint8_t*>(PART == 1 ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), y,
+                PART == 1 ? a.pool.kg : a.pool.vg, live && page >= 0, (o & 1) == 0);
     }
+  };
+  // A part's heads over the row's warps, HB steps of a warp in flight: their loads come before
+  // the first store (which might alias them).  Each part starts behind the last one's warps.
+  constexpr int HB = 4;
+  const int warps = wpr * a.slices;
+  int first = blockIdx.y * wpr + warp % wpr;
+  auto part_of = [&](auto part, const void* src, long long ld, int H) {
+    const T* p = static_cast<const T*>(src) + n * ld + 8 * o;
+    const int steps = (H + hpw - 1) / hpw;   // of hpw heads
+    for (int i0 = first; i0 < steps; i0 += HB * warps) {
+      Raw8<T> raw[HB];
 #pragma unroll
-    for (int i = 0; i < HB; ++i)
-      if (h0 + i * step < heads) turn(h0 + i * step + sub, live[i], raw[i]);
+      for (int i = 0; i < HB; ++i) {
+        const int h = (i0 + i * warps) * hpw + sub;
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(2 * sizeof(T)); ++e) raw[i].w[e] = 0u;
+        if (in_warp && h < H) raw[i] = load_raw8(p + static_cast<long long>(h) * a.hd);
+      }
+#pragma unroll
+      for (int i = 0; i < HB; ++i) {
+        const int h = (i0 + i * warps) * hpw + sub;
+        if (i0 + i * warps < steps) put(part, h, in_warp && h < H, raw[i]);
+      }
+    }
+    first = (first + warps - steps % warps) % warps;
+  };
+  if (a.Hq) part_of(std::integral_constant<int, 0>{}, a.q, a.q_ld, a.Hq);
+  if constexpr (CACHE != 0) {
+    part_of(std::integral_constant<int, 1>{}, a.k, a.k_ld, a.Hk);
+    part_of(std::integral_constant<int, 2>{}, a.v, a.v_ld, a.Hv);
   }
 }
 
