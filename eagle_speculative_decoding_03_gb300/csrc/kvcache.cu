@@ -40,8 +40,8 @@ eagle_status_t kv_pool(const eagle_kv_cache_t* c, const char* who, KvPool* out) 
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null cache pointer", who);
   if (!aligned16(c->k) || !aligned16(c->v) || (f4 && (!aligned16(c->k_scale) || !aligned16(c->v_scale))))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: cache pointers must be 16-byte aligned", who);
-  if (f4 && !(c->k_global > 0.f && c->v_global > 0.f && std::isfinite(c->k_global) && std::isfinite(c->v_global)))
-    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: k_global and v_global must be finite and positive", who);
+  if (f4 && !(c->k_global >= 1e-30f && c->v_global >= 1e-30f && c->k_global <= 1e30f && c->v_global <= 1e30f))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: k_global and v_global must lie in 1e-30 .. 1e30", who);
   out->k = c->k;
   out->v = c->v;
   out->ks = c->k_scale;
@@ -132,32 +132,54 @@ EAGLE_DEV void store8(float* p, const float* x) {
 EAGLE_DEV uint4 pack8(const float* x) { return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])); }
 EAGLE_DEV void store8(__nv_bfloat16* p, const float* x) { *reinterpret_cast<uint4*>(p) = pack8(x); }
 
-// 8 dims of a cached row in 4 bits; the 16-dim group's other half is in lane ^ 1.  The values
-// are rounded to bf16 first, so the scale and the codes depend on the stored precision alone
-// and not on how the rotation was rounded.  Called by whole warps; `live` lanes store.
-EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, const float* x, float global, bool live, bool even) {
+EAGLE_DEV float max_nan2(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+// 8 dims of a cached row in 4 bits; the 16-dim group's other half is in lane ^ 1.  `w` holds them
+// as bf16: the scale and the codes depend on the stored precision alone and not on how the rotation
+// was rounded.  Called by whole warps; `live` lanes store.
+//
+// Quotients are products with reciprocals, then rounded to fewer bits so that a quotient that lies
+// on a border between two codes lies on it exactly (an IEEE division each took half the kernel's
+// time):
+//   scale: largest / (6 global) to 18 bits (Veltkamp's splitting; borders have 5);
+//   code:  value / unit, off by less than 2^-19 up to 6, to multiples of 2^-18 (adding and taking
+//          away 48; borders are multiples of 1/4, and a bf16 value over a 4-bit scale that is not
+//          on one is 2^-11 or more away).
+EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, float inv6, bool live, bool even) {
   float y[8];
-  float top = 0.f;
+  unpack8(Raw8<__nv_bfloat16>{{w.x, w.y, w.z, w.w}}, y);
+  float top = max_nan2(max_nan2(max_nan2(fabsf(y[0]), fabsf(y[1])), max_nan2(fabsf(y[2]), fabsf(y[3]))),
+                       max_nan2(max_nan2(fabsf(y[4]), fabsf(y[5])), max_nan2(fabsf(y[6]), fabsf(y[7]))));
+  top = max_nan2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  if (__any_sync(0xffffffffu, top != top)) {   // NaN has no code: stored as 0
+    top = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    y[e] = bf16_to_f32(f32_to_bf16(x[e]));
-    if (y[e] != y[e]) y[e] = 0.f;            // NaN has no code: stored as 0
-    top = fmaxf(top, fabsf(y[e]));
+    for (int e = 0; e < 8; ++e) {
+      y[e] = y[e] != y[e] ? 0.f : y[e];
+      top = fmaxf(top, fabsf(y[e]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   }
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  const uint32_t s = f32_to_e4m3(__fdiv_rn(top, 6.0f * global));
+  float ratio = fminf(__fmul_rn(top, inv6), 1024.f);   // (past 448 the scale saturates)
+  const float cut = __fmul_rn(ratio, 65.f);
+  ratio = __fsub_rn(cut, __fsub_rn(cut, ratio));
+  const uint32_t s = f32_to_e4m3(ratio);
   const float unit = e4m3_to_f32(s) * global;
-  // value / unit as a product with the reciprocal, off by less than 2^-20 up to 6; rounded to
-  // multiples of 2^-18 (adding and taking away 48), so that a value on a border between two codes,
-  // whose quotient is a multiple of 1/4, is on it exactly (a bf16 value over a 4-bit scale that is
-  // not on the border is 2^-11 or more away; an IEEE division each took half the kernel's time)
-  const float inv = unit > 0.f ? __fdiv_rn(1.0f, unit) : 0.f;
-  auto ratio = [&](float v) { return copysignf(__fadd_rn(__fmaf_rn(fabsf(v), inv, 48.f), -48.f), v); };
-  uint32_t w = 0;
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(unit));
+  if (!(unit > 0.f)) inv = 0.f;
+  uint32_t q = 0;
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) w |= e2m1x2(ratio(y[e]), ratio(y[e + 1])) << (4 * e);
+  for (int e = 0; e < 8; e += 2) {
+    const float a = copysignf(__fadd_rn(__fmaf_rn(fabsf(y[e]), inv, 48.f), -48.f), y[e]);
+    const float b = copysignf(__fadd_rn(__fmaf_rn(fabsf(y[e + 1]), inv, 48.f), -48.f), y[e + 1]);
+    q |= e2m1x2(a, b) << (4 * e);
+  }
   if (live) {
-    *reinterpret_cast<uint32_t*>(code) = w;
+    *reinterpret_cast<uint32_t*>(code) = q;
     if (even) *scale = static_cast<uint8_t>(s);
   }
 }
@@ -174,6 +196,19 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
   __shared__ int s_page[RT_WARPS], s_tok[RT_WARPS], s_req[RT_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.rows_per_cta, row0 = blockIdx.x * rows;
+  // many rows: they come into L2 while their places are found (a chain of five loads; without it
+  // append_prompt_f4 took 61 us, now 55; eagle_rotary, which has no places to find, lost by it)
+  if (CACHE != 0 && rows >= 4 && blockIdx.y == 0) {
+    auto fetch = [&](const void* p, long long ld, int H) {
+      const int lines = (H * a.hd * static_cast<int>(sizeof(T)) + 127) >> 7;
+      for (int r = warp; r < rows && row0 + r < a.N; r += RT_WARPS)
+        for (int i = lane; i < lines; i += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(static_cast<const T*>(p) + (row0 + r) * ld) + i * 128));
+    };
+    if (a.Hq) fetch(a.q, a.q_ld, a.Hq);
+    fetch(a.k, a.k_ld, a.Hk);
+    fetch(a.v, a.v_ld, a.Hv);
+  }
   if (CACHE != 0 && tid < rows) {
     const int n = row0 + tid;
     const int b = n < a.N ? row_owner(a.cu, a.B, n) : -1;
@@ -223,6 +258,8 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
   const int page = CACHE != 0 ? s_page[r] : -1;
   const size_t row0_of = CACHE != 0 && page >= 0 ? kv_row(a.pool, page, 0, s_tok[r]) : 0;   // head 0's pool row
   const int head_rows = CACHE != 0 ? 1 << a.pool.ps_log : 0;                                // from head to head
+  const float inv6k = CACHE == EAGLE_CACHE_F4 ? __fdiv_rn(1.f, 6.f * a.pool.kg) : 0.f;
+  const float inv6v = CACHE == EAGLE_CACHE_F4 ? __fdiv_rn(1.f, 6.f * a.pool.vg) : 0.f;
   // PART 0: rotated to q_out; 1: rotated to the keys' pages; 2: as they are to the values' pages
   auto put = [&](auto part, int h, bool live, const Raw8<T>& raw) {
     constexpr int PART = decltype(part)::value;
@@ -256,9 +293,13 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
         store8(static_cast<__nv_bfloat16*>(PART == 1 ? a.pool.k : a.pool.v) + (row0_of + static_cast<size_t>(h) * head_rows) * a.hd + 8 * o, y);
     } else if constexpr (CACHE == EAGLE_CACHE_F4) {
       const size_t row = row0_of + static_cast<size_t>(h) * head_rows;
+      uint4 w;
+      if constexpr (PART == 2 && sizeof(T) == 2) w = make_uint4(raw.w[0], raw.w[1], raw.w[2], raw.w[3]);
+      else w = pack8(y);
+      const float global = PART == 1 ? a.pool.kg : a.pool.vg;
       store8_f4(static_cast<uint8_t*>(PART == 1 ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
-                static_cast<uint8_t*>(PART == 1 ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), y,
-                PART == 1 ? a.pool.kg : a.pool.vg, live && page >= 0, (o & 1) == 0);
+                static_cast<uint8_t*>(PART == 1 ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), w, global,
+                PART == 1 ? inv6k : inv6v, live && page >= 0, (o & 1) == 0);
     }
   };
   // A part's heads over the row's warps, HB steps of a warp in flight: their loads come before
@@ -499,12 +540,12 @@ eagle_status_t rope_table(const eagle_rope_t* r, int hd, const char* who, RopeTa
 
 // Rows per CTA and head slices: the more rows, the fewer warps share one, and the more heads its
 // cos / sin serve; few rows are spread over warps and CTAs so that each warp has few heads.  (At
-// 8,000 rows 4 to a CTA take 64 us of append_prompt_f4 where 8 take 66.)
+// 8,000 rows rotary_prompt takes 85 us with 4 to a CTA, 87 with 8; append_prompt_f4 57 and 55.)
 void rotate_shape(RotArgs* a) {
   const int heads = a->Hq + a->Hk + a->Hv, hpw = 32 / (a->hd / 8);
   const int iters = (heads + hpw - 1) / hpw;            // warp steps per row
   const int sms = std::max(1, num_sms());
-  a->rows_per_cta = a->N >= 128 * sms ? 8 : a->N >= 4 * sms ? 4 : a->N >= 2 * sms ? 2 : 1;
+  a->rows_per_cta = a->N >= (a->Hk ? 16 : 128) * sms ? 8 : a->N >= 4 * sms ? 4 : a->N >= 2 * sms ? 2 : 1;
   const int wpr = RT_WARPS / a->rows_per_cta;
   const long long ctas = (a->N + a->rows_per_cta - 1) / a->rows_per_cta;
   const int most = std::max(1, (iters + wpr - 1) / wpr);

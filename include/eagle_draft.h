@@ -498,7 +498,7 @@ typedef struct {
   void*   v;
   void*   k_scale;            /* F4 only */
   void*   v_scale;
-  float   k_global, v_global; /* F4 only: finite, > 0 */
+  float   k_global, v_global; /* F4 only: 1e-30 .. 1e30 */
   const int32_t* page_table;  /* [B][max_pages] */
 } eagle_kv_cache_t;
 
@@ -522,7 +522,7 @@ EAGLE_API eagle_status_t eagle_rotary(int32_t dtype, const void* x, int64_t x_st
 
 /* The rows of one step: request b's rows are n = cu_rows[b] .. cu_rows[b + 1] - 1; row i of
  * them becomes the request's key lens[b] + i.  Rows outside [cu_rows[0], cu_rows[B]) belong
- * to no request: nothing of them is read or written.  No two rows may share a place. */
+ * to no request: nothing of them is written.  No two rows may share a place. */
 typedef struct {
   int32_t B, N;               /* requests, rows (the buffers' extent) */
   const int32_t* cu_rows;     /* [B + 1] ascending, within [0, N] */
