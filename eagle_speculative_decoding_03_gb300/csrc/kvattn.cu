@@ -25,6 +25,7 @@ constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes
 constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
 constexpr uint32_t KA_MISC = 2048;
 constexpr int KA_MAX_SLOTS = 14;
+constexpr int KA_MAX_JOIN = 8;             // ranges that join in a cluster
 constexpr int KA_FIXED = 12;              // a CTA's fixed cost in tiles
 constexpr int KS_FIXED = 2;               // the same for the kernel for few query vectors
 
@@ -33,6 +34,7 @@ struct KaArgs {
   int B, N, Hq, G, max_rows, max_len, S;
   int blocks;                              // query-vector blocks per request
   int tiles_per_cta, splits;
+  int joined;                              // the ranges of a request are one cluster and join in it
   const int* cu;
   const int* lens;
   const __nv_bfloat16* q;
@@ -60,6 +62,26 @@ EAGLE_DEV Req request(const KaArgs& a, int b) {
   if (r.row0 != c0 || r.R != c1 - c0 || r.ctx != l) atomicOr(a.err, DEVERR_PREFIX);
   r.len = r.ctx + r.R;
   return r;
+}
+
+EAGLE_DEV void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the float at this CTA's shared address `p` in CTA `rank` of the cluster
+EAGLE_DEV float remote(const float* p, int rank) {
+  uint32_t a;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+EAGLE_DEV float4 remote4(const float* p, int rank) {
+  uint32_t a;
+  float4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
 }
 
 // 128 bits of key visibility
@@ -235,6 +257,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 348);
   const uint32_t bar_rf = misc_u + 352, bar_re = misc_u + 408;            // raw tiles full / free
   volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 464);   // pages each holds (bits)
+  float* mcta = reinterpret_cast<float*>(misc + 1024);   // [128] joined: this CTA's maximum per vector, its sum
+  float* lcta = mcta + KA_QV;
+  float* state = reinterpret_cast<float*>(sm);           // [128][HD + 4] joined: its output (in the ring, at the end)
+  constexpr int ST_LD = HD + 4;
   unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [128] tree mask rows
 
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / a.blocks, blk0 = blockIdx.z - b * a.blocks;
@@ -251,9 +277,12 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   // keys this block can see, and this CTA's tiles of them
   const int seen = a.mask ? rq.len : min(rq.len, rq.ctx + i_last + 1);
   const int all_tiles = (seen + KA_CH - 1) / KA_CH;
-  const int t_begin = split * a.tiles_per_cta;
-  if (t_begin * KA_CH >= rq.len) return;             // (not a range of this request at all)
-  const int T = max(0, min(all_tiles - t_begin, a.tiles_per_cta));
+  // (a cluster shares the tiles there are; separate ranges are cut by the call's bounds)
+  const bool joined = NB == 1 && a.joined;
+  const int per_cta = joined ? (all_tiles + a.splits - 1) / a.splits : a.tiles_per_cta;
+  const int t_begin = split * per_cta;
+  if (!joined && t_begin * KA_CH >= rq.len) return;  // (not a range of this request at all)
+  const int T = max(0, min(all_tiles - t_begin, per_cta));
   const int nb = uniform(NB == 2 && qv > KA_QV ? 2 : 1);
   const int nq0 = min(4, (min(qv, KA_QV) + 31) / 32), nq1 = nb == 2 ? (qv - KA_QV + 31) / 32 : nq0;
   const int ps = 1 << a.pool.ps_log;
@@ -707,7 +736,13 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
               x[e] = fmaf(p, __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.v)[row + c0 + e]), x[e]);
           }
         }
-        if (live && a.splits > 1) {
+        if (joined) {
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(state + lv * ST_LD + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        } else if (live && a.splits > 1) {
           if (!none) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
 #pragma unroll
@@ -728,7 +763,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       }
       if (live) {
         const float m2 = none ? -INFINITY : m_run * row_scale - LIFT;
-        if (a.splits > 1) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, l_run);
+        if (joined) {
+          mcta[lv] = m2;
+          lcta[lv] = l_run;
+        } else if (a.splits > 1) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, l_run);
         else if (a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(l_run)) * 0.6931471805599453f;
       }
     }
@@ -736,6 +774,39 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (joined) {   // the cluster's ranges, in rank order
+    cluster_sync();
+    const float vg = F4 ? a.pool.vg : 1.f;
+    for (int x = split * THREADS + tid; x < qv * (HD / 4); x += a.splits * THREADS) {
+      const int v = x / (HD / 4), d = 4 * (x - v * (HD / 4));
+      float m[KA_MAX_JOIN], M = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < KA_MAX_JOIN; ++r) {
+        m[r] = r < a.splits ? remote(mcta + v, r) : -INFINITY;
+        M = max_nan(M, m[r]);
+      }
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < KA_MAX_JOIN; ++r) {
+        if (m[r] == -INFINITY) continue;     // (a range without a key of this vector)
+        const float f = M == INFINITY ? (m[r] == INFINITY ? 1.f : 0.f) : exp2f(m[r] - M);
+        const float4 y = remote4(state + v * ST_LD + d, r);
+        L = fmaf(f, remote(lcta + v, r), L);
+        o.x = fmaf(f, y.x, o.x);
+        o.y = fmaf(f, y.y, o.y);
+        o.z = fmaf(f, y.z, o.z);
+        o.w = fmaf(f, y.w, o.w);
+      }
+      const bool none = L == 0.f;
+      const float inv = none ? 0.f : vg / L;
+      const int i = (v0 + v) / a.G, n = rq.row0 + i, h = kvh * a.G + (v0 + v - i * a.G);
+      *reinterpret_cast<uint2*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + d) =
+          none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (d == 0 && a.lse) a.lse[static_cast<size_t>(n) * a.Hq + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+    cluster_sync();                          // (the others' shared memory stays until it is read)
+  }
 }
 
 // ------------------------------------------------------------------ few query vectors, 4 bits
@@ -799,7 +870,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   __shared__ __align__(8) uint64_t s_full[KS_STAGES], s_free[KS_STAGES];
   __shared__ uint32_t s_pages[KS_STAGES];
   __shared__ int s_abort;
-  __shared__ float s_m[KS_WARPS][KS_QV], s_l[KS_WARPS][KS_QV];
+  __shared__ float s_m[KS_WARPS][KS_QV], s_l[KS_WARPS][KS_QV], s_jm[KS_QV], s_jl[KS_QV];
   __shared__ unsigned long long s_bits[KS_QV];
   float (*s_o)[HD][KS_QV] = reinterpret_cast<float (*)[HD][KS_QV]>(ks_raw);   // (after the last tile)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
@@ -807,10 +878,11 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   pdl_trigger();
   const Req rq = request(a, b);
   const int qv = rq.R * a.G;
-  const int kb = split * a.tiles_per_cta * KA_CH;
-  if (qv <= 0 || kb >= rq.len) return;
-  const int ke = min(rq.len, kb + a.tiles_per_cta * KA_CH);
-  const int tiles = (ke - kb + KA_CH - 1) / KA_CH;
+  const int per_cta = a.joined ? ((rq.len + KA_CH - 1) / KA_CH + a.splits - 1) / a.splits : a.tiles_per_cta;
+  const int kb = split * per_cta * KA_CH;
+  if (qv <= 0 || (!a.joined && kb >= rq.len)) return;
+  const int ke = min(rq.len, kb + per_cta * KA_CH);
+  const int tiles = max(0, (ke - kb + KA_CH - 1) / KA_CH);
   if (tid == 0) {
     for (int i = 0; i < KS_STAGES; ++i) {
       mbar_init(smem_u32(s_full + i), 1);
@@ -1089,7 +1161,14 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
     const size_t at = static_cast<size_t>(rq.row0 + i) * a.Hq + kvh * a.G + (v - i * a.G);
     const bool none = L == 0.f;
     const float m2 = none ? -INFINITY : M - 7.f;
-    if (a.splits > 1) {
+    if (a.joined) {                          // (this thread alone reads these two places)
+      s_o[0][d][v] = y0;
+      s_o[0][d + 1][v] = y1;
+      if (d == 0) {
+        s_jm[v] = m2;
+        s_jl[v] = L;
+      }
+    } else if (a.splits > 1) {
       if (!none)
         *reinterpret_cast<float2*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + d) =
             make_float2(y0 * a.pool.vg, y1 * a.pool.vg);
@@ -1100,6 +1179,35 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
           none ? 0u : pack_bf16(y0 * inv, y1 * inv);
       if (d == 0 && a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(L)) * 0.6931471805599453f;
     }
+  }
+  if (a.joined) {   // the cluster's ranges, in rank order
+    __syncthreads();
+    cluster_sync();
+    constexpr int THREADS = 32 * KS_WARPS + 32;
+    for (int x = split * THREADS + tid; x < qv * (HD / 2); x += a.splits * THREADS) {
+      const int v = x / (HD / 2), d = 2 * (x - v * (HD / 2));
+      float m[KA_MAX_JOIN], M = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < KA_MAX_JOIN; ++r) {
+        m[r] = r < a.splits ? remote(s_jm + v, r) : -INFINITY;
+        M = max_nan(M, m[r]);
+      }
+      float L = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int r = 0; r < KA_MAX_JOIN; ++r) {
+        if (m[r] == -INFINITY) continue;
+        const float f = exp2f(m[r] - M);
+        L = fmaf(f, remote(s_jl + v, r), L);
+        y0 = fmaf(f, remote(&s_o[0][d][v], r), y0);
+        y1 = fmaf(f, remote(&s_o[0][d + 1][v], r), y1);
+      }
+      const bool none = L == 0.f;
+      const float inv = none ? 0.f : a.pool.vg / L;
+      const int i = v / a.G, n = rq.row0 + i, h = kvh * a.G + (v - i * a.G);
+      *reinterpret_cast<uint32_t*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + d) = none ? 0u : pack_bf16(y0 * inv, y1 * inv);
+      if (d == 0 && a.lse) a.lse[static_cast<size_t>(n) * a.Hq + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+    cluster_sync();                          // (the others' shared memory stays until it is read)
   }
 }
 
@@ -1144,6 +1252,7 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
 // How a call is cut: query-vector tiles per CTA, blocks per request, key ranges.
 struct Plan {
   bool step;                               // the kernel for few vectors of a 4-bit cache
+  bool joined;                             // a request's ranges are a cluster
   int nb, blocks, tiles_per_cta, splits;
 };
 Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
@@ -1154,17 +1263,25 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
   const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
-  // key ranges: the split whose waves of CTAs (one per SM) take least, a CTA costing its tiles
-  // and `fixed` more for its start and its result, and four ranges a tile's time where they join
-  const long long sms = std::max(1, num_sms()) * (p.step ? KS_CTAS : 1), fixed = p.step ? KS_FIXED : KA_FIXED;
+  // Key ranges: the split whose waves of CTAs take least, a CTA costing its tiles and `fixed` more
+  // for its start and its result.  Up to 8 ranges join in a cluster where the device holds all
+  // clusters at once (each within one of its groups of about 19 SMs); in several waves the ranges of
+  // requests of different lengths keep each other waiting (150 us of attention_step_b32_f4 where
+  // separate ranges take 131).  Others join in a second kernel, which costs `second` tiles and
+  // another for every four ranges (attention_step_b1: 13.2 us, joined 12.2, and 8 us less host time).
+  const long long per_sm = p.step ? KS_CTAS : 1, sms = num_sms() > 0 ? num_sms() : 152, slots = sms * per_sm;   // (152: without a device, a GB300's)
+  const long long fixed = p.step ? KS_FIXED : KA_FIXED, second = p.step ? 3 : 4;
   long long per = tiles, best = -1;
-  const long long most = std::min(tiles, 8 * sms / base + 1);   // (beyond 8 waves more ranges only cost)
+  p.joined = false;
+  const long long most = std::min(tiles, 8 * slots / base + 1);   // (beyond 8 waves more ranges only cost)
   for (long long n = 1; n <= most; ++n) {
-    const long long t = (tiles + n - 1) / n;
-    const long long cost = (base * ((tiles + t - 1) / t) + sms - 1) / sms * (t + fixed) + n / 4;
+    const long long t = (tiles + n - 1) / n, ranges = (tiles + t - 1) / t;
+    const bool join = ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= sms / 19 * (19 * per_sm / ranges);
+    const long long cost = (base * ranges + slots - 1) / slots * (t + fixed) + (ranges == 1 || join ? 0 : second + ranges / 4);
     if (best < 0 || cost < best) {
       best = cost;
       per = t;
+      p.joined = join;
     }
   }
   p.tiles_per_cta = static_cast<int>(per);
@@ -1185,6 +1302,24 @@ eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t*
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: a mask needs max_rows <= mask_slots <= 64", who);
   if (!std::isfinite(w->scale) || w->scale < 0.f) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: scale must be finite and not negative", who);
   return EAGLE_OK;
+}
+
+// The ranges of a request (grid x) as one cluster where they join in it.
+template <typename... P, typename... A>
+cudaError_t launch_ranges(const KaArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t st, void (*kernel)(P...), const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.joined ? a.splits : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.attrs = attr;
+  cfg.numAttrs = a.joined ? 1 : 0;
+  cfg.stream = st;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 template <int HD, int CACHE, int NB>
@@ -1209,8 +1344,8 @@ cudaError_t launch_tc(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaAr
   const size_t fixed = (NB == 2 ? 2 * ka_entry(HD) : 0) + (CACHE == EAGLE_CACHE_F4 ? KA_RAW * ka_raw_bytes(HD) : 0) + KA_MISC + 1024;
   const int ns = std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
   const size_t smem = fixed + static_cast<size_t>(ns) * ka_entry(HD);
-  kv_attention_tc<HD, CACHE, NB><<<dim3(a.splits, a.pool.Hkv, a.B * a.blocks), ka_threads(CACHE, NB), smem, st>>>(tmk, tmv, a, ns);
-  return cudaGetLastError();
+  return launch_ranges(a, dim3(a.splits, a.pool.Hkv, a.B * a.blocks), ka_threads(CACHE, NB), smem, st,
+                       kv_attention_tc<HD, CACHE, NB>, tmk, tmv, a, ns);
 }
 
 template <int HD>
@@ -1225,8 +1360,7 @@ cudaError_t launch_step(const KaArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(1);
   }
-  kv_attention_step_f4<HD><<<dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS + 32, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_ranges(a, dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS + 32, smem, st, kv_attention_step_f4<HD>, a);
 }
 
 template <int HD>
@@ -1237,7 +1371,7 @@ cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
     e = launch_step<HD>(a, st);
   } else if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
   else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || a.splits == 1 || a.joined) return e;
   const long long warps = static_cast<long long>(a.N) * a.Hq;
   // (starts while the ranges still run and waits for them: their results, and nothing before)
   cudaLaunchAttribute attr[1];
@@ -1258,7 +1392,7 @@ extern "C" int64_t eagle_kv_attention_workspace(const eagle_kv_cache_t* cache, c
   KvPool pool;
   if (check_args(cache, args, "kv_attention_workspace", &pool) != EAGLE_OK) return -1;
   const Plan p = plan(cache, args);
-  if (p.splits == 1) return 0;
+  if (p.splits == 1 || p.joined) return 0;
   return static_cast<int64_t>(p.splits) * args->N * args->n_heads * (4 * cache->head_dim + 8);
 }
 
@@ -1293,6 +1427,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   a.blocks = p.blocks;
   a.tiles_per_cta = p.tiles_per_cta;
   a.splits = p.splits;
+  a.joined = p.joined;
   a.cu = w->cu_rows;
   a.lens = w->lens;
   a.q = static_cast<const __nv_bfloat16*>(w->q);

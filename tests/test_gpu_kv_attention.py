@@ -79,6 +79,9 @@ KINDS = ["bf16", "f4"]
     (128, 128, 1, 8, [1000, 37], [1, 1]),            # a page larger than what is left of it
     (64, 128, 2, 64, [200], [1]),                    # the largest group
     (128, 32, 2, 7, [5000, 3, 0], [1, 1, 0]),        # several key ranges; a request without rows
+    (128, 64, 1, 4, [20000], [2]),                   # more ranges than a cluster takes
+    (64, 64, 1, 20, [20001, 140], [1, 1]),           # the same, the second request in the first range
+    (128, 64, 8, 2, [1500, 130, 1], [4, 4, 4]),      # ranges of a cluster, some of them empty
 ])
 def test_single_tokens(kind, hd, ps, Hkv, G, ctx, rows):
     run(np.random.default_rng(hd + ps + G), kind, hd, ps, Hkv, G, ctx, rows)

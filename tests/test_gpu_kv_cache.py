@@ -329,7 +329,7 @@ def test_bindings_refuse_what_the_kernels_cannot_take():
            lambda: eb.kv_attention(cache, q.float(), c1, n1, 1, 20), lambda: eb.kv_attention(cache, q[:, :3], c1, n1, 1, 20),
            lambda: eb.kv_attention(cache, q, c1, n1, 1, 20, mask=torch.ones(1, 1, 1, device="cuda")),
            lambda: eb.kv_attention(cache, q, c1, n1, 0, 20), lambda: eb.kv_attention(cache, q, c1, n1, 1, 20, out=q.float()),
-           lambda: eb.kv_attention(cache, q, c1, n1, 1, 5000, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: eb.kv_attention(cache, q, c1, n1, 1, 500000, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
            lambda: eb.kv_gather(cache, dev(cu([1, 1, 1])), 3), lambda: eb.kv_gather(cache, c1, -1),
            lambda: eb.kv_gather(cache, c1, 1, k_out=torch.empty(2, 2, 128, dtype=torch.bfloat16, device="cuda")),
            lambda: eb.kv_accept([], n1, n1, n1[None]), lambda: eb.kv_accept(cache, n1, n1.long(), n1[None]),
