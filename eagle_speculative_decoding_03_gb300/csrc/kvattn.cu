@@ -5,8 +5,9 @@
 //
 // All query heads of a KV group and all rows of a request share one pass over the keys: the
 // query vectors v = row * G + head of the group fill the 128 TMEM lanes of a tcgen05 tile (one
-// or two tiles per CTA), 128 keys to a step.  A CTA takes a range of the keys; the ranges of a
-// request meet in a combine kernel (fixed order, deterministic).
+// or two tiles per CTA).  A CTA takes a range of the keys; the ranges of a request meet in a
+// cluster or in a combine kernel (in rank order: deterministic).  Three kernels: tensor cores for
+// any shape, mma.sync on 4-bit pages for up to 8 query vectors, and the combine kernel.
 #include "kvcache.cuh"
 
 #include <algorithm>
@@ -23,7 +24,7 @@ constexpr int KA_CH = 128;                 // keys per tile (a ring entry)
 constexpr int KA_H = 64;                   // keys per unit of work (half a tile)
 constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes)
 constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
-constexpr uint32_t KA_MISC = 2048;
+constexpr uint32_t KA_MISC = 2048;         // barriers (0), tree mask rows (512), joined states' m and l (1024)
 constexpr int KA_MAX_SLOTS = 14;
 constexpr int KA_MAX_JOIN = 8;             // ranges that join in a cluster
 constexpr int KA_FIXED = 12;              // a CTA's fixed cost in tiles
@@ -261,7 +262,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   float* lcta = mcta + KA_QV;
   float* state = reinterpret_cast<float*>(sm);           // [128][HD + 4] joined: its output (in the ring, at the end)
   constexpr int ST_LD = HD + 4;
-  unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [128] tree mask rows
+  unsigned long long* rowbits = reinterpret_cast<unsigned long long*>(misc + 512);   // [64] tree mask rows
 
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z / a.blocks, blk0 = blockIdx.z - b * a.blocks;
   pdl_trigger();                             // (the combine kernel may start and wait)
@@ -388,8 +389,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     if (lane == 0) mbar_arrive(bar_q);       // (the producer's copies are under way meanwhile)
   }
   // Registers move from the control and converter warps to the softmax warps, whose threads hold
-  // a row of 128 scores (each role's branch opens with its share; the shares stay within what the
-  // launch gave the CTA).
+  // 64 scores (each role's branch opens with its share; the shares stay within what the launch
+  // gave the CTA).
   constexpr bool MOVE = F4;
   bool ok = true;
   if (warp < 4) {
@@ -1409,6 +1410,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   if (w->q_stride < width || w->out_stride < width || w->q_stride % 8 || w->out_stride % 8 ||
       reinterpret_cast<uintptr_t>(w->q) % 16 || reinterpret_cast<uintptr_t>(w->out) % 16)
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
+  if (w->q == w->out) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: out may not be q (ranges and blocks read q at different times)", who);
   const int64_t need = eagle_kv_attention_workspace(cache, w);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || reinterpret_cast<uintptr_t>(w->workspace) % 16))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));

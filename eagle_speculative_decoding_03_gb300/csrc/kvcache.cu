@@ -694,6 +694,9 @@ extern "C" eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_
     if (x.kind != y.kind || x.n_kv_heads != y.n_kv_heads || x.head_dim != y.head_dim || x.page_size != y.page_size ||
         x.num_pages != y.num_pages || x.max_pages != y.max_pages || x.page_table != y.page_table)
       return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: the caches must share one shape and page table", who);
+    for (int j = 0; j < i; ++j)
+      if (x.k == caches[j].k || x.v == caches[j].v || x.k == caches[j].v || x.v == caches[j].k)
+        return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: caches %d and %d share a pool", who, j, i);
     if (i == 0) a.pool = p;
     ac.p[4 * i] = static_cast<char*>(p.k);
     ac.p[4 * i + 1] = static_cast<char*>(p.v);

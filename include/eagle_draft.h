@@ -553,8 +553,8 @@ EAGLE_API eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t 
  * slot order (root first).  Keeps the root and the accept_len[b] accepted slots
  * accept_slots[b][..] (ascending, as eagle_verify_tree and eagle_speculative_accept write
  * them): slot accept_slots[b][j] moves to key lens[b] + 1 + j in every one of the n_caches
- * caches (HOST array, 1..64, e.g. one per layer; all of one shape, and of caches[0]'s page
- * table), and new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens). */
+ * caches (HOST array, 1..64, e.g. one per layer; all of one shape, of caches[0]'s page
+ * table and each with its own pool), and new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens). */
 EAGLE_API eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_t n_caches, int32_t B, int32_t S,
                                          const int32_t* lens, const int32_t* accept_len, const int32_t* accept_slots,
                                          int32_t* new_lens, uint32_t* err_word, void* stream);
@@ -578,7 +578,7 @@ typedef struct {
   int64_t q_stride;
   const uint8_t* mask;        /* [B][S][S] or NULL: causal */
   float   scale;              /* 0: 1 / sqrt(hd) */
-  void*   out;                /* bf16 [N][Hq][hd], rows out_stride apart */
+  void*   out;                /* bf16 [N][Hq][hd], rows out_stride apart; may not overlap q */
   int64_t out_stride;
   float*  lse;                /* [N][Hq] log-sum-exp of the scaled scores, or NULL */
   void*   workspace;          /* eagle_kv_attention_workspace bytes, 16-byte aligned (NULL if 0) */

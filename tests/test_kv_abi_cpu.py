@@ -70,7 +70,7 @@ def test_bad_caches_are_refused_everywhere(lib, kw, status):
     assert lib.eagle_kv_append(C.byref(c), C.byref(w), C.byref(rope()), P, None) == status
     assert lib.eagle_kv_gather(C.byref(c), 1, P, 8, P, P, P, None) == status
     assert lib.eagle_kv_accept(C.byref(c), 1, 1, 4, P, P, P, P, P, None) == status
-    a = eb.KVAttention(B=1, N=1, n_heads=8, max_rows=1, max_len=10, cu_rows=P, lens=P, q=P, q_stride=1024, out=P, out_stride=1024)
+    a = eb.KVAttention(B=1, N=1, n_heads=8, max_rows=1, max_len=10, cu_rows=P, lens=P, q=P, q_stride=1024, out=2 * P, out_stride=1024)
     assert lib.eagle_kv_attention(C.byref(c), C.byref(a), P, None) == status
     assert lib.eagle_kv_attention_workspace(C.byref(c), C.byref(a)) == -1
     assert lib.eagle_draft_last_error()
@@ -128,17 +128,19 @@ def test_gather_and_accept_arguments(lib):
         assert ac(**kw) == 1, kw
     assert lib.eagle_kv_accept(None, 1, 1, 4, P, P, P, P, P, None) == 1
     for kw in (dict(n_kv_heads=4), dict(page_size=32), dict(max_pages=9), dict(page_table=P + 64), dict(num_pages=99), dict(kind=1)):
-        assert ac(n=2, cs=(eb.KVCacheC * 2)(cache(), cache(**kw))) == 1, kw
+        assert ac(n=2, cs=(eb.KVCacheC * 2)(cache(), cache(k=2 * P, v=3 * P, **kw))) == 1, kw
+    for kw in (dict(), dict(k=2 * P), dict(v=2 * P), dict(k=2 * P, v=P)):       # two caches over one pool
+        assert ac(n=2, cs=(eb.KVCacheC * 2)(cache(k=P, v=4 * P), cache(**{**dict(k=P, v=4 * P), **kw}))) == 1, kw
 
 
 def test_attention_arguments(lib):
     c = cache()
     def call(err=P, **kw):
-        d = dict(B=1, N=1, n_heads=8, max_rows=1, max_len=10, cu_rows=P, lens=P, q=P, q_stride=1024, out=P, out_stride=1024)
+        d = dict(B=1, N=1, n_heads=8, max_rows=1, max_len=10, cu_rows=P, lens=P, q=P, q_stride=1024, out=2 * P, out_stride=1024)
         d.update(kw)
         return lib.eagle_kv_attention(C.byref(c), C.byref(eb.KVAttention(**d)), err, None)
     for kw in (dict(B=0), dict(N=-1), dict(n_heads=0), dict(n_heads=12), dict(n_heads=8 * 65), dict(max_rows=0), dict(max_len=0),
-               dict(cu_rows=None), dict(lens=None), dict(q=None), dict(out=None), dict(err=None), dict(q=P + 8), dict(q_stride=1000),
+               dict(cu_rows=None), dict(lens=None), dict(q=None), dict(out=None), dict(err=None), dict(out=P), dict(q=P + 8), dict(q_stride=1000),
                dict(q_stride=1028), dict(out_stride=512), dict(scale=-1.0), dict(scale=float("nan")),
                dict(mask=P, mask_slots=0), dict(mask=P, mask_slots=65), dict(mask=P, mask_slots=4, max_rows=5),
                dict(max_len=100000)):      # (ranges need a workspace)
@@ -148,7 +150,8 @@ def test_attention_arguments(lib):
     a = eb.KVAttention(B=2, N=2, n_heads=32, max_rows=1, max_len=100000)
     need = lib.eagle_kv_attention_workspace(C.byref(c), C.byref(a))
     assert need > 0
-    a.cu_rows = a.lens = a.q = a.out = a.workspace = P
+    a.cu_rows = a.lens = a.q = a.workspace = P
+    a.out = 2 * P
     a.q_stride = a.out_stride = 4096
     a.workspace_bytes = need - 1
     assert lib.eagle_kv_attention(C.byref(c), C.byref(a), P, None) == 1
