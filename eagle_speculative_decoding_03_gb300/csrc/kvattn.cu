@@ -1212,13 +1212,16 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   }
 }
 
-// Joins the key ranges of a request: one warp per (row, query head), HD / 32 dims per lane.
-template <int HD>
+// Joins the key ranges of a request: WARPS warps per (row, query head), each a share of the ranges,
+// HD / 32 dims per lane.  (One warp walking 57 ranges of a few rows took 10 us on its own.)
+template <int HD, int WARPS>
 __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
   constexpr int E = HD / 32;
+  __shared__ float s_o[4][HD], s_l[4];
   pdl_wait();                                // the ranges' results
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int n = w / a.Hq, h = w - n * a.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
+  const long long w = static_cast<long long>(blockIdx.x) * (4 / WARPS) + warp / WARPS;
+  const int n = static_cast<int>(w / a.Hq), h = static_cast<int>(w - static_cast<long long>(n) * a.Hq);
   if (n >= a.N) return;
   const int b = row_owner(a.cu, a.B, n);
   if (b < 0) return;
@@ -1233,7 +1236,7 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < used; ++s) {
+  for (int s = part; s < used; s += WARPS) {
     const float2 ml = a.part_ml[s * step + at];
     if (ml.x == -INFINITY) continue;
     const float f = M == INFINITY ? (ml.x == INFINITY ? 1.f : 0.f) : exp2f(ml.x - M);
@@ -1241,6 +1244,19 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
     const float* p = a.part_o + (s * step + at) * HD + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e], o[e]);
+  }
+  if constexpr (WARPS > 1) {                 // (the CTA is one row's: it is here whole)
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[part][lane * E + e] = o[e];
+    if (lane == 0) s_l[part] = L;
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int r = 1; r < WARPS; ++r) {
+      L += s_l[r];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += s_o[r][lane * E + e];
+    }
   }
   const bool none = L == 0.f;
   const float inv = none ? 0.f : 1.f / L;
@@ -1264,7 +1280,7 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
   const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
   const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
-  // Key ranges: the split whose waves of CTAs take least, a CTA costing its tiles and `fixed` more
+  // Key ranges: the split that takes least, a CTA costing its tiles and `fixed` more
   // for its start and its result.  Up to 8 ranges join in a cluster where the device holds all
   // clusters at once (each within one of its groups of about 19 SMs); in several waves the ranges of
   // requests of different lengths keep each other waiting (150 us of attention_step_b32_f4 where
@@ -1272,13 +1288,18 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   // another for every four ranges (attention_step_b1: 13.2 us, joined 12.2, and 8 us less host time).
   const long long per_sm = p.step ? KS_CTAS : 1, sms = num_sms() > 0 ? num_sms() : 152, slots = sms * per_sm;   // (152: without a device, a GB300's)
   const long long fixed = p.step ? KS_FIXED : KA_FIXED, second = p.step ? 3 : 4;
-  long long per = tiles, best = -1;
+  long long per = tiles;
+  double best = -1.;
   p.joined = false;
   const long long most = std::min(tiles, 8 * slots / base + 1);   // (beyond 8 waves more ranges only cost)
   for (long long n = 1; n <= most; ++n) {
     const long long t = (tiles + n - 1) / n, ranges = (tiles + t - 1) / t;
     const bool join = ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= sms / 19 * (19 * per_sm / ranges);
-    const long long cost = (base * ranges + slots - 1) / slots * (t + fixed) + (ranges == 1 || join ? 0 : second + ranges / 4);
+    // the requests all as long as the bound, and (of several requests) of lengths spread below it:
+    // then the longest CTA, or the work of the average request on all slots
+    const double even = static_cast<double>((base * ranges + slots - 1) / slots * (t + fixed));
+    const double spread = std::max<double>(t + fixed, base * (0.5 * tiles + fixed * 0.5 * (ranges + 1)) / slots);
+    const double cost = (w->B > 1 ? 0.5 * (even + spread) : even) + (ranges == 1 || join ? 0. : second + 0.25 * ranges);
     if (best < 0 || cost < best) {
       best = cost;
       per = t;
@@ -1373,7 +1394,8 @@ cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
   } else if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
   else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
   if (e != cudaSuccess || a.splits == 1 || a.joined) return e;
-  const long long warps = static_cast<long long>(a.N) * a.Hq;
+  const long long rows = static_cast<long long>(a.N) * a.Hq;
+  const bool wide = a.splits > 8 && rows < 1ll << 31;   // (fewer ranges: a warp each row)
   // (starts while the ranges still run and waits for them: their results, and nothing before)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1382,9 +1404,9 @@ cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(128);
-  return cudaLaunchKernelEx(&cfg, kv_attention_combine<HD>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, kv_attention_combine<HD, 4>, a) : cudaLaunchKernelEx(&cfg, kv_attention_combine<HD, 1>, a);
 }
 
 }  // namespace

@@ -342,3 +342,100 @@ def test_bindings_refuse_what_the_kernels_cannot_take():
             f()
             raise AssertionError(f"case {i} was taken")
     assert cache.check() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+def test_a_captured_step_replays_on_the_lengths_of_the_day(kind):
+    """append -> attention -> accept with the lengths updated in place, captured once: three
+    replays equal three eager steps on a copy of the state, bit for bit."""
+    rng = np.random.default_rng(20)
+    B, S, H, G, hd, ps = 3, 5, 2, 4, 128, 16
+    lens0 = [0, 30, 129]
+    def state():
+        c, _ = make_cache(np.random.default_rng(21), kind, hd, ps, H, lens0, room=[n + 40 for n in lens0])
+        return c, dev(np.array(lens0, np.int32))
+    mask = np.tril(np.ones((S, S), np.uint8))[None].repeat(B, 0)
+    mask[:, 3, 2] = 0                                                # slot 3 branches off slot 1
+    slots = np.full((B, S), -1, np.int32)
+    slots[:, :2] = [1, 3]
+    acc, slots, mask = dev(np.array([2, 0, 2], np.int32)), dev(slots), dev(mask)
+    cr, rope = dev(cu([S] * B)), eb.Rope(64, theta=1e4, interleaved=True)
+    qkv = torch.randn(B * S, (H * G + 2 * H) * hd, device="cuda").to(torch.bfloat16)
+    q, k, v = (x.unflatten(1, (-1, hd)) for x in qkv.split([H * G * hd, H * hd, H * hd], 1))
+    off = torch.arange(S, dtype=torch.int32, device="cuda").repeat(B)
+    def step(c, lens, out):
+        pos = lens.repeat_interleave(S, output_size=B * S) + off
+        qr = eb.kv_append(c, k, v, cr, lens, positions=pos, rope=rope, q=q)
+        eb.kv_attention(c, qr, cr, lens, max_rows=S, max_len=200, mask=mask, out=out)
+        eb.kv_accept(c, lens, acc, slots, new_lens=lens)
+    c1, l1 = state()
+    want, outs = torch.zeros(B * S, H * G, hd, dtype=torch.bfloat16, device="cuda"), []
+    for _ in range(3):
+        step(c1, l1, want)
+        outs.append(want.clone())
+    c2, l2 = state()
+    got = torch.zeros_like(want)
+    warm, lw = state()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(warm, lw, got.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(c2, l2, got)
+    for i in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, outs[i]), i
+    assert l1.tolist() == l2.tolist() == [9, 33, 138] and c1.check() == 0 and c2.check() == 0
+    for x, y in ((c1.k, c2.k), (c1.v, c2.v)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_two_streams_at_once():
+    """Caches of their own on two streams: what each gives alone."""
+    made = []
+    for i, kind in enumerate(("bf16", "f4")):
+        c, _ = make_cache(np.random.default_rng(30 + i), kind, 128, 64, 4, [3000, 700])
+        q = torch.randn(2, 16, 128, device="cuda").to(torch.bfloat16)
+        made.append((c, q, dev(cu([1, 1])), dev(np.array([2999, 699], np.int32)), dev(cu([3000, 700]))))
+    def work(m, stream=None):
+        c, q, cr, n, cs = m
+        return (eb.kv_attention(c, q, cr, n, 1, 3000, stream=stream),) + eb.kv_gather(c, cs, 3700, stream=stream)
+    want = [work(m) for m in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[work(m, s) for _ in range(20)] for m, s in zip(made, streams)]
+    torch.cuda.synchronize()
+    for w, gs in zip(want, got):
+        for x in gs:
+            assert all(torch.equal(a, b) for a, b in zip(w, x))
+
+
+def test_many_requests_and_rows():
+    """More requests than a warp, rows of one request spread over many CTAs, an empty call."""
+    rng = np.random.default_rng(40)
+    rows = rng.integers(0, 9, 300).tolist()
+    table, P = pages(rng, rows, 16)
+    cache = eb.KVCache.empty(P, 16, 1, 64, dev(table))
+    N = sum(rows)
+    x = torch.randn(N, 1, 64, device="cuda").to(torch.bfloat16)
+    zero = torch.zeros(300, dtype=torch.int32, device="cuda")
+    eb.kv_append(cache, x, x, dev(cu(rows)), zero)
+    k, v = eb.kv_gather(cache, dev(cu(rows)), N)
+    assert cache.check() == 0 and torch.equal(k, x) and torch.equal(v, x)
+    q = torch.randn(N, 2, 64, device="cuda").to(torch.bfloat16)
+    o = eb.kv_attention(cache, q, dev(cu(rows)), zero, max_rows=8, max_len=8)
+    at = cu(rows)
+    for b in (0, 150, 299):
+        if rows[b]:
+            s = slice(at[b], at[b + 1])
+            ref = K.attention(q[s].double().cpu().numpy(), x[s].double().cpu().numpy(), x[s].double().cpu().numpy(),
+                              see_matrix(0, rows[b]), 64 ** -0.5)
+            # (p rounded to 8 bits at least, the output to bf16; |out| <= sum p |v| / sum p)
+            assert (np.abs(o[s].double().cpu().numpy() - ref[0]) <= (2.0 ** -7 + 2.0 ** -14) * ref[2]).all()
+    none = x[:0]
+    assert eb.kv_append(cache, none, none, dev(cu([0])), zero[:1]) is None
+    assert eb.kv_attention(cache, q[:0], dev(cu([0])), zero[:1], 1, 1).shape == (0, 2, 64)
+    assert eb.kv_gather(cache, dev(cu([0])), 0)[0].shape == (0, 1, 64)
