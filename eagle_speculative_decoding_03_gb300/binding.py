@@ -577,7 +577,8 @@ def _tensor(t, name: str, dtype, shape, dev: int, contiguous: bool = True):
         _bad(f"{name} must be on the current CUDA device")
     if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
         _bad(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
-    _bad(f"{name} must be contiguous")
+    if contiguous and not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
 
 
 def _ints(t, name: str, n, dev: int) -> int:
@@ -588,14 +589,19 @@ def _ints(t, name: str, n, dev: int) -> int:
     return t.numel()
 
 
-def _rows(t, name: str, dtype, shape, dev: int) -> int:
-    """Rows [N, H, hd] whose heads are contiguous: the row stride in elements."""
-    _tensor(t, name, dtype, shape, dev, contiguous=False)
-    n, h, d = t.shape
-    s0, s1, s2 = t.stride()
-    if n and ((s2 != 1 and d > 1) or (h > 1 and s1 != d)):
-        _bad(f"{name}: the heads of a row must be contiguous")
-    return s0 if n > 1 else h * d
+def _rows(t, name: str, dtype, n, h, d, dev: int) -> int:
+    """Rows [N, H, hd] (sizes n, h, d where given) whose heads are contiguous: the row stride in
+    elements."""
+    try:
+        tn, th, td = t.shape
+        s0, s1, s2 = t.stride()
+        if t.dtype is dtype and t.get_device() == dev and (n is None or n == tn) and (h is None or h == th) and \
+                (d is None or d == td) and ((s2 == 1 and (s1 == td or th == 1)) or tn == 0):
+            return s0 if tn > 1 else th * td
+    except (AttributeError, ValueError):
+        pass
+    _tensor(t, name, dtype, (n, h, d), dev, contiguous=False)
+    _bad(f"{name}: the heads of a row must be contiguous")
 
 
 def _new(like, shape, dtype, stream):
@@ -669,14 +675,14 @@ def rotary(x, positions, rope: Rope, out=None, stream=None):
     """x [N, H, hd] (float32 or bfloat16) rotated at int32 positions [N]; out may be x."""
     torch, dev, st = _here(stream)
     kind = _float_kind(x, "x")
-    ld = _rows(x, "x", x.dtype, (None, None, None), dev)
+    ld = _rows(x, "x", x.dtype, None, None, None, dev)
     N, H, hd = x.shape
     _ints(positions, "positions", N, dev)
     if out is None:
         out = _new(x, (N, H, hd), x.dtype, stream)
         old = H * hd
     else:
-        old = _rows(out, "out", x.dtype, (N, H, hd), dev)
+        old = _rows(out, "out", x.dtype, N, H, hd, dev)
     if N:
         _check(load().eagle_rotary(kind, x.data_ptr(), ld, N, H, hd, positions.data_ptr(), rope.ref, out.data_ptr(), old, st))
     return out
@@ -739,20 +745,20 @@ def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | 
     torch, dev, st = _here(stream)
     H, hd = cache.n_kv_heads, cache.head_dim
     kind = _float_kind(k, "k")
-    k_ld = _rows(k, "k", k.dtype, (None, H, hd), dev)
+    k_ld = _rows(k, "k", k.dtype, None, H, hd, dev)
     N = k.shape[0]
-    v_ld = _rows(v, "v", k.dtype, (N, H, hd), dev)
+    v_ld = _rows(v, "v", k.dtype, N, H, hd, dev)
     B = _requests(cache, cu_rows, lens, dev)
     if rope is not None:
         _ints(positions, "positions", N, dev)
     Hq = q_ld = qo_ld = 0
     if q is not None:
-        q_ld = _rows(q, "q", k.dtype, (N, None, hd), dev)
+        q_ld = _rows(q, "q", k.dtype, N, None, hd, dev)
         Hq = q.shape[1]
         if q_out is None:   # (rows of no request are not written)
             q_out, qo_ld = _new(q, (N, Hq, hd), k.dtype, stream), Hq * hd
         else:
-            qo_ld = _rows(q_out, "q_out", k.dtype, (N, Hq, hd), dev)
+            qo_ld = _rows(q_out, "q_out", k.dtype, N, Hq, hd, dev)
     if N:
         w = KVRows(B, N, cu_rows.data_ptr(), lens.data_ptr(), None if rope is None else positions.data_ptr(), kind, Hq,
                    k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out) if Hq else None, k_ld, v_ld, q_ld, qo_ld)
@@ -822,7 +828,7 @@ def kv_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, 
     or (out, lse [N, Hq]) with lse=True or a tensor.  ``workspace``: a uint8 tensor to keep
     (at least kv_attention_workspace bytes); else one is taken from torch's allocator."""
     torch, dev, st = _here(stream)
-    q_ld = _rows(q, "q", torch.bfloat16, (None, None, cache.head_dim), dev)
+    q_ld = _rows(q, "q", torch.bfloat16, None, None, cache.head_dim, dev)
     N, Hq, hd = q.shape
     B = _requests(cache, cu_rows, lens, dev)
     S = 0
@@ -832,7 +838,7 @@ def kv_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, 
     if out is None:
         out, out_ld = _new(q, (N, Hq, hd), torch.bfloat16, stream), Hq * hd
     else:
-        out_ld = _rows(out, "out", torch.bfloat16, (N, Hq, hd), dev)
+        out_ld = _rows(out, "out", torch.bfloat16, N, Hq, hd, dev)
     if lse is True:
         lse = _new(q, (N, Hq), torch.float32, stream)
     elif lse is False:

@@ -1292,8 +1292,10 @@ Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
   double best = -1.;
   p.joined = false;
   const long long most = std::min(tiles, 8 * slots / base + 1);   // (beyond 8 waves more ranges only cost)
-  for (long long n = 1; n <= most; ++n) {
-    const long long t = (tiles + n - 1) / n, ranges = (tiles + t - 1) / t;
+  // (only the n at which the tiles per range change: about twice the root of the tiles)
+  for (long long n = 1, t = 0; n <= most; n = t > 1 ? (tiles + t - 2) / (t - 1) : most + 1) {
+    t = (tiles + n - 1) / n;
+    const long long ranges = (tiles + t - 1) / t;
     const bool join = ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= sms / 19 * (19 * per_sm / ranges);
     // the requests all as long as the bound, and (of several requests) of lengths spread below it:
     // then the longest CTA, or the work of the average request on all slots
@@ -1411,12 +1413,15 @@ cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
 
 }  // namespace
 
+static int64_t workspace_bytes(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args, const Plan& p) {
+  if (p.splits == 1 || p.joined) return 0;
+  return static_cast<int64_t>(p.splits) * args->N * args->n_heads * (4 * cache->head_dim + 8);
+}
+
 extern "C" int64_t eagle_kv_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args) {
   KvPool pool;
   if (check_args(cache, args, "kv_attention_workspace", &pool) != EAGLE_OK) return -1;
-  const Plan p = plan(cache, args);
-  if (p.splits == 1 || p.joined) return 0;
-  return static_cast<int64_t>(p.splits) * args->N * args->n_heads * (4 * cache->head_dim + 8);
+  return workspace_bytes(cache, args, plan(cache, args));
 }
 
 extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* w, uint32_t* err_word,
@@ -1433,11 +1438,11 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
       reinterpret_cast<uintptr_t>(w->q) % 16 || reinterpret_cast<uintptr_t>(w->out) % 16)
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
   if (w->q == w->out) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: out may not be q (ranges and blocks read q at different times)", who);
-  const int64_t need = eagle_kv_attention_workspace(cache, w);
+  const Plan p = plan(cache, w);
+  const int64_t need = workspace_bytes(cache, w, p);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || reinterpret_cast<uintptr_t>(w->workspace) % 16))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
-  const Plan p = plan(cache, w);
   const long long rows_heads = static_cast<long long>(w->N) * w->n_heads;
   if (rows_heads > (1ll << 31) - 8 || cache->n_kv_heads > 65535 || static_cast<long long>(w->B) * p.blocks > 65535)
     return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: too many rows, heads or requests for one launch", who);
