@@ -1375,18 +1375,6 @@ bool make_kv_map(CUtensorMap* tm, const void* cache, long long tokens, int Hkv) 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn || !pool) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(hd) * 2 * page_size};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool make_act_map(CUtensorMap* tm, const void* hl, int rows, int K, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;

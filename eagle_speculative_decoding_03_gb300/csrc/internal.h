@@ -41,9 +41,6 @@ bool make_weight_map(CUtensorMap* tm, const void* w, int M, int K, int box_rows 
 // 3-D map over a bf16 prefix cache [tokens][Hkv][128]: boxes of 64 tokens x 64 dims of one
 // KV head, 128-byte swizzle (the attention kernel's key / value tiles).
 bool make_kv_map(CUtensorMap* tm, const void* cache, long long tokens, int Hkv);
-// 3-D map over a paged bf16 cache [pages * Hkv][page_size][hd]: boxes of one page's rows of one
-// KV head x 64 dims, 128-byte swizzle; rows outside the page or the pool read as zeros.
-bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks);
 
 // A GEMM over weights [M][K] (rows [0, m_split) from map / pointer 0, the rest from 1),
 // with the caller's split-K scratch, arrival counters and device error word.

@@ -19,6 +19,37 @@ using namespace eagle;
 
 namespace {
 
+// Instruction descriptor of tcgen05.mma kind::f16 with fp16 A and B, f32 D, both K-major (as
+// idesc_bf16_f32, whose operands are bf16).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// 3-D map over a paged bf16 cache [pages * Hkv][page_size][hd]: boxes of one page's rows of one
+// KV head x 64 dims, 128-byte swizzle; rows outside the page or the pool read as zeros.
+bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> known{nullptr};
+  Encode fn = known.load();
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      return false;
+    fn = reinterpret_cast<Encode>(p);
+    known.store(fn);
+  }
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(hd) * 2 * page_size};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int KA_MAX_GROUP = 64;
 constexpr int KA_CH = 128;                 // keys per tile (a ring entry)
 constexpr int KA_H = 64;                   // keys per unit of work (half a tile)
