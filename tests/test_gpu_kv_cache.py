@@ -439,3 +439,34 @@ def test_many_requests_and_rows():
     assert eb.kv_append(cache, none, none, dev(cu([0])), zero[:1]) is None
     assert eb.kv_attention(cache, q[:0], dev(cu([0])), zero[:1], 1, 1).shape == (0, 2, 64)
     assert eb.kv_gather(cache, dev(cu([0])), 0)[0].shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("kg,vg", [(0.37, 3.1), (1e-3, 700.0), (2.0 ** -20, 2.0 ** 20)])
+def test_four_bit_store_with_any_global_factor(kg, vg):
+    """Scales and codes equal the definition's but where a quotient lies within the kernel's own
+    rounding of a border: the scale's quotient is rounded to 18 bits (2^-18 relative with the
+    product's error), a code's to multiples of 2^-18 (off by less than 2^-17 in all)."""
+    rng = np.random.default_rng(50)
+    n, H, hd = 400, 4, 128
+    kg32, vg32 = float(np.float32(kg)), float(np.float32(vg))
+    table, P = pages(rng, [n], 32)
+    cache = eb.KVCache.empty(P, 32, H, hd, dev(table), four_bit=True, k_global=kg, v_global=vg)
+    x = K.bf16(rng.standard_normal((n, H, hd)) * np.exp2(rng.integers(-6, 7, (n, H, 1))))
+    k, v = K.bf16(x * kg32), K.bf16(x * vg32)
+    eb.kv_append(cache, dev(k, torch.bfloat16), dev(v, torch.bfloat16), dev(cu([n])), dev(np.array([0], np.int32)))
+    assert cache.check() == 0
+    got = held_rows(cache, table, 0, n, 32)
+    for i, (src, g) in enumerate(((k, kg32), (v, vg32))):
+        code, sc, _ = K.quantise(src, g)
+        gsc, gc = got[2 + i], got[i]
+        ratio = np.abs(src.reshape(n, H, -1, 16)).max(-1) / (6 * g)
+        off = gsc != sc
+        mid = (K.E4M3[1:] + K.E4M3[:-1]) / 2
+        near = np.abs(ratio[..., None] / mid - 1).min(-1) < 2.0 ** -17
+        assert (near | ~off).all() and off.mean() < 1e-2
+        gcode = np.stack([gc & 15, gc >> 4], -1).reshape(n, H, hd)
+        unit = (K.E4M3[gsc] * g)[..., None]
+        mag = np.abs(src.reshape(n, H, -1, 16)) / np.where(unit > 0, unit, 1)
+        border = (K.E2M1[1:] + K.E2M1[:-1]) / 2
+        near = (np.abs(mag[..., None] - border).min(-1) < 2.0 ** -17).reshape(n, H, hd) | off.repeat(16, -1)
+        assert (near | (gcode == code)).all()
