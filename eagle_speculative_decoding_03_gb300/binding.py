@@ -798,7 +798,7 @@ def kv_gather(cache: KVCache, cu_seqlens, total: int, k_out=None, v_out=None, st
 def kv_accept(caches, lens, accept_len, accept_slots, new_lens=None, stream=None):
     """Keep the accepted path of a verified tree (appended behind lens[b] keys in slot order) in
     every cache of the list (one per layer, one shape and page table); returns the new lengths
-    lens + 1 + accept_len (new_lens may be lens)."""
+    lens + 1 + accept_len (new_lens may be lens).  Device errors go to the first cache's word."""
     torch, dev, st = _here(stream)
     caches = [caches] if isinstance(caches, KVCache) else list(caches)
     if not caches:

@@ -189,7 +189,9 @@ EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, f
 // half-layout pair's other dim comes from another lane of the head by a shuffle, so every load
 // of a head precedes its stores (in place is safe).  The CTA computes the cos / sin of its rows
 // once into shared memory; a warp keeps one row's in registers over all the heads it takes.
-// CACHE: 0 eagle_rotary, else eagle_cache_kind_t.
+// CACHE: 0 eagle_rotary, else eagle_cache_kind_t.  Bound by bytes where there are many rows
+// (8,191 x 64 fp32 heads: 85 us, 92% of the measured copy rate); with 4-bit stores by issue and the
+// chain that finds a row's place (8,188 rows, 48 heads: 44 us, 176 MB).
 template <typename T, int CACHE>
 __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, const RopeTab rt) {
   __shared__ float2 cs[RT_WARPS][RT_MAX_PAIRS];
@@ -351,7 +353,8 @@ struct GatherArgs {
 
 // A CTA writes GA_TOKENS packed rows of K (blockIdx.y = 0) or V, 16 bytes per thread and step,
 // consecutive threads consecutive bytes of the output; reads come in runs of one head's row.
-// Loads of GA_STEPS steps are issued before the first store.
+// Loads of GA_STEPS steps are issued before the first store.  67,966 tokens of 8 heads out of 4
+// bits: 58 us, 90% of the measured copy rate.
 template <int HD, int CACHE>
 __global__ void __launch_bounds__(GA_THREADS) gather_kernel(const GatherArgs a) {
   constexpr int OCT = HD / 8, ROWS = GA_THREADS / OCT;     // rows (token, head) a step covers
@@ -459,7 +462,8 @@ EAGLE_DEV void move_rows(const KvPool& c, char* base, int bytes, int count, cons
   }
 }
 
-// One CTA per (request, cache, key / value).
+// One CTA per (request, cache, key / value).  32 trees of 49 slots in 16 layers: 11 us, 68% of the
+// measured copy rate for the bytes that move.
 __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __grid_constant__ AcceptCaches caches) {
   __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_end[2];
   const int b = blockIdx.x, tid = threadIdx.x;

@@ -475,7 +475,8 @@ EAGLE_API eagle_status_t eagle_speculative_accept(int32_t B, int32_t S, int32_t 
  *     Appending takes the row's bf16 value (a rotated key is rounded to bf16 first) and stores
  *     scale = e4m3(largest magnitude of the 16 dims / (6 global)), code = e2m1(value / (scale
  *     global)), both rounded to nearest, ties to even, saturating; NaN is stored as 0, and a
- *     group whose scale rounds to 0 as zeros.  0.5625 bytes per element instead of 2.
+ *     group whose scale rounds to 0 as zeros.  0.5625 bytes per element instead of 2.  (A caller
+ *     that fills pages itself writes no NaN scale, 0x7f or 0xff, into a row that is read.)
  *
  * All calls are stream-ordered, allocate nothing and keep no state: calls on one cache (or
  * one workspace) must be ordered by the caller where they touch the same rows.  Device
