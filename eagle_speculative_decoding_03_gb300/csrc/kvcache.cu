@@ -439,9 +439,8 @@ struct KeepArgs {
 };
 
 // Moves count rows of `bytes` per (head, row) in units of U: a thread owns a column (head,
-// unit) and moves its units in path order, 8 reads in flight.  Slots ascend and slot j >= j + 1,
-// so a place written is never the source of a later move: only reads before writes matter, and
-// those are one thread's own.
+// unit) and moves its units in list order, 8 reads in flight.  No place written is the source of
+// a later move of the list, so only reads before writes matter, and those are one thread's own.
 template <typename U>
 EAGLE_DEV void move_rows(const KvPool& c, char* base, int bytes, int count, const int* src_page, const int* src_tok,
                          const int* dst_page, const int* dst_tok) {
@@ -465,10 +464,12 @@ EAGLE_DEV void move_rows(const KvPool& c, char* base, int bytes, int count, cons
 // One CTA per (request, cache, key / value).  32 trees of 49 slots in 16 layers: 11 us, 68% of the
 // measured copy rate for the bytes that move.
 __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __grid_constant__ AcceptCaches caches) {
-  __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_end[2];
+  __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_end[2], s_run[2];
   const int b = blockIdx.x, tid = threadIdx.x;
   const int base = __ldg(a.lens + b);
-  // the path: ascending slots behind the root; anything else ends it
+  // The path: strictly ascending slots of the tree; anything else ends it.  So slot j >= j, and
+  // move j writes place j + 1: the source of a later move only where the path starts with the
+  // slots 0, 1, 2, ... (one that names the root).  That run is moved back to front.
   const int want = __ldg(a.accept_len + b);
   int n = min(max(want, 0), a.S - 1);
   bool wrong = false;
@@ -476,23 +477,26 @@ __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __gri
   if (tid < 64) {
     s = tid < n ? __ldg(a.slots + static_cast<size_t>(b) * a.S + tid) : 0;
     src_tok[tid] = s;
-    s_end[tid >> 5] = 64;
+    s_end[tid >> 5] = s_run[tid >> 5] = 64;
   }
   __syncthreads();
   if (tid < 64) {
-    wrong = tid < n && (s <= (tid ? src_tok[tid - 1] : 0) || s >= a.S);
+    wrong = tid < n && (s <= (tid ? src_tok[tid - 1] : -1) || s >= a.S);
     const unsigned bits = __ballot_sync(0xffffffffu, wrong);
+    const unsigned off = __ballot_sync(0xffffffffu, s != tid);
     if ((tid & 31) == 0 && bits) s_end[tid >> 5] = tid + __ffs(bits) - 1;
+    if ((tid & 31) == 0 && off) s_run[tid >> 5] = tid + __ffs(off) - 1;
   }
   __syncthreads();
   const int end = min(s_end[0], s_end[1]);
   if (tid == 0 && (want != n || end < n)) atomicOr(a.err, DEVERR_TOKEN);
   n = min(n, end);
   if (tid < n) {
-    src_tok[tid] = base + s;
-    dst_tok[tid] = base + 1 + tid;
-    src_page[tid] = s == tid + 1 ? -1 : kv_page(a.pool, b, base + s, a.err);   // (already in place)
-    dst_page[tid] = kv_page(a.pool, b, base + 1 + tid, a.err);
+    const int run = min(min(s_run[0], s_run[1]), n), i = tid < run ? run - 1 - tid : tid;
+    src_tok[i] = base + s;
+    dst_tok[i] = base + 1 + tid;
+    src_page[i] = s == tid + 1 ? -1 : kv_page(a.pool, b, base + s, a.err);   // (already in place)
+    dst_page[i] = kv_page(a.pool, b, base + 1 + tid, a.err);
   }
   // new_lens apart from lens: written here; in place, after every CTA has read lens
   if (tid == 0 && a.new_lens != a.lens && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + 1 + n;
@@ -511,7 +515,7 @@ __global__ void keep_lens_kernel(const KeepArgs a) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= a.B) return;
   const int n = min(max(__ldg(a.accept_len + b), 0), a.S - 1);
-  int prev = 0, j = 0;
+  int prev = -1, j = 0;
   for (; j < n; ++j) {
     const int s = __ldg(a.slots + static_cast<size_t>(b) * a.S + j);
     if (s <= prev || s >= a.S) break;

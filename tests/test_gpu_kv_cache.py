@@ -189,13 +189,14 @@ def test_gather(kind, hd, ps, Hkv, keys):
 @pytest.mark.parametrize("hd,ps,Hkv,layers", [(128, 16, 2, 1), (64, 32, 3, 5), (128, 64, 1, 64)])
 def test_accept(kind, hd, ps, Hkv, layers):
     rng = np.random.default_rng(layers)
-    S, lens = 24, [0, 30, 61, 5, 17]
+    S, lens = 24, [0, 30, 61, 5, 17, 40]
     B = len(lens)
-    acc = np.array([0, 1, S - 1, 9, 5], np.int32)
+    acc = np.array([0, 1, S - 1, 9, 5, 20], np.int32)
     slots = np.full((B, S), -1, np.int32)
     for b in range(B):
         slots[b, :acc[b]] = np.sort(rng.choice(np.arange(1, S), acc[b], replace=False))
     slots[4, :5] = [1, 2, 3, 4, 5]                                  # nothing to move
+    slots[5, :20] = np.arange(20)                                   # each move's source is the next one's place
     room = [n + S for n in lens]
     made = [make_cache(np.random.default_rng(7), kind, hd, ps, Hkv, room) for _ in range(layers)]
     table = made[0][0].page_table                                   # (one shape, one table)
