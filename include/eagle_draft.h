@@ -552,10 +552,11 @@ EAGLE_API eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t 
 
 /* After a verification: request b's tree of S slots was appended behind its lens[b] keys in
  * slot order (root first).  Keeps the root and the accept_len[b] accepted slots
- * accept_slots[b][..] (strictly ascending, as eagle_verify_tree and eagle_speculative_accept write
- * them; the root's slot 0 is as good as any): slot accept_slots[b][j] moves to key lens[b] + 1 + j in every one of the n_caches
- * caches (HOST array, 1..64, e.g. one per layer; all of one shape, of caches[0]'s page
- * table and each with its own pool), and new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens). */
+ * accept_slots[b][..] (strictly ascending, as eagle_verify_tree and eagle_speculative_accept
+ * write them; slot 0, the root's, may be among them): slot accept_slots[b][j] moves to key
+ * lens[b] + 1 + j in every one of the n_caches caches (HOST array, 1..64, e.g. one per layer;
+ * all of one shape, of caches[0]'s page table and each with its own pool), and
+ * new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens). */
 EAGLE_API eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_t n_caches, int32_t B, int32_t S,
                                          const int32_t* lens, const int32_t* accept_len, const int32_t* accept_slots,
                                          int32_t* new_lens, uint32_t* err_word, void* stream);
