@@ -541,7 +541,9 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         while (clock64() - t0 < 4000000) {
         }
       }
-      tc_commit(bar_fin);
+      // (a range behind all its block sees has no tile: nothing to commit, and nobody waits, so an
+      // arrival could land after the CTA has left)
+      if (T > 0) tc_commit(bar_fin);
     }
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {

@@ -111,6 +111,15 @@ def test_causal_chunks(kind, hd, ps, Hkv, G, ctx, rows):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_ranges_behind_what_a_causal_block_sees(kind):
+    """A prompt cut into key ranges: its first blocks of rows see none of the last ranges' keys, and
+    those ranges contribute nothing to them."""
+    rng = np.random.default_rng(17)
+    cache, _ = run(rng, kind, 128, 64, 1, 8, [0], [1000], pad=2)
+    assert eb.kv_attention_workspace(cache, 8, 1002, 1, 1000, 1000) > 0      # (several ranges, not joined)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("ctx", [0, 50])
 def test_rows_that_see_nothing(kind, ctx):
     """Mask rows of zeros: without a context zeros and -inf, with one the context alone."""
