@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
+#include <cstdint>
 #include <cstdio>
 #include <cstring>
 #include <type_traits>
@@ -202,10 +203,10 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
   // append_prompt_f4 took 61 us, now 55; eagle_rotary, which has no places to find, lost by it)
   if (CACHE != 0 && rows >= 4 && blockIdx.y == 0) {
     auto fetch = [&](const void* p, long long ld, int H) {
-      const int lines = (H * a.hd * static_cast<int>(sizeof(T)) + 127) >> 7;
+      const int lines = static_cast<int>((static_cast<long long>(H) * a.hd * sizeof(T) + 127) >> 7);
       for (int r = warp; r < rows && row0 + r < a.N; r += RT_WARPS)
         for (int i = lane; i < lines; i += 32)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(static_cast<const T*>(p) + (row0 + r) * ld) + i * 128));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(static_cast<const T*>(p) + (row0 + r) * ld) + i * 128ll));
     };
     if (a.Hq) fetch(a.q, a.q_ld, a.Hq);
     fetch(a.k, a.k_ld, a.Hk);
@@ -575,6 +576,10 @@ bool bad_rows(const void* p, long long ld, int H, int hd, int dtype) {
   const int es = dtype == EAGLE_DTYPE_BF16 ? 2 : 4;
   return !aligned16(p) || ld < static_cast<long long>(H) * hd || (ld * es) % 16;
 }
+// The kernels count rows, and the elements of one row, in 32 bits; a grid's last CTA looks at row
+// numbers a few past the end.
+constexpr int KV_MAX_ROWS = INT32_MAX - 64;
+bool too_large(int N, long long heads, int hd) { return N > KV_MAX_ROWS || heads * hd > INT32_MAX; }
 
 }  // namespace
 }  // namespace eagle
@@ -590,6 +595,7 @@ extern "C" eagle_status_t eagle_rotary(int32_t dtype, const void* x, int64_t x_s
   if (N < 0 || H < 1) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need N >= 0 and H >= 1", who);
   if (head_dim < 16 || head_dim > 256 || head_dim % 8)
     return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: head_dim must be a multiple of 8 in 16..256, not %d", who, head_dim);
+  if (too_large(N, H, head_dim)) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: more than 2^31 - 65 rows, or 2^31 - 1 elements in one", who);
   if (bad_rows(x, x_stride, H, head_dim, dtype) || bad_rows(out, out_stride, H, head_dim, dtype))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
   if (x == out && x_stride != out_stride) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: in place needs equal strides", who);
@@ -623,6 +629,8 @@ extern "C" eagle_status_t eagle_kv_append(const eagle_kv_cache_t* cache, const e
   if (w->B < 1 || w->N < 0 || (w->q && w->n_heads < 1)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need B >= 1, N >= 0, n_heads >= 1", who);
   if (w->q && !rope) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: queries need a rope", who);
   const int hd = cache->head_dim, Hkv = cache->n_kv_heads;
+  if (too_large(w->N, std::max(Hkv, w->q ? w->n_heads : 0), hd))
+    return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: more than 2^31 - 65 rows, or 2^31 - 1 elements in one", who);
   if (bad_rows(w->k, w->k_stride, Hkv, hd, w->dtype) || bad_rows(w->v, w->v_stride, Hkv, hd, w->dtype) ||
       (w->q && (bad_rows(w->q, w->q_stride, w->n_heads, hd, w->dtype) || bad_rows(w->q_out, w->q_out_stride, w->n_heads, hd, w->dtype))))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
@@ -660,6 +668,7 @@ extern "C" eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t
   const eagle_status_t r = kv_pool(cache, who, &a.pool);
   if (r != EAGLE_OK) return r;
   if (B < 1 || total < 0) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need B >= 1 and total >= 0", who);
+  if (total > KV_MAX_ROWS) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: more than 2^31 - 65 rows", who);
   if (total == 0) return EAGLE_OK;
   if (!cu_seqlens || !k_out || !v_out || !err_word) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
   if (!aligned16(k_out) || !aligned16(v_out)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: outputs must be 16-byte aligned", who);

@@ -481,7 +481,8 @@ EAGLE_API eagle_status_t eagle_speculative_accept(int32_t B, int32_t S, int32_t 
  * All calls are stream-ordered, allocate nothing and keep no state: calls on one cache (or
  * one workspace) must be ordered by the caller where they touch the same rows.  Device
  * pointers except where marked; pointers of rows 16-byte aligned, strides in elements and
- * multiples of 16 bytes.  Kernel-side problems set bits of *err_word (device, caller-owned):
+ * multiples of 16 bytes; at most 2^31 - 65 rows of heads x head_dim < 2^31 elements each
+ * (EAGLE_ERR_UNSUPPORTED past that).  Kernel-side problems set bits of *err_word (device, caller-owned):
  * EAGLE_DEVERR_PAGE for a place outside the table or pool (the row is skipped, or read as
  * zeros), EAGLE_DEVERR_PREFIX for lengths or row ranges outside the call's bounds (clamped),
  * EAGLE_DEVERR_TOKEN for an accepted path that is not ascending slots of the tree.

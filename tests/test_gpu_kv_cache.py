@@ -72,6 +72,17 @@ def test_rotary_scaled_frequencies_amplitude_and_strides():
     assert eb.rotary(x[:0], dev(pos[:0].astype(np.int32)), rope).shape == (0, 5, 128)
 
 
+def test_rotary_of_the_longest_row():
+    """2^31 - 128 elements in one row: its first and last heads are what they are alone."""
+    H = (1 << 24) - 1
+    x = torch.zeros(1, H, 128, dtype=torch.bfloat16, device="cuda")
+    ends = torch.randn(1, 6, 128, device="cuda").to(torch.bfloat16)
+    x[:, :3], x[:, -3:] = ends[:, :3], ends[:, 3:]
+    pos = dev(np.array([77], np.int32))
+    y, want = eb.rotary(x, pos, eb.Rope(128)), eb.rotary(ends, pos, eb.Rope(128))
+    assert torch.equal(y[:, :3], want[:, :3]) and torch.equal(y[:, -3:], want[:, 3:]) and (y[:, 3:-3] == 0).all()
+
+
 def held_rows(cache, table, b, n, ps):
     """Request b's first n rows of every pool tensor, on the host."""
     t = np.arange(n)

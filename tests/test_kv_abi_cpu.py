@@ -157,3 +157,21 @@ def test_attention_arguments(lib):
     assert lib.eagle_kv_attention(C.byref(c), C.byref(a), P, None) == 1
     a.workspace_bytes, a.workspace = need, P + 8
     assert lib.eagle_kv_attention(C.byref(c), C.byref(a), P, None) == 1
+
+
+def test_rows_past_32_bit_arithmetic_are_refused(lib):
+    """The kernels index a row's elements and the rows in 32 bits: larger calls are refused before
+    any launch."""
+    big = 1 << 24                                     # heads: 2^31 elements a row at 128
+    for H, hd, N in ((big, 128, 1), (1 << 30, 16, 1), (1, 128, 2 ** 31 - 1), (1, 128, 2 ** 31 - 8)):
+        rp = C.byref(rope(rot_dim=16))
+        assert lib.eagle_rotary(1, P, H * hd, N, H, hd, P, rp, P, H * hd, None) == 2, (H, hd, N)
+    def append(c, **kw):
+        d = dict(B=1, N=1, cu_rows=P, lens=P, positions=P, dtype=1, n_heads=16, k=P, v=P, q=P, q_out=P, k_stride=1 << 40,
+                 v_stride=1 << 40, q_stride=1 << 40, q_out_stride=1 << 40)
+        d.update(kw)
+        return lib.eagle_kv_append(C.byref(c), C.byref(eb.KVRows(**d)), C.byref(rope()), P, None)
+    assert append(cache(), n_heads=big) == 2
+    assert append(cache(), N=2 ** 31 - 1) == 2
+    assert append(cache(n_kv_heads=1 << 24, num_pages=1, page_size=16)) == 2
+    assert lib.eagle_kv_gather(C.byref(cache()), 1, P, 2 ** 31 - 1, P, 2 * P, P, None) == 2
