@@ -581,6 +581,14 @@ bool bad_rows(const void* p, long long ld, int H, int hd, int dtype) {
 constexpr int KV_MAX_ROWS = INT32_MAX - 64;
 bool too_large(int N, long long heads, int hd) { return N > KV_MAX_ROWS || heads * hd > INT32_MAX; }
 
+// A call that writes pages: keys, values and scales must be pools of their own.
+bool shared_pools(const eagle_kv_cache_t& x, const eagle_kv_cache_t& y, bool same_cache) {
+  if (x.k == y.v || x.v == y.k || (!same_cache && (x.k == y.k || x.v == y.v))) return true;
+  if (x.kind != EAGLE_CACHE_F4) return false;
+  return x.k_scale == y.v_scale || x.v_scale == y.k_scale ||
+         (!same_cache && (x.k_scale == y.k_scale || x.v_scale == y.v_scale));
+}
+
 }  // namespace
 }  // namespace eagle
 
@@ -639,6 +647,7 @@ extern "C" eagle_status_t eagle_kv_append(const eagle_kv_cache_t* cache, const e
   RopeTab rt;
   if ((r = rope_table(rope, hd, who, &rt)) != EAGLE_OK) return r;
   if (w->N == 0) return EAGLE_OK;
+  if (shared_pools(*cache, *cache, true)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: keys and values share a pool", who);
   a.q = w->q;
   a.k = w->k;
   a.v = w->v;
@@ -671,6 +680,7 @@ extern "C" eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t
   if (total > KV_MAX_ROWS) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: more than 2^31 - 65 rows", who);
   if (total == 0) return EAGLE_OK;
   if (!cu_seqlens || !k_out || !v_out || !err_word) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
+  if (k_out == v_out) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: k_out and v_out must be buffers of their own", who);
   if (!aligned16(k_out) || !aligned16(v_out)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: outputs must be 16-byte aligned", who);
   a.B = B;
   a.total = total;
@@ -711,8 +721,8 @@ extern "C" eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_
     if (x.kind != y.kind || x.n_kv_heads != y.n_kv_heads || x.head_dim != y.head_dim || x.page_size != y.page_size ||
         x.num_pages != y.num_pages || x.max_pages != y.max_pages || x.page_table != y.page_table)
       return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: the caches must share one shape and page table", who);
-    for (int j = 0; j < i; ++j)
-      if (x.k == caches[j].k || x.v == caches[j].v || x.k == caches[j].v || x.v == caches[j].k)
+    for (int j = 0; j <= i; ++j)
+      if (shared_pools(x, caches[j], j == i))
         return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: caches %d and %d share a pool", who, j, i);
     if (i == 0) a.pool = p;
     ac.p[4 * i] = static_cast<char*>(p.k);
@@ -720,6 +730,8 @@ extern "C" eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_
     ac.p[4 * i + 2] = static_cast<char*>(p.ks);
     ac.p[4 * i + 3] = static_cast<char*>(p.vs);
   }
+  if (new_lens == accept_len || new_lens == accept_slots)   // (every CTA of a request reads the path)
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: new_lens may be lens, but not the path", who);
   a.f4 = caches[0].kind == EAGLE_CACHE_F4;
   a.B = B;
   a.S = S;

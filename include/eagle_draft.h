@@ -467,7 +467,8 @@ EAGLE_API eagle_status_t eagle_speculative_accept(int32_t B, int32_t S, int32_t 
  *
  * Pages: a pool of num_pages pages of page_size tokens; token t of request b sits in row
  * t % page_size of page page_table[b][t / page_size].  Per page and KV head the rows are
- * contiguous.  Requests may share pages that no call writes.
+ * contiguous.  Requests may share pages that no call writes.  Keys, values and scales are pools
+ * of their own wherever a call writes pages.
  *   EAGLE_CACHE_BF16: k, v bf16 [num_pages][Hkv][page_size][hd].
  *   EAGLE_CACHE_F4:   k, v e2m1 codes [num_pages][Hkv][page_size][hd / 2] (even dim in the low
  *     nibble; bit 3 the sign, magnitudes 0 .5 1 1.5 2 3 4 6), k_scale, v_scale e4m3
@@ -547,7 +548,7 @@ EAGLE_API eagle_status_t eagle_kv_append(const eagle_kv_cache_t* cache, const ea
 /* The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every request as bf16
  * [total][Hkv][hd] at rows cu_seqlens[b]..: the packed prefix of eagle_draft_tree and
  * eagle_verify_tree.  `total` is the outputs' extent; rows outside the requests are left as
- * they were. */
+ * they were.  k_out and v_out may not overlap each other or the pools. */
 EAGLE_API eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t B, const int32_t* cu_seqlens,
                                          int32_t total, void* k_out, void* v_out, uint32_t* err_word, void* stream);
 
@@ -557,7 +558,7 @@ EAGLE_API eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t 
  * write them; slot 0, the root's, may be among them): slot accept_slots[b][j] moves to key
  * lens[b] + 1 + j in every one of the n_caches caches (HOST array, 1..64, e.g. one per layer;
  * all of one shape, of caches[0]'s page table and each with its own pool), and
- * new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens). */
+ * new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens, but may not overlap the path). */
 EAGLE_API eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_t n_caches, int32_t B, int32_t S,
                                          const int32_t* lens, const int32_t* accept_len, const int32_t* accept_slots,
                                          int32_t* new_lens, uint32_t* err_word, void* stream);

@@ -175,3 +175,22 @@ def test_rows_past_32_bit_arithmetic_are_refused(lib):
     assert append(cache(), N=2 ** 31 - 1) == 2
     assert append(cache(n_kv_heads=1 << 24, num_pages=1, page_size=16)) == 2
     assert lib.eagle_kv_gather(C.byref(cache()), 1, P, 2 ** 31 - 1, P, 2 * P, P, None) == 2
+
+
+def test_buffers_that_calls_write_are_not_shared(lib):
+    """Keys and values of one launch are written by CTAs in no order: one buffer for both, scales
+    in common, or new lengths over the path that other CTAs still read are refused."""
+    own = dict(k=P, v=2 * P, k_scale=3 * P, v_scale=4 * P)
+    w = eb.KVRows(B=1, N=1, cu_rows=P, lens=P, positions=P, dtype=1, k=P, v=P, k_stride=1024, v_stride=1024)
+    for kw in (dict(v=P), dict(v_scale=3 * P)):
+        c = cache(**{**own, **kw})
+        assert lib.eagle_kv_append(C.byref(c), C.byref(w), None, P, None) == 1, kw
+        assert lib.eagle_kv_accept(C.byref(c), 1, 1, 4, P, 2 * P, 3 * P, 4 * P, P, None) == 1, kw
+    two = dict(k=5 * P, v=6 * P, k_scale=7 * P, v_scale=8 * P)
+    for kw in (dict(k_scale=3 * P), dict(v_scale=4 * P), dict(k_scale=4 * P), dict(v_scale=3 * P)):
+        cs = (eb.KVCacheC * 2)(cache(**own), cache(**{**two, **kw}))
+        assert lib.eagle_kv_accept(cs, 2, 1, 4, P, 2 * P, 3 * P, 4 * P, P, None) == 1, kw
+    c = cache(**own)
+    assert lib.eagle_kv_gather(C.byref(c), 1, P, 8, 5 * P, 5 * P, P, None) == 1
+    for new in (2 * P, 3 * P):
+        assert lib.eagle_kv_accept(C.byref(c), 1, 1, 4, P, 2 * P, 3 * P, new, P, None) == 1
