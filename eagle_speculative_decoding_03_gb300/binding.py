@@ -624,12 +624,15 @@ def _float_kind(t, name: str) -> int:
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, linear: float = 1.0, banded: tuple | None = None,
                      ramped: tuple | None = None) -> list:
     """Inverse frequencies theta^(-2i/rot_dim), scaled for contexts longer than trained on.
-    ``linear``: all divided by the factor.  ``banded`` (factor, low, high, original): waves
-    longer than original/low positions are divided by the factor, those shorter than
-    original/high kept, a smooth blend between.  ``ramped`` (factor, fast, slow, original):
-    pairs that turn more than ``fast`` times within ``original`` positions are kept, those that
-    turn less than ``slow`` times divided by the factor, a linear ramp over the pair index
-    between."""
+    ``linear``: all divided by the factor (position interpolation).  ``banded`` (factor, low,
+    high, original): waves longer than original/low positions are divided by the factor, those
+    shorter than original/high kept, between them a blend linear in the turns within the original
+    context (the rule of the Llama-3 family's long contexts).  ``ramped`` (factor, fast, slow,
+    original): pairs that turn more than ``fast`` times within ``original`` positions are kept,
+    those that turn less than ``slow`` times divided by the factor, between them a linear ramp
+    over the pair index (NTK by parts: Peng et al., "YaRN", 2023).  The ramp's ends are whole
+    indices, rounded outwards and kept within 0 .. rot_dim - 1: it may end behind the last pair,
+    none of which is then divided whole."""
     import math
     if rot_dim < 2 or rot_dim % 2 or not theta > 0 or not linear > 0 or (banded and ramped):
         _bad("rope_frequencies: bad arguments")
@@ -647,9 +650,9 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, linear: float = 1.0, 
     if ramped:
         factor, fast, slow, original = ramped
         index = lambda turns: rot_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
-        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rot_dim // 2 - 1)
+        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rot_dim - 1)
         for i, f in enumerate(w):
-            part = min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3)))
+            part = 1.0 if i >= hi else 0.0 if i <= lo else (i - lo) / (hi - lo)
             w[i] = f * (1.0 - part + part / factor)
     return w
 

@@ -89,3 +89,24 @@ def test_rope_frequencies():
                 dict(rot_dim=64, ramped=(0, 32, 1, 4096))):
         with pytest.raises(eb.EagleError):
             eb.rope_frequencies(**bad)
+
+
+@pytest.mark.parametrize("rot,theta,factor,fast,slow,original", [
+    (64, 1e4, 8.0, 32, 1, 131072),       # the ramp ends behind the last pair (index 34 of 0 .. 31)
+    (64, 1e4, 4.0, 32, 1, 4096), (128, 5e5, 16.0, 32, 1, 8192), (16, 1e4, 2.0, 8, 2, 100000), (32, 1e4, 8.0, 64, 4, 10 ** 9),
+    (64, 1e4, 8.0, 2, 1, 4), (2, 1e4, 8.0, 32, 1, 64)])
+def test_ramped_frequencies_follow_the_correction_range(rot, theta, factor, fast, slow, original):
+    """The published range: index of a pair that turns n times = rot ln(original / (2 pi n)) / (2 ln
+    theta), ends rounded outwards and clamped to [0, rot - 1]; and what the rule promises of the
+    pairs outside it."""
+    w = np.array(eb.rope_frequencies(rot, theta))
+    got = np.array(eb.rope_frequencies(rot, theta, ramped=(factor, fast, slow, original))) / w
+    ends = [rot * np.log(original / (2 * np.pi * n)) / (2 * np.log(theta)) for n in (fast, slow)]
+    lo, hi = max(np.floor(ends[0]), 0), min(np.ceil(ends[1]), rot - 1)
+    if lo < hi:
+        ramp = np.clip((np.arange(rot // 2) - lo) / (hi - lo), 0, 1)
+        assert np.allclose(got, (1 - ramp) + ramp / factor, rtol=1e-12)
+    turns = original * w / (2 * np.pi)
+    assert np.allclose(got[turns > fast], 1.0) and (got[turns > slow] > 1.0 / factor).all()
+    whole = np.arange(rot // 2) >= np.ceil(ends[1])
+    assert np.allclose(got[whole], 1.0 / factor) and np.allclose(got[turns < slow], 1.0 / factor)
