@@ -638,8 +638,8 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, linear: float = 1.0, 
         _bad("rope_frequencies: bad arguments")
     if banded and not (banded[0] > 0 and banded[2] > banded[1] >= 0 and banded[3] > 0):
         _bad("rope_frequencies: banded needs factor > 0, high > low >= 0, original > 0")
-    if ramped and not (ramped[0] > 0 and ramped[1] > ramped[2] > 0 and ramped[3] > 0 and theta != 1):
-        _bad("rope_frequencies: ramped needs factor > 0, fast > slow > 0, original > 0")
+    if ramped and not (ramped[0] > 0 and ramped[1] > ramped[2] > 0 and ramped[3] > 0 and theta > 1):
+        _bad("rope_frequencies: ramped needs factor > 0, fast > slow > 0, original > 0, theta > 1")
     w = [theta ** (-2.0 * i / rot_dim) / linear for i in range(rot_dim // 2)]
     if banded:
         factor, low, high, original = banded

@@ -110,3 +110,9 @@ def test_ramped_frequencies_follow_the_correction_range(rot, theta, factor, fast
     assert np.allclose(got[turns > fast], 1.0) and (got[turns > slow] > 1.0 / factor).all()
     whole = np.arange(rot // 2) >= np.ceil(ends[1])
     assert np.allclose(got[whole], 1.0 / factor) and np.allclose(got[turns < slow], 1.0 / factor)
+
+
+def test_a_ramp_needs_falling_frequencies():
+    for theta in (1.0, 0.5):
+        with pytest.raises(eb.EagleError):
+            eb.rope_frequencies(64, theta, ramped=(4.0, 32, 1, 4096))
