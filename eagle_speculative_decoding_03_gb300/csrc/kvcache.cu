@@ -217,13 +217,18 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
     const int b = n < a.N ? row_owner(a.cu, a.B, n) : -1;
     int page = -1, t = 0;
     if (b >= 0) {
-      t = __ldg(a.lens + b) + (n - __ldg(a.cu + b));
-      page = kv_page(a.pool, b, t, a.err);
+      const int len = __ldg(a.lens + b);
+      if (len >= 0) {                        // (rows behind a negative length are skipped; flagged below)
+        t = static_cast<int>(static_cast<unsigned>(len) + static_cast<unsigned>(n - __ldg(a.cu + b)));   // (past 2^31: no page)
+        page = kv_page(a.pool, b, t, a.err);
+      }
     }
     s_req[tid] = b;
     s_page[tid] = page;
     s_tok[tid] = t;
   }
+  // (the warps that find no places, while warp 0 does)
+  if (CACHE != 0 && blockIdx.x == 0 && blockIdx.y == 0 && warp > 0) check_ranges(a.cu, a.lens, a.B, a.N, tid - 32, RT_THREADS - 32, a.err);
   for (int i = tid; i < rows * rt.pairs; i += RT_THREADS) {
     const int r = i / rt.pairs, j = i - r * rt.pairs;
     if (row0 + r < a.N) {
@@ -372,6 +377,7 @@ __global__ void __launch_bounds__(GA_THREADS) gather_kernel(const GatherArgs a) 
     s_page[tid] = page;
     s_tok[tid] = t;
   }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid >= 32) check_ranges(a.cu, nullptr, a.B, a.total, tid - 32, GA_THREADS - 32, a.err);
   __syncthreads();
   const bool is_v = blockIdx.y != 0;
   const uint8_t* pool = static_cast<const uint8_t*>(is_v ? a.pool.v : a.pool.k);
@@ -468,6 +474,13 @@ __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __gri
   __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_end[2], s_run[2];
   const int b = blockIdx.x, tid = threadIdx.x;
   const int base = __ldg(a.lens + b);
+  if (base < 0) {                            // no places: nothing moves, the length stays
+    if (tid == 0) {
+      atomicOr(a.err, DEVERR_PREFIX);
+      if (a.new_lens != a.lens && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base;
+    }
+    return;
+  }
   // The path: strictly ascending slots of the tree; anything else ends it.  So slot j >= j, and
   // move j writes place j + 1: the source of a later move only where the path starts with the
   // slots 0, 1, 2, ... (one that names the root).  That run is moved back to front.
@@ -514,7 +527,7 @@ __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __gri
 // The new lengths in place of the old (every CTA of the moves reads those).
 __global__ void keep_lens_kernel(const KeepArgs a) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= a.B) return;
+  if (b >= a.B || a.lens[b] < 0) return;
   const int n = min(max(__ldg(a.accept_len + b), 0), a.S - 1);
   int prev = -1, j = 0;
   for (; j < n; ++j) {

@@ -53,6 +53,17 @@ EAGLE_DEV int row_owner(const int* cu, int B, int n) {
   return lo;
 }
 
+// Flags ranges cu [B + 1] that descend or leave [0, n], and negative lengths (lens may be null).
+// Thread `i` of `threads` (in one CTA of a grid: the word is the call's).
+EAGLE_DEV void check_ranges(const int* cu, const int* lens, int B, int n, int i, int threads, unsigned* err) {
+  bool bad = false;
+  for (; i < B; i += threads) {
+    const int c0 = __ldg(cu + i), c1 = __ldg(cu + i + 1);
+    bad |= c0 < 0 || c1 < c0 || c1 > n || (lens && __ldg(lens + i) < 0);
+  }
+  if (bad) atomicOr(err, DEVERR_PREFIX);
+}
+
 // Two floats to e2m1 codes in a byte (a in the low nibble), nearest, ties to even, saturating.
 EAGLE_DEV uint32_t e2m1x2(float a, float b) {
   uint32_t r;

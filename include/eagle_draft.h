@@ -485,7 +485,9 @@ EAGLE_API eagle_status_t eagle_speculative_accept(int32_t B, int32_t S, int32_t 
  * multiples of 16 bytes; at most 2^31 - 65 rows of heads x head_dim < 2^31 elements each
  * (EAGLE_ERR_UNSUPPORTED past that).  Kernel-side problems set bits of *err_word (device, caller-owned):
  * EAGLE_DEVERR_PAGE for a place outside the table or pool (the row is skipped, or read as
- * zeros), EAGLE_DEVERR_PREFIX for lengths or row ranges outside the call's bounds (clamped),
+ * zeros), EAGLE_DEVERR_PREFIX for negative lengths, and for lengths or row ranges that descend
+ * or pass the call's bounds (rows past the bounds are left out; of a request with a negative
+ * length nothing is stored or moved, and attention takes the length as 0),
  * EAGLE_DEVERR_TOKEN for an accepted path that is not ascending slots of the tree.
  * ------------------------------------------------------------------------------------ */
 typedef enum { EAGLE_CACHE_BF16 = 1, EAGLE_CACHE_F4 = 2 } eagle_cache_kind_t;

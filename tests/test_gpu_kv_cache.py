@@ -482,3 +482,69 @@ def test_four_bit_store_with_any_global_factor(kg, vg):
         border = (K.E2M1[1:] + K.E2M1[:-1]) / 2
         near = (np.abs(mag[..., None] - border).min(-1) < 2.0 ** -17).reshape(n, H, hd) | off.repeat(16, -1)
         assert (near | (gcode == code)).all()
+
+
+def reported(cache, word):
+    with pytest.raises(eb.EagleError) as e:
+        cache.check()
+    assert str(e.value).endswith(f"0x{word:x}") and cache.check() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+def test_gather_reports_ranges_past_its_bounds(kind):
+    """Packed rows that the outputs have no room for, or that descend, are reported; the rows
+    inside are right."""
+    rng = np.random.default_rng(60)
+    cache, held = make_cache(rng, kind, 128, 16, 2, [20, 30])
+    k, v = eb.kv_gather(cache, dev(cu([20, 30])), 45)                # five rows short
+    reported(cache, eb.DEVERR_PREFIX)
+    for got, i in ((k, 0), (v, 1)):
+        assert (got.double().cpu().numpy() == np.concatenate([h[i] for h in held])[:45]).all()
+    for ranges in ([-2, 18, 40], [0, 20, 10]):
+        eb.kv_gather(cache, dev(np.array(ranges, np.int32)), 40)
+        reported(cache, eb.DEVERR_PREFIX)
+    eb.kv_gather(cache, dev(np.array([3, 20, 40], np.int32)), 41)    # rows of no request at both ends
+    assert cache.check() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+def test_append_reports_ranges_past_its_bounds(kind):
+    rng = np.random.default_rng(61)
+    table, P = pages(rng, [32, 32], 16)
+    x = torch.randn(6, 2, 64, device="cuda").to(torch.bfloat16)
+    def fresh():
+        return eb.KVCache.empty(P, 16, 2, 64, dev(table), four_bit=kind == "f4")
+    def call(ranges, lens):
+        c = fresh()
+        eb.kv_append(c, x, x, dev(np.array(ranges, np.int32)), dev(np.array(lens, np.int32)))
+        return c
+    want = call([0, 2, 6], [5, 7])
+    assert want.check() == 0
+    c = call([0, 2, 9], [5, 7])                                      # rows 6 to 8 are not there
+    reported(c, eb.DEVERR_PREFIX)
+    assert torch.equal(c.k.view(torch.uint8), want.k.view(torch.uint8)) and torch.equal(c.v.view(torch.uint8), want.v.view(torch.uint8))
+    reported(call([0, 4, 3], [5, 7]), eb.DEVERR_PREFIX)
+    reported(call([-1, 2, 6], [5, 7]), eb.DEVERR_PREFIX)
+    c = call([0, 2, 6], [-1, 7])                                     # a negative length: that request is skipped
+    reported(c, eb.DEVERR_PREFIX)
+    w = fresh()
+    eb.kv_append(w, x, x, dev(np.array([2, 2, 6], np.int32)), dev(np.array([0, 7], np.int32)))
+    assert w.check() == 0 and torch.equal(c.k.view(torch.uint8), w.k.view(torch.uint8))
+    reported(call([0, 2, 6], [2 ** 31 - 1, 7]), eb.DEVERR_PAGE)      # past every page
+
+
+def test_accept_reports_negative_lengths():
+    rng = np.random.default_rng(62)
+    cache, held = make_cache(rng, "bf16", 64, 16, 1, [30, 30])
+    slots = dev(np.array([[2, 5, -1, -1, -1, -1], [2, 5, -1, -1, -1, -1]], np.int32))
+    acc, lens = dev(np.array([2, 2], np.int32)), dev(np.array([-2, 20], np.int32))
+    new = eb.kv_accept(cache, lens, acc, slots)
+    reported(cache, eb.DEVERR_PREFIX)
+    assert new.tolist() == [-2, 23]
+    k, _ = eb.kv_gather(cache, dev(cu([30, 30])), 60)
+    want = np.concatenate([held[0][0], held[1][0]])
+    want[30 + 21], want[30 + 22] = held[1][0][22], held[1][0][25]
+    assert (k.double().cpu().numpy() == want).all()
+    eb.kv_accept(cache, lens, acc, slots, new_lens=lens)             # in place
+    reported(cache, eb.DEVERR_PREFIX)
+    assert lens.tolist() == [-2, 23]
