@@ -73,6 +73,7 @@ struct KaArgs {
   long long q_ld;
   const unsigned char* mask;
   float scale_log2;                        // scale * log2(e)
+  float vg;                                // the values' global factor (1 with bf16 pages)
   __nv_bfloat16* out;
   long long out_ld;
   float* lse;
@@ -738,8 +739,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         }
         again = bad && live;
       }
-      const float vg = F4 ? a.pool.vg : 1.f;
-      const float inv = l_run == 0.f ? 0.f : vg / l_run;
+      const float inv = l_run == 0.f ? 0.f : a.vg / l_run;
       const bool none = l_run == 0.f;
 #pragma unroll 1
       for (int c0 = 0; c0 < HD; c0 += 32) {
@@ -780,7 +780,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           if (!none) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e] * vg, x[4 * e + 1] * vg, x[4 * e + 2] * vg, x[4 * e + 3] * vg);
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + c0);
@@ -810,7 +810,6 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   if (warp == 1) tmem_dealloc(tmem, 512);
   if (joined) {   // the cluster's ranges, in rank order
     cluster_sync();
-    const float vg = F4 ? a.pool.vg : 1.f;
     for (int x = split * THREADS + tid; x < qv * (HD / 4); x += a.splits * THREADS) {
       const int v = x / (HD / 4), d = 4 * (x - v * (HD / 4));
       float m[KA_MAX_JOIN], M = -INFINITY;
@@ -833,7 +832,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         o.w = fmaf(f, y.w, o.w);
       }
       const bool none = L == 0.f;
-      const float inv = none ? 0.f : vg / L;
+      const float inv = none ? 0.f : a.vg / L;
       const int i = (v0 + v) / a.G, n = rq.row0 + i, h = kvh * a.G + (v0 + v - i * a.G);
       *reinterpret_cast<uint2*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + d) =
           none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
@@ -1205,10 +1204,10 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
     } else if (a.splits > 1) {
       if (!none)
         *reinterpret_cast<float2*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + d) =
-            make_float2(y0 * a.pool.vg, y1 * a.pool.vg);
+            make_float2(y0, y1);
       if (d == 0) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, L);
     } else {
-      const float inv = none ? 0.f : a.pool.vg / L;
+      const float inv = none ? 0.f : a.vg / L;
       *reinterpret_cast<uint32_t*>(a.out + (rq.row0 + i) * a.out_ld + static_cast<long long>(kvh * a.G + v - i * a.G) * HD + d) =
           none ? 0u : pack_bf16(y0 * inv, y1 * inv);
       if (d == 0 && a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(L)) * 0.6931471805599453f;
@@ -1236,7 +1235,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
         y1 = fmaf(f, remote(&s_o[0][d + 1][v], r), y1);
       }
       const bool none = L == 0.f;
-      const float inv = none ? 0.f : a.pool.vg / L;
+      const float inv = none ? 0.f : a.vg / L;
       const int i = v / a.G, n = rq.row0 + i, h = kvh * a.G + (v - i * a.G);
       *reinterpret_cast<uint32_t*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + d) = none ? 0u : pack_bf16(y0 * inv, y1 * inv);
       if (d == 0 && a.lse) a.lse[static_cast<size_t>(n) * a.Hq + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
@@ -1292,7 +1291,9 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
     }
   }
   const bool none = L == 0.f;
-  const float inv = none ? 0.f : 1.f / L;
+  // (the values' global factor last: a range's sum, of p up to 2^15 times values up to 2688, has room
+  // for none of 1e30)
+  const float inv = none ? 0.f : a.vg / L;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = none ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
@@ -1496,6 +1497,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   a.q_ld = w->q_stride;
   a.mask = w->mask;
   a.scale_log2 = (w->scale > 0.f ? w->scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f;
+  a.vg = cache->kind == EAGLE_CACHE_F4 ? a.pool.vg : 1.f;
   a.out = static_cast<__nv_bfloat16*>(w->out);
   a.out_ld = w->out_stride;
   a.lse = w->lse;

@@ -137,6 +137,30 @@ def test_sharp_and_scaled_scores(kind):
     run(np.random.default_rng(6), kind, 128, 32, 1, 4, [300], [2], qscale=1e-18)
 
 
+@pytest.mark.parametrize("vg", [1e30, 1e-30])
+@pytest.mark.parametrize("G,rows,ctx", [(4, 1, 60000), (20, 1, 20000), (4, 61, 12000), (4, 1, 300)])
+def test_extreme_global_factors_of_the_values(vg, G, rows, ctx):
+    """Values of 2688 (code 6, scale 448) times the largest and smallest factor: the same finite
+    answer however the keys are cut into ranges."""
+    rng = np.random.default_rng(18)
+    cache, held = make_cache(rng, "f4", 128, 64, 1, [ctx + rows], k_global=1.0, v_global=vg)
+    vg32 = float(np.float32(vg))
+    sign = np.where(rng.random((1, 1, 128)) < 0.2, -1.0, 1.0)
+    code = np.broadcast_to(np.where(sign > 0, 7, 15), (ctx + rows, 1, 128)).astype(np.uint8)
+    t = np.arange(ctx + rows)
+    pg, r = cache.page_table.cpu().numpy()[0, t // 64], t % 64
+    v, vs = cache.v.cpu().numpy(), cache.v_scale.cpu().numpy()
+    v[pg, :, r], vs[pg, :, r] = code[..., 0::2] | (code[..., 1::2] << 4), 0x7E          # 0x7e: 448
+    cache.v.copy_(dev(v)), cache.v_scale.copy_(dev(vs))
+    V = np.broadcast_to(sign * 2688 * vg32, (ctx + rows, 1, 128))
+    q = K.bf16(rng.standard_normal((rows, G, 128)))
+    out, lse = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu([rows])), dev(np.array([ctx], np.int32)), max_rows=rows,
+                               max_len=ctx + rows, lse=True)
+    assert cache.check() == 0
+    ref = K.attention(q, held[0][0], V, see_matrix(ctx, rows), 128 ** -0.5)
+    check(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, 128)
+
+
 def test_non_finite_values_in_masked_keys():
     """Infinite and NaN keys and values of rows that a row's mask hides do not reach it; a row
     that sees them gets what the sums give."""
