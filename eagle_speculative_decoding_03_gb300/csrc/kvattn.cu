@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -208,6 +209,10 @@ EAGLE_DEV void dequant8(uint32_t code, uint32_t s, uint32_t* h) {
   h[3] = mul_f16x2(e2m1_pair<3>(code), s);
 }
 
+// A vector's score factor, kept within the normal numbers: a factor that fell to 0 would make NaN of
+// a masked score (-inf * 0), one that overflowed of a score of 0.
+EAGLE_DEV float finite_scale(float x) { return fminf(fmaxf(x, FLT_MIN), FLT_MAX); }
+
 // a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
 // registers (the operands of tcgen05.mma)
 EAGLE_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -388,7 +393,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       int ex = static_cast<int>(top >> 7);              // biased exponent of the largest magnitude
       ex = ex == 255 ? 127 : max(ex, 30);               // (infinities and NaN pass; tiny vectors)
       up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
-      row_scale *= __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+      row_scale = finite_scale(row_scale * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23));
     }
 #pragma unroll 1
     for (int c0 = 0; c0 < HD / 8; c0 += 4) {            // 32 dims: 16 packed columns
@@ -995,7 +1000,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
     int ex = static_cast<int>(top >> 7);
     ex = ex == 255 ? 127 : max(ex, 30);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
-    up_scale = a.scale_log2 * a.pool.kg * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+    up_scale = finite_scale(a.scale_log2 * a.pool.kg * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23));
 #pragma unroll
     for (int s = 0; s < ST; ++s)
 #pragma unroll
@@ -1496,7 +1501,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   a.q = static_cast<const __nv_bfloat16*>(w->q);
   a.q_ld = w->q_stride;
   a.mask = w->mask;
-  a.scale_log2 = (w->scale > 0.f ? w->scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f;
+  a.scale_log2 = std::min((w->scale > 0.f ? w->scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f, FLT_MAX);
   a.vg = cache->kind == EAGLE_CACHE_F4 ? a.pool.vg : 1.f;
   a.out = static_cast<__nv_bfloat16*>(w->out);
   a.out_ld = w->out_stride;

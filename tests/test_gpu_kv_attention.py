@@ -161,6 +161,35 @@ def test_extreme_global_factors_of_the_values(vg, G, rows, ctx):
     check(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, 128)
 
 
+@pytest.mark.parametrize("kg,size", [(1e-30, 0.0), (1e-12, 0.0), (1e30, 1e15)])
+@pytest.mark.parametrize("G,rows", [(4, 1), (4, 2), (20, 3), (8, 40)])
+def test_score_factors_that_leave_fp32(kg, size, G, rows):
+    """A zero query over a small factor of the keys, a large query over zero codes and a large factor:
+    every score is 0, and the keys a row does not see stay out of it."""
+    rng = np.random.default_rng(19)
+    ctx = 150
+    cache, held = make_cache(rng, "f4", 64, 16, 1, [ctx + rows], k_global=kg)
+    if size:
+        cache.k.zero_()
+    q = K.bf16(np.full((rows, G, 64), size))
+    out, lse = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu([rows])), dev(np.array([ctx], np.int32)), max_rows=rows,
+                               max_len=ctx + rows, lse=True)
+    assert cache.check() == 0
+    ref = K.attention(q * 0, held[0][0] * 0, held[0][1], see_matrix(ctx, rows), 0.125)
+    check(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, 64)
+
+
+def test_largest_scale():
+    """A scale whose product with log2(e) passes fp32, over zero queries: equal weights."""
+    rng = np.random.default_rng(20)
+    cache, held = make_cache(rng, "bf16", 64, 16, 1, [70])
+    q = np.zeros((3, 4, 64))
+    out, lse = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu([3])), dev(np.array([67], np.int32)), max_rows=3, max_len=70,
+                               scale=3e38, lse=True)
+    ref = K.attention(q, held[0][0] * 0, held[0][1], see_matrix(67, 3), 1.0)
+    check(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, 64)
+
+
 def test_non_finite_values_in_masked_keys():
     """Infinite and NaN keys and values of rows that a row's mask hides do not reach it; a row
     that sees them gets what the sums give."""
