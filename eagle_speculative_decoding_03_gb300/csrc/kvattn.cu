@@ -270,6 +270,69 @@ __host__ __device__ constexpr uint32_t ka_entry(int hd) { return static_cast<uin
 constexpr int KA_RAW = 3;
 __host__ __device__ constexpr uint32_t ka_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_CH + hd / 16 * KA_CH; }
 
+// The keys of a range that one vector sees.
+struct VisibleKeys {
+  const KvPool& pool;
+  int b, kvh, begin, end, ctx, row;
+  bool tree;
+  unsigned long long bits;                 // tree mask row
+  EAGLE_DEV bool see(int k) const {
+    const int j = k - ctx;
+    return k < end && (j < 0 || (tree ? (bits >> j) & 1ull : j <= row));
+  }
+};
+// sum p v over them by a warp, from bf16 pages: lane l takes dims [l hd / 32, (l + 1) hd / 32).  The rare
+// path (non-finite values in the cache), bound by the latency of its loads: 0.9 us a vector and 8 keys
+// (15 ms where a request of 61 rows x 64 heads holds an infinite value among 4,096 keys; a thread
+// per vector took 277).
+template <int HD>
+EAGLE_DEV void visible_sum(const VisibleKeys& keys, const __nv_bfloat16* qp, float row_scale, float m, float* o, int lane, unsigned* err) {
+  constexpr int E = HD / 32, KB = 8;       // keys in flight (of one page)
+  auto load = [&](const __nv_bfloat16* p, float* x) {
+    uint32_t w[E / 2];
+    if constexpr (E == 4) {
+      const uint2 t = *reinterpret_cast<const uint2*>(p + E * lane);
+      w[0] = t.x;
+      w[1] = t.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p + E * lane);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+  };
+  float q[E];
+  load(qp, q);
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  int page = -1;
+  for (int k = keys.begin; k < keys.end; k += KB) {   // (begin is a multiple of the page size)
+    if ((k & ((1 << keys.pool.ps_log) - 1)) == 0) page = kv_page(keys.pool, keys.b, k, err);
+    if (page < 0) continue;                // (reads as zeros)
+    const size_t at = kv_row(keys.pool, page, keys.kvh, k) * HD;
+    float s[KB], kk[KB][E], vv[KB][E];
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {         // (the page is there whole: rows nobody sees are read and dropped)
+      load(static_cast<const __nv_bfloat16*>(keys.pool.k) + at + i * HD, kk[i]);
+      load(static_cast<const __nv_bfloat16*>(keys.pool.v) + at + i * HD, vv[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      s[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[i] = fmaf(q[e], kk[i][e], s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < KB; ++i) s[i] = warp_sum(s[i]);
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      if (!keys.see(k + i)) continue;
+      const float p = fast_exp2(fmaf(s[i], row_scale, -m * row_scale));
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(p, vv[i][e], o[e]);
+    }
+  }
+}
+
 template <int HD, int CACHE, int NB>
 __global__ void __launch_bounds__(ka_threads(CACHE, NB), 1)
 kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const KaArgs a, const int NS) {
@@ -729,10 +792,12 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       tc_fence_after();
       const int n = rq.row0 + irow, h = kvh * a.G + (v - irow * a.G);
       const size_t at = static_cast<size_t>(n) * a.Hq + h;
-      // A non-finite V in a row that the step masks reaches every lane of its tile as 0 * NaN.
-      // Such sums are formed again from the visible keys alone.
-      bool again = false;
-      if (!F4 && T > 0 && (t_begin + T) * KA_CH > rq.ctx) {
+      const bool none = l_run == 0.f;
+      // A non-finite V reaches vectors that have nothing of it: in a row that the step masks as 0 *
+      // NaN, and with p in two parts the lower part (0 or negative) makes NaN of a visible infinity.
+      // Such sums are formed again from the visible keys alone, a vector at a time by the whole warp
+      // (unless the vector's own sum of p is NaN: then so is its output).
+      if (!F4 && T > 0 && (HILO || (t_begin + T) * KA_CH > rq.ctx)) {
         bool bad = false;
 #pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += 32) {
@@ -742,10 +807,32 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 32; ++e) bad |= !(fabsf(x[e]) < INFINITY);
         }
-        again = bad && live;
+        unsigned todo = __ballot_sync(0xffffffffu, bad && live && !none && l_run < INFINITY);
+        for (; todo; todo &= todo - 1) {
+          const int u = __ffs(todo) - 1, ui = __shfl_sync(0xffffffffu, irow, u);
+          const VisibleKeys keys{a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), rq.ctx, ui,
+                                 a.mask != nullptr, __shfl_sync(0xffffffffu, tree_bits, u)};
+          const __nv_bfloat16* qp = a.q + (rq.row0 + ui) * a.q_ld + static_cast<long long>(kvh * a.G + v - lane + u - ui * a.G) * HD;
+          float o[HD / 32];
+          visible_sum<HD>(keys, qp, row_scale, __shfl_sync(0xffffffffu, m_run, u), o, lane, a.err);
+#pragma unroll
+          for (int c0 = 0; c0 < HD; c0 += 32) {   // (the other lanes' sums go back as they were)
+            float x[32];
+            __syncwarp();
+            tmem_ld32(tO + c0, x);
+            tmem_wait_ld();
+            uint32_t y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float mine = __shfl_sync(0xffffffffu, o[(c0 + e) % (HD / 32)], (c0 + e) / (HD / 32));
+              y[e] = __float_as_uint(lane == u ? mine : x[e]);
+            }
+            tmem_st32(tO + c0, y);
+          }
+          tmem_wait_st();
+        }
       }
-      const float inv = l_run == 0.f ? 0.f : a.vg / l_run;
-      const bool none = l_run == 0.f;
+      const float inv = none ? 0.f : a.vg / l_run;
 #pragma unroll 1
       for (int c0 = 0; c0 < HD; c0 += 32) {
         float x[32];
@@ -754,26 +841,6 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         if (T > 0) {
           tmem_ld32(tO + c0, x);
           tmem_wait_ld();
-        }
-        if (again) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0.f;
-          const __nv_bfloat16* qp = a.q + n * a.q_ld + static_cast<long long>(h) * HD;
-          const int k_end = min(rq.len, (t_begin + T) * KA_CH);
-          for (int k = t_begin * KA_CH; k < k_end; ++k) {
-            const int j = k - rq.ctx;
-            if (j >= 0 && !(a.mask ? (tree_bits >> j) & 1ull : j <= irow)) continue;
-            const int page = kv_page(a.pool, b, k, a.err);
-            if (page < 0) continue;
-            const size_t row = kv_row(a.pool, page, kvh, k) * HD;
-            float s = 0.f;
-            for (int d = 0; d < HD; ++d)
-              s = fmaf(__bfloat162float(qp[d]), __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.k)[row + d]), s);
-            const float p = fast_exp2(fmaf(s, row_scale, -m_run * row_scale));
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              x[e] = fmaf(p, __bfloat162float(static_cast<const __nv_bfloat16*>(a.pool.v)[row + c0 + e]), x[e]);
-          }
         }
         if (joined) {
           if (live) {

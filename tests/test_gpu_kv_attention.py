@@ -225,6 +225,63 @@ def test_non_finite_values_in_masked_keys():
     assert np.isnan(out[2, 1]).all() and np.isfinite(np.delete(out.reshape(R * 4, 128), 2 * 4 + 1, 0)).all()
 
 
+@pytest.mark.parametrize("hd,G,rows,ctx,pages", [
+    (128, 4, 1, 100, 16),                    # one range
+    (64, 4, 1, 1500, 64),                    # ranges of a cluster
+    (128, 5, 3, 30000, 64),                  # ranges that the combine kernel joins
+    (128, 8, 40, 700, 32), (64, 16, 20, 260, 128)])   # two query tiles
+def test_visible_non_finite_values_in_cached_keys(hd, G, rows, ctx, pages):
+    """An infinity or a NaN among the cached values reaches its own dim of every row, as the sum has
+    it, and nothing else."""
+    rng = np.random.default_rng(21)
+    cache, held = make_cache(rng, "bf16", hd, pages, 1, [ctx + rows])
+    tab = cache.page_table.cpu().numpy()
+    kk, vv = held[0]
+    for key, dim, val in ((3, 5, np.inf), (ctx // 2, 17, -np.inf), (ctx - 1, 30, np.nan), (1, 63, np.inf), (2, 63, -np.inf)):
+        cache.v[tab[0, key // pages], 0, key % pages, dim] = float(val)
+        vv[key, 0, dim] = 0.0                                      # (the other dims' reference)
+    q = K.bf16(rng.standard_normal((rows, G, hd)))
+    mask = np.tril(np.ones((rows, rows), np.uint8))[None]
+    for m in (None, dev(mask)):
+        out, lse = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu([rows])), dev(np.array([ctx], np.int32)), max_rows=rows,
+                                   max_len=ctx + rows, mask=m, lse=True)
+        assert cache.check() == 0
+        o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        assert (o[..., 5] == np.inf).all() and (o[..., 17] == -np.inf).all() and np.isnan(o[..., [30, 63]]).all()
+        ref = K.attention(q, kk, vv, see_matrix(ctx, rows), hd ** -0.5)
+        rest = np.delete(np.arange(hd), [5, 17, 30, 63])
+        check(o[..., rest], l, (ref[0][..., rest], ref[1], ref[2][..., rest], ref[3], ref[4][..., rest]), hd)
+
+
+def test_a_nan_query_costs_no_second_pass():
+    """NaN queries give NaN rows, in about the time of any others: their sums are not formed again
+    (a walk of one thread over 20,000 keys would take some hundred times the call)."""
+    rng = np.random.default_rng(22)
+    ctx, R, G = 20000, 61, 8
+    cache, _ = make_cache(rng, "bf16", 128, 64, 1, [ctx + R], poison=False)
+    q = torch.randn(R, G, 128, device="cuda").to(torch.bfloat16)
+    bad = q.clone()
+    bad[::7, 3, 9] = float("nan")
+    args = (dev(cu([R])), dev(np.array([ctx], np.int32)))
+    def timed(x):
+        best = float("inf")
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            o = eb.kv_attention(cache, x, *args, max_rows=R, max_len=ctx + R)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best, o
+    t0, good = timed(q)
+    t1, o = timed(bad)
+    assert torch.isnan(o[::7, 3]).all()
+    keep = torch.ones(R, G, dtype=torch.bool, device="cuda")
+    keep[::7, 3] = False
+    assert torch.equal(o[keep], good[keep])
+    assert t1 < 5 * t0 + 0.2, (t0, t1)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_strided_rows_graph_and_streams(kind):
     """q and out as slices of wider rows; the same call replayed from a CUDA graph after the cache
