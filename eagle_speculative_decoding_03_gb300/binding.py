@@ -541,7 +541,7 @@ class EagleDFlash:
 
 # ------------------------------------------------------------- the caller's paged cache
 # These calls run on `stream`, or on torch's current stream where none is given; tensors they
-# allocate belong to that stream.  Tensors must be on the current device.  (The checks take a
+# allocate belong to that stream.  Tensors, caches and streams must be of the current device.  (The checks take a
 # fast path first: a single-token step's calls are as short as their host time.)
 
 def _bad(msg: str):
@@ -558,6 +558,8 @@ def _here(stream):
         import torch
         _torch = torch
     dev = _torch.cuda.current_device()
+    if stream is not None and stream.device_index != dev:
+        _bad("the stream must be of the current CUDA device")
     return _torch, dev, (_torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
@@ -691,6 +693,11 @@ def rotary(x, positions, rope: Rope, out=None, stream=None):
     return out
 
 
+def _cache_here(cache, dev: int):
+    if cache.device_index != dev:
+        _bad("the cache must be on the current CUDA device")
+
+
 class KVCache:
     """Paged keys and values of one layer (eagle_kv_cache_t) over the caller's tensors:
     bf16 [pages, Hkv, page_size, hd], or uint8 codes [pages, Hkv, page_size, hd / 2] with uint8
@@ -710,7 +717,7 @@ class KVCache:
         elif k_scale is not None or v_scale is not None:
             _bad("scales belong to a 4-bit cache")
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
-        self.kind, self.n_kv_heads, self.head_dim = (CACHE_F4 if f4 else CACHE_BF16), H, hd
+        self.kind, self.n_kv_heads, self.head_dim, self.device_index = (CACHE_F4 if f4 else CACHE_BF16), H, hd, dev
         self.err = torch.zeros((1,), dtype=torch.int32, device=k.device)
         self.c = KVCacheC(kind=self.kind, n_kv_heads=H, head_dim=hd, page_size=ps, num_pages=P,
                           max_pages=page_table.shape[1], k=_ptr(k), v=_ptr(v), k_scale=_ptr(k_scale),
@@ -770,6 +777,7 @@ def kv_append(cache: KVCache, k, v, cu_rows, lens, positions=None, rope: Rope | 
 
 
 def _requests(cache: KVCache, cu_rows, lens, dev: int) -> int:
+    _cache_here(cache, dev)
     B = _ints(lens, "lens", None, dev)
     _ints(cu_rows, "cu_rows", B + 1, dev)
     if cache.max_requests < B:
@@ -781,6 +789,7 @@ def kv_gather(cache: KVCache, cu_seqlens, total: int, k_out=None, v_out=None, st
     """The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every request, packed bf16
     [total, Hkv, hd]: the k_cache / v_cache of EagleDraft.tree and EagleVerify.verify."""
     torch, dev, st = _here(stream)
+    _cache_here(cache, dev)
     B, total = _ints(cu_seqlens, "cu_seqlens", None, dev) - 1, int(total)
     if B < 1 or total < 0 or cache.max_requests < B:
         _bad("kv_gather: cu_seqlens needs 1 .. page_table rows requests, total must not be negative")
@@ -806,6 +815,8 @@ def kv_accept(caches, lens, accept_len, accept_slots, new_lens=None, stream=None
     caches = [caches] if isinstance(caches, KVCache) else list(caches)
     if not caches:
         _bad("kv_accept: no caches")
+    for c in caches:
+        _cache_here(c, dev)
     _tensor(accept_slots, "accept_slots", torch.int32, (None, None), dev)
     B, S = accept_slots.shape
     _ints(lens, "lens", B, dev)

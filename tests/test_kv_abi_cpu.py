@@ -194,3 +194,34 @@ def test_buffers_that_calls_write_are_not_shared(lib):
     assert lib.eagle_kv_gather(C.byref(c), 1, P, 8, 5 * P, 5 * P, P, None) == 1
     for new in (2 * P, 3 * P):
         assert lib.eagle_kv_accept(C.byref(c), 1, 1, 4, P, 2 * P, 3 * P, new, P, None) == 1
+
+
+def test_caches_and_streams_of_another_device_are_refused(monkeypatch):
+    """Tensors of the current device beside a cache (or on a stream) of another: refused before the
+    library is reached.  Devices are played here by numbers: CPU tensors are on device -1."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+    at = [-1]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: at[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    def reached():
+        raise AssertionError("the library was reached")
+    monkeypatch.setattr(eb, "load", reached)
+    def pool():
+        return torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    table, one = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    x, cu = pool()[:1, :, 0].contiguous(), torch.tensor([0, 1], dtype=torch.int32)
+    here, there = eb.KVCache(pool(), pool(), table), eb.KVCache(pool(), pool(), table)
+    there.device_index = 1                            # (its own tensors are only looked at when it is made)
+    calls = [lambda c, s: eb.kv_append(c, x, x, cu, one, stream=s), lambda c, s: eb.kv_gather(c, cu, 1, stream=s),
+             lambda c, s: eb.kv_attention(c, x, cu, one, 1, 8, stream=s), lambda c, s: eb.kv_accept(c, one, one, one[None], stream=s),
+             lambda c, s: eb.kv_accept([here, c], one, one, one[None], stream=s)]
+    for f in calls:
+        with pytest.raises(AssertionError, match="library was reached"):
+            f(here, None)
+        with pytest.raises(eb.EagleError, match="cache must be on the current"):
+            f(there, None)
+        with pytest.raises(eb.EagleError, match="stream must be of the current"):
+            f(here, SimpleNamespace(cuda_stream=0, device_index=0))
+    with pytest.raises(eb.EagleError, match="stream must be of the current"):
+        eb.rotary(x, one, eb.Rope(64), stream=SimpleNamespace(cuda_stream=0, device_index=0))
