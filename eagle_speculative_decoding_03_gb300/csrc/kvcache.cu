@@ -64,8 +64,8 @@ constexpr int RT_THREADS = 256;
 constexpr int RT_WARPS = RT_THREADS / 32;
 constexpr int RT_MAX_PAIRS = 128;            // rot_dim <= 256
 
-// inv_freq as fractions of a turn in 64-bit fixed point: position * turn[i] mod 2^64 is the
-// angle's fraction of a turn, exact but for |position| 2^-65 turns.
+// inv_freq as fractions of a turn in 64-bit fixed point, to the nearest: position * turn[i] mod 2^64
+// is the angle's fraction of a turn, exact but for |position| 2^-65 turns.
 struct RopeTab {
   unsigned long long turn[RT_MAX_PAIRS];
   int pairs;                                 // rot_dim / 2 (0: no rotation)
@@ -233,8 +233,20 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
     const int r = i / rt.pairs, j = i - r * rt.pairs;
     if (row0 + r < a.N) {
       const unsigned long long ph = static_cast<unsigned long long>(static_cast<long long>(__ldg(a.positions + row0 + r))) * rt.turn[j];
+      // the nearest quarter turn and what is left of it, at most an eighth: only that is rounded to fp32
+      const unsigned long long up = ph + (1ull << 61);
+      const long long left = static_cast<long long>(up & ((1ull << 62) - 1)) - (1ll << 61);
       float s, c;
-      sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 4.656612873077393e-10f, &s, &c);   // half turns: 2^-31
+      sincospif(__ll2float_rn(left) * 1.0842021724855044e-19f, &s, &c);   // half turns: 2^-63
+      if ((up >> 62) & 1) {
+        const float t = s;
+        s = c;
+        c = -t;
+      }
+      if (up >> 63) {
+        s = -s;
+        c = -c;
+      }
       cs[r][j] = make_float2(c * rt.amp, s * rt.amp);
     }
   }
@@ -538,6 +550,7 @@ __global__ void keep_lens_kernel(const KeepArgs a) {
   a.new_lens[b] = a.lens[b] + 1 + j;
 }
 
+constexpr double INV_2PI = 0.15915494309189535, INV_2PI_LOW = -9.839338337591243e-18;   // 1 / (2 pi) = their sum
 eagle_status_t rope_table(const eagle_rope_t* r, int hd, const char* who, RopeTab* t) {
   memset(t, 0, sizeof(*t));
   if (!r) return EAGLE_OK;
@@ -553,9 +566,11 @@ eagle_status_t rope_table(const eagle_rope_t* r, int hd, const char* who, RopeTa
   for (int i = 0; i < t->pairs; ++i) {
     const double f = r->inv_freq ? r->inv_freq[i] : std::pow(r->theta, -2.0 * i / r->rot_dim);
     if (!std::isfinite(f) || f < 0.0 || f > 1e6) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: inv_freq must lie in [0, 1e6]", who);
-    const double turns = f / 6.283185307179586476925286766559;
-    const double frac = turns - std::floor(turns);      // whole turns per position change nothing
-    t->turn[i] = static_cast<unsigned long long>(std::ldexp(frac, 64) < 18446744073709551616.0 ? std::ldexp(frac, 64) : 0.0);
+    // f / (2 pi) to twice a double's bits, then its fraction to 64
+    const double turns = f * INV_2PI, low = std::fma(f, INV_2PI_LOW, std::fma(f, INV_2PI, -turns));
+    const double frac = std::ldexp(turns - std::floor(turns), 64);   // whole turns per position change nothing
+    const double whole = std::floor(frac);
+    t->turn[i] = static_cast<unsigned long long>(whole) + static_cast<unsigned long long>(std::llrint(frac - whole + std::ldexp(low, 64)));
   }
   return EAGLE_OK;
 }

@@ -509,7 +509,8 @@ typedef struct {
 
 /* Rotary positions: the first rot_dim dims of a head are rotated in pairs by the angle
  * position * inv_freq[i], scaled by `amplitude`; the others are copied.  Angles are formed
- * as exact fractions of a turn (64-bit fixed point), so far positions lose nothing. */
+ * as fractions of a turn in 64-bit fixed point (off by at most |position| 2^-65 turns), and cos
+ * and sin are taken of the distance to the nearest quarter turn, so far positions lose nothing. */
 typedef struct {
   int32_t rot_dim;            /* multiple of 16, <= head_dim */
   int32_t interleaved;        /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */

@@ -72,6 +72,44 @@ def test_rotary_scaled_frequencies_amplitude_and_strides():
     assert eb.rotary(x[:0], dev(pos[:0].astype(np.int32)), rope).shape == (0, 5, 128)
 
 
+def turn_fractions(pos, w):
+    """pos * w / (2 pi) as (nearest quarter turn mod 4, signed rest in turns), to 40 digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    q, r = np.zeros((len(pos), len(w)), int), np.zeros((len(pos), len(w)))
+    for i, p in enumerate(pos):
+        for j, f in enumerate(w):
+            t = Decimal(int(p)) * Decimal(float(f)) / turn * 4
+            k = t.to_integral_value()
+            q[i, j], r[i, j] = int(k) % 4, float(t - k) / 4
+    return q, r
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("theta,far", [(1e4, 5000), (5e5, 10 ** 6), (5e5, 2 ** 31 - 1)])
+def test_angles_keep_their_precision_at_any_position(inter, theta, far):
+    """The cosine and sine themselves (rows of ones and zeros), relative to their own size.  An angle is
+    rounded once, as a distance t of at most an eighth of a turn from a quarter: 2^-24 t, which is at
+    most 2^-24 of the sine (t <= tan t) and of the cosine; sincospif is off by an ulp, 2^-23.  With a
+    rounding to spare 2^-22 relative, and |position| 2^-65 turns from the fixed point."""
+    rng = np.random.default_rng(70)
+    w = eb.rope_frequencies(32, theta)
+    pos = np.concatenate([rng.integers(far // 2, far, 250, endpoint=True), -rng.integers(far // 2, far, 50), [0, 1, far]])
+    x = torch.zeros(len(pos), 1, 32, device="cuda")
+    i = np.arange(16)
+    a, b = (2 * i, 2 * i + 1) if inter else (i, i + 16)
+    x[:, 0, a] = 1.0
+    y = eb.rotary(x, dev(pos.astype(np.int32)), eb.Rope(32, theta=theta, interleaved=inter)).double().cpu().numpy()[:, 0]
+    q, r = turn_fractions(pos, w)
+    c, s = np.cos(2 * np.pi * r), np.sin(2 * np.pi * r)
+    cos, sin = np.choose(q, [c, -s, -c, s]), np.choose(q, [s, c, -s, -c])
+    slack = 2 * np.pi * np.abs(pos)[:, None] * 2.0 ** -64 + 1e-37
+    for got, ref in ((y[:, a], cos), (y[:, b], sin)):
+        tol = 2.0 ** -22 * np.abs(ref) + slack
+        assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) / tol).max())
+
+
 def test_rotary_of_the_longest_row():
     """2^31 - 128 elements in one row: its first and last heads are what they are alone."""
     H = (1 << 24) - 1
