@@ -557,8 +557,9 @@ EAGLE_API eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t 
 
 /* After a verification: request b's tree of S slots was appended behind its lens[b] keys in
  * slot order (root first).  Keeps the root and the accept_len[b] accepted slots
- * accept_slots[b][..] (strictly ascending, as eagle_verify_tree and eagle_speculative_accept
- * write them; slot 0, the root's, may be among them): slot accept_slots[b][j] moves to key
+ * accept_slots[b][..] (at most S - 1, strictly ascending, as eagle_verify_tree and
+ * eagle_speculative_accept write them; a path that names slot 0 too keeps the root a second
+ * time; a longer path is cut and flagged): slot accept_slots[b][j] moves to key
  * lens[b] + 1 + j in every one of the n_caches caches (HOST array, 1..64, e.g. one per layer;
  * all of one shape, of caches[0]'s page table and each with its own pool), and
  * new_lens[b] = lens[b] + 1 + accept_len[b] (new_lens may be lens, but may not overlap the path). */

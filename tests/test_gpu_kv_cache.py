@@ -273,6 +273,20 @@ def test_accept(kind, hd, ps, Hkv, layers):
     assert same is lens_t and lens_t.cpu().tolist() == [n + 1 for n in lens]
 
 
+def test_accept_cuts_paths_of_more_than_the_tree_without_its_root():
+    """S slots, the root's among them, and a tree of its root alone: S - 1 are kept, and reported."""
+    for S in (1, 4):
+        cache, held = make_cache(np.random.default_rng(63), "bf16", 64, 16, 1, [30])
+        new = eb.kv_accept(cache, dev(np.array([20], np.int32)), dev(np.array([S], np.int32)), dev(np.arange(S, dtype=np.int32)[None]))
+        with pytest.raises(eb.EagleError) as e:
+            cache.check()
+        assert "0x4" in str(e.value) and new.tolist() == [20 + S]
+        k, _ = eb.kv_gather(cache, dev(cu([30])), 30)
+        want = held[0][0].copy()
+        want[21:20 + S] = held[0][0][20:19 + S]
+        assert (k.double().cpu().numpy() == want).all()
+
+
 def test_accept_refuses_paths_that_do_not_ascend():
     rng = np.random.default_rng(8)
     cache, held = make_cache(rng, "bf16", 64, 16, 1, [30, 30, 30])
