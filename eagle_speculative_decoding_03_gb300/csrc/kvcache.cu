@@ -179,6 +179,7 @@ EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, f
     const float b = copysignf(__fadd_rn(__fmaf_rn(fabsf(y[e + 1]), inv, 48.f), -48.f), y[e + 1]);
     q |= e2m1x2(a, b) << (4 * e);
   }
+  if (!(unit > 0.f)) q = 0u;                 // (of a scale of 0 the codes are 0, not the codes of -0)
   if (live) {
     *reinterpret_cast<uint32_t*>(code) = q;
     if (even) *scale = static_cast<uint8_t>(s);

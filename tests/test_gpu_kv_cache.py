@@ -600,3 +600,12 @@ def test_accept_reports_negative_lengths():
     eb.kv_accept(cache, lens, acc, slots, new_lens=lens)             # in place
     reported(cache, eb.DEVERR_PREFIX)
     assert lens.tolist() == [-2, 23]
+
+
+def test_four_bit_groups_of_scale_zero_are_zeros():
+    """Values whose scale rounds to 0, of either sign: codes and scales are 0."""
+    cache = eb.KVCache.empty(2, 16, 1, 64, dev(np.zeros((1, 1), np.int32)), four_bit=True, k_global=64.0, v_global=50.1)
+    x = torch.full((4, 1, 64), -0.01, device="cuda").to(torch.bfloat16)
+    eb.kv_append(cache, x, x, dev(cu([4])), dev(np.array([0], np.int32)))
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        assert (t == 0).all()
