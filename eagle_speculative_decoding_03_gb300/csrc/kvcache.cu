@@ -138,17 +138,30 @@ EAGLE_DEV float max_nan2(float x, float y) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
 }
+// Of the codes `less` and `more` on either side of `border` (in units of `unit`, whose product with it is
+// exact) the one of x: nearest, the even code where x lies on it.
+EAGLE_DEV uint32_t nearer(float x, uint32_t less, uint32_t more, float border, double unit) {
+  const double m = static_cast<double>(border) * unit, v = static_cast<double>(x);
+  return v > m || (v == m && (more & 1u) == 0u) ? more : less;
+}
 // 8 dims of a cached row in 4 bits; the 16-dim group's other half is in lane ^ 1.  `w` holds them
 // as bf16: the scale and the codes depend on the stored precision alone and not on how the rotation
 // was rounded.  Called by whole warps; `live` lanes store.
 //
-// Quotients are products with reciprocals, then rounded to fewer bits so that a quotient that lies
-// on a border between two codes lies on it exactly (an IEEE division each took half the kernel's
-// time):
+// Quotients are products with reciprocals (an IEEE division each took half the kernel's time), so one
+// next to a border between two codes needs care.  With a power of two as global factor it is enough
+// to round the quotient to fewer bits, so that one that lies on a border lies on it exactly:
 //   scale: largest / (6 global) to 18 bits (Veltkamp's splitting; borders have 5);
 //   code:  value / unit, off by less than 2^-19 up to 6, to multiples of 2^-18 (adding and taking
 //          away 48; borders are multiples of 1/4, and a bf16 value over a 4-bit scale that is not
 //          on one is 2^-11 or more away).
+// With another factor a quotient may lie as close to a border as it likes.  Rounded like this it still
+// never crosses one; where one meets a multiple of 1/4 (the scale's: where the codes of a little less
+// and a little more differ) the warp compares its values with the borders themselves, whose products
+// with the scale and the factor have at most 32 bits (exact in a double; rare, but for zeros and for a
+// factor that is a simple multiple of a bf16 value).  POW2: both factors are powers of two; the two forms in one
+// kernel cost append_prompt_f4's append 51 us where it takes 46, other factors take 49.
+template <bool POW2>
 EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, float inv6, bool live, bool even) {
   float y[8];
   unpack8(Raw8<__nv_bfloat16>{{w.x, w.y, w.z, w.w}}, y);
@@ -166,18 +179,39 @@ EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, f
   }
   float ratio = fminf(__fmul_rn(top, inv6), 1024.f);   // (past 448 the scale saturates)
   const float cut = __fmul_rn(ratio, 65.f);
-  ratio = __fsub_rn(cut, __fsub_rn(cut, ratio));
-  const uint32_t s = f32_to_e4m3(ratio);
-  const float unit = e4m3_to_f32(s) * global;
-  float inv;
+  uint32_t s = f32_to_e4m3(__fsub_rn(cut, __fsub_rn(cut, ratio)));
+  float unit = e4m3_to_f32(s) * global, inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(unit));
   if (!(unit > 0.f)) inv = 0.f;
-  uint32_t q = 0;
+  uint32_t q = 0, near = 0xFFFFu;
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
-    const float a = copysignf(__fadd_rn(__fmaf_rn(fabsf(y[e]), inv, 48.f), -48.f), y[e]);
-    const float b = copysignf(__fadd_rn(__fmaf_rn(fabsf(y[e + 1]), inv, 48.f), -48.f), y[e + 1]);
-    q |= e2m1x2(a, b) << (4 * e);
+    const float r0 = __fmaf_rn(fabsf(y[e]), inv, 48.f), r1 = __fmaf_rn(fabsf(y[e + 1]), inv, 48.f);
+    if (!POW2) near = min(near, min(__float_as_uint(r0) & 0xFFFFu, __float_as_uint(r1) & 0xFFFFu));   // (0: a multiple of 1/4)
+    q |= e2m1x2(copysignf(__fadd_rn(r0, -48.f), y[e]), copysignf(__fadd_rn(r1, -48.f), y[e + 1])) << (4 * e);
+  }
+  if constexpr (!POW2) {
+    const uint32_t less = f32_to_e4m3(ratio * (1.f - 0x1p-20f)), more = f32_to_e4m3(ratio * (1.f + 0x1p-20f));
+    const bool pow2 = (__float_as_uint(global) & 0x7FFFFFu) == 0u;   // (of this tensor alone)
+    if (__any_sync(0xffffffffu, !pow2 && (near == 0u || less != more))) {
+      if (less != more) s = nearer(top, less, more, 0.5f * (e4m3_to_f32(less) + e4m3_to_f32(more)), 6.0 * static_cast<double>(global));
+      const double step = static_cast<double>(e4m3_to_f32(s)) * static_cast<double>(global);
+      unit = static_cast<float>(step);
+      inv = unit > 0.f ? 1.f / unit : 0.f;
+      q = 0;
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {          // (one value at a time: the kernel holds this block eight times)
+        const uint32_t pair = e & 4 ? (e & 2 ? w.w : w.z) : (e & 2 ? w.y : w.x);
+        const float x = __uint_as_float(e & 1 ? pair & 0xFFFF0000u : pair << 16), mag = x == x ? fabsf(x) : 0.f, t = mag * inv;
+        const uint32_t both = e2m1x2(t * (1.f - 0x1p-20f), t * (1.f + 0x1p-20f));
+        uint32_t c = both & 15u;
+        if (c != both >> 4) {
+          const float2 f = e2m1_pair_f32(both);
+          c = nearer(mag, c, both >> 4, 0.5f * (f.x + f.y), step);
+        }
+        q |= (x == x ? c | (__float_as_uint(x) >> 31) << 3 : 0u) << (4 * e);
+      }
+    }
   }
   if (!(unit > 0.f)) q = 0u;                 // (of a scale of 0 the codes are 0, not the codes of -0)
   if (live) {
@@ -193,8 +227,9 @@ EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, f
 // once into shared memory; a warp keeps one row's in registers over all the heads it takes.
 // CACHE: 0 eagle_rotary, else eagle_cache_kind_t.  Bound by bytes where there are many rows
 // (8,191 x 64 fp32 heads: 85 us, 92% of the measured copy rate); with 4-bit stores by issue and the
-// chain that finds a row's place (8,188 rows, 48 heads: 44 us, 176 MB).
-template <typename T, int CACHE>
+// chain that finds a row's place (8,188 rows, 48 heads: 44 us, 176 MB).  POW2: the 4-bit cache's global
+// factors are powers of two.
+template <typename T, int CACHE, bool POW2>
 __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, const RopeTab rt) {
   __shared__ float2 cs[RT_WARPS][RT_MAX_PAIRS];
   __shared__ int s_page[RT_WARPS], s_tok[RT_WARPS], s_req[RT_WARPS];
@@ -318,7 +353,7 @@ __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, con
       if constexpr (PART == 2 && sizeof(T) == 2) w = make_uint4(raw.w[0], raw.w[1], raw.w[2], raw.w[3]);
       else w = pack8(y);
       const float global = PART == 1 ? a.pool.kg : a.pool.vg;
-      store8_f4(static_cast<uint8_t*>(PART == 1 ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
+      store8_f4<POW2>(static_cast<uint8_t*>(PART == 1 ? a.pool.k : a.pool.v) + row * (a.hd >> 1) + 4 * o,
                 static_cast<uint8_t*>(PART == 1 ? a.pool.ks : a.pool.vs) + row * (a.hd >> 4) + (o >> 1), w, global,
                 PART == 1 ? inv6k : inv6v, live && page >= 0, (o & 1) == 0);
     }
@@ -590,12 +625,12 @@ void rotate_shape(RotArgs* a) {
   a->slices = static_cast<int>(std::min<long long>(most, std::max<long long>(1, 4ll * sms / std::max(1ll, ctas))));
 }
 
-template <int CACHE>
+template <int CACHE, bool POW2 = true>
 eagle_status_t launch_rotate(RotArgs& a, const RopeTab& rt, int dtype, const char* who, cudaStream_t st) {
   rotate_shape(&a);
   const dim3 grid((a.N + a.rows_per_cta - 1) / a.rows_per_cta, a.slices);
-  if (dtype == EAGLE_DTYPE_BF16) rotate_kernel<__nv_bfloat16, CACHE><<<grid, RT_THREADS, 0, st>>>(a, rt);
-  else rotate_kernel<float, CACHE><<<grid, RT_THREADS, 0, st>>>(a, rt);
+  if (dtype == EAGLE_DTYPE_BF16) rotate_kernel<__nv_bfloat16, CACHE, POW2><<<grid, RT_THREADS, 0, st>>>(a, rt);
+  else rotate_kernel<float, CACHE, POW2><<<grid, RT_THREADS, 0, st>>>(a, rt);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }
@@ -695,8 +730,10 @@ extern "C" eagle_status_t eagle_kv_append(const eagle_kv_cache_t* cache, const e
   a.lens = w->lens;
   a.err = err_word;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cache->kind == EAGLE_CACHE_BF16 ? launch_rotate<EAGLE_CACHE_BF16>(a, rt, w->dtype, who, st)
-                                         : launch_rotate<EAGLE_CACHE_F4>(a, rt, w->dtype, who, st);
+  if (cache->kind == EAGLE_CACHE_BF16) return launch_rotate<EAGLE_CACHE_BF16>(a, rt, w->dtype, who, st);
+  int e;
+  const bool pow2 = std::frexp(cache->k_global, &e) == 0.5f && std::frexp(cache->v_global, &e) == 0.5f;
+  return pow2 ? launch_rotate<EAGLE_CACHE_F4>(a, rt, w->dtype, who, st) : launch_rotate<EAGLE_CACHE_F4, false>(a, rt, w->dtype, who, st);
 }
 
 extern "C" eagle_status_t eagle_kv_gather(const eagle_kv_cache_t* cache, int32_t B, const int32_t* cu_seqlens, int32_t total,

@@ -609,3 +609,35 @@ def test_four_bit_groups_of_scale_zero_are_zeros():
     eb.kv_append(cache, x, x, dev(cu([4])), dev(np.array([0], np.int32)))
     for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
         assert (t == 0).all()
+
+
+def test_four_bit_store_next_to_the_borders():
+    """Global factors that put a scale's or a code's quotient within fp32's last places of a border
+    between two codes, on either side and on it: scales and codes are the definition's."""
+    rng = np.random.default_rng(64)
+    n, H, hd = 32, 1, 64
+    table, P = pages(rng, [n], 32)
+    mids = (K.E4M3[1:] + K.E4M3[:-1]) / 2
+    halves = (K.E2M1[1:] + K.E2M1[:-1]) / 2
+    for trial in range(120):
+        top = float(K.bf16(np.exp2(rng.uniform(-3, 3, 1)))[0])
+        if trial % 2:      # a scale's quotient, top / (6 g), beside the middle of two scales
+            g = np.float32(top / (6.0 * rng.choice(mids[mids > 2.0 ** -7])))
+        else:              # a value's, x / (scale g), beside the middle of two codes
+            g = np.float32(top / (rng.choice(halves) * rng.choice(K.E4M3[8:])))
+        for step in (-1, 0, 1):
+            glob = float(np.nextafter(g, np.float32(step * np.inf))) if step else float(g)
+            x = rng.standard_normal((n, H, hd)) * top / 4
+            x[:, :, 0] = top
+            x[::2, :, 16:32] *= 2.0 ** -3
+            if trial % 2 == 0:                                  # groups whose largest is another: the scale varies
+                x[:, 0, 1] = top * np.exp2(rng.uniform(0, 4, n))
+            x = K.bf16(x)
+            cache = eb.KVCache.empty(P, 32, H, hd, dev(table), four_bit=True, k_global=glob, v_global=glob)
+            t = dev(x, torch.bfloat16)
+            eb.kv_append(cache, t, t, dev(cu([n])), dev(np.array([0], np.int32)))
+            got = held_rows(cache, table, 0, n, 32)
+            code, sc, _ = K.quantise(x, glob)
+            for i in (0, 1):
+                assert (got[2 + i] == sc).all(), (trial, glob, np.argwhere(got[2 + i] != sc)[:4])
+                assert (got[i] == pack_codes(code)).all(), (trial, glob, np.argwhere(got[i] != pack_codes(code))[:4])
