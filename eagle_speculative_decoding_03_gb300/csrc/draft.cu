@@ -469,7 +469,7 @@ static eagle_status_t run_gemm(eagle_draft* h, GemmPlan& p, int N, cudaStream_t 
   const EpiKind ek = static_cast<EpiKind>(p.args.e.kind);
   if (p.tc && p.args.b_tma && N > MAX_ROWS_PER_BLOCK && N <= 2 * MAX_ROWS_PER_BLOCK &&
       (ek == EPI_STORE || ek == EPI_QKV || ek == EPI_SWIGLU || ek == EPI_LOGITS)) {
-    // up to 256 rows: one launch of CTA pairs, each weight stage loaded once for both halves
+    // up to 256 rows: one launch of CTA pairs, the halves' CTAs side by side on each weight tile
     GemmPlan q = p;
     if (plan_gemm_pair(q, N, part_half())) {
       ProfScope ps(h, kind, st);

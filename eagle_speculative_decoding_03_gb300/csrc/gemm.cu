@@ -681,17 +681,18 @@ constexpr uint32_t TC_SMEM_OCC2 = 113 * 1024;   // two CTAs per SM
 // NT = TC_THREADS (converter warps present, one CTA per SM) or 7 warps (operand by TMA only;
 // MINB = 1: the whole register file, MINB = 2: two CTAs per SM).
 //
-// PAIR: a cluster of two CTAs on the same (tile, K block) units, rank r on its own rows (its
-// own argument block g_r and operand map tmB_r): rank 0 loads each weight stage once, by TMA
-// multicast into both CTAs; each CTA's MMA commits release the stage in both, so a stage is
-// refilled only when both have consumed it.
+// PAIR: neighbouring CTAs 2 i and 2 i + 1 take the same (tile, K block) units, each on its own rows (its
+// own argument block g_r and operand map tmB_r) and with its own load of each weight stage; the
+// second of the two loads finds the stage in L2.  (One load for both, by cluster multicast, took
+// the B=32 tree 5.09 ms where this takes 5.14; a library that also runs on machines of several
+// GPUs does without such loads.)
 template <int NT, int MINB, bool SEG, bool PAIR = false>
 __global__ void __launch_bounds__(NT, MINB)
 gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ GemmArgs g0,
                const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ GemmArgs g1) {
   uint32_t crank = 0;
-  if (PAIR) crank = cooperative_groups::this_cluster().block_rank();
+  if (PAIR) crank = blockIdx.x & 1u;
   const GemmArgs& g = (PAIR && crank) ? g1 : g0;
   const CUtensorMap& tmB = (PAIR && crank) ? tmB1 : tmB0;
   const int cta = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);   // schedule index
@@ -731,7 +732,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(bar_full + 8 * s, 2);            // weight bytes + activation (TMA bytes or converter)
-      mbar_init(bar_empty + 8 * s, PAIR ? 2 : 1);   // tcgen05.commit (of both CTAs of a pair)
+      mbar_init(bar_empty + 8 * s, 1);           // tcgen05.commit
       mbar_init(bar_bfull + 8 * s, 1);           // bulk-copy bytes of the source rows
     }
     for (int b = 0; b < 2; ++b) {
@@ -753,7 +754,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (PAIR) cooperative_groups::this_cluster().sync();   // both CTAs' barriers exist before any remote use
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
 
@@ -780,16 +780,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
               if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, g.err, abort_flag, wlim)) { ok = false; break; }
               const uint32_t dst = sbase + stage * L.stage_bytes;
               mbar_arrive_expect_tx(bar_full + 8 * stage, nk * A_STAGE_BYTES);
-              for (int u = 0; u < nk && (!PAIR || crank == 0); ++u) {
+              for (int u = 0; u < nk; ++u) {
                 const uint32_t du = dst + u * A_STAGE_BYTES;
-                if (PAIR) {      // one load, into both CTAs of the pair
-                  if (g.a_pair) {
-                    tma_load_2d_mc(du, &tm0, (kb + u) * BK, mrow, bar_full + 8 * stage, pol, 3);
-                    tma_load_2d_mc(du + A_STAGE_BYTES / 2, &tm1, (kb + u) * BK, mrow, bar_full + 8 * stage, pol, 3);
-                  } else {
-                    tma_load_2d_mc(du, tm, (kb + u) * BK, mrow, bar_full + 8 * stage, pol, 3);
-                  }
-                } else if (g.a_pair) {  // rows 0-63 from map 0 (gate), rows 64-127 from map 1 (up)
+                if (g.a_pair) {  // rows 0-63 from map 0 (gate), rows 64-127 from map 1 (up)
                   tma_load_2d(du, &tm0, (kb + u) * BK, mrow, bar_full + 8 * stage, pol);
                   tma_load_2d(du + A_STAGE_BYTES / 2, &tm1, (kb + u) * BK, mrow, bar_full + 8 * stage, pol);
                 } else {
@@ -807,13 +800,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
         // let copies already issued land before the CTA releases its shared memory
         const long long t0 = clock64();
         while (clock64() - t0 < 4000000) {
-        }
-      } else if (PAIR) {
-        // every stage released once more: all of both CTAs' commits (remote arrivals on this
-        // CTA's barriers) have landed before the pair's closing cluster barrier
-        for (int s = 0; s < g.stages && ok; ++s) {
-          ok = mbar_wait(bar_empty + 8 * stage, phase ^ 1, g.err, abort_flag, wlim);
-          if (++stage == g.stages) { stage = 0; phase ^= 1; }
         }
       }
     }
@@ -851,8 +837,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   #pragma unroll
                 for (int j = 0; j < BK / 16; ++j)   // 16 bf16 of K = 32 bytes = 2 descriptor units
                   tc_mma_bf16(d, ad + 2 * j, bd + 2 * j, idesc, (kb > kb0 || j > 0) ? 1u : 0u);
-                if (PAIR) tc_commit_mc(bar_empty + 8 * stage, 3);
-                else tc_commit(bar_empty + 8 * stage);
+                tc_commit(bar_empty + 8 * stage);
                 if (++stage == g.stages) { stage = 0; phase ^= 1; }
               }
             }
@@ -870,8 +855,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
                 for (int j = 0; j < BK / 16; ++j)
                   tc_mma_bf16(d, ad + astep2 + 2 * j, bd + bstep2 + 2 * j, idesc, 1u);
               }
-              if (PAIR) tc_commit_mc(bar_empty + 8 * stage, 3);
-              else tc_commit(bar_empty + 8 * stage);
+              tc_commit(bar_empty + 8 * stage);
               if (++stage == g.stages) { stage = 0; phase ^= 1; }
               kb += 2;
             }
@@ -1258,7 +1242,6 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
     tc_fence_after();
     tmem_dealloc(tmem, g.tmem_cols);
   }
-  if (PAIR) cooperative_groups::this_cluster().sync();   // neither CTA leaves while the other may signal it
 }
 
 // ============================================================ SIMT mainloop (f32)
@@ -1640,13 +1623,12 @@ cudaError_t launch_gemm(const GemmPlan& p, cudaStream_t st, bool pdl) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.tc && (p.args.csplit > 1 || p.pair) ? 2 : 1;
+  cfg.numAttrs = p.tc && p.args.csplit > 1 ? 2 : 1;
   cfg.stream = st;
   cfg.dynamicSmemBytes = p.smem;
   if (p.tc) {
     cfg.gridDim = dim3(p.grid, 1, 1);
-    if (p.pair) {   // clusters of two CTAs sharing the weight stream
-      attr[1].val.clusterDim.x = 2;
+    if (p.pair) {
       cfg.blockDim = dim3(TC_THREADS_TMA, 1, 1);
       return cudaLaunchKernelEx(&cfg, gemm_tc_kernel<TC_THREADS_TMA, 1, false, true>, p.tm0, p.tm1, p.tmB, p.args,
                                 p.tmB1, p.args1);

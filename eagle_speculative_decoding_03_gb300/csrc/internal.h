@@ -21,7 +21,7 @@ struct GemmPlan {
   size_t smem = 0;
   int occ = 1;                   // tc with TMA operand: 2 = two CTAs per SM (smaller ring)
   bool stream_k = false;         // force the stream-K schedule (no per-tile CTA clusters)
-  // pair: clusters of two CTAs sharing the weight stream, rank 1 on the rows of args1 / tmB1
+  // pair: two neighbouring CTAs per weight tile, the second on the rows of args1 / tmB1
   bool pair = false;
   GemmArgs args1{};
   CUtensorMap tmB1;

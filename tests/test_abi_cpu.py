@@ -127,3 +127,14 @@ def test_noalloc_binding_rejects_wrong_dtypes(lib):
         with pytest.raises(eb.EagleError) as ei:
             eb.lm_head_topk_noalloc(w, a, 2)
         assert ei.value.status == eb.EAGLE_ERR_INVALID_ARG
+
+
+def test_no_bulk_load_with_cluster_multicast():
+    """The library also runs as one replica per GPU on machines of several: its tiles are loaded by
+    plain TMA, each CTA its own."""
+    import glob
+    from eagle_speculative_decoding_03_gb300 import build
+    files = glob.glob(os.path.join(build.CSRC, "*"))
+    assert len(files) >= 10
+    for f in files:
+        assert ".multicast::cluster" not in open(f).read(), f
