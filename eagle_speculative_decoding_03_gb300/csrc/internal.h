@@ -37,6 +37,11 @@ bool plan_gemm_pair(GemmPlan& p, int N, size_t part_half);
 cudaError_t allow_max_smem(const void* func, size_t* granted = nullptr);
 size_t max_dyn_smem(const void* func);
 
+// cuTensorMapEncodeTiled of the loaded driver (null: not there)
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
 bool make_weight_map(CUtensorMap* tm, const void* w, int M, int K, int box_rows = BM);
 // 3-D map over a bf16 prefix cache [tokens][Hkv][128]: boxes of 64 tokens x 64 dims of one
 // KV head, 128-byte swizzle (the attention kernel's key / value tiles).

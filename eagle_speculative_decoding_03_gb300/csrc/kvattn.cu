@@ -29,19 +29,8 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 // 3-D map over a paged bf16 cache [pages * Hkv][page_size][hd]: boxes of one page's rows of one
 // KV head x 64 dims, 128-byte swizzle; rows outside the page or the pool read as zeros.
 bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static std::atomic<Encode> known{nullptr};
-  Encode fn = known.load();
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<Encode>(p);
-    known.store(fn);
-  }
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(hd) * 2 * page_size};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
@@ -145,12 +134,7 @@ EAGLE_DEV uint32_t ka_sw(int r, int c) {
 EAGLE_DEV void st_smem16(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
-// the larger of two, NaN if either is: a NaN score must reach the output
-EAGLE_DEV float max_nan(float x, float y) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-  return r;
-}
+// the largest of three, NaN if any is: a NaN score must reach the output
 EAGLE_DEV float max3_nan(float x, float y, float z) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -172,11 +156,6 @@ EAGLE_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
                : "memory");
-}
-EAGLE_DEV uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 EAGLE_DEV uint32_t pack_f16(float lo, float hi) {
   uint32_t r;

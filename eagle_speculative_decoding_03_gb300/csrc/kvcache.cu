@@ -121,23 +121,13 @@ EAGLE_DEV void unpack8(const Raw8<__nv_bfloat16>& r, float* x) {
     x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
   }
 }
-EAGLE_DEV uint32_t pack2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
 EAGLE_DEV void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-EAGLE_DEV uint4 pack8(const float* x) { return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])); }
+EAGLE_DEV uint4 pack8(const float* x) { return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])); }
 EAGLE_DEV void store8(__nv_bfloat16* p, const float* x) { *reinterpret_cast<uint4*>(p) = pack8(x); }
 
-EAGLE_DEV float max_nan2(float x, float y) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-  return r;
-}
 // Of the codes `less` and `more` on either side of `border` (in units of `unit`, whose product with it is
 // exact) the one of x: nearest, the even code where x lies on it.
 EAGLE_DEV uint32_t nearer(float x, uint32_t less, uint32_t more, float border, double unit) {
@@ -165,9 +155,9 @@ template <bool POW2>
 EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, float inv6, bool live, bool even) {
   float y[8];
   unpack8(Raw8<__nv_bfloat16>{{w.x, w.y, w.z, w.w}}, y);
-  float top = max_nan2(max_nan2(max_nan2(fabsf(y[0]), fabsf(y[1])), max_nan2(fabsf(y[2]), fabsf(y[3]))),
-                       max_nan2(max_nan2(fabsf(y[4]), fabsf(y[5])), max_nan2(fabsf(y[6]), fabsf(y[7]))));
-  top = max_nan2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  float top = max_nan(max_nan(max_nan(fabsf(y[0]), fabsf(y[1])), max_nan(fabsf(y[2]), fabsf(y[3]))),
+                       max_nan(max_nan(fabsf(y[4]), fabsf(y[5])), max_nan(fabsf(y[6]), fabsf(y[7]))));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
   if (__any_sync(0xffffffffu, top != top)) {   // NaN has no code: stored as 0
     top = 0.f;
 #pragma unroll

@@ -64,6 +64,18 @@ EAGLE_DEV void check_ranges(const int* cu, const int* lens, int B, int n, int i,
   if (bad) atomicOr(err, DEVERR_PREFIX);
 }
 
+// the larger of two, NaN if either is
+EAGLE_DEV float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+// two floats to a packed bf16 pair (the first in the low half)
+EAGLE_DEV uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // Two floats to e2m1 codes in a byte (a in the low nibble), nearest, ties to even, saturating.
 EAGLE_DEV uint32_t e2m1x2(float a, float b) {
   uint32_t r;
