@@ -216,9 +216,10 @@ EAGLE_DEV void store8_f4(uint8_t* code, uint8_t* scale, uint4 w, float global, f
 // of a head precedes its stores (in place is safe).  The CTA computes the cos / sin of its rows
 // once into shared memory; a warp keeps one row's in registers over all the heads it takes.
 // CACHE: 0 eagle_rotary, else eagle_cache_kind_t.  Bound by bytes where there are many rows
-// (8,191 x 64 fp32 heads: 85 us, 92% of the measured copy rate); with 4-bit stores by issue and the
-// chain that finds a row's place (8,188 rows, 48 heads: 44 us, 176 MB).  POW2: the 4-bit cache's global
-// factors are powers of two.
+// (8,191 x 64 fp32 heads: 85 us, 92% of the measured copy rate); with 4-bit stores by latency, of its
+// loads and of the chain that finds a row's place, at 24 warps an SM (80 registers; issue in 0.56 of
+// the cycles, loads the largest stall): 8,188 rows, 48 heads: 46 us, 26 of them its 176 MB.  POW2:
+// the 4-bit cache's global factors are powers of two.
 template <typename T, int CACHE, bool POW2>
 __global__ void __launch_bounds__(RT_THREADS) rotate_kernel(const RotArgs a, const RopeTab rt) {
   __shared__ float2 cs[RT_WARPS][RT_MAX_PAIRS];

@@ -573,7 +573,12 @@ EAGLE_API eagle_status_t eagle_kv_accept(const eagle_kv_cache_t* caches, int32_t
  * (causal).  out = softmax(scale q k) v per query head; grouped heads as in
  * eagle_draft_config_t.  A row that sees nothing, or only keys of score -infinity, gets zeros
  * and lse -infinity; keys a row does not see have no influence on it whatever they hold.
- * bf16 queries and outputs; scores, softmax and sums in fp32. */
+ * bf16 queries and outputs; scores, softmax statistics and sums in fp32.  For the product with the
+ * values the probabilities p = exp(score - maximum) are rounded: with 4-bit pages to 11 bits
+ * (fp16), with bf16 pages to 16 where max_rows * Hq / Hkv <= 128 and to 8 (bf16) above, which
+ * adds at most 2^-8 sum p |v| / sum p (2.3e-3 of the output's norm in all against 64 bits, 1.7e-3
+ * with 16 bits: the bf16 output alone).  So a row's last bits depend on the call's max_rows, as
+ * they do on max_len, which cuts the keys into ranges. */
 typedef struct {
   int32_t B, N;               /* requests, rows */
   int32_t n_heads;            /* Hq, a multiple of Hkv with Hq / Hkv <= 64 */

@@ -190,6 +190,25 @@ def test_largest_scale():
     check(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, 64)
 
 
+@pytest.mark.parametrize("kind,hd,G,ctx,rows,p_step", [
+    ("bf16", 128, 4, 900, 3, 2.0 ** -16), ("bf16", 64, 16, 3000, 8, 2.0 ** -16),    # one query tile: hi + lo
+    ("bf16", 128, 8, 900, 40, 2.0 ** -8),                                           # two: 8 bits
+    ("f4", 128, 4, 900, 3, 2.0 ** -11), ("f4", 128, 2, 900, 2, 2.0 ** -11), ("f4", 64, 8, 700, 40, 2.0 ** -11)])
+def test_bits_of_the_probabilities(kind, hd, G, ctx, rows, p_step):
+    """The second product's probabilities have the bits that the header states: hi + lo parts of 8 are
+    off by 2^-8 of the lower part, 2^-16 of p; fp16 by 2^-11 (and 2^-32 of the largest where it is
+    subnormal); one bf16 by 2^-8.  The rest of the bound is the file's."""
+    rng = np.random.default_rng(23)
+    cache, held = make_cache(rng, kind, hd, 32, 2, [ctx + rows])
+    q = K.bf16(rng.standard_normal((rows, 2 * G, hd)))
+    out = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu([rows])), dev(np.array([ctx], np.int32)), max_rows=rows,
+                          max_len=ctx + rows).double().cpu().numpy()
+    o, _, mag, qk, vsum = K.attention(q, held[0][0], held[0][1], see_matrix(ctx, rows), hd ** -0.5)
+    eps = 2 * ((hd + 4) * 2.0 ** -24 * qk + 2.0 ** -21 * (1 + qk))[..., None] + (hd + 128) * 2.0 ** -24
+    tol = (p_step + eps) * mag + 2.0 ** -8 * np.abs(o) + 2.0 ** -32 * vsum + 1e-30
+    assert (np.abs(out - o) <= tol).all(), float((np.abs(out - o) / tol).max())
+
+
 def test_non_finite_values_in_masked_keys():
     """Infinite and NaN keys and values of rows that a row's mask hides do not reach it; a row
     that sees them gets what the sums give."""
