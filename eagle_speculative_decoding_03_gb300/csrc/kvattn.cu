@@ -774,21 +774,59 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       const int n = rq.row0 + irow, h = kvh * a.G + (v - irow * a.G);
       const size_t at = static_cast<size_t>(n) * a.Hq + h;
       const bool none = l_run == 0.f;
+      const float inv = none ? 0.f : a.vg / l_run;
       // A non-finite V reaches vectors that have nothing of it: in a row that the step masks as 0 *
       // NaN, and with p in two parts the lower part (0 or negative) makes NaN of a visible infinity.
       // Such sums are formed again from the visible keys alone, a vector at a time by the whole warp
-      // (unless the vector's own sum of p is NaN: then so is its output).
-      if (!F4 && T > 0 && (HILO || (t_begin + T) * KA_CH > rq.ctx)) {
-        bool bad = false;
+      // (unless the vector's own sum of p is NaN: then so is its output), and written once more.
+      const bool recheck = !F4 && T > 0 && (HILO || (t_begin + T) * KA_CH > rq.ctx);
+      for (bool again = false;; again = true) {
+        float2 z0 = make_float2(0.f, 0.f), z1 = z0;
 #pragma unroll 1
         for (int c0 = 0; c0 < HD; c0 += 32) {
           float x[32];
-          tmem_ld32(tO + c0, x);
-          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) bad |= !(fabsf(x[e]) < INFINITY);
+          for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          if (T > 0) {
+            tmem_ld32(tO + c0, x);
+            tmem_wait_ld();
+          }
+          if (!F4) {                           // (0 unless some sum is not finite)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              z0 = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(0.f, 0.f), z0);
+              z1 = __ffma2_rn(make_float2(x[e + 2], x[e + 3]), make_float2(0.f, 0.f), z1);
+            }
+          }
+          if (joined) {
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(state + lv * ST_LD + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+          } else if (live && a.splits > 1) {
+            if (!none) {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+          } else if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + c0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = none ? 0u : pack_bf16(x[8 * e + 2 * k] * inv, x[8 * e + 2 * k + 1] * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();                        // (the next TMEM load is the whole warp's)
         }
+        if (again || !recheck) break;
+        const bool bad = !((z0.x + z0.y) + (z1.x + z1.y) == 0.f);
         unsigned todo = __ballot_sync(0xffffffffu, bad && live && !none && l_run < INFINITY);
+        if (!todo) break;
         for (; todo; todo &= todo - 1) {
           const int u = __ffs(todo) - 1, ui = __shfl_sync(0xffffffffu, irow, u);
           const VisibleKeys keys{a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), rq.ctx, ui,
@@ -812,41 +850,6 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           }
           tmem_wait_st();
         }
-      }
-      const float inv = none ? 0.f : a.vg / l_run;
-#pragma unroll 1
-      for (int c0 = 0; c0 < HD; c0 += 32) {
-        float x[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0.f;
-        if (T > 0) {
-          tmem_ld32(tO + c0, x);
-          tmem_wait_ld();
-        }
-        if (joined) {
-          if (live) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(state + lv * ST_LD + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-          }
-        } else if (live && a.splits > 1) {
-          if (!none) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-          }
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + n * a.out_ld + static_cast<long long>(h) * HD + c0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = none ? 0u : pack_bf16(x[8 * e + 2 * k] * inv, x[8 * e + 2 * k + 1] * inv);
-            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        __syncwarp();                        // (the next TMEM load is the whole warp's)
       }
       if (live) {
         const float m2 = none ? -INFINITY : m_run * row_scale - LIFT;

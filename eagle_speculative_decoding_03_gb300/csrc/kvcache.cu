@@ -512,7 +512,7 @@ EAGLE_DEV void move_rows(const KvPool& c, char* base, int bytes, int count, cons
 __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __grid_constant__ AcceptCaches caches) {
   __shared__ int src_page[64], src_tok[64], dst_page[64], dst_tok[64], s_end[2], s_run[2];
   const int b = blockIdx.x, tid = threadIdx.x;
-  const int base = __ldg(a.lens + b);
+  const int base = __ldg(a.lens + b), want = __ldg(a.accept_len + b);
   if (base < 0) {                            // no places: nothing moves, the length stays
     if (tid == 0) {
       atomicOr(a.err, DEVERR_PREFIX);
@@ -523,7 +523,6 @@ __global__ void __launch_bounds__(256) keep_kernel(const KeepArgs a, const __gri
   // The path: strictly ascending slots of the tree; anything else ends it.  So slot j >= j, and
   // move j writes place j + 1: the source of a later move only where the path starts with the
   // slots 0, 1, 2, ... (one that names the root).  That run is moved back to front.
-  const int want = __ldg(a.accept_len + b);
   int n = min(max(want, 0), a.S - 1);
   bool wrong = false;
   int s = 0;
