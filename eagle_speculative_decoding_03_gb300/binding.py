@@ -138,6 +138,27 @@ class KVAttention(C.Structure):
          ("lse", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
 
 
+class KVCross(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "N", "n_heads", "max_rows", "max_len")] + \
+        [("cu_rows", C.c_void_p), ("lens", C.c_void_p), ("q", C.c_void_p), ("q_stride", C.c_int64),
+         ("scale", C.c_float), ("out", C.c_void_p), ("out_stride", C.c_int64), ("lse", C.c_void_p),
+         ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
+class KVGroups(C.Structure):
+    _fields_ = [("n_groups", C.c_int32), ("cu_groups", C.c_void_p), ("lens", C.c_void_p), ("max_rows", C.c_int32),
+                ("max_len", C.c_int32)]
+
+
+MAX_PARTS = 16
+
+
+class AttentionParts(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("parts", "N", "H", "head_dim", "dtype", "out_dtype")] + \
+        [("outs", C.POINTER(C.c_void_p)), ("strides", C.POINTER(C.c_int64)), ("lses", C.POINTER(C.c_void_p)),
+         ("out", C.c_void_p), ("out_stride", C.c_int64), ("lse", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -204,6 +225,18 @@ def load(path: str = LIB_PATH):
     lib.eagle_kv_attention_workspace.restype = C.c_int64
     lib.eagle_kv_attention.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVAttention), P, P]
     lib.eagle_kv_attention.restype = C.c_int
+    lib.eagle_kv_cross_attention_workspace.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVCross)]
+    lib.eagle_kv_cross_attention_workspace.restype = C.c_int64
+    lib.eagle_kv_cross_attention.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVCross), P, P]
+    lib.eagle_kv_cross_attention.restype = C.c_int
+    lib.eagle_kv_shared_attention_workspace.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVGroups), C.POINTER(KVCacheC),
+                                                        C.POINTER(KVAttention)]
+    lib.eagle_kv_shared_attention_workspace.restype = C.c_int64
+    lib.eagle_kv_shared_attention.argtypes = [C.POINTER(KVCacheC), C.POINTER(KVGroups), C.POINTER(KVCacheC),
+                                              C.POINTER(KVAttention), P, P]
+    lib.eagle_kv_shared_attention.restype = C.c_int
+    lib.eagle_attention_merge.argtypes = [C.POINTER(AttentionParts), P]
+    lib.eagle_attention_merge.restype = C.c_int
     lib.eagle_draft_last_error.argtypes = []
     lib.eagle_draft_last_error.restype = C.c_char_p
     _lib = lib
@@ -874,6 +907,148 @@ def kv_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, 
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     if N:
         _check(lib.eagle_kv_attention(cache.ref, ref, cache.err_ptr, st))
+    return out if lse is None else (out, lse)
+
+
+def _outputs(q, out, lse, N, Hq, hd, dev, stream):
+    """(out, its row stride, lse or None) of an attention call: given, or new."""
+    if out is None:
+        out, ld = _new(q, (N, Hq, hd), _torch.bfloat16, stream), Hq * hd
+    else:
+        ld = _rows(out, "out", _torch.bfloat16, N, Hq, hd, dev)
+    if lse is True:
+        lse = _new(q, (N, Hq), _torch.float32, stream)
+    elif lse is False:
+        lse = None
+    elif lse is not None:
+        _tensor(lse, "lse", _torch.float32, (N, Hq), dev)
+    return out, ld, lse
+
+
+def _workspace(a, need: int, workspace, like, dev: int, stream):
+    """Gives the call's struct its workspace; returns the tensor, to be kept until the launch."""
+    if need < 0:
+        _bad(load().eagle_draft_last_error().decode())
+    if need:
+        if workspace is None:
+            workspace = _new(like, (need,), _torch.uint8, stream)
+        else:
+            _tensor(workspace, "workspace", _torch.uint8, (None,), dev)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return workspace
+
+
+def kv_cross_attention(cache: KVCache, q, cu_rows, lens, max_rows: int, max_len: int, scale: float = 0.0, out=None,
+                       lse=False, workspace=None, stream=None):
+    """Cross attention: rows cu_rows[b] .. cu_rows[b + 1] of bf16 q [N, Hq, hd] over all lens[b] keys
+    in row b of the cache's page table (an encoder's states, a document; 0 keys give zeros and lse
+    -inf).  max_rows / max_len bound one request's rows and keys.  out, lse and workspace as in
+    kv_attention."""
+    torch, dev, st = _here(stream)
+    q_ld = _rows(q, "q", torch.bfloat16, None, None, cache.head_dim, dev)
+    N, Hq, hd = q.shape
+    B = _requests(cache, cu_rows, lens, dev)
+    out, out_ld, lse = _outputs(q, out, lse, N, Hq, hd, dev, stream)
+    a = KVCross(B, N, Hq, int(max_rows), int(max_len), cu_rows.data_ptr(), lens.data_ptr(), q.data_ptr(), q_ld, float(scale),
+                out.data_ptr(), out_ld, _ptr(lse))
+    ref = C.byref(a)
+    lib = load()
+    if N:
+        workspace = _workspace(a, lib.eagle_kv_cross_attention_workspace(cache.ref, ref), workspace, q, dev, stream)
+        _check(lib.eagle_kv_cross_attention(cache.ref, ref, cache.err_ptr, st))
+    return out if lse is None else (out, lse)
+
+
+def kv_cross_attention_workspace(cache: KVCache, n_heads: int, N: int, B: int, max_rows: int, max_len: int) -> int:
+    """Bytes of workspace that kv_cross_attention needs for these sizes."""
+    a = KVCross(B=B, N=N, n_heads=n_heads, max_rows=max_rows, max_len=max_len)
+    need = load().eagle_kv_cross_attention_workspace(C.byref(cache.c), C.byref(a))
+    if need < 0:
+        _bad(load().eagle_draft_last_error().decode())
+    return need
+
+
+def kv_shared_attention(prefix: KVCache, cu_groups, prefix_lens, cache: KVCache, q, cu_rows, lens, max_group_rows: int,
+                        max_prefix: int, max_rows: int, max_len: int, mask=None, scale: float = 0.0, out=None, lse=False,
+                        workspace=None, stream=None):
+    """Attention of requests behind shared prefixes: requests cu_groups[g] .. cu_groups[g + 1] see the
+    prefix_lens[g] keys in row g of ``prefix``'s page table, computed once for all of them, and
+    their own keys in ``cache`` as kv_attention takes them (lens, max_len and mask count own keys;
+    the step's rows are appended to ``cache`` before, at positions behind the prefix).
+    max_group_rows / max_prefix bound one group's rows and prefix.  Device errors go to ``cache``'s
+    word.  out, lse and workspace as in kv_attention."""
+    torch, dev, st = _here(stream)
+    q_ld = _rows(q, "q", torch.bfloat16, None, None, cache.head_dim, dev)
+    N, Hq, hd = q.shape
+    B = _requests(cache, cu_rows, lens, dev)
+    _cache_here(prefix, dev)
+    n_groups = _ints(prefix_lens, "prefix_lens", None, dev)
+    _ints(cu_groups, "cu_groups", n_groups + 1, dev)
+    if prefix.max_requests < n_groups:
+        _bad("the prefix's page table has fewer rows than prefix_lens")
+    S = 0
+    if mask is not None:
+        S = mask.shape[-1]
+        _tensor(mask, "mask", torch.uint8, (B, S, S), dev)
+    out, out_ld, lse = _outputs(q, out, lse, N, Hq, hd, dev, stream)
+    g = KVGroups(n_groups, cu_groups.data_ptr(), prefix_lens.data_ptr(), int(max_group_rows), int(max_prefix))
+    a = KVAttention(B, N, Hq, int(max_rows), int(max_len), S, cu_rows.data_ptr(), lens.data_ptr(), q.data_ptr(), q_ld,
+                    _ptr(mask), float(scale), out.data_ptr(), out_ld, _ptr(lse))
+    gref, ref = C.byref(g), C.byref(a)
+    lib = load()
+    if N:
+        need = lib.eagle_kv_shared_attention_workspace(prefix.ref, gref, cache.ref, ref)
+        workspace = _workspace(a, need, workspace, q, dev, stream)
+        _check(lib.eagle_kv_shared_attention(prefix.ref, gref, cache.ref, ref, cache.err_ptr, st))
+    return out if lse is None else (out, lse)
+
+
+def kv_shared_attention_workspace(prefix: KVCache, cache: KVCache, n_heads: int, N: int, n_groups: int, B: int,
+                                  max_group_rows: int, max_prefix: int, max_rows: int, max_len: int) -> int:
+    """Bytes of workspace that kv_shared_attention needs for these sizes."""
+    g = KVGroups(n_groups=n_groups, max_rows=max_group_rows, max_len=max_prefix)
+    a = KVAttention(B=B, N=N, n_heads=n_heads, max_rows=max_rows, max_len=max_len)
+    need = load().eagle_kv_shared_attention_workspace(C.byref(prefix.c), C.byref(g), C.byref(cache.c), C.byref(a))
+    if need < 0:
+        _bad(load().eagle_draft_last_error().decode())
+    return need
+
+
+def attention_merge(outs, lses, dtype=None, out=None, lse=False, stream=None):
+    """Joins attention results of the same queries over disjoint keys: outs [N, H, hd] (float32 or
+    bfloat16, at most 16), lses float32 [N, H] (-inf: the part adds nothing).  The result has
+    ``dtype`` (the parts' if not given); out may be one of the parts.  Returns out, or (out, lse)
+    with lse=True or a tensor."""
+    torch, dev, st = _here(stream)
+    outs, lses = list(outs), list(lses)
+    n = len(outs)
+    if not 1 <= n <= MAX_PARTS or len(lses) != n:
+        _bad(f"attention_merge: need 1..{MAX_PARTS} parts, each with its lse")
+    x = outs[0]
+    kind = _float_kind(x, "outs")
+    lds = [_rows(x, "outs", x.dtype, None, None, None, dev)]
+    N, H, hd = x.shape
+    for t in outs[1:]:
+        lds.append(_rows(t, "outs", x.dtype, N, H, hd, dev))
+    for t in lses:
+        _tensor(t, "lses", torch.float32, (N, H), dev)
+    if out is None:
+        out, out_ld = _new(x, (N, H, hd), x.dtype if dtype is None else dtype, stream), H * hd
+    else:
+        if dtype is not None and out.dtype != dtype:
+            _bad("attention_merge: out has another dtype")
+        out_ld = _rows(out, "out", out.dtype, N, H, hd, dev)
+    okind = _float_kind(out, "out")
+    if lse is True:
+        lse = _new(x, (N, H), torch.float32, stream)
+    elif lse is False:
+        lse = None
+    elif lse is not None:
+        _tensor(lse, "lse", torch.float32, (N, H), dev)
+    a = AttentionParts(n, N, H, hd, kind, okind, (C.c_void_p * n)(*[t.data_ptr() for t in outs]), (C.c_int64 * n)(*lds),
+                       (C.c_void_p * n)(*[t.data_ptr() for t in lses]), out.data_ptr(), out_ld, _ptr(lse))
+    if N:
+        _check(load().eagle_attention_merge(C.byref(a), st))
     return out if lse is None else (out, lse)
 
 

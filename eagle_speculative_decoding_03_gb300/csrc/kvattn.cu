@@ -8,215 +8,14 @@
 // or two tiles per CTA).  A CTA takes a range of the keys; the ranges of a request meet in a
 // cluster or in a combine kernel (in rank order: deterministic).  Three kernels: tensor cores for
 // any shape, mma.sync on 4-bit pages for up to 8 query vectors, and the combine kernel.
-#include "kvcache.cuh"
+#include "kvattn.cuh"
 
 #include <algorithm>
 #include <atomic>
-#include <cfloat>
-#include <cmath>
-#include <cstring>
 
 using namespace eagle;
 
 namespace {
-
-// Instruction descriptor of tcgen05.mma kind::f16 with fp16 A and B, f32 D, both K-major (as
-// idesc_bf16_f32, whose operands are bf16).
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// 3-D map over a paged bf16 cache [pages * Hkv][page_size][hd]: boxes of one page's rows of one
-// KV head x 64 dims, 128-byte swizzle; rows outside the page or the pool read as zeros.
-bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks) {
-  const EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(hd) * 2 * page_size};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-constexpr int KA_MAX_GROUP = 64;
-constexpr int KA_CH = 128;                 // keys per tile (a ring entry)
-constexpr int KA_H = 64;                   // keys per unit of work (half a tile)
-constexpr int KA_QV = 128;                 // query vectors per tile (TMEM lanes)
-constexpr float KA_RESCALE = 8.0f;         // log2 units: the running maximum may lag by this much
-constexpr uint32_t KA_MISC = 2048;         // barriers (0), tree mask rows (512), joined states' m and l (1024)
-constexpr int KA_MAX_SLOTS = 14;
-constexpr int KA_MAX_JOIN = 8;             // ranges that join in a cluster
-constexpr int KA_FIXED = 12;              // a CTA's fixed cost in tiles
-constexpr int KS_FIXED = 2;               // the same for the kernel for few query vectors
-
-struct KaArgs {
-  KvPool pool;
-  int B, N, Hq, G, max_rows, max_len, S;
-  int blocks;                              // query-vector blocks per request
-  int tiles_per_cta, splits;
-  int joined;                              // the ranges of a request are one cluster and join in it
-  const int* cu;
-  const int* lens;
-  const __nv_bfloat16* q;
-  long long q_ld;
-  const unsigned char* mask;
-  float scale_log2;                        // scale * log2(e)
-  float vg;                                // the values' global factor (1 with bf16 pages)
-  __nv_bfloat16* out;
-  long long out_ld;
-  float* lse;
-  float* part_o;                           // [splits][N][Hq][hd] unnormalised outputs (splits > 1)
-  float2* part_ml;                         // [splits][N][Hq] running maximum (log2 units) and sum
-  unsigned* err;
-};
-
-// Request b's rows and keys, clamped to what the call allows.
-struct Req {
-  int row0, R, ctx, len;
-};
-EAGLE_DEV Req request(const KaArgs& a, int b) {
-  Req r;
-  const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), l = __ldg(a.lens + b);
-  r.row0 = min(max(c0, 0), a.N);
-  r.R = min(max(min(c1, a.N) - r.row0, 0), min(a.max_rows, a.max_len));
-  r.ctx = min(max(l, 0), a.max_len - r.R);
-  if (r.row0 != c0 || r.R != c1 - c0 || r.ctx != l) atomicOr(a.err, DEVERR_PREFIX);
-  r.len = r.ctx + r.R;
-  return r;
-}
-
-EAGLE_DEV void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the float at this CTA's shared address `p` in CTA `rank` of the cluster
-EAGLE_DEV float remote(const float* p, int rank) {
-  uint32_t a;
-  float v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
-}
-EAGLE_DEV float4 remote4(const float* p, int rank) {
-  uint32_t a;
-  float4 v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
-}
-
-// 128 bits of key visibility
-struct Bits {
-  unsigned long long lo, hi;
-};
-EAGLE_DEV Bits bits_below(int n) {         // bits [0, n)
-  Bits r;
-  r.lo = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
-  r.hi = n >= 128 ? ~0ull : n <= 64 ? 0ull : (1ull << (n - 64)) - 1ull;
-  return r;
-}
-EAGLE_DEV Bits shift_up(unsigned long long m, int n) {   // m << n; n < 0: m >> -n
-  Bits r{0ull, 0ull};
-  if (n <= -64 || n >= 128) return r;
-  if (n < 0) r.lo = m >> -n;
-  else if (n == 0) r.lo = m;
-  else if (n < 64) { r.lo = m << n; r.hi = m >> (64 - n); }
-  else r.hi = m << (n - 64);
-  return r;
-}
-
-// byte offset of 16-byte chunk c (0-7) of row r in a 128-byte-swizzled block of 128-byte rows
-EAGLE_DEV uint32_t ka_sw(int r, int c) {
-  return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
-}
-EAGLE_DEV void st_smem16(uint32_t addr, const uint32_t* v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-// the largest of three, NaN if any is: a NaN score must reach the output
-EAGLE_DEV float max3_nan(float x, float y, float z) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-// (x, y) * (a, a) + (b, b) and (x, y) + (z, w), two fp32 lanes an instruction
-EAGLE_DEV void fma2(float& x, float& y, float a, float b) {
-  const float2 r = __ffma2_rn(make_float2(x, y), make_float2(a, a), make_float2(b, b));
-  x = r.x;
-  y = r.y;
-}
-EAGLE_DEV void add2(float& x, float& y, float z, float w) {
-  const float2 r = __fadd2_rn(make_float2(x, y), make_float2(z, w));
-  x = r.x;
-  y = r.y;
-}
-// `bytes` (a multiple of 16) of global memory into shared memory, completing on `bar`
-EAGLE_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
-EAGLE_DEV uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// byte B of w, two e2m1 codes -> fp16 pair (low nibble in the low half)
-template <int B>
-EAGLE_DEV uint32_t e2m1_pair(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t<4>;\n\tmov.b32 {t0, t1, t2, t3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t%2;\n\t}" : "=r"(r) : "r"(w), "n"(B));
-  return r;
-}
-EAGLE_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// 8 consecutive dims of a cached row: 4 code bytes and the pair of their scale -> 8 fp16 values (exact:
-// a code has 2 significant bits and a scale 4; the range is 2^-10 .. 2688)
-EAGLE_DEV uint32_t scale_pair(uint32_t scale) {
-  uint32_t s;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s) : "r"(scale * 0x101u));
-  return s;
-}
-EAGLE_DEV void dequant8(uint32_t code, uint32_t s, uint32_t* h) {
-  h[0] = mul_f16x2(e2m1_pair<0>(code), s);
-  h[1] = mul_f16x2(e2m1_pair<1>(code), s);
-  h[2] = mul_f16x2(e2m1_pair<2>(code), s);
-  h[3] = mul_f16x2(e2m1_pair<3>(code), s);
-}
-
-// A vector's score factor, kept within the normal numbers: a factor that fell to 0 would make NaN of
-// a masked score (-inf * 0), one that overflowed of a score of 0.
-EAGLE_DEV float finite_scale(float x) { return fminf(fmaxf(x, FLT_MIN), FLT_MAX); }
-
-// a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
-// registers (the operands of tcgen05.mma)
-EAGLE_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-// A place in the ring of NS entries: slot and the parity of its turn.  (Stepped, not computed: a
-// division by NS costs the MMA warp as much as it takes to issue a unit.)
-struct RingPos {
-  int slot, turn;
-  EAGLE_DEV void step(int n, int NS) {
-    slot += n;
-    if (slot >= NS) {
-      slot -= NS;
-      turn ^= 1;
-    }
-  }
-};
-// one thread of a converged warp, the same one every time
-EAGLE_DEV bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-template <int R>
-EAGLE_DEV void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-EAGLE_DEV void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // The tensor-core kernel.  HD 64 or 128; CACHE the cache kind; NB: query-vector tiles per CTA.
 //
@@ -363,7 +162,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   const bool joined = NB == 1 && a.joined;
   const int per_cta = joined ? (all_tiles + a.splits - 1) / a.splits : a.tiles_per_cta;
   const int t_begin = split * per_cta;
-  if (!joined && t_begin * KA_CH >= rq.len) return;  // (not a range of this request at all)
+  if (!joined && split > 0 && t_begin * KA_CH >= rq.len) return;  // (not a range of this request at all)
   const int T = max(0, min(all_tiles - t_begin, per_cta));
   const int nb = uniform(NB == 2 && qv > KA_QV ? 2 : 1);
   const int nq0 = min(4, (min(qv, KA_QV) + 31) / 32), nq1 = nb == 2 ? (qv - KA_QV + 31) / 32 : nq0;
@@ -658,6 +457,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const int irow = live ? v / a.G : i_last;
     const unsigned long long tree_bits = a.mask && live ? rowbits[irow - i_first] : 0ull;
+    const int own = a.cross ? 0 : irow + 1;            // the step's rows that it sees without a mask
     const uint32_t tO = tmem + lane_base + T_O + 128 * g;
     float m_run = -INFINITY, l_run = 0.f;              // raw scores' maximum; sum of p
     if (g < nb && (warp & 3) < (g == 0 ? nq0 : nq1)) {
@@ -682,7 +482,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             seen_cols.lo |= own.lo;
             seen_cols.hi |= own.hi;
           } else {
-            seen_cols = bits_below(off + irow + 1);
+            seen_cols = bits_below(off + own);
           }
           const int at = (end_page << a.pool.ps_log) - kt, sh = ps - end_rows;   // the last page's first column
           if (end_rows && at >= 0 && at < KA_CH) {   // columns from `at` on move up by sh (1 .. 127)
@@ -804,7 +604,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(state + lv * ST_LD + c0 + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
             }
-          } else if (live && a.splits > 1) {
+          } else if (live && a.parts) {
             if (!none) {
               float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + c0);
 #pragma unroll
@@ -829,7 +629,8 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         if (!todo) break;
         for (; todo; todo &= todo - 1) {
           const int u = __ffs(todo) - 1, ui = __shfl_sync(0xffffffffu, irow, u);
-          const VisibleKeys keys{a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), rq.ctx, ui,
+          const VisibleKeys keys{a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), rq.ctx,
+                                 a.cross ? -1 : ui,
                                  a.mask != nullptr, __shfl_sync(0xffffffffu, tree_bits, u)};
           const __nv_bfloat16* qp = a.q + (rq.row0 + ui) * a.q_ld + static_cast<long long>(kvh * a.G + v - lane + u - ui * a.G) * HD;
           float o[HD / 32];
@@ -856,7 +657,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         if (joined) {
           mcta[lv] = m2;
           lcta[lv] = l_run;
-        } else if (a.splits > 1) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, l_run);
+        } else if (a.parts) a.part_ml[static_cast<size_t>(split) * a.N * a.Hq + at] = make_float2(m2, l_run);
         else if (a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(l_run)) * 0.6931471805599453f;
       }
     }
@@ -970,7 +771,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   const int qv = rq.R * a.G;
   const int per_cta = a.joined ? ((rq.len + KA_CH - 1) / KA_CH + a.splits - 1) / a.splits : a.tiles_per_cta;
   const int kb = split * per_cta * KA_CH;
-  if (qv <= 0 || (!a.joined && kb >= rq.len)) return;
+  if (qv <= 0 || (!a.joined && split > 0 && kb >= rq.len)) return;
   const int ke = min(rq.len, kb + per_cta * KA_CH);
   const int tiles = max(0, (ke - kb + KA_CH - 1) / KA_CH);
   if (tid == 0) {
@@ -1258,7 +1059,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
         s_jm[v] = m2;
         s_jl[v] = L;
       }
-    } else if (a.splits > 1) {
+    } else if (a.parts) {
       if (!none)
         *reinterpret_cast<float2*>(a.part_o + (static_cast<size_t>(split) * a.N * a.Hq + at) * HD + d) =
             make_float2(y0, y1);
@@ -1357,53 +1158,6 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
   if (a.lse && lane == 0) a.lse[at] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// How a call is cut: query-vector tiles per CTA, blocks per request, key ranges.
-struct Plan {
-  bool step;                               // the kernel for few vectors of a 4-bit cache
-  bool joined;                             // a request's ranges are a cluster
-  int nb, blocks, tiles_per_cta, splits;
-};
-Plan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
-  Plan p;
-  const long long qv = static_cast<long long>(w->max_rows) * (w->n_heads / c->n_kv_heads);
-  p.step = c->kind == EAGLE_CACHE_F4 && qv <= KS_QV;
-  p.nb = qv > KA_QV ? 2 : 1;
-  p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
-  const long long base = static_cast<long long>(w->B) * c->n_kv_heads * p.blocks;
-  const long long tiles = (static_cast<long long>(w->max_len) + KA_CH - 1) / KA_CH;
-  // Key ranges: the split that takes least, a CTA costing its tiles and `fixed` more
-  // for its start and its result.  Up to 8 ranges join in a cluster where the device holds all
-  // clusters at once (each within one of its groups of about 19 SMs); in several waves the ranges of
-  // requests of different lengths keep each other waiting (150 us of attention_step_b32_f4 where
-  // separate ranges take 131).  Others join in a second kernel, which costs `second` tiles and
-  // another for every four ranges (attention_step_b1: 13.2 us, joined 12.2, and 8 us less host time).
-  const long long per_sm = p.step ? KS_CTAS : 1, sms = num_sms() > 0 ? num_sms() : 152, slots = sms * per_sm;   // (152: without a device, a GB300's)
-  const long long fixed = p.step ? KS_FIXED : KA_FIXED, second = p.step ? 3 : 4;
-  long long per = tiles;
-  double best = -1.;
-  p.joined = false;
-  const long long most = std::min(tiles, 8 * slots / base + 1);   // (beyond 8 waves more ranges only cost)
-  // (only the n at which the tiles per range change: about twice the root of the tiles)
-  for (long long n = 1, t = 0; n <= most; n = t > 1 ? (tiles + t - 2) / (t - 1) : most + 1) {
-    t = (tiles + n - 1) / n;
-    const long long ranges = (tiles + t - 1) / t;
-    const bool join = ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= sms / 19 * (19 * per_sm / ranges);
-    // the requests all as long as the bound, and (of several requests) of lengths spread below it:
-    // then the longest CTA, or the work of the average request on all slots
-    const double even = static_cast<double>((base * ranges + slots - 1) / slots * (t + fixed));
-    const double spread = std::max<double>(t + fixed, base * (0.5 * tiles + fixed * 0.5 * (ranges + 1)) / slots);
-    const double cost = (w->B > 1 ? 0.5 * (even + spread) : even) + (ranges == 1 || join ? 0. : second + 0.25 * ranges);
-    if (best < 0 || cost < best) {
-      best = cost;
-      per = t;
-      p.joined = join;
-    }
-  }
-  p.tiles_per_cta = static_cast<int>(per);
-  p.splits = static_cast<int>((tiles + per - 1) / per);
-  return p;
-}
-
 eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w, const char* who, KvPool* pool) {
   const eagle_status_t r = kv_pool(c, who, pool);
   if (r != EAGLE_OK) return r;
@@ -1417,24 +1171,6 @@ eagle_status_t check_args(const eagle_kv_cache_t* c, const eagle_kv_attention_t*
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: a mask needs max_rows <= mask_slots <= 64", who);
   if (!std::isfinite(w->scale) || w->scale < 0.f) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: scale must be finite and not negative", who);
   return EAGLE_OK;
-}
-
-// The ranges of a request (grid x) as one cluster where they join in it.
-template <typename... P, typename... A>
-cudaError_t launch_ranges(const KaArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t st, void (*kernel)(P...), const A&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.joined ? a.splits : 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.attrs = attr;
-  cfg.numAttrs = a.joined ? 1 : 0;
-  cfg.stream = st;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 template <int HD, int CACHE, int NB>
@@ -1478,15 +1214,66 @@ cudaError_t launch_step(const KaArgs& a, cudaStream_t st) {
   return launch_ranges(a, dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS + 32, smem, st, kv_attention_step_f4<HD>, a);
 }
 
+}  // namespace
+
+KaPlan eagle::ka_plan(int kind, int Hkv, int G, int B, int max_rows, int max_len, bool may_join) {
+  KaPlan p;
+  const long long qv = static_cast<long long>(max_rows) * G;
+  p.step = kind == EAGLE_CACHE_F4 && qv <= KS_QV;
+  p.nb = qv > KA_QV ? 2 : 1;
+  p.blocks = static_cast<int>((qv + KA_QV * p.nb - 1) / (KA_QV * p.nb));
+  const long long base = static_cast<long long>(B) * Hkv * p.blocks;
+  const long long tiles = (static_cast<long long>(max_len) + KA_CH - 1) / KA_CH;
+  // Key ranges: the split that takes least, a CTA costing its tiles and `fixed` more
+  // for its start and its result.  Up to 8 ranges join in a cluster where the device holds all
+  // clusters at once (each within one of its groups of about 19 SMs); in several waves the ranges of
+  // requests of different lengths keep each other waiting (150 us of attention_step_b32_f4 where
+  // separate ranges take 131).  Others join in a second kernel, which costs `second` tiles and
+  // another for every four ranges (attention_step_b1: 13.2 us, joined 12.2, and 8 us less host time).
+  const long long per_sm = p.step ? KS_CTAS : 1, sms = num_sms() > 0 ? num_sms() : 152, slots = sms * per_sm;   // (152: without a device, a GB300's)
+  const long long fixed = p.step ? KS_FIXED : KA_FIXED, second = p.step ? 3 : 4;
+  long long per = tiles;
+  double best = -1.;
+  p.joined = false;
+  const long long most = std::min(tiles, 8 * slots / base + 1);   // (beyond 8 waves more ranges only cost)
+  // (only the n at which the tiles per range change: about twice the root of the tiles)
+  for (long long n = 1, t = 0; n <= most; n = t > 1 ? (tiles + t - 2) / (t - 1) : most + 1) {
+    t = (tiles + n - 1) / n;
+    const long long ranges = (tiles + t - 1) / t;
+    const bool join = may_join && ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= sms / 19 * (19 * per_sm / ranges);
+    // the requests all as long as the bound, and (of several requests) of lengths spread below it:
+    // then the longest CTA, or the work of the average request on all slots
+    const double even = static_cast<double>((base * ranges + slots - 1) / slots * (t + fixed));
+    const double spread = std::max<double>(t + fixed, base * (0.5 * tiles + fixed * 0.5 * (ranges + 1)) / slots);
+    const double cost = (B > 1 ? 0.5 * (even + spread) : even) + (ranges == 1 || join ? 0. : second + 0.25 * ranges);
+    if (best < 0 || cost < best) {
+      best = cost;
+      per = t;
+      p.joined = join;
+    }
+  }
+  p.tiles_per_cta = static_cast<int>(per);
+  p.splits = static_cast<int>((tiles + per - 1) / per);
+  return p;
+}
+
+
 template <int HD>
-cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, bool f4, const Plan& p, cudaStream_t st) {
-  cudaError_t e;
-  const int nb = p.nb;
-  if (p.step) {
-    e = launch_step<HD>(a, st);
-  } else if (f4) e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
-  else e = nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
-  if (e != cudaSuccess || a.splits == 1 || a.joined) return e;
+static cudaError_t launch_kind(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, bool f4, const KaPlan& p, cudaStream_t st) {
+  if (p.step) return launch_step<HD>(a, st);
+  if (f4) return p.nb == 2 ? launch_tc<HD, EAGLE_CACHE_F4, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_F4, 1>(tmk, tmv, a, st);
+  return p.nb == 2 ? launch_tc<HD, EAGLE_CACHE_BF16, 2>(tmk, tmv, a, st) : launch_tc<HD, EAGLE_CACHE_BF16, 1>(tmk, tmv, a, st);
+}
+
+cudaError_t eagle::ka_launch(KaArgs* a, const KaPlan& p, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t st) {
+  a->blocks = p.blocks;
+  a->tiles_per_cta = p.tiles_per_cta;
+  a->splits = p.splits;
+  a->joined = p.joined;
+  return a->pool.hd == 64 ? launch_kind<64>(tmk, tmv, *a, f4, p, st) : launch_kind<128>(tmk, tmv, *a, f4, p, st);
+}
+
+cudaError_t eagle::ka_combine(const KaArgs& a, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.N) * a.Hq;
   const bool wide = a.splits > 8 && rows < 1ll << 31;   // (fewer ranges: a warp each row)
   // (starts while the ranges still run and waits for them: their results, and nothing before)
@@ -1499,14 +1286,17 @@ cudaError_t launch_all(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
   cfg.stream = st;
   cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(128);
-  return wide ? cudaLaunchKernelEx(&cfg, kv_attention_combine<HD, 4>, a) : cudaLaunchKernelEx(&cfg, kv_attention_combine<HD, 1>, a);
+  if (a.pool.hd == 64) return wide ? cudaLaunchKernelEx(&cfg, kv_attention_combine<64, 4>, a) : cudaLaunchKernelEx(&cfg, kv_attention_combine<64, 1>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, kv_attention_combine<128, 4>, a) : cudaLaunchKernelEx(&cfg, kv_attention_combine<128, 1>, a);
 }
 
-}  // namespace
+static KaPlan plan(const eagle_kv_cache_t* c, const eagle_kv_attention_t* w) {
+  return ka_plan(c->kind, c->n_kv_heads, w->n_heads / c->n_kv_heads, w->B, w->max_rows, w->max_len, true);
+}
 
-static int64_t workspace_bytes(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args, const Plan& p) {
+static int64_t workspace_bytes(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args, const KaPlan& p) {
   if (p.splits == 1 || p.joined) return 0;
-  return static_cast<int64_t>(p.splits) * args->N * args->n_heads * (4 * cache->head_dim + 8);
+  return p.splits * ka_part_bytes(args->N, args->n_heads, cache->head_dim);
 }
 
 extern "C" int64_t eagle_kv_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args) {
@@ -1529,7 +1319,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
       reinterpret_cast<uintptr_t>(w->q) % 16 || reinterpret_cast<uintptr_t>(w->out) % 16)
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and not overlap", who);
   if (w->q == w->out) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: out may not be q (ranges and blocks read q at different times)", who);
-  const Plan p = plan(cache, w);
+  const KaPlan p = plan(cache, w);
   const int64_t need = workspace_bytes(cache, w, p);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || reinterpret_cast<uintptr_t>(w->workspace) % 16))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
@@ -1544,10 +1334,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   a.max_rows = w->max_rows;
   a.max_len = w->max_len;
   a.S = w->mask_slots;
-  a.blocks = p.blocks;
-  a.tiles_per_cta = p.tiles_per_cta;
-  a.splits = p.splits;
-  a.joined = p.joined;
+  a.parts = p.splits > 1;
   a.cu = w->cu_rows;
   a.lens = w->lens;
   a.q = static_cast<const __nv_bfloat16*>(w->q);
@@ -1569,6 +1356,7 @@ extern "C" eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, cons
   const long long blocks = static_cast<long long>(cache->num_pages) * cache->n_kv_heads;
   if (!f4 && (!make_page_map(&tmk, cache->k, hd, cache->page_size, blocks) || !make_page_map(&tmv, cache->v, hd, cache->page_size, blocks)))
     return kv_fail(EAGLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  const cudaError_t e = hd == 64 ? launch_all<64>(tmk, tmv, a, f4, p, st) : launch_all<128>(tmk, tmv, a, f4, p, st);
+  cudaError_t e = ka_launch(&a, p, f4, tmk, tmv, st);
+  if (e == cudaSuccess && p.splits > 1 && !p.joined) e = ka_combine(a, st);
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }

@@ -604,6 +604,93 @@ EAGLE_API int64_t eagle_kv_attention_workspace(const eagle_kv_cache_t* cache, co
 EAGLE_API eagle_status_t eagle_kv_attention(const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args,
                                             uint32_t* err_word, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * Attention over keys that are not the rows' own sequence.
+ *
+ * Cross attention: request b's rows over all lens[b] cached keys of another sequence (an
+ * encoder's states, an image, a document), request b's row of the page table.  The rows are no
+ * keys of that cache: there is no mask and no order among them.
+ *
+ * Shared attention: requests that continue one long prefix (samples, beams or draft trees of one
+ * prompt, users behind one system prompt).  The prefix lies once in a cache of its own, one table
+ * row per group of requests; each request's own keys lie in another cache.  The prefix is computed
+ * once for the rows of all requests of a group (eagle_kv_attention reads a shared page once per
+ * request), the own keys as eagle_kv_attention takes them, and both are joined: the result is one
+ * softmax over [prefix keys ; own keys].
+ *
+ * Merge: the same join for partial results that the caller holds: attention of the same queries
+ * over disjoint keys, each with its log-sum-exp.
+ * ------------------------------------------------------------------------------------ */
+typedef struct {
+  int32_t B, N;               /* sequences, rows */
+  int32_t n_heads;            /* Hq, a multiple of Hkv with Hq / Hkv <= 64 */
+  int32_t max_rows;           /* most rows of one request */
+  int32_t max_len;            /* most keys of one sequence, >= 1 (a sequence may have none) */
+  const int32_t* cu_rows;     /* [B + 1] as in eagle_kv_rows_t */
+  const int32_t* lens;        /* [B] */
+  const void* q;              /* bf16 [N][Hq][hd], rows q_stride apart */
+  int64_t q_stride;
+  float   scale;              /* 0: 1 / sqrt(hd) */
+  void*   out;                /* bf16 [N][Hq][hd], rows out_stride apart; may not overlap q */
+  int64_t out_stride;
+  float*  lse;                /* [N][Hq] log-sum-exp of the scaled scores, or NULL */
+  void*   workspace;          /* eagle_kv_cross_attention_workspace bytes, 16-byte aligned (NULL if 0) */
+  int64_t workspace_bytes;
+} eagle_kv_cross_t;
+
+/* out = softmax(scale q k) v over all keys of the sequence, in the types and with the rounding of
+ * eagle_kv_attention.  A row of a sequence without keys, or whose scores are all -infinity, gets
+ * zeros and lse -infinity.  Rows past max_rows, and keys past max_len, are left out and flagged
+ * (EAGLE_DEVERR_PREFIX). */
+EAGLE_API int64_t eagle_kv_cross_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* args);
+EAGLE_API eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* args,
+                                                  uint32_t* err_word, void* stream);
+
+/* Group g is the requests cu_groups[g] .. cu_groups[g + 1] - 1 (consecutive, so their rows are too);
+ * every request belongs to a group: cu_groups[0] = 0 and cu_groups[n_groups] = B. */
+typedef struct {
+  int32_t n_groups;
+  const int32_t* cu_groups;   /* [n_groups + 1] ascending, within [0, B] */
+  const int32_t* lens;        /* [n_groups] keys of each group's prefix; 0: none */
+  int32_t max_rows;           /* most rows of one group */
+  int32_t max_len;            /* most keys of one prefix, >= 1 */
+} eagle_kv_groups_t;
+
+/* Row i of request b of group g sees the lens[g] keys of row g of `prefix`'s page table, the
+ * args->lens[b] keys of `cache` before the step and of the step's own rows (appended to `cache`
+ * before) what args->mask says, or j <= i: args is as in eagle_kv_attention, but for the workspace
+ * (eagle_kv_shared_attention_workspace bytes).  Positions are the caller's: append the own keys
+ * with positions behind the prefix.  The two caches have the same heads and head_dim; their kinds,
+ * page sizes and pools are their own.  Rows of a request outside every group, and rows past
+ * groups->max_rows, are left as they were; groups that descend, leave [0, B] or leave requests out
+ * are flagged (EAGLE_DEVERR_PREFIX). */
+EAGLE_API int64_t eagle_kv_shared_attention_workspace(const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* groups,
+                                                      const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args);
+EAGLE_API eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* groups,
+                                                   const eagle_kv_cache_t* cache, const eagle_kv_attention_t* args,
+                                                   uint32_t* err_word, void* stream);
+
+#define EAGLE_MAX_PARTS 16
+
+typedef struct {
+  int32_t parts;              /* 1 .. EAGLE_MAX_PARTS */
+  int32_t N, H, head_dim;     /* rows, heads; head_dim a multiple of 8 up to 256 */
+  int32_t dtype, out_dtype;   /* of the parts, of out: EAGLE_DTYPE_F32 or _BF16 */
+  const void* const* outs;    /* HOST [parts] of [N][H][hd], 16-byte aligned */
+  const int64_t* strides;     /* HOST [parts] elements between a part's rows, multiples of 16 bytes; NULL: H hd */
+  const float* const* lses;   /* HOST [parts] of [N][H], contiguous */
+  void*   out;                /* [N][H][hd], rows out_stride apart */
+  int64_t out_stride;
+  float*  lse;                /* [N][H] or NULL */
+} eagle_attention_parts_t;
+
+/* out = sum_i w_i outs_i / sum_i w_i and lse = log sum_i w_i, w_i = exp(lses_i), in fp32 and rounded
+ * once.  A part whose lse is -infinity adds nothing, whatever its output holds; where all are, out is
+ * 0 and lse -infinity.  Parts of lse +infinity share the result evenly; a NaN lse makes the row of
+ * that head NaN.  out may be one of the parts (same dtype and stride), and overlaps them in no other
+ * way; lse may overlap no other buffer. */
+EAGLE_API eagle_status_t eagle_attention_merge(const eagle_attention_parts_t* args, void* stream);
+
 /* Thread-local description of the last error (never NULL). */
 EAGLE_API const char* eagle_draft_last_error(void);
 
