@@ -41,15 +41,6 @@ namespace {
 // 175; the output is 2.3e-3 of its norm from 64 bits, with both parts 1.7e-3, which is its own
 // rounding to bf16.  l sums the unrounded p.
 __host__ __device__ constexpr int ka_threads(int cache, int nb) { return 128 + 128 * nb + (cache == EAGLE_CACHE_F4 ? 256 : 0); }
-// registers per thread of the 4-bit kernel's roles after they moved (the launch checks their sum)
-constexpr int KA_REG_CTRL = 40;
-__host__ __device__ constexpr int ka_reg_softmax(int nb) { return nb == 2 ? 136 : 152; }
-__host__ __device__ constexpr int ka_reg_conv(int nb) { return nb == 2 ? 80 : 128; }
-__host__ __device__ constexpr uint32_t ka_entry(int hd) { return static_cast<uint32_t>(hd) * 2 * KA_CH; }
-// 4-bit caches: a ring of raw tiles (128 rows of codes, then their scales) behind the entries
-constexpr int KA_RAW = 3;
-__host__ __device__ constexpr uint32_t ka_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_CH + hd / 16 * KA_CH; }
-
 // The keys of a range that one vector sees.
 struct VisibleKeys {
   const KvPool& pool;

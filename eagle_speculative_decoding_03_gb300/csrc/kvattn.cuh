@@ -41,6 +41,15 @@ constexpr int KA_MAX_JOIN = 8;             // ranges that join in a cluster
 constexpr int KA_FIXED = 12;              // a CTA's fixed cost in tiles
 constexpr int KS_FIXED = 2;               // the same for the kernel for few query vectors
 
+// registers per thread of the 4-bit kernel's roles after they moved (the launch checks their sum)
+constexpr int KA_REG_CTRL = 40;
+__host__ __device__ constexpr int ka_reg_softmax(int nb) { return nb == 2 ? 136 : 152; }
+__host__ __device__ constexpr int ka_reg_conv(int nb) { return nb == 2 ? 80 : 128; }
+__host__ __device__ constexpr uint32_t ka_entry(int hd) { return static_cast<uint32_t>(hd) * 2 * KA_CH; }
+// 4-bit caches: a ring of raw tiles (128 rows of codes, then their scales) behind the entries
+constexpr int KA_RAW = 3;
+__host__ __device__ constexpr uint32_t ka_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_CH + hd / 16 * KA_CH; }
+
 struct KaArgs {
   KvPool pool;
   int B, N, Hq, G, max_rows, max_len, S;
@@ -234,6 +243,18 @@ cudaError_t ka_launch(KaArgs* a, const KaPlan& p, bool f4, const CUtensorMap& tm
 cudaError_t ka_combine(const KaArgs& a, cudaStream_t st);
 // Bytes of one range's partial results.
 inline int64_t ka_part_bytes(long long N, int Hq, int hd) { return N * Hq * (4ll * hd + 8); }
+
+// The same for many query vectors of cross attention (kvcross.cu): its CTAs, and the bytes of
+// workspace (`parts`) for items that they divide.  `own`: partial results of the rows' own keys, of a
+// kernel launched before on the same stream, to be joined.
+struct KxPlan {
+  int ctas;
+  int64_t bytes;
+};
+constexpr int KX_FROM = 9;                 // query vectors per KV head of a request from which it is taken
+KxPlan kx_plan(int Hkv, int hd, int G, int B, int max_rows, int max_len);
+cudaError_t kx_launch(const KaArgs& a, const KaArgs* own, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, const KxPlan& p,
+                      float* parts, cudaStream_t st);
 
 // The ranges of a request (grid x) as one cluster where they join in it.
 template <typename... P, typename... A>

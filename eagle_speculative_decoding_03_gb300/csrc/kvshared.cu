@@ -222,19 +222,42 @@ float log2_scale(float scale, int hd) {
   return std::min((scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f, FLT_MAX);
 }
 
-eagle_status_t check_cross(const char* who, const eagle_kv_cache_t* cache, const eagle_kv_cross_t* w, KvPool* pool, KaPlan* p) {
+// How a cross call is cut: by ranges (few query vectors) or in line over the SMs.
+struct CrossPlan {
+  bool wide;
+  KaPlan ranges;
+  KxPlan line;
+};
+CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int max_len, bool may_join) {
+  CrossPlan p;
+  p.wide = static_cast<long long>(max_rows) * G >= KX_FROM;
+  if (p.wide) p.line = kx_plan(c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
+  else p.ranges = ka_plan(c->kind, c->n_kv_heads, G, B, max_rows, max_len, may_join);
+  return p;
+}
+
+eagle_status_t check_cross(const char* who, const eagle_kv_cache_t* cache, const eagle_kv_cross_t* w, KvPool* pool, CrossPlan* p) {
   eagle_status_t r = kv_pool(cache, who, pool);
   if (r != EAGLE_OK) return r;
   if (!w) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null arguments", who);
   r = check_extent(who, w->max_rows, w->max_len);
   if (r == EAGLE_OK) r = check_rows(who, cache->n_kv_heads, cache->head_dim, w->B, w->N, w->n_heads, w->q, w->q_stride, w->out, w->out_stride, w->scale);
   if (r != EAGLE_OK) return r;
-  *p = ka_plan(cache->kind, cache->n_kv_heads, w->n_heads / cache->n_kv_heads, w->B, w->max_rows, w->max_len, true);
-  return check_plan(who, w->B, *p);
+  *p = cross_plan(cache, w->n_heads / cache->n_kv_heads, w->B, w->max_rows, w->max_len, true);
+  return p->wide ? EAGLE_OK : check_plan(who, w->B, p->ranges);
+}
+
+int64_t cross_bytes(const eagle_kv_cross_t* w, int hd, const CrossPlan& p) {
+  if (p.wide) return p.line.bytes;
+  return p.ranges.splits == 1 || p.ranges.joined ? 0 : p.ranges.splits * ka_part_bytes(w->N, w->n_heads, hd);
+}
+
+int64_t shared_bytes(const eagle_kv_attention_t* w, int hd, const CrossPlan& pre, const KaPlan& own) {
+  return (own.splits + (pre.wide ? 0 : pre.ranges.splits)) * ka_part_bytes(w->N, w->n_heads, hd) + (pre.wide ? pre.line.bytes : 0);
 }
 
 eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* g, const eagle_kv_cache_t* cache,
-                            const eagle_kv_attention_t* w, KvPool* pre, KvPool* own, KaPlan* pp, KaPlan* po) {
+                            const eagle_kv_attention_t* w, KvPool* pre, KvPool* own, CrossPlan* pp, KaPlan* po) {
   eagle_status_t r = kv_pool(prefix, who, pre);
   if (r == EAGLE_OK) r = kv_pool(cache, who, own);
   if (r != EAGLE_OK) return r;
@@ -249,9 +272,9 @@ eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, con
   if (w->mask && (w->mask_slots < 1 || w->mask_slots > 64 || w->max_rows > w->mask_slots))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: a mask needs max_rows <= mask_slots <= 64", who);
   const int G = w->n_heads / cache->n_kv_heads;
-  *pp = ka_plan(prefix->kind, prefix->n_kv_heads, G, g->n_groups, g->max_rows, g->max_len, false);
+  *pp = cross_plan(prefix, G, g->n_groups, g->max_rows, g->max_len, false);
   *po = ka_plan(cache->kind, cache->n_kv_heads, G, w->B, w->max_rows, w->max_len, false);
-  r = check_plan(who, g->n_groups, *pp);
+  if (!pp->wide) r = check_plan(who, g->n_groups, pp->ranges);
   return r != EAGLE_OK ? r : check_plan(who, w->B, *po);
 }
 
@@ -259,9 +282,9 @@ eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, con
 
 extern "C" int64_t eagle_kv_cross_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* w) {
   KvPool pool;
-  KaPlan p;
+  CrossPlan p;
   if (check_cross("kv_cross_attention_workspace", cache, w, &pool, &p) != EAGLE_OK) return -1;
-  return p.splits == 1 || p.joined ? 0 : p.splits * ka_part_bytes(w->N, w->n_heads, cache->head_dim);
+  return cross_bytes(w, cache->head_dim, p);
 }
 
 extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* w, uint32_t* err_word,
@@ -270,11 +293,11 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
   if (w && (!err_word || !w->cu_rows || !w->lens || !w->q || !w->out)) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: null pointer argument", who);
   KaArgs a;
   memset(&a, 0, sizeof(a));
-  KaPlan p;
+  CrossPlan p;
   eagle_status_t r = check_cross(who, cache, w, &a.pool, &p);
   if (r != EAGLE_OK) return r;
-  const bool f4 = cache->kind == EAGLE_CACHE_F4, separate = p.splits > 1 && !p.joined;
-  const int64_t need = separate ? p.splits * ka_part_bytes(w->N, w->n_heads, cache->head_dim) : 0;
+  const bool f4 = cache->kind == EAGLE_CACHE_F4, separate = !p.wide && p.ranges.splits > 1 && !p.ranges.joined;
+  const int64_t need = cross_bytes(w, cache->head_dim, p);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || !aligned(w->workspace)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
@@ -296,13 +319,13 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
   a.out_ld = w->out_stride;
   a.lse = w->lse;
   a.part_o = static_cast<float*>(w->workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(p.splits) * w->N * w->n_heads * cache->head_dim);
+  if (separate) a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(p.ranges.splits) * w->N * w->n_heads * cache->head_dim);
   a.err = err_word;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tmk, tmv;
   r = page_maps(who, cache, &tmk, &tmv);
   if (r != EAGLE_OK) return r;
-  cudaError_t e = ka_launch(&a, p, f4, tmk, tmv, st);
+  cudaError_t e = p.wide ? kx_launch(a, nullptr, f4, tmk, tmv, p.line, a.part_o, st) : ka_launch(&a, p.ranges, f4, tmk, tmv, st);
   if (e == cudaSuccess && separate) e = ka_combine(a, st);
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }
@@ -310,9 +333,10 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
 extern "C" int64_t eagle_kv_shared_attention_workspace(const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* g,
                                                        const eagle_kv_cache_t* cache, const eagle_kv_attention_t* w) {
   KvPool pre, own;
-  KaPlan pp, po;
+  CrossPlan pp;
+  KaPlan po;
   if (check_shared("kv_shared_attention_workspace", prefix, g, cache, w, &pre, &own, &pp, &po) != EAGLE_OK) return -1;
-  return (pp.splits + po.splits) * ka_part_bytes(w->N, w->n_heads, cache->head_dim);
+  return shared_bytes(w, cache->head_dim, pp, po);
 }
 
 extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* g,
@@ -324,11 +348,13 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   KaArgs a, x;                               // the own keys, the prefix
   memset(&a, 0, sizeof(a));
   memset(&x, 0, sizeof(x));
-  KaPlan pp, po;
+  CrossPlan pp;
+  KaPlan po;
   eagle_status_t r = check_shared(who, prefix, g, cache, w, &x.pool, &a.pool, &pp, &po);
   if (r != EAGLE_OK) return r;
   const int hd = cache->head_dim;
-  const int64_t need = (pp.splits + po.splits) * ka_part_bytes(w->N, w->n_heads, hd);
+  const int64_t need = shared_bytes(w, hd, pp, po);
+  const int ranges = po.splits + (pp.wide ? 0 : pp.ranges.splits);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || !aligned(w->workspace)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
@@ -352,7 +378,7 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   a.out_ld = w->out_stride;
   a.lse = w->lse;
   a.part_o = static_cast<float*>(w->workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (pp.splits + po.splits) * outs * hd);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + ranges * outs * hd);
   a.err = err_word;
   const KvPool pool = x.pool;
   x = a;
@@ -369,16 +395,18 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   x.part_o = a.part_o + po.splits * outs * hd;
   x.part_ml = a.part_ml + po.splits * outs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUtensorMap tmk, tmv;
-  r = page_maps(who, prefix, &tmk, &tmv);
+  CUtensorMap tmk, tmv, pmk, pmv;
+  r = page_maps(who, cache, &tmk, &tmv);
+  if (r == EAGLE_OK) r = page_maps(who, prefix, &pmk, &pmv);
   if (r != EAGLE_OK) return r;
-  cudaError_t e = ka_launch(&x, pp, prefix->kind == EAGLE_CACHE_F4, tmk, tmv, st);
-  if (e == cudaSuccess) {
-    r = page_maps(who, cache, &tmk, &tmv);
-    if (r != EAGLE_OK) return r;
-    e = ka_launch(&a, po, cache->kind == EAGLE_CACHE_F4, tmk, tmv, st);
+  const bool pf4 = prefix->kind == EAGLE_CACHE_F4;
+  cudaError_t e = ka_launch(&a, po, cache->kind == EAGLE_CACHE_F4, tmk, tmv, st);
+  if (e == cudaSuccess && pp.wide) {
+    e = kx_launch(x, &a, pf4, pmk, pmv, pp.line, reinterpret_cast<float*>(a.part_ml + ranges * outs), st);
+  } else if (e == cudaSuccess) {
+    e = ka_launch(&x, pp.ranges, pf4, pmk, pmv, st);
+    if (e == cudaSuccess) e = hd == 64 ? launch_join<64>(a, x, st) : launch_join<128>(a, x, st);
   }
-  if (e == cudaSuccess) e = hd == 64 ? launch_join<64>(a, x, st) : launch_join<128>(a, x, st);
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }
 

@@ -84,7 +84,7 @@ def test_other_refusals(lib):  # noqa: F811
     assert need > 0
     for ws in (dict(), dict(workspace=P, workspace_bytes=need - 1), dict(workspace=P + 8, workspace_bytes=need)):
         assert lib.eagle_kv_cross_attention(c, C.byref(cross(**many, **ws)), P, None) == 1
-    assert lib.eagle_kv_cross_attention(c, C.byref(cross(B=40000, max_rows=20000)), P, None) == 2
+    assert lib.eagle_kv_cross_attention(c, C.byref(cross(B=70000)), P, None) == 2
     # q and out as slices of one buffer: rows that interleave are taken, rows that meet refused
     wide = dict(q_stride=8192, out_stride=8192, N=0)
     assert lib.eagle_kv_cross_attention(c, C.byref(cross(out=P + 4096, **wide)), P, None) == 0
