@@ -28,20 +28,26 @@ using namespace eagle;
 namespace {
 
 constexpr int KX_QV = 256;                 // query vectors of a block
+static_assert(KX_QV == 1 << 8, "Line divides by a shift");
 constexpr int KX_DESCS = 4;                // segments in flight between the scheduler and the roles
 constexpr int KX_MIN_UNITS = 3;            // units that are worth a CTA
-constexpr uint32_t KX_MISC = 3072;         // barriers (0), segments (512), the states of an item that both groups take (1024)
+// barriers (0), segments (640), exchange between warps (1024), score factors (3072, 4 bits)
+__host__ __device__ constexpr uint32_t kx_misc(int cache) { return cache == EAGLE_CACHE_F4 ? 5120 : 3072; }
+constexpr int KX_SOFTMAX = 512;            // softmax threads: two per query vector
 // registers per thread of the 4-bit kernel's roles (the launch checks their sum)
-constexpr int KX_REG_CTRL = 56, KX_REG_SOFTMAX = 144, KX_REG_CONV = 64;
+constexpr int KX_REG_CTRL = 40, KX_REG_SOFTMAX = 88, KX_REG_CONV = 56;
 constexpr int KX_JOIN_V = 32, KX_JOIN_WARPS = 8;
 
-__host__ __device__ constexpr int kx_threads(int cache) { return 384 + (cache == EAGLE_CACHE_F4 ? 256 : 0); }
+__host__ __device__ constexpr int kx_threads(int cache) { return 128 + KX_SOFTMAX + (cache == EAGLE_CACHE_F4 ? 256 : 0); }
 // floats of a partial result: [hd / 4][256] float4 outputs, [256] (maximum, sum)
 __host__ __device__ constexpr size_t kx_slot(int hd) { return static_cast<size_t>(KX_QV) * (hd + 2); }
 
 // Part of an item: tiles [t0, t0 + T) of query vectors [v0, v0 + qv) of sequence b.
 struct Seg {
   int valid, b, kvh, row0, len, v0, qv, t0, T, slot;   // slot: partial result, -1: the item is whole
+  // both groups have the same vectors, every other tile each
+  EAGLE_DEV bool both() const { return qv <= KA_QV; }
+  EAGLE_DEV bool tiles_of(int g) const { return T > (both() ? g : 0); }
 };
 
 // How the units lie in line: per sequence b, KV heads x blocks x tiles (at least 1, to write the
@@ -51,11 +57,15 @@ struct Line {
   int blocks, tiles;
   EAGLE_DEV Line(const KaArgs& a, int b) {
     rq = request(a, b);
-    blocks = (static_cast<long long>(rq.R) * a.G + KX_QV - 1) / KX_QV;
+    blocks = static_cast<int>((static_cast<long long>(rq.R) * a.G + KX_QV - 1) >> 8);
     tiles = max((rq.len + KA_CH - 1) / KA_CH, 1);
   }
   EAGLE_DEV long long units(const KaArgs& a) const { return static_cast<long long>(a.pool.Hkv) * blocks * tiles; }
 };
+// x / y (x >= 0, y > 0), by 32 bits where they do
+EAGLE_DEV long long quotient(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
 // Units of the call, and of a CTA.  By a whole warp.
 EAGLE_DEV long long all_units(const KaArgs& a, int lane) {
   long long n = 0;
@@ -65,7 +75,7 @@ EAGLE_DEV long long all_units(const KaArgs& a, int lane) {
   for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
   return n;
 }
-EAGLE_DEV long long units_per_cta(long long all, int ctas) { return max((all + ctas - 1) / ctas, static_cast<long long>(KX_MIN_UNITS)); }
+EAGLE_DEV long long units_per_cta(long long all, int ctas) { return max(quotient(all + ctas - 1, ctas), static_cast<long long>(KX_MIN_UNITS)); }
 // The sequence that holds unit u, and u's place among its units.  By a whole warp.
 EAGLE_DEV int find_unit(const KaArgs& a, int lane, long long u, long long* rest) {
   for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -117,13 +127,58 @@ EAGLE_DEV void add_part(float* x, float f, float4 y) {
   x[3] = fmaf(f, y.w, x[3]);
 }
 
+// 32 scores x -> p = 2^(x rs - mb), packed two to a word (fp16 or bf16), their sum into p8; MORE: and the
+// largest of them and of 32 others.  The pipes need 4 cycles a warp for each ex2 and 2 for each maximum,
+// product, sum and conversion of a pair: in the order written (volatile), the products two pairs ahead
+// of ex2, sums and conversions four behind, they overlap.
+EAGLE_DEV void ordered_max3(float& m, float x, float y) { asm volatile("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(x), "f"(y)); }
+EAGLE_DEV void ordered_exp2(float& x) { asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x)); }
+EAGLE_DEV void ordered_fma2(float& x, float& y, float a, float b) {
+  asm volatile("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\tfma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+               : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+EAGLE_DEV void ordered_add2(float& x, float& y, float z, float w) {
+  asm volatile("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+               : "+f"(x), "+f"(y) : "f"(z), "f"(w));
+}
+template <bool F16>
+EAGLE_DEV float ordered_pack(float lo, float hi) {
+  uint32_t r;
+  if constexpr (F16) asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return __uint_as_float(r);
+}
+template <bool F16, bool MORE>
+EAGLE_DEV float powers32(float* x, const float* others, float rs, float mb, float* p8, float* pk) {
+  constexpr int AHEAD = 2, BEHIND = 4;
+  float m[4] = {x[0], x[2], x[4], x[6]};
+#pragma unroll
+  for (int i = -AHEAD; i < 16 + BEHIND; ++i) {
+    const int u = i + AHEAD, w = i - BEHIND;
+    if (i >= 0 && i < 16) ordered_exp2(x[2 * i]);
+    if (u < 16) {
+      if (MORE) ordered_max3(m[u & 3], x[2 * u], x[2 * u + 1]);
+      ordered_fma2(x[2 * u], x[2 * u + 1], rs, -mb);
+    }
+    if (i >= 0 && i < 16) {
+      ordered_exp2(x[2 * i + 1]);
+      if (MORE) ordered_max3(m[i & 3], others[2 * i], others[2 * i + 1]);
+    }
+    if (w >= 0) {
+      ordered_add2(p8[(2 * w) & 7], p8[((2 * w) & 7) + 1], x[2 * w], x[2 * w + 1]);
+      pk[w] = ordered_pack<F16>(x[2 * w], x[2 * w + 1]);
+    }
+  }
+  return max_nan(max3_nan(m[0], m[1], m[2]), m[3]);
+}
+
 template <int HD, int CACHE>
 __global__ void __launch_bounds__(kx_threads(CACHE), 1)
 kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const KaArgs a, const KaArgs own,
               const int with_own, float* parts, const int NS) {
   constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
   constexpr float LIFT = F4 ? 7.f : 0.f;     // fp16 p is held times 2^7 (as in kv_attention_tc)
-  constexpr int THREADS = kx_threads(CACHE), CONV_WARP = 12, CONV = THREADS - 32 * CONV_WARP;
+  constexpr int THREADS = kx_threads(CACHE), CONV_WARP = 4 + KX_SOFTMAX / 32, CONV = THREADS - 32 * CONV_WARP;
   constexpr uint32_t ENTRY = ka_entry(HD), HALF = KA_CH * 128, RAW = ka_raw_bytes(HD), RAW_SCALES = HD / 2 * KA_CH;
   constexpr uint32_t T_O = 256;
   extern __shared__ __align__(1024) uint8_t kx_sm[];   // (no byte is left to align it by hand: ring, queries, misc take all)
@@ -134,16 +189,16 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   uint8_t* raw = sm + static_cast<uint32_t>(NS + 2) * ENTRY;
   uint8_t* misc = raw + (F4 ? KA_RAW * RAW : 0);
   const uint32_t misc_u = smem_u32(misc);
-  // ring full / free, scores there, first / second half of p there, P V done, queries there, raw
-  // tiles full / free, segments full / free, the two groups' states exchanged / read
+  // ring full / free, scores there, first / second part of p there, P V done, queries there, segment
+  // done, raw tiles full / free, segments full / free, an item of both groups: states there / read,
+  // the two warps of 32 vectors
   const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 240, bar_pe = misc_u + 272,
                  bar_q = misc_u + 288, bar_fin = misc_u + 304, bar_rf = misc_u + 320, bar_re = misc_u + 344, bar_df = misc_u + 368,
-                 bar_de = misc_u + 400, bar_x = misc_u + 432;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 448);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 452);
-  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 456);
-  Seg* segs = reinterpret_cast<Seg*>(misc + 512);
-  float2* states = reinterpret_cast<float2*>(misc + 1024);   // [2][128]
+                 bar_de = misc_u + 400, bar_x = misc_u + 432, bar_m = misc_u + 448;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 512);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 516);
+  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 520);
+  Seg* segs = reinterpret_cast<Seg*>(misc + 640);
 
   pdl_trigger();
   if (ring_u & 1023u) {                      // (the swizzled tiles' alignment)
@@ -157,12 +212,13 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bar_sf + 8 * g, 1);
-      mbar_init(bar_pf + 16 * g, 4);
-      mbar_init(bar_pf + 16 * g + 8, 4);
+      mbar_init(bar_pf + 16 * g, 8);
+      mbar_init(bar_pf + 16 * g + 8, 8);
       mbar_init(bar_pe + 8 * g, 1);
-      mbar_init(bar_q + 8 * g, 4);
+      for (int w = 0; w < 4; ++w) mbar_init(bar_m + 32 * g + 8 * w, 2);
+      mbar_init(bar_q + 8 * g, 8);
       mbar_init(bar_fin + 8 * g, 1);
-      mbar_init(bar_x + 8 * g, 8);
+      mbar_init(bar_x + 8 * g, KX_SOFTMAX / 32);
     }
     for (int s = 0; F4 && s < KA_RAW; ++s) {
       mbar_init(bar_rf + 8 * s, 1);
@@ -170,7 +226,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     }
     for (int s = 0; s < KX_DESCS; ++s) {
       mbar_init(bar_df + 8 * s, 1);
-      mbar_init(bar_de + 8 * s, 3 + 8 + (F4 ? CONV / 32 : 0));
+      mbar_init(bar_de + 8 * s, 3 + KX_SOFTMAX / 32 + (F4 ? CONV / 32 : 0));
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -269,11 +325,11 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
             ++b;
             l = Line(a, b);
           }
-          const long long item = rest / l.tiles;
+          const long long item = quotient(rest, l.tiles);
           s.valid = 1;
           s.b = b;
           s.t0 = static_cast<int>(rest - item * l.tiles);
-          s.kvh = static_cast<int>(item / l.blocks);
+          s.kvh = static_cast<int>(quotient(item, l.blocks));
           s.row0 = l.rq.row0;
           s.len = l.rq.len;
           s.v0 = static_cast<int>(item - static_cast<long long>(s.kvh) * l.blocks) * KX_QV;
@@ -305,13 +361,17 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
       const uint32_t tS = tmem + 128 * g, tO = tmem + T_O + 128 * g;
       RingPos base{0, 0};                    // the segment's first entry
-      uint32_t n = 0, turn = 0;              // tiles of this group so far; segments
-      for (;; dp.step(1, KX_DESCS), turn ^= 1) {
+      uint32_t n = 0, other = 0, turn = 0;   // tiles of this group so far, of the other one; segments with a tile
+      bool after_1 = false;                  // the last segment's last tile was group 1's
+      for (;; dp.step(1, KX_DESCS)) {
         const Seg s = segment(dp);
         if (!ok || !s.valid) break;
-        const bool both = s.qv <= KA_QV;     // both groups have the same vectors, every other tile each
+        const bool both = s.both(), work = s.tiles_of(g);
         const int step = both ? 2 : 1;
-        ok = mbar_wait(bar_q + 8 * g, turn, a.err, abort_flag);
+        if (work) {
+          ok = mbar_wait(bar_q + 8 * g, turn, a.err, abort_flag);
+          turn ^= 1;
+        }
         tc_fence_after();
         RingPos kp = base;
         if (both && g) kp.step(2, NS);
@@ -319,6 +379,13 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           RingPos vp = kp;
           vp.step(1, NS);
           ok = mbar_wait(bar_kvf + 8 * kp.slot, kp.turn, a.err, abort_flag);
+          // The groups take turns, in one order for the whole call: a tile's scores start when those of
+          // the tile before, where that is the other group's, are there.  So one group's softmax falls on
+          // the other's products; left to themselves they fall into step, both waiting for their softmax
+          // at once.  (The other group's next scores come after this tile in the order, so the barrier
+          // cannot be a turn ahead.)
+          const uint32_t before = other + (both ? t >> 1 : t) + g - 1;
+          if (g || t || after_1) ok = ok && mbar_wait(bar_sf + 8 * (g ^ 1), before & 1, a.err, abort_flag);
           if (n) ok = ok && mbar_wait(bar_pe + 8 * g, (n - 1) & 1, a.err, abort_flag);   // (P lies over S)
           if (!ok) break;
           tc_fence_after();
@@ -340,7 +407,10 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int j = 4 * h; j < 4 * h + 4; ++j) tc_mma_bf16_ta(tO, tS + 8 * j, dv + j * 128, id2, first && j == 0 ? 0u : 1u);
+            for (int x = 0; x < 4; ++x) {    // keys 16 j .. 16 j + 15: part h is 32 keys of each half
+              const int j = 4 * (x >> 1) + 2 * h + (x & 1);
+              tc_mma_bf16_ta(tO, tS + KA_H * (j >> 2) + 8 * (j & 3), dv + j * 128, id2, first && h == 0 && x == 0 ? 0u : 1u);
+            }
           }
           if (!ok) break;
           tc_commit(bar_pe + 8 * g);
@@ -350,7 +420,9 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           if (both) kp.step(2, NS);
         }
         if (!ok) break;
-        tc_commit(bar_fin + 8 * g);
+        other += both ? (s.T + g) >> 1 : s.T;
+        if (s.T > 0) after_1 = !both || (s.T & 1) == 0;
+        if (work) tc_commit(bar_fin + 8 * g);
         const uint32_t at = base.slot + 2u * s.T;
         base.turn ^= (at / NS) & 1;
         base.slot = at % NS;
@@ -426,193 +498,178 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   } else {
     if constexpr (F4) set_regs_up<KX_REG_SOFTMAX>();
     // ------------------------------------------------------------ softmax of group g
-    const int g = (warp - 4) >> 2, lv = (tid - 128) & 127;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lane_base + 128 * g, to = tmem + lane_base + T_O + 128 * g;
+    // Two threads per vector: half hf has columns [64 hf, 64 hf + 64) of the scores.  (Latencies of TMEM
+    // and barriers of one warp fall on the ex2 of the other; one thread per vector takes 1530 cycles
+    // from the scores to the last p.)
+    const int g = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, quad = warp & 3, lv = 32 * quad + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t ts = tmem + lane_base + 128 * g + KA_H * hf, to = tmem + lane_base + T_O + 128 * g;
     const int ps = 1 << a.pool.ps_log;
-    // this thread's vector of a segment into the group's query tile; returns its score factor
+    float2* states = reinterpret_cast<float2*>(misc + 1024);                  // [group][128]
+    float* xch = reinterpret_cast<float*>(misc + 1024) + (4 * g + quad) * 64;   // the pair's [2][32], in the same place
+    float* factors = reinterpret_cast<float*>(misc + 3072) + (4 * g + quad) * 32;
+    const uint32_t bar_pair = bar_m + 32 * g + 8 * quad;
+    uint32_t mturn = 0;
+    auto pair_arrive = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_pair);
+    };
+    auto pair_wait = [&]() {
+      ok = mbar_wait(bar_pair, mturn, a.err, abort_flag) && ok;
+      mturn ^= 1;
+    };
+    // 16 of the pair's 32 vectors of a segment into the group's query tile, LR lanes a row (a lane a row
+    // would touch 32 rows with every load: 4096 cycles a segment)
     auto stage = [&](const Seg& s) {
-      const int v = s.v0 + lv + (s.qv <= KA_QV ? 0 : KA_QV * g);
+      constexpr int LR = HD / 8, ROWS = 32 / LR, N = 16 / ROWS;   // lanes a row, rows a load, loads
+      const int v = s.v0 + lv + (s.both() ? 0 : KA_QV * g), c = lane % LR, i = v / a.G;
       const bool live = v - s.v0 < s.qv;
-      float rs = a.scale_log2 * (F4 ? a.pool.kg : 1.f), up = 1.f;
-      const int i = v / a.G;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (s.row0 + (live ? i : 0)) * a.q_ld +
-                                                        static_cast<long long>(s.kvh * a.G + (live ? v - i * a.G : 0)) * HD);
-      if (F4) {   // (a power of two, so that the largest magnitude lies in [2^14, 2^15))
-        uint32_t top = 0;
-#pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint4 x = __ldg(src + c);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const long long at = live ? (s.row0 + i) * a.q_ld + static_cast<long long>(s.kvh * a.G + v - i * a.G) * HD : -1;
+      uint4 x[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const long long from = __shfl_sync(0xffffffffu, at, 16 * hf + ROWS * k + lane / LR);
+        x[k] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + from) + c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        const int r = 16 * hf + ROWS * k + lane / LR;
+        if (F4) {   // fp16, times a power of two: the vector's largest magnitude lies in [2^14, 2^15)
+          uint32_t top = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        }
-        int ex = static_cast<int>(top >> 7);
-        ex = ex == 255 ? 127 : max(ex, 30);
-        up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
-        rs = finite_scale(rs * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23));
-      }
-#pragma unroll 1
-      for (int c0 = 0; c0 < HD / 8; c0 += 4) {
-        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 x = live ? __ldg(src + c0 + c) : make_uint4(0u, 0u, 0u, 0u);
-          w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
-        }
-        if (F4) {
+          for (int d = 1; d < LR; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          int ex = static_cast<int>(top >> 7);
+          ex = ex == 255 ? 127 : max(ex, 30);  // (infinities and NaN pass; tiny vectors)
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - ex) << 23);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+          for (int e = 0; e < 4; ++e) w[e] = pack_f16(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+          if (c == 0) factors[r] = finite_scale(a.scale_log2 * a.pool.kg * __uint_as_float(static_cast<uint32_t>(ex - 14) << 23));
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) st_smem16(q_u + g * ENTRY + ((c0 + c) >> 3) * HALF + ka_sw(lv, (c0 + c) & 7), w + 4 * c);
+        st_smem16(q_u + g * ENTRY + (c >> 3) * HALF + ka_sw(32 * quad + r, c & 7), w);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_q + 8 * g);
-      return rs;
     };
-    uint32_t n = 0, turn = 0, xturn = 0;     // tiles of this group so far; segments; items that both groups took
+    // the score factor of this thread's vector, once both warps have staged
+    auto factor = [&]() {
+      if (!F4) return a.scale_log2;
+      pair_arrive();
+      pair_wait();
+      return factors[lane];
+    };
+    uint32_t n = 0, turn = 0, xturn = 0;     // tiles of this group so far; segments with a tile; items that both groups took
     bool waited = false;                     // for the own keys' results
     Seg s = segment(dp);
-    float rs = 0.f;
-    if (s.valid) rs = stage(s);
+    if (__all_sync(0xffffffffu, ok && s.valid && s.tiles_of(g))) stage(s);
     while (__all_sync(0xffffffffu, ok && s.valid)) {
-      const bool both = s.qv <= KA_QV;
+      const bool both = s.both(), work = s.tiles_of(g);
+      const float rs = work ? factor() : 0.f;
       const int step = both ? 2 : 1;
-      const bool idle = both && 32 * (warp & 3) >= s.qv;   // a warp without vectors
+      const bool idle = 32 * quad >= s.qv - (both ? 0 : KA_QV * g);   // a pair without vectors
       const int end_page = s.len >> a.pool.ps_log, end_rows = F4 ? 0 : s.len & (ps - 1);
       float m_run = -INFINITY, l_run = 0.f;
-      int t = both ? g : 0;
-      for (; t < s.T; t += step, ++n) {
+      for (int t = both ? g : 0; t < s.T; t += step, ++n) {
         ok = ok && mbar_wait(bar_sf + 8 * g, n & 1, a.err, abort_flag);
         tc_fence_after();
         if (!idle) {
-          float x[64], y[32];
-          tmem_ld32(ts, x);
-          tmem_ld32(ts + 32, x + 32);
-          tmem_ld32(ts + 64, y);
-          const int kt = (s.t0 + t) * KA_CH;
-          // the columns that hold keys; the page that the keys end inside has them at its end
-          const bool whole = kt + KA_CH <= s.len;
-          Bits vis{~0ull, ~0ull};
-          if (!whole) {
-            const int at = (end_page << a.pool.ps_log) - kt;
-            vis = bits_below(end_rows ? at + ps : s.len - kt);
-            if (end_rows) {
-              const Bits lo = bits_below(at), hi = bits_below(at + ps - end_rows);
-              vis.lo &= lo.lo | ~hi.lo;
-              vis.hi &= lo.hi | ~hi.hi;
+          // The first 32 scores become p with the maximum so far, which mostly stays, while this tile's
+          // is found; where that rose too far they are read again.
+          float x[KA_H], p8[8], pk[16];
+          for (bool again = false;;) {
+            tmem_ld32(ts, x);
+            tmem_ld32(ts + 32, x + 32);
+            const int kt = (s.t0 + t) * KA_CH;
+            tmem_wait_ld();
+            if (kt + KA_CH > s.len) {        // columns without a key; the page that the keys end inside has its own at its end
+              const int at = (end_page << a.pool.ps_log) - kt;
+              Bits vis = bits_below(end_rows ? at + ps : s.len - kt);
+              if (end_rows) {
+                const Bits lo = bits_below(at), hi = bits_below(at + ps - end_rows);
+                vis.lo &= lo.lo | ~hi.lo;
+                vis.hi &= lo.hi | ~hi.hi;
+              }
+              const unsigned long long bits = hf ? vis.hi : vis.lo;
+#pragma unroll
+              for (int e = 0; e < KA_H; ++e) x[e] = (bits >> e) & 1ull ? x[e] : -INFINITY;
             }
-          }
-          auto hide = [&](float* f, unsigned bits) {
+            // (a row without a key so far takes the maximum as 0: every score is -inf, every p is 0)
+            const float mb = (m_run == -INFINITY ? 0.f : m_run * rs) - LIFT;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = (bits >> e) & 1u ? f[e] : -INFINITY;
-          };
-          auto top32 = [&](const float* f, float m) {
-            float m4[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m4[k] = max_nan(f[k], f[k + 4]);
-#pragma unroll
-            for (int e = 8; e < 32; e += 8)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) m4[k] = max3_nan(m4[k], f[e + k], f[e + 4 + k]);
-            return max_nan(max3_nan(m4[0], m4[1], m4[2]), max_nan(m4[3], m));
-          };
-          tmem_wait_ld();
-          if (!whole) {
-            hide(x, static_cast<unsigned>(vis.lo));
-            hide(x + 32, static_cast<unsigned>(vis.lo >> 32));
-            hide(y, static_cast<unsigned>(vis.hi));
-          }
-          float mt = top32(y, -INFINITY);
-          tmem_ld32(ts + 96, y);
-          mt = top32(x + 32, top32(x, mt));
-          tmem_wait_ld();
-          if (!whole) hide(y, static_cast<unsigned>(vis.hi >> 32));
-          mt = top32(y, mt);
-          float f = 1.f;
-          bool resc = false;
-          if (mt != -INFINITY) {
-            if (m_run == -INFINITY) {
-              m_run = mt;
-            } else if ((mt - m_run) * rs > KA_RESCALE) {
-              f = fast_exp2((m_run - mt) * rs);
-              m_run = mt;
-              resc = true;
-            }
-          }
-          if (__any_sync(0xffffffffu, resc)) {   // (the scores are there, so the P V before them is done)
+            for (int e = 0; e < 8; ++e) p8[e] = 0.f;
+            float mt = powers32<F4, true>(x, x + 32, rs, mb, p8, pk);
+            if (again) break;
+            xch[32 * hf + lane] = mt;        // (the other warp read the last tile's before P V, and so before these scores)
+            pair_arrive();
+            pair_wait();
+            mt = max_nan(mt, xch[32 * (hf ^ 1) + lane]);
+            const bool rose = mt != -INFINITY && (m_run == -INFINITY || (mt - m_run) * rs > KA_RESCALE);
+            if (!__any_sync(0xffffffffu, rose)) break;
+            const bool resc = rose && m_run != -INFINITY;
+            const float f = resc ? fast_exp2((m_run - mt) * rs) : 1.f;
+            if (rose) m_run = mt;
+            if (__any_sync(0xffffffffu, resc)) {   // (the scores are there, so the P V before them is done)
 #pragma unroll 1
-            for (int c0 = 0; c0 < HD; c0 += 32) {
-              float z[32];
-              tmem_ld32(to + c0, z);
-              tmem_wait_ld();
-              uint32_t w[32];
+              for (int c0 = 0; c0 < HD / 2; c0 += 16) {
+                float z[16];
+                tmem_ld16(to + hf * (HD / 2) + c0, z);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(z[e] * f);
-              tmem_st32(to + c0, w);
+                for (int e = 0; e < 16; ++e) z[e] *= f;
+                tmem_st16(to + hf * (HD / 2) + c0, z);
+              }
             }
+            l_run *= f;
+            again = true;
           }
-          l_run *= f;
-          const float mb = (m_run == -INFINITY ? 0.f : m_run * rs) - LIFT;
-          float p8[8] = {};
-          // 32 scores -> p -> 16 packed columns
-          auto turn32 = [&](float* z, uint32_t dst) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              fma2(z[e], z[e + 1], rs, -mb);
-              z[e] = fast_exp2(z[e]);
-              z[e + 1] = fast_exp2(z[e + 1]);
-              add2(p8[e & 7], p8[(e & 7) + 1], z[e], z[e + 1]);
-            }
-            float pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = __uint_as_float(F4 ? pack_f16(z[2 * e], z[2 * e + 1]) : pack_bf16(z[2 * e], z[2 * e + 1]));
-            tmem_st16(dst, pk);
-          };
-          turn32(x, ts);
-          turn32(x + 32, ts + 16);
+          tmem_st16(ts, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_pf + 16 * g);
-          tmem_ld32(ts + 64, x);
-          turn32(y, ts + 48);
-          tmem_wait_ld();
-          if (!whole) hide(x, static_cast<unsigned>(vis.hi));
-          turn32(x, ts + 32);
+          powers32<F4, false>(x + 32, x, rs, (m_run == -INFINITY ? 0.f : m_run * rs) - LIFT, p8, pk);
+          tmem_st16(ts + 16, pk);
           tmem_wait_st();
-          l_run += ((p8[0] + p8[1]) + (p8[2] + p8[3])) + ((p8[4] + p8[5]) + (p8[6] + p8[7]));
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_pf + 16 * g + 8);
+          l_run += ((p8[0] + p8[1]) + (p8[2] + p8[3])) + ((p8[4] + p8[5]) + (p8[6] + p8[7]));
         } else if (lane == 0) {
           mbar_arrive(bar_pf + 16 * g);
           mbar_arrive(bar_pf + 16 * g + 8);
         }
       }
-      // ---- the next segment's queries, as soon as this one's are read (its last scores are there; a
-      // group without a tile waits for its MMA thread, which would otherwise miss the barrier's turn)
-      const bool early = s.T > (both ? g : 0);
+      // ---- the next segment's queries, as soon as this one's are read (its last scores are there).
+      // The barriers of queries and of the segment's end turn only in segments where the group has a
+      // tile: each of their turns then waits for every warp to have seen the one before.
       RingPos np = dp;
       np.step(1, KX_DESCS);
-      float rs2 = 0.f;
-      if (!early) ok = mbar_wait_sleepy(bar_fin + 8 * g, turn, a.err, abort_flag) && ok;
       const bool so_far = ok;
       const Seg s2 = segment(np);
       ok = __all_sync(0xffffffffu, ok && so_far);
-      if (ok && s2.valid) rs2 = stage(s2);
-      if (early) ok = mbar_wait(bar_fin + 8 * g, turn, a.err, abort_flag) && ok;
-      turn ^= 1;
+      if (ok && s2.valid && s2.tiles_of(g)) stage(s2);
+      if (work) {
+        ok = mbar_wait(bar_fin + 8 * g, turn, a.err, abort_flag) && ok;
+        turn ^= 1;
+      }
       tc_fence_after();
-      // ---- this segment's result: of state g alone, or of both groups' (then half of the dims each)
+      // ---- this segment's result: half of the dims of state g, or a quarter of both groups' states
       const int v = s.v0 + lv + (both ? 0 : KA_QV * g), i = v / a.G, h = s.kvh * a.G + (v - i * a.G);
       const bool live = v - s.v0 < s.qv;
+      if (!idle) {
+        xch[32 * hf + lane] = l_run;
+        pair_arrive();
+        pair_wait();
+        l_run += xch[32 * (hf ^ 1) + lane];
+        pair_arrive();                       // (both have read)
+        pair_wait();
+      }
       float2 st[2] = {make_float2(l_run == 0.f ? -INFINITY : m_run * rs - LIFT, l_run), make_float2(-INFINITY, 0.f)};
       if (both) {
-        states[128 * g + lv] = st[0];
+        if (hf == 0) states[128 * g + lv] = st[0];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_x);
         ok = mbar_wait(bar_x, xturn, a.err, abort_flag) && ok;
@@ -621,15 +678,16 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         st[1] = states[128 + lv];
       }
       const uint32_t o0 = tmem + lane_base + T_O + (both ? 0 : 128 * g), o1 = tmem + lane_base + T_O + 128;
-      const int c_lo = both ? g * (HD / 2) : 0, c_hi = both ? c_lo + HD / 2 : HD;
+      constexpr int CW = HD / 4, BW = CW / 4;  // dims of a chunk, of a block
+      const int c_lo = both ? (2 * g + hf) * CW : 2 * hf * CW, c_hi = c_lo + (both ? CW : 2 * CW);
       float M = max_nan(st[0].x, st[1].x);
       const bool join = with_own && s.slot < 0;
       if (join && !waited) {
         pdl_wait();
         waited = true;
       }
-      const size_t row = static_cast<size_t>(s.row0 + i);
-      Own mine(own, live && join ? static_cast<int>(row) : -1, h);
+      const int row = s.row0 + i;
+      Own mine(own, live && join ? row : -1, h);
       for (int k = 0; k < mine.used; ++k) M = max_nan(M, mine.ml(k).x);
       const float f0 = part_factor(st[0].x, M), f1 = part_factor(st[1].x, M);
       float L = fmaf(f0, st[0].y, f1 * st[1].y);
@@ -642,61 +700,91 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       const float inv = s.slot >= 0 ? 1.f : none ? 0.f : a.vg / L, own_inv = none ? 0.f : own.vg / L;
       float* part = parts + (s.slot >= 0 ? static_cast<size_t>(s.slot) : 0) * kx_slot(HD);
       const int pv = v - s.v0;
+      // Four lanes' rows in chunks of hd / 4 dims are turned so that four lanes hold one row: a store then
+      // touches 8 rows instead of 32.
+      const long long at = row * a.out_ld + static_cast<long long>(h) * HD;
+      const int ranges = join ? __reduce_max_sync(0xffffffffu, mine.used) : 0;
 #pragma unroll 1
-      for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-        float x[32];
+      for (int c0 = c_lo; c0 < c_hi; c0 += CW) {
+        float x[CW];
         __syncwarp();
-        tmem_ld32(o0 + c0, x);
+        if constexpr (CW == 32) tmem_ld32(o0 + c0, x);
+        else tmem_ld16(o0 + c0, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = f0 == 0.f ? 0.f : f0 * x[e];
+        for (int e = 0; e < CW; ++e) x[e] = f0 == 0.f ? 0.f : f0 * x[e];
         if (both) {
-          float y[32];
-          tmem_ld32(o1 + c0, y);
+          float y[CW];
+          if constexpr (CW == 32) tmem_ld32(o1 + c0, y);
+          else tmem_ld16(o1 + c0, y);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = f1 == 0.f ? x[e] : fmaf(f1, y[e], x[e]);
+          for (int e = 0; e < CW; ++e) x[e] = f1 == 0.f ? x[e] : fmaf(f1, y[e], x[e]);
         }
-        if (!writes) continue;
         if (s.slot >= 0) {
           float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>(c0 / 4) * KX_QV + pv;
+          if (writes) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e * KX_QV] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            for (int e = 0; e < CW / 4; ++e) dst[e * KX_QV] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          }
           continue;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] *= inv;
-        for (int k = 0; k < mine.used; ++k) {
-          const float f = part_factor(mine.ml(k).x, M) * own_inv;
-          const float4* src = reinterpret_cast<const float4*>(own.part_o + mine.place(k) * HD + c0);
+        for (int e = 0; e < CW; ++e) x[e] = none ? 0.f : x[e] * inv;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) add_part(x + 4 * e, f, src[e]);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(a.out + row * a.out_ld + static_cast<long long>(h) * HD + c0);
+        for (int d = 1; d < 4; d <<= 1)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
+          for (int b = 0; b < 4; ++b) {
+            if (b & d) continue;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = none ? 0u : pack_bf16(x[8 * e + 2 * k], x[8 * e + 2 * k + 1]);
-          dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < BW; ++e) {
+              float& lo = x[b * BW + e];
+              float& hi = x[(b + d) * BW + e];
+              const float got = __shfl_xor_sync(0xffffffffu, lane & d ? lo : hi, d);
+              if (lane & d) lo = got;
+              else hi = got;
+            }
+          }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {        // block r: lane's dims [c0 + BW (lane % 4), ...) of row (lane & ~3) + r
+          const int from = (lane & ~3) + r;
+          float* y = x + r * BW;
+          const long long to_row = __shfl_sync(0xffffffffu, at, from);
+          const bool put = __shfl_sync(0xffffffffu, static_cast<int>(writes), from) != 0;
+          const int d0 = c0 + BW * (lane & 3);
+          for (int k = 0; k < ranges; ++k) {
+            float f = 0.f;
+            if (k < mine.used) f = part_factor(mine.ml(k).x, M) * own_inv;
+            f = __shfl_sync(0xffffffffu, f, from);
+            const size_t place = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(mine.place(k)), from);
+            const float4* src = reinterpret_cast<const float4*>(own.part_o + place * HD + d0);
+            if (f != 0.f) {
+#pragma unroll
+              for (int e = 0; e < BW / 4; ++e) add_part(y + 4 * e, f, src[e]);
+            }
+          }
+          if (!put) continue;
+          if constexpr (BW == 8)
+            *reinterpret_cast<uint4*>(a.out + to_row + d0) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+          else *reinterpret_cast<uint2*>(a.out + to_row + d0) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
         }
       }
-      if (writes && (!both || g == 0)) {
+      if (writes && hf == 0 && (!both || g == 0)) {
         if (s.slot >= 0) reinterpret_cast<float2*>(part + static_cast<size_t>(KX_QV) * HD)[pv] = make_float2(none ? -INFINITY : M, L);
-        else if (a.lse) a.lse[row * a.Hq + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        else if (a.lse) a.lse[static_cast<size_t>(row) * a.Hq + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       }
-      if (both) {                            // (both have read O and the states before either goes on)
+      if (both) {                            // (all have read O and the states before any goes on)
         __syncwarp();
         tc_fence_before();
         if (lane == 0) mbar_arrive(bar_x + 8);
         ok = mbar_wait(bar_x + 8, xturn, a.err, abort_flag) && ok;
         xturn ^= 1;
       }
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_de + 8 * dp.slot);
       dp = np;
       s = s2;
-      rs = rs2;
     }
   }
   tc_fence_before();
@@ -721,15 +809,15 @@ __global__ void __launch_bounds__(32 * KX_JOIN_WARPS) kv_cross_wide_join(const K
       long long rest;
       s.b = find_unit(a, lane, end - 1, &rest);
       const Line l(a, s.b);
-      const long long item = rest / l.tiles, first = end - 1 - (rest - item * l.tiles), behind = first + l.tiles;
+      const long long item = quotient(rest, l.tiles), first = end - 1 - (rest - item * l.tiles), behind = first + l.tiles;
       if (behind > end && first >= begin) {
         s.valid = 1;
-        s.kvh = static_cast<int>(item / l.blocks);
+        s.kvh = static_cast<int>(quotient(item, l.blocks));
         s.row0 = l.rq.row0;
         s.v0 = static_cast<int>(item - static_cast<long long>(s.kvh) * l.blocks) * KX_QV;
         s.qv = static_cast<int>(min(static_cast<long long>(l.rq.R) * a.G - s.v0, static_cast<long long>(KX_QV)));
         s.slot = 2 * c + (first == begin ? 0 : 1);
-        last = static_cast<int>((behind - 1) / per);
+        last = static_cast<int>(quotient(behind - 1, per));
       }
     }
     if (lane == 0) {
@@ -816,12 +904,12 @@ cudaError_t launch_wide(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
       cudaFuncAttributes fa;
       e = cudaFuncGetAttributes(&fa, kv_cross_wide<HD, CACHE>);
       if (e != cudaSuccess) return e;
-      const int need = 128 * KX_REG_CTRL + 256 * KX_REG_SOFTMAX + 256 * KX_REG_CONV;
+      const int need = 128 * KX_REG_CTRL + KX_SOFTMAX * KX_REG_SOFTMAX + 256 * KX_REG_CONV;
       if (fa.numRegs / 8 * 8 * kx_threads(CACHE) < need || fa.numRegs < KX_REG_CONV) return cudaErrorInvalidConfiguration;
     }
     if (dev < 64) granted[dev].store(cap);
   }
-  const size_t fixed = 2 * ka_entry(HD) + (CACHE == EAGLE_CACHE_F4 ? KA_RAW * ka_raw_bytes(HD) : 0) + KX_MISC;
+  const size_t fixed = 2 * ka_entry(HD) + (CACHE == EAGLE_CACHE_F4 ? KA_RAW * ka_raw_bytes(HD) : 0) + kx_misc(CACHE);
   const int ns = std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
   if (cap < fixed || ns < 4) return cudaErrorInvalidConfiguration;   // (a shared item steps 4 entries)
   e = launch_after(with_own, dim3(ctas), kx_threads(CACHE), fixed + static_cast<size_t>(ns) * ka_entry(HD), st, kv_cross_wide<HD, CACHE>,

@@ -176,6 +176,22 @@ def test_strided_rows_graph_and_streams(kind, rows):
     assert cache.check() == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [3, 40, 70])
+def test_many_short_sequences_repeat(kind, rows):
+    """Sequences of one tile, two, none and a few in turn, so that every CTA has items with and without
+    a tile for each of its halves, and cuts fall anywhere: right, and the same bits every time."""
+    rng = np.random.default_rng(31)
+    lens = [int(x) for x in rng.choice([0, 1, 100, 128, 129, 250, 256, 384, 400, 1000], 60)]
+    G = 4
+    cache, held, q, out, lse = run(rng, kind, 64, 32, 2, G, lens, [rows] * 60)
+    args = (cache, dev(q, torch.bfloat16), dev(cu([rows] * 60)), dev(np.array(lens, np.int32)))
+    for _ in range(20):
+        o, l = eb.kv_cross_attention(*args, max_rows=rows, max_len=max(lens), lse=True)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    assert cache.check() == 0
+
+
 def test_bad_pages_rows_and_lengths_are_reported():
     rng = np.random.default_rng(10)
     for rows in ([1, 1], [40, 40]):
