@@ -53,6 +53,7 @@ __host__ __device__ constexpr uint32_t ka_raw_bytes(int hd) { return static_cast
 struct KaArgs {
   KvPool pool;
   int B, N, Hq, G, max_rows, max_len, S;
+  uint32_t g_inverse;                      // 2^32 / G (kvcross.cu)
   int blocks;                              // query-vector blocks per request
   int tiles_per_cta, splits;
   int joined;                              // the ranges of a request are one cluster and join in it

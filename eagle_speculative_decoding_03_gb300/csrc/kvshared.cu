@@ -305,6 +305,7 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
   a.N = w->N;
   a.Hq = w->n_heads;
   a.G = w->n_heads / cache->n_kv_heads;
+  a.g_inverse = static_cast<uint32_t>(std::min((1ull << 32) / a.G, (1ull << 32) - 1));
   a.max_rows = w->max_rows;
   a.max_len = w->max_len;
   a.cross = 1;
@@ -363,6 +364,7 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   a.N = w->N;
   a.Hq = w->n_heads;
   a.G = w->n_heads / cache->n_kv_heads;
+  a.g_inverse = static_cast<uint32_t>(std::min((1ull << 32) / a.G, (1ull << 32) - 1));
   a.max_rows = w->max_rows;
   a.max_len = w->max_len;
   a.S = w->mask_slots;
