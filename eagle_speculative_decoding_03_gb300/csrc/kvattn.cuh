@@ -16,14 +16,14 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 3-D map over a paged bf16 cache [pages * Hkv][page_size][hd]: boxes of one page's rows of one
-// KV head x 64 dims, 128-byte swizzle; rows outside the page or the pool read as zeros.
-inline bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks) {
+// 3-D map over a paged bf16 cache [pages * Hkv][page_size][hd]: boxes of `rows` rows (0: all) of a page
+// of one KV head x 64 dims, 128-byte swizzle; rows outside the page or the pool read as zeros.
+inline bool make_page_map(CUtensorMap* tm, const void* pool, int hd, int page_size, long long blocks, int rows = 0) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(blocks)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(hd) * 2 * page_size};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows ? rows : page_size), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -256,6 +256,13 @@ constexpr int KX_FROM = 9;                 // query vectors per KV head of a req
 KxPlan kx_plan(int Hkv, int hd, int G, int B, int max_rows, int max_len);
 cudaError_t kx_launch(const KaArgs& a, const KaArgs* own, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, const KxPlan& p,
                       float* parts, cudaStream_t st);
+
+// The same for few query vectors (kvfew.cu: at most KF_QV a KV head and request, bf16 pages, every row
+// sees all its keys).  Writes out and lse, or with a.parts the one partial result of every row; the
+// plan's members of `a` are filled in here.
+constexpr int KF_QV = 8;
+KxPlan kf_plan(int Hkv, int hd, int B, int max_len);
+cudaError_t kf_launch(KaArgs* a, const eagle_kv_cache_t* cache, const KxPlan& p, float* parts, cudaStream_t st);
 
 // The ranges of a request (grid x) as one cluster where they join in it.
 template <typename... P, typename... A>

@@ -18,7 +18,7 @@
 // bf16 p (8 bits) against bf16 values, fp16 p (11 bits) against 4-bit ones; l sums the unrounded p.
 // No key that a row does not see enters a product (rows behind the last key are loaded as zeros), so
 // values that are not finite reach the rows that see them, and need no second pass.
-#include "kvattn.cuh"
+#include "kvline.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -28,10 +28,10 @@ using namespace eagle;
 namespace {
 
 constexpr int KX_QV = 256;                 // query vectors of a block
-static_assert(KX_QV == 1 << 8, "Line divides by a shift");
 constexpr int KX_DESCS = 4;                // segments in flight between the scheduler and the roles
 constexpr int KX_MIN_UNITS = 3;            // units that are worth a CTA
-constexpr uint32_t KX_MISC = 3072;         // barriers (0), segments (640), states of an item that both groups take (1024)
+constexpr int KX_MAX_RAW = 12;             // raw tiles of a 4-bit pool in flight
+constexpr uint32_t KX_MISC = 3072;         // barriers (0), segments (704), states of an item that both groups take (1024)
 constexpr int KX_SOFTMAX = 256;            // softmax threads: one per query vector
 // registers per thread of the 4-bit kernel's roles (the launch checks their sum)
 constexpr int KX_REG_CTRL = 48, KX_REG_SOFTMAX = 152, KX_REG_CONV = 64;
@@ -40,11 +40,8 @@ constexpr int KX_JOIN_V = 32, KX_JOIN_WARPS = 8;
 __host__ __device__ constexpr int kx_threads(int cache) { return 128 + KX_SOFTMAX + (cache == EAGLE_CACHE_F4 ? 256 : 0); }
 // floats of a partial result: [hd / 4][256] float4 outputs, [256] (maximum, sum)
 __host__ __device__ constexpr size_t kx_slot(int hd) { return static_cast<size_t>(KX_QV) * (hd + 2); }
-// An item whose first part is CTA c's last segment, and the last CTA with a part of it (0: none).
-// [CTAs], ahead of the parts.
-struct Cut {
-  int last, kvh, row0, v0, qv, slot, pad[2];
-};
+
+using KxLine = Line<8, KA_CH>;             // (blocks of KX_QV vectors)
 
 // Part of an item: tiles [t0, t0 + T) of query vectors [v0, v0 + qv) of sequence b.
 struct Seg {
@@ -60,82 +57,6 @@ struct Seg {
   }
   EAGLE_DEV bool tiles_of(int g) const { return T > (both() ? g : 0); }
 };
-
-// Waits of this kernel, bounded by a count of polls (a quarter of a second and more) and small: its
-// code must not grow past the instruction cache (94 KB of it took 10,000 cycles from one segment to
-// the next).  SLEEP: for roles that may wake up late.
-template <bool SLEEP = false>
-EAGLE_DEV bool kx_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile int* abort_flag) {
-#pragma unroll 1
-  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
-    if (SLEEP) __nanosleep(32);
-    if ((i & 255u) == 255u && (*abort_flag || i > (SLEEP ? 1u << 22 : 1u << 24))) {
-      if (!*abort_flag) atomicOr(err, DEVERR_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
-// How the units lie in line: per sequence b, KV heads x blocks x tiles (at least 1, to write the
-// rows of a sequence without keys).
-struct Line {
-  Req rq;
-  int blocks, tiles;
-  EAGLE_DEV Line(const KaArgs& a, int b) {
-    rq = request(a, b);
-    blocks = static_cast<int>((static_cast<long long>(rq.R) * a.G + KX_QV - 1) >> 8);
-    tiles = max((rq.len + KA_CH - 1) / KA_CH, 1);
-  }
-  EAGLE_DEV long long units(const KaArgs& a) const { return static_cast<long long>(a.pool.Hkv) * blocks * tiles; }
-};
-// x / y (x >= 0, y > 0), by 32 bits where they do
-__device__ __noinline__ long long quotient64(long long x, long long y) { return x / y; }
-EAGLE_DEV long long quotient(long long x, long long y) {
-  return (x | y) >> 32 ? quotient64(x, y) : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
-}
-// Units of the call, and of a CTA.  By a whole warp.
-EAGLE_DEV long long all_units(const KaArgs& a, int lane) {
-  long long n = 0;
-  if (a.groups && lane == 0 && (__ldg(a.groups) != 0 || __ldg(a.groups + a.B) != a.requests)) atomicOr(a.err, DEVERR_PREFIX);
-#pragma unroll 1
-  for (int b = lane; b < a.B; b += 32) n += Line(a, b).units(a);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-  return n;
-}
-EAGLE_DEV long long units_per_cta(long long all, int ctas) { return max(quotient(all + ctas - 1, ctas), static_cast<long long>(KX_MIN_UNITS)); }
-// The sequence that holds unit u, and u's place among its units.  By a whole warp.
-EAGLE_DEV int find_unit(const KaArgs& a, int lane, long long u, long long* rest) {
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long n = b0 + lane < a.B ? Line(a, b0 + lane).units(a) : 0;
-    long long upto = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += x;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, upto > u);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      *rest = u - __shfl_sync(0xffffffffu, upto - n, k);
-      return b0 + k;
-    }
-    u -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  *rest = 0;
-  return a.B;
-}
-
-// v / G of a query vector: the row's index
-EAGLE_DEV int row_of(const KaArgs& a, int v) {
-  int q = static_cast<int>(__umulhi(static_cast<uint32_t>(v), a.g_inverse));   // off by one at most
-  const int r = v - q * a.G;
-  q += r >= a.G ? 1 : r < 0 ? -1 : 0;
-  return q;
-}
 
 // The partial results of a row's own keys (shared attention), behind the prefix's.
 struct Own {
@@ -153,10 +74,6 @@ struct Own {
   EAGLE_DEV size_t place(int s) const { return s * (static_cast<size_t>(a.N) * a.Hq) + at; }
   EAGLE_DEV float2 ml(int s) const { return a.part_ml[place(s)]; }
 };
-// 2^(m - M) where m is a part's maximum and M the largest
-EAGLE_DEV float part_factor(float m, float M) {
-  return m == -INFINITY ? 0.f : M == INFINITY ? (m == INFINITY ? 1.f : 0.f) : exp2f(m - M);
-}
 // x[0 .. 3] += f y, nothing of a part without weight (whatever it holds)
 EAGLE_DEV void add_part(float* x, float f, float4 y) {
   if (f == 0.f) return;
@@ -211,7 +128,7 @@ EAGLE_DEV float powers64(float* x, float rs, float mb, float* p8, float* pk) {
 template <int HD, int CACHE, bool OWN>
 __global__ void __launch_bounds__(kx_threads(CACHE), 1)
 kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const KaArgs a, const KaArgs own,
-              float* parts, const int NS) {
+              float* parts, const int NS, const int NR) {
   constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
   constexpr float LIFT = F4 ? 7.f : 0.f;     // fp16 p is held times 2^7 (as in kv_attention_tc)
   constexpr int THREADS = kx_threads(CACHE), CONV_WARP = 4 + KX_SOFTMAX / 32, CONV = THREADS - 32 * CONV_WARP;
@@ -223,18 +140,18 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   const uint32_t ring_u = uniform(smem_u32(sm));
   const uint32_t q_u = ring_u + static_cast<uint32_t>(NS) * ENTRY;
   uint8_t* raw = sm + static_cast<uint32_t>(NS + 2) * ENTRY;
-  uint8_t* misc = raw + (F4 ? KA_RAW * RAW : 0);
+  uint8_t* misc = raw + (F4 ? NR * RAW : 0);
   const uint32_t misc_u = smem_u32(misc);
   // ring full / free; per score buffer (group, 64 columns): scores there, p there, P V done; per group:
   // queries there, segment done; raw tiles full / free, segments full / free; an item of both groups:
   // states there / read
   const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 256, bar_pe = misc_u + 288,
-                 bar_q = misc_u + 320, bar_fin = misc_u + 336, bar_rf = misc_u + 352, bar_re = misc_u + 376, bar_df = misc_u + 400,
-                 bar_de = misc_u + 432, bar_x = misc_u + 464;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 512);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 516);
-  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 520);
-  Seg* segs = reinterpret_cast<Seg*>(misc + 640);
+                 bar_q = misc_u + 320, bar_fin = misc_u + 336, bar_df = misc_u + 352, bar_de = misc_u + 384, bar_x = misc_u + 416,
+                 bar_rf = misc_u + 432, bar_re = misc_u + 528;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 624);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 628);
+  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 632);
+  Seg* segs = reinterpret_cast<Seg*>(misc + 704);
 
   pdl_trigger();
   if (ring_u & 1023u) {                      // (the swizzled tiles' alignment)
@@ -256,7 +173,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       mbar_init(bar_fin + 8 * g, 1);
       mbar_init(bar_x + 8 * g, KX_SOFTMAX / 32);
     }
-    for (int s = 0; F4 && s < KA_RAW; ++s) {
+    for (int s = 0; F4 && s < KX_MAX_RAW; ++s) {
       mbar_init(bar_rf + 8 * s, 1);
       mbar_init(bar_re + 8 * s, F4 ? CONV / 32 : 1);
     }
@@ -298,7 +215,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     if (warp == 0) {
       // ------------------------------------------------------------ producer: lane = page of the tile
       const uint64_t pol = policy_evict_normal();   // (the other blocks of the sequence read the keys too)
-      const int ps = 1 << a.pool.ps_log, per = KA_CH >> a.pool.ps_log, slots = F4 ? KA_RAW : NS;
+      const int ps = 1 << a.pool.ps_log, per = KA_CH >> a.pool.ps_log, slots = F4 ? NR : NS;
       RingPos rp{0, 0};
       int e = 0;
       for (;; dp.step(1, KX_DESCS)) {
@@ -307,12 +224,14 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         if (!ok || !s.valid) break;
         const int end_page = s.len >> a.pool.ps_log, end_rows = F4 ? 0 : s.len & (ps - 1);
         int page = -1;
+        Pages pages;
+        pages.open(a, s.b, s.t0 * KA_CH, s.len, ps, lane);
 #pragma unroll 1
         for (int x = 0; x < 2 * s.T && ok; ++x, rp.step(1, slots)) {
           const int slot = rp.slot, pi = (s.t0 + (x >> 1)) * per + lane;
-          if (!(x & 1)) {
-            page = -1;
-            if (lane < per && (pi << a.pool.ps_log) < s.len) page = kv_page(a.pool, s.b, pi << a.pool.ps_log, a.err);
+          if (!(x & 1)) {                    // the tile's keys and values are in the same pages
+            page = pages.get(a, s.b, s.t0 * KA_CH, s.len, ps, lane, (x >> 1) * per);
+            if (lane >= per) page = -1;
           }
           const uint32_t bar = (F4 ? bar_rf : bar_kvf) + 8 * slot;
           if (e >= slots) ok = kx_wait<true>((F4 ? bar_re : bar_kve) + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
@@ -355,10 +274,10 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ scheduler
-      const long long all = all_units(a, lane), per = units_per_cta(all, gridDim.x);
+      const long long all = all_units<KxLine>(a, lane), per = units_per_cta(all, gridDim.x, KX_MIN_UNITS);
       const long long begin = min(per * blockIdx.x, all), end = min(begin + per, all);
       long long u = begin, rest = 0;
-      int b = u < end ? find_unit(a, lane, u, &rest) : 0;
+      int b = u < end ? find_unit<KxLine>(a, lane, u, &rest) : 0;
       Cut cut;
       cut.last = 0;
       int n = 0;
@@ -367,12 +286,12 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         Seg s;
         s.valid = 0;
         if (u < end) {
-          Line l(a, b);
+          KxLine l(a, b);
 #pragma unroll 1
           while (rest >= l.units(a)) {       // (the next sequence that has units)
             rest -= l.units(a);
             ++b;
-            l = Line(a, b);
+            l = KxLine(a, b);
           }
           const long long item = quotient(rest, l.tiles);
           s.valid = 1;
@@ -507,7 +426,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || !s.valid) break;
 #pragma unroll 1
-        for (int e = 0; e < 2 * s.T; ++e, rp.step(1, NS), wp.step(1, KA_RAW)) {
+        for (int e = 0; e < 2 * s.T; ++e, rp.step(1, NS), wp.step(1, NR)) {
           ok = kx_wait<true>(bar_rf + 8 * wp.slot, wp.turn, a.err, abort_flag);
           const uint8_t* src = raw + wp.slot * RAW;
           const uint32_t have = raw_pages[wp.slot];
@@ -895,21 +814,6 @@ __global__ void __launch_bounds__(32 * KX_JOIN_WARPS) kv_cross_wide_join(const K
   if (warp == 0 && a.lse) a.lse[row * a.Hq + h] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-template <typename K, typename... A>
-cudaError_t launch_after(bool overlap, dim3 grid, int threads, size_t smem, cudaStream_t st, K kernel, const A&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
-  cfg.stream = st;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int HD, int CACHE, bool OWN>
 cudaError_t launch_wide(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaArgs& a, const KaArgs& own, float* parts,
                         int ctas, cudaStream_t st) {
@@ -930,11 +834,14 @@ cudaError_t launch_wide(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
     }
     if (dev < 64) granted[dev].store(cap);
   }
-  const size_t fixed = 2 * ka_entry(HD) + (CACHE == EAGLE_CACHE_F4 ? KA_RAW * ka_raw_bytes(HD) : 0) + KX_MISC;
-  const int ns = std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
-  if (cap < fixed || ns < 4) return cudaErrorInvalidConfiguration;   // (a shared item steps 4 entries)
-  e = launch_after(OWN, dim3(ctas), kx_threads(CACHE), fixed + static_cast<size_t>(ns) * ka_entry(HD), st, kv_cross_wide<HD, CACHE, OWN>,
-                   tmk, tmv, a, own, parts, ns);
+  const size_t fixed = 2 * ka_entry(HD) + KX_MISC;
+  const int ns = CACHE == EAGLE_CACHE_F4 ? (HD == 64 ? 6 : 4) : std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
+  const size_t left = cap - fixed - static_cast<size_t>(ns) * ka_entry(HD);
+  const int nr = CACHE == EAGLE_CACHE_F4 ? std::min<int>(KX_MAX_RAW, static_cast<int>(left / ka_raw_bytes(HD))) : 0;
+  if (cap < fixed + 4 * ka_entry(HD) || ns < 4 ||   // (a shared item needs 4: its next keys come before its last values are free)
+       (CACHE == EAGLE_CACHE_F4 && nr < 2)) return cudaErrorInvalidConfiguration;
+  e = launch_after(OWN, dim3(ctas), kx_threads(CACHE), fixed + static_cast<size_t>(ns) * ka_entry(HD) + static_cast<size_t>(nr) * ka_raw_bytes(HD), st, kv_cross_wide<HD, CACHE, OWN>,
+                   tmk, tmv, a, own, parts, ns, nr);
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_after(true, dim3(ctas, KX_QV / KX_JOIN_V), 32 * KX_JOIN_WARPS, 0, st, kv_cross_wide_join<HD>, a, own, OWN ? 1 : 0,
                       static_cast<const float*>(parts));

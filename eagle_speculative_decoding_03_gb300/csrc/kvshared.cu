@@ -222,17 +222,26 @@ float log2_scale(float scale, int hd) {
   return std::min((scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f, FLT_MAX);
 }
 
-// How a cross call is cut: by ranges (few query vectors) or in line over the SMs.
+// How a call over keys that all rows see is cut: in line over the SMs, or (4-bit pages with few query
+// vectors, and steps whose ranges join in a cluster) by ranges.  FEW also takes a step's own keys, of one
+// row a request, which sees them all.
+enum class Cutting { RANGES, WIDE, FEW };
 struct CrossPlan {
-  bool wide;
+  Cutting by;
   KaPlan ranges;
   KxPlan line;
+  bool separate() const { return by == Cutting::RANGES && ranges.splits > 1 && !ranges.joined; }
+  int64_t line_bytes() const { return by == Cutting::RANGES ? 0 : line.bytes; }
 };
 CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int max_len, bool may_join) {
   CrossPlan p;
-  p.wide = static_cast<long long>(max_rows) * G >= KX_FROM;
-  if (p.wide) p.line = kx_plan(c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
-  else p.ranges = ka_plan(c->kind, c->n_kv_heads, G, B, max_rows, max_len, may_join);
+  const long long qv = static_cast<long long>(max_rows) * G;
+  p.by = qv >= KX_FROM ? Cutting::WIDE : c->kind == EAGLE_CACHE_BF16 ? Cutting::FEW : Cutting::RANGES;
+  if (p.by != Cutting::WIDE) p.ranges = ka_plan(c->kind, c->n_kv_heads, G, B, max_rows, max_len, may_join);
+  // (a step's few ranges in one cluster each: no second launch.  cross_step_b1 10 us, in line 16)
+  if (p.by == Cutting::FEW && p.ranges.joined) p.by = Cutting::RANGES;
+  if (p.by == Cutting::WIDE) p.line = kx_plan(c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
+  if (p.by == Cutting::FEW) p.line = kf_plan(c->n_kv_heads, c->head_dim, B, max_len);
   return p;
 }
 
@@ -244,20 +253,22 @@ eagle_status_t check_cross(const char* who, const eagle_kv_cache_t* cache, const
   if (r == EAGLE_OK) r = check_rows(who, cache->n_kv_heads, cache->head_dim, w->B, w->N, w->n_heads, w->q, w->q_stride, w->out, w->out_stride, w->scale);
   if (r != EAGLE_OK) return r;
   *p = cross_plan(cache, w->n_heads / cache->n_kv_heads, w->B, w->max_rows, w->max_len, true);
-  return p->wide ? EAGLE_OK : check_plan(who, w->B, p->ranges);
+  return p->by != Cutting::RANGES ? EAGLE_OK : check_plan(who, w->B, p->ranges);
 }
 
 int64_t cross_bytes(const eagle_kv_cross_t* w, int hd, const CrossPlan& p) {
-  if (p.wide) return p.line.bytes;
-  return p.ranges.splits == 1 || p.ranges.joined ? 0 : p.ranges.splits * ka_part_bytes(w->N, w->n_heads, hd);
+  return p.line_bytes() + (p.separate() ? p.ranges.splits * ka_part_bytes(w->N, w->n_heads, hd) : 0);
 }
 
-int64_t shared_bytes(const eagle_kv_attention_t* w, int hd, const CrossPlan& pre, const KaPlan& own) {
-  return (own.splits + (pre.wide ? 0 : pre.ranges.splits)) * ka_part_bytes(w->N, w->n_heads, hd) + (pre.wide ? pre.line.bytes : 0);
+// Ranges of partial results of a shared call: the own keys', then the prefix's.
+int own_ranges(const CrossPlan& own) { return own.by == Cutting::RANGES ? own.ranges.splits : 1; }
+int pre_ranges(const CrossPlan& pre) { return pre.by == Cutting::WIDE ? 0 : own_ranges(pre); }
+int64_t shared_bytes(const eagle_kv_attention_t* w, int hd, const CrossPlan& pre, const CrossPlan& own) {
+  return pre.line_bytes() + own.line_bytes() + (own_ranges(own) + pre_ranges(pre)) * ka_part_bytes(w->N, w->n_heads, hd);
 }
 
 eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* g, const eagle_kv_cache_t* cache,
-                            const eagle_kv_attention_t* w, KvPool* pre, KvPool* own, CrossPlan* pp, KaPlan* po) {
+                            const eagle_kv_attention_t* w, KvPool* pre, KvPool* own, CrossPlan* pp, CrossPlan* po) {
   eagle_status_t r = kv_pool(prefix, who, pre);
   if (r == EAGLE_OK) r = kv_pool(cache, who, own);
   if (r != EAGLE_OK) return r;
@@ -273,9 +284,14 @@ eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, con
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: a mask needs max_rows <= mask_slots <= 64", who);
   const int G = w->n_heads / cache->n_kv_heads;
   *pp = cross_plan(prefix, G, g->n_groups, g->max_rows, g->max_len, false);
-  *po = ka_plan(cache->kind, cache->n_kv_heads, G, w->B, w->max_rows, w->max_len, false);
-  if (!pp->wide) r = check_plan(who, g->n_groups, pp->ranges);
-  return r != EAGLE_OK ? r : check_plan(who, w->B, *po);
+  if (w->max_rows == 1 && !w->mask && cache->kind == EAGLE_CACHE_BF16 && G <= KF_QV) {
+    *po = cross_plan(cache, G, w->B, 1, w->max_len, false);
+  } else {
+    po->by = Cutting::RANGES;
+    po->ranges = ka_plan(cache->kind, cache->n_kv_heads, G, w->B, w->max_rows, w->max_len, false);
+  }
+  if (pp->by == Cutting::RANGES) r = check_plan(who, g->n_groups, pp->ranges);
+  return r != EAGLE_OK || po->by != Cutting::RANGES ? r : check_plan(who, w->B, po->ranges);
 }
 
 }  // namespace
@@ -296,7 +312,7 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
   CrossPlan p;
   eagle_status_t r = check_cross(who, cache, w, &a.pool, &p);
   if (r != EAGLE_OK) return r;
-  const bool f4 = cache->kind == EAGLE_CACHE_F4, separate = !p.wide && p.ranges.splits > 1 && !p.ranges.joined;
+  const bool f4 = cache->kind == EAGLE_CACHE_F4, separate = p.separate();
   const int64_t need = cross_bytes(w, cache->head_dim, p);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || !aligned(w->workspace)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
@@ -326,7 +342,10 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
   CUtensorMap tmk, tmv;
   r = page_maps(who, cache, &tmk, &tmv);
   if (r != EAGLE_OK) return r;
-  cudaError_t e = p.wide ? kx_launch(a, nullptr, f4, tmk, tmv, p.line, a.part_o, st) : ka_launch(&a, p.ranges, f4, tmk, tmv, st);
+  float* parts = static_cast<float*>(w->workspace);
+  cudaError_t e = p.by == Cutting::WIDE ? kx_launch(a, nullptr, f4, tmk, tmv, p.line, parts, st)
+                  : p.by == Cutting::FEW ? kf_launch(&a, cache, p.line, parts, st)
+                                         : ka_launch(&a, p.ranges, f4, tmk, tmv, st);
   if (e == cudaSuccess && separate) e = ka_combine(a, st);
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
 }
@@ -334,8 +353,7 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
 extern "C" int64_t eagle_kv_shared_attention_workspace(const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* g,
                                                        const eagle_kv_cache_t* cache, const eagle_kv_attention_t* w) {
   KvPool pre, own;
-  CrossPlan pp;
-  KaPlan po;
+  CrossPlan pp, po;
   if (check_shared("kv_shared_attention_workspace", prefix, g, cache, w, &pre, &own, &pp, &po) != EAGLE_OK) return -1;
   return shared_bytes(w, cache->head_dim, pp, po);
 }
@@ -349,13 +367,12 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   KaArgs a, x;                               // the own keys, the prefix
   memset(&a, 0, sizeof(a));
   memset(&x, 0, sizeof(x));
-  CrossPlan pp;
-  KaPlan po;
+  CrossPlan pp, po;
   eagle_status_t r = check_shared(who, prefix, g, cache, w, &x.pool, &a.pool, &pp, &po);
   if (r != EAGLE_OK) return r;
   const int hd = cache->head_dim;
   const int64_t need = shared_bytes(w, hd, pp, po);
-  const int ranges = po.splits + (pp.wide ? 0 : pp.ranges.splits);
+  const int own = own_ranges(po), ranges = own + pre_ranges(pp);
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || !aligned(w->workspace)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
@@ -379,7 +396,9 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   a.out = static_cast<__nv_bfloat16*>(w->out);
   a.out_ld = w->out_stride;
   a.lse = w->lse;
-  a.part_o = static_cast<float*>(w->workspace);
+  float* pre_parts = static_cast<float*>(w->workspace);   // (what is dealt in line first: it keeps 16-byte alignment)
+  float* own_parts = pre_parts + pp.line_bytes() / 4;
+  a.part_o = own_parts + po.line_bytes() / 4;
   a.part_ml = reinterpret_cast<float2*>(a.part_o + ranges * outs * hd);
   a.err = err_word;
   const KvPool pool = x.pool;
@@ -394,19 +413,20 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   x.lens = g->lens;
   x.mask = nullptr;
   x.vg = prefix->kind == EAGLE_CACHE_F4 ? x.pool.vg : 1.f;
-  x.part_o = a.part_o + po.splits * outs * hd;
-  x.part_ml = a.part_ml + po.splits * outs;
+  x.part_o = a.part_o + own * outs * hd;
+  x.part_ml = a.part_ml + own * outs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tmk, tmv, pmk, pmv;
   r = page_maps(who, cache, &tmk, &tmv);
   if (r == EAGLE_OK) r = page_maps(who, prefix, &pmk, &pmv);
   if (r != EAGLE_OK) return r;
   const bool pf4 = prefix->kind == EAGLE_CACHE_F4;
-  cudaError_t e = ka_launch(&a, po, cache->kind == EAGLE_CACHE_F4, tmk, tmv, st);
-  if (e == cudaSuccess && pp.wide) {
-    e = kx_launch(x, &a, pf4, pmk, pmv, pp.line, reinterpret_cast<float*>(a.part_ml + ranges * outs), st);
+  cudaError_t e = po.by == Cutting::FEW ? kf_launch(&a, cache, po.line, own_parts, st)
+                                        : ka_launch(&a, po.ranges, cache->kind == EAGLE_CACHE_F4, tmk, tmv, st);
+  if (e == cudaSuccess && pp.by == Cutting::WIDE) {
+    e = kx_launch(x, &a, pf4, pmk, pmv, pp.line, pre_parts, st);
   } else if (e == cudaSuccess) {
-    e = ka_launch(&x, pp.ranges, pf4, pmk, pmv, st);
+    e = pp.by == Cutting::FEW ? kf_launch(&x, prefix, pp.line, pre_parts, st) : ka_launch(&x, pp.ranges, pf4, pmk, pmv, st);
     if (e == cudaSuccess) e = hd == 64 ? launch_join<64>(a, x, st) : launch_join<128>(a, x, st);
   }
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));

@@ -57,6 +57,9 @@ def run(rng, kind, hd, ps, Hkv, G, lens, rows, pad=0, max_len=None, max_rows=Non
     (128, 64, 1, 2, [20001, 0, 140], [1, 2, 4]),
     (64, 64, 1, 20, [20001, 140], [1, 1]),
     (128, 64, 8, 2, [1500, 0, 130, 1], [4, 4, 4, 4]),  # ranges of a cluster, some of them empty
+    (64, 16, 16, 1, [100 * i for i in range(25)], [1] * 25),
+    (128, 128, 4, 8, [64 * i + 1 for i in range(30)], [1] * 30),
+    (128, 32, 1, 1, [40000, 63, 64, 65], [7, 8, 0, 5]),
 ])
 def test_few_rows(kind, hd, ps, Hkv, G, lens, rows):
     run(np.random.default_rng(hd + ps + G), kind, hd, ps, Hkv, G, lens, rows, pad=1)
@@ -177,7 +180,7 @@ def test_strided_rows_graph_and_streams(kind, rows):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("rows", [3, 40, 70])
+@pytest.mark.parametrize("rows", [1, 2, 3, 40, 70])
 def test_many_short_sequences_repeat(kind, rows):
     """Sequences of one tile, two, none and a few in turn, so that every CTA has items with and without
     a tile for each of its halves, and cuts fall anywhere: right, and the same bits every time."""

@@ -65,6 +65,9 @@ KINDS = [("bf16", "bf16"), ("f4", "bf16"), ("bf16", "f4"), ("f4", "f4")]
     (128, (64, 64), 8, 4, [4100, 257], [0, 20, 40], list(range(40)), [1] * 40),
     (64, (128, 16), 1, 64, [130], [0, 2], [0, 9], [1, 1]),
     (128, (64, 64), 2, 2, [300, 40, 60], [0, 0, 2, 2], [9, 8], [1, 1]),     # groups without requests
+    (128, (128, 128), 1, 3, [500], [0, 5], [9, 800, 0, 127, 128], [1] * 5),  # odd numbers of rows and heads
+    (64, (32, 64), 3, 5, [70, 4000], [0, 1, 3], [63, 64, 900], [1, 1, 1]),
+    (128, (16, 16), 2, 8, [64, 65], [0, 30, 60], [(37 * i) % 700 for i in range(60)], [1] * 60),
 ])
 def test_single_tokens(kinds, hd, ps, Hkv, G, plens, groups, ctx, rows):
     run(np.random.default_rng(hd + G + sum(plens)), kinds, hd, ps, Hkv, G, plens, groups, ctx, rows, pad=2)
