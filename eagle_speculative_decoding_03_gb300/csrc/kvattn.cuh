@@ -253,7 +253,7 @@ struct KxPlan {
   int64_t bytes;
 };
 constexpr int KX_FROM = 9;                 // query vectors per KV head of a request from which it is taken
-KxPlan kx_plan(int Hkv, int hd, int G, int B, int max_rows, int max_len);
+KxPlan kx_plan(int kind, int Hkv, int hd, int G, int B, int max_rows, int max_len);
 cudaError_t kx_launch(const KaArgs& a, const KaArgs* own, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, const KxPlan& p,
                       float* parts, cudaStream_t st);
 
@@ -262,6 +262,7 @@ cudaError_t kx_launch(const KaArgs& a, const KaArgs* own, bool f4, const CUtenso
 // plan's members of `a` are filled in here.
 constexpr int KF_QV = 8;
 KxPlan kf_plan(int Hkv, int hd, int B, int max_len);
+bool kf_worth(int Hkv, int B, int max_len);   // whether the SMs have several tiles each
 cudaError_t kf_launch(KaArgs* a, const eagle_kv_cache_t* cache, const KxPlan& p, float* parts, cudaStream_t st);
 
 // The ranges of a request (grid x) as one cluster where they join in it.

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int KX_QV = 256;                 // query vectors of a block
 constexpr int KX_DESCS = 4;                // segments in flight between the scheduler and the roles
-constexpr int KX_MIN_UNITS = 3;            // units that are worth a CTA
+constexpr int KX_MIN_KEYS = 384;           // keys of an item that are worth a CTA
 constexpr int KX_MAX_RAW = 12;             // raw tiles of a 4-bit pool in flight
 constexpr uint32_t KX_MISC = 3072;         // barriers (0), segments (704), states of an item that both groups take (1024)
 constexpr int KX_SOFTMAX = 256;            // softmax threads: one per query vector
@@ -41,19 +41,26 @@ __host__ __device__ constexpr int kx_threads(int cache) { return 128 + KX_SOFTMA
 // floats of a partial result: [hd / 4][256] float4 outputs, [256] (maximum, sum)
 __host__ __device__ constexpr size_t kx_slot(int hd) { return static_cast<size_t>(KX_QV) * (hd + 2); }
 
-using KxLine = Line<8, KA_CH>;             // (blocks of KX_QV vectors)
+// Keys of a tile, a ring entry: two units of bf16 keys; one of 4-bit ones, whose converted tiles must be
+// in order and four of which at a time left the groups of a shared item waiting for each other's values.
+__host__ __device__ constexpr int kx_keys(int cache) { return cache == EAGLE_CACHE_F4 ? KA_H : KA_CH; }
+__host__ __device__ constexpr uint32_t kx_entry(int hd, int cache) { return static_cast<uint32_t>(hd) * 2 * kx_keys(cache); }
+__host__ __device__ constexpr uint32_t kx_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_H + hd / 16 * KA_H; }
+template <int CACHE>
+using KxLine = Line<8, kx_keys(CACHE)>;    // (blocks of KX_QV vectors)
 
 // Part of an item: tiles [t0, t0 + T) of query vectors [v0, v0 + qv) of sequence b.
 struct Seg {
   int valid, b, kvh, row0, len, v0, qv, t0, T, slot;   // slot: partial result, -1: the item is whole
   // both groups have the same vectors, every other tile each
   EAGLE_DEV bool both() const { return qv <= KA_QV; }
-  // units of 64 keys that group g has of it: `last` of them (1 or 2) in the last tile
+  // units of 64 keys that group g has of it, UPT to a tile and `last` in the last one
+  template <int UPT>
   EAGLE_DEV int units_of(int g, int last) const {
     if (T == 0) return 0;
-    if (!both()) return 2 * T - 2 + last;
+    if (!both()) return UPT * (T - 1) + last;
     const int n = (T + 1 - g) >> 1;          // its tiles
-    return n == 0 ? 0 : 2 * n - (((T - 1) & 1) == g ? 2 - last : 0);
+    return n == 0 ? 0 : UPT * n - (((T - 1) & 1) == g ? UPT - last : 0);
   }
   EAGLE_DEV bool tiles_of(int g) const { return T > (both() ? g : 0); }
 };
@@ -132,14 +139,16 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
   constexpr float LIFT = F4 ? 7.f : 0.f;     // fp16 p is held times 2^7 (as in kv_attention_tc)
   constexpr int THREADS = kx_threads(CACHE), CONV_WARP = 4 + KX_SOFTMAX / 32, CONV = THREADS - 32 * CONV_WARP;
-  constexpr uint32_t ENTRY = ka_entry(HD), HALF = KA_CH * 128, RAW = ka_raw_bytes(HD), RAW_SCALES = HD / 2 * KA_CH;
+  constexpr int KEYS = kx_keys(CACHE), UPT = KEYS / KA_H;
+  constexpr uint32_t ENTRY = kx_entry(HD, CACHE), HALF = KEYS * 128, RAW = kx_raw_bytes(HD), RAW_SCALES = HD / 2 * KEYS;
+  constexpr uint32_t Q_TILE = ka_entry(HD), Q_HALF = KA_QV * 128;
   constexpr uint32_t T_O = 256;
   extern __shared__ __align__(1024) uint8_t kx_sm[];   // (no byte is left to align it by hand: ring, queries, misc take all)
   uint8_t* sm = kx_sm;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t ring_u = uniform(smem_u32(sm));
   const uint32_t q_u = ring_u + static_cast<uint32_t>(NS) * ENTRY;
-  uint8_t* raw = sm + static_cast<uint32_t>(NS + 2) * ENTRY;
+  uint8_t* raw = sm + static_cast<uint32_t>(NS) * ENTRY + 2 * Q_TILE;
   uint8_t* misc = raw + (F4 ? NR * RAW : 0);
   const uint32_t misc_u = smem_u32(misc);
   // ring full / free; per score buffer (group, 64 columns): scores there, p there, P V done; per group:
@@ -160,7 +169,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   }
   if (tid == 0) {
     for (int s = 0; s < KA_MAX_SLOTS; ++s) {
-      mbar_init(bar_kvf + 8 * s, F4 ? CONV / 32 : 1);
+      mbar_init(bar_kvf + 8 * s, F4 ? 2 : 1);
       mbar_init(bar_kve + 8 * s, 2);
     }
     for (int b = 0; b < 4; ++b) {
@@ -175,7 +184,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     }
     for (int s = 0; F4 && s < KX_MAX_RAW; ++s) {
       mbar_init(bar_rf + 8 * s, 1);
-      mbar_init(bar_re + 8 * s, F4 ? CONV / 32 : 1);
+      mbar_init(bar_re + 8 * s, 2);
     }
     for (int s = 0; s < KX_DESCS; ++s) {
       mbar_init(bar_df + 8 * s, 1);
@@ -205,8 +214,9 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   // how many of a segment's last tile's two units hold columns of keys (the page that the keys end inside
   // has its rows at its end)
   auto last_units = [&](const Seg& s) {
-    const int ps = 1 << a.pool.ps_log, kt = (s.t0 + s.T - 1) * KA_CH;
-    const int columns = F4 || !(s.len & (ps - 1)) ? s.len : ((s.len >> a.pool.ps_log) + 1) << a.pool.ps_log;
+    if (UPT == 1) return 1;
+    const int ps = 1 << a.pool.ps_log, kt = (s.t0 + s.T - 1) * KEYS;
+    const int columns = !(s.len & (ps - 1)) ? s.len : ((s.len >> a.pool.ps_log) + 1) << a.pool.ps_log;
     return columns - kt > KA_H ? 2 : 1;
   };
 
@@ -215,7 +225,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     if (warp == 0) {
       // ------------------------------------------------------------ producer: lane = page of the tile
       const uint64_t pol = policy_evict_normal();   // (the other blocks of the sequence read the keys too)
-      const int ps = 1 << a.pool.ps_log, per = KA_CH >> a.pool.ps_log, slots = F4 ? NR : NS;
+      const int ps = 1 << a.pool.ps_log, box = min(ps, KEYS), per = KEYS / box, slots = F4 ? NR : NS;
       RingPos rp{0, 0};
       int e = 0;
       for (;; dp.step(1, KX_DESCS)) {
@@ -225,42 +235,49 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         const int end_page = s.len >> a.pool.ps_log, end_rows = F4 ? 0 : s.len & (ps - 1);
         int page = -1;
         Pages pages;
-        pages.open(a, s.b, s.t0 * KA_CH, s.len, ps, lane);
+        pages.open(a, s.b, s.t0 * KEYS, s.len, box, lane);
 #pragma unroll 1
         for (int x = 0; x < 2 * s.T && ok; ++x, rp.step(1, slots)) {
-          const int slot = rp.slot, pi = (s.t0 + (x >> 1)) * per + lane;
-          if (!(x & 1)) {                    // the tile's keys and values are in the same pages
-            page = pages.get(a, s.b, s.t0 * KA_CH, s.len, ps, lane, (x >> 1) * per);
-            if (lane >= per) page = -1;
-          }
+          const int slot = uniform(rp.slot), tile = s.t0 + (x >> 1);
+          if (!(x & 1)) page = pages.get(a, s.b, s.t0 * KEYS, s.len, box, lane, (x >> 1) * per);   // (the values are in the keys' pages)
           const uint32_t bar = (F4 ? bar_rf : bar_kvf) + 8 * slot;
-          if (e >= slots) ok = kx_wait<true>((F4 ? bar_re : bar_kve) + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
+          if (e >= slots) ok = kx_wait((F4 ? bar_re : bar_kve) + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
           else ++e;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          // One lane copies box after box, all that the copies take being the same for the whole warp: a lane a
+          // box, each with values of its own, took 200 cycles a copy.
           if (F4) {
-            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-            const uint32_t codes = static_cast<uint32_t>(ps) * (HD / 2), scales = static_cast<uint32_t>(ps) * (HD / 16);
-            if (lane == 0) {
+            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0 && lane < per);
+            const uint32_t codes = static_cast<uint32_t>(box) * (HD / 2), scales = static_cast<uint32_t>(box) * (HD / 16);
+            if (elect_one()) {
               raw_pages[slot] = have;
               mbar_arrive_expect_tx(bar, __popc(have) * (codes + scales));
             }
             __syncwarp();
-            if (page >= 0) {
-              const size_t row = kv_row(a.pool, page, s.kvh, 0);
-              const uint32_t dst = smem_u32(raw + slot * RAW);
-              bulk_load(dst + lane * codes, static_cast<const uint8_t*>(x & 1 ? a.pool.v : a.pool.k) + row * (HD / 2), codes, bar);
-              bulk_load(dst + RAW_SCALES + lane * scales, static_cast<const uint8_t*>(x & 1 ? a.pool.vs : a.pool.ks) + row * (HD / 16), scales, bar);
+#pragma unroll 1
+            for (int i = 0; i < per; ++i) {
+              const int pg = __shfl_sync(0xffffffffu, page, i);
+              const size_t row = kv_row(a.pool, pg, s.kvh, tile * KEYS + i * box);
+              const uint32_t dst = smem_u32(raw) + slot * RAW;
+              if (pg >= 0 && elect_one()) {
+                bulk_load(dst + i * codes, static_cast<const uint8_t*>(x & 1 ? a.pool.v : a.pool.k) + row * (HD / 2), codes, bar);
+                bulk_load(dst + RAW_SCALES + i * scales, static_cast<const uint8_t*>(x & 1 ? a.pool.vs : a.pool.ks) + row * (HD / 16), scales, bar);
+              }
             }
           } else {
-            if (lane == 0) mbar_arrive_expect_tx(bar, ENTRY);
+            if (elect_one()) mbar_arrive_expect_tx(bar, ENTRY);
             __syncwarp();
-            if (lane < per) {   // (a page that is not there reads as zeros: a block outside the map)
-              const int blk = page >= 0 ? page * a.pool.Hkv + s.kvh : a.pool.num_pages * a.pool.Hkv;
-              const uint32_t dst = ring_u + slot * ENTRY + lane * (ps * 128);
+#pragma unroll 1
+            for (int i = 0; i < per; ++i) {    // (a page that is not there reads as zeros: a block outside the map)
+              const int pg = __shfl_sync(0xffffffffu, page, i), pi = tile * per + i;
+              const int blk = pg >= 0 ? pg * a.pool.Hkv + s.kvh : a.pool.num_pages * a.pool.Hkv;
               const int row = pi == end_page && end_rows ? end_rows - ps : 0;
+              const uint32_t dst = ring_u + slot * ENTRY + i * (ps * 128);
+              if (elect_one()) {
 #pragma unroll
-              for (int h = 0; h < HD / 64; ++h) tma_load_3d(dst + h * HALF, x & 1 ? &tmv : &tmk, 64 * h, row, blk, bar, pol);
+                for (int h = 0; h < HD / 64; ++h) tma_load_3d(dst + h * HALF, x & 1 ? &tmv : &tmk, 64 * h, row, blk, bar, pol);
+              }
             }
           }
         }
@@ -274,10 +291,10 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ scheduler
-      const long long all = all_units<KxLine>(a, lane), per = units_per_cta(all, gridDim.x, KX_MIN_UNITS);
+      const long long all = all_units<KxLine<CACHE>>(a, lane), per = units_per_cta(all, gridDim.x, KX_MIN_KEYS / KEYS);
       const long long begin = min(per * blockIdx.x, all), end = min(begin + per, all);
       long long u = begin, rest = 0;
-      int b = u < end ? find_unit<KxLine>(a, lane, u, &rest) : 0;
+      int b = u < end ? find_unit<KxLine<CACHE>>(a, lane, u, &rest) : 0;
       Cut cut;
       cut.last = 0;
       int n = 0;
@@ -286,12 +303,12 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         Seg s;
         s.valid = 0;
         if (u < end) {
-          KxLine l(a, b);
+          KxLine<CACHE> l(a, b);
 #pragma unroll 1
           while (rest >= l.units(a)) {       // (the next sequence that has units)
             rest -= l.units(a);
             ++b;
-            l = KxLine(a, b);
+            l = KxLine<CACHE>(a, b);
           }
           const long long item = quotient(rest, l.tiles);
           s.valid = 1;
@@ -336,7 +353,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       const int g = warp - 2;
       const uint32_t id1 = F4 ? idesc_f16_f32(128, KA_H) : idesc_bf16_f32(128, KA_H);
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
-      const uint64_t dq = smem_desc_sw128(q_u + g * ENTRY);
+      const uint64_t dq = smem_desc_sw128(q_u + g * Q_TILE);
       const uint32_t tO = tmem + T_O + 128 * g;
       RingPos base{0, 0};                    // the segment's first entry
       uint32_t n = 0, turn = 0;              // units of this group so far; segments with a tile
@@ -349,7 +366,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           turn ^= 1;
         }
         tc_fence_after();
-        const int W = s.units_of(g, last_units(s));
+        const int W = s.units_of<UPT>(g, last_units(s));
         RingPos kp = base;
         if (both && g) kp.step(2, NS);
         RingPos vp = kp;
@@ -359,19 +376,19 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           if (w < W) {
             // S = Q K^T of unit w, once P V of the unit before the last (same buffer) is done
             const uint32_t u = n + w, buf = 2 * g + (u & 1);
-            if (!(w & 1)) ok = kx_wait(bar_kvf + 8 * kp.slot, kp.turn, a.err, abort_flag);
+            if (UPT == 1 || !(w & 1)) ok = kx_wait(bar_kvf + 8 * kp.slot, kp.turn, a.err, abort_flag);
             ok = ok && kx_wait(bar_pe + 8 * buf, ((u >> 1) & 1) ^ 1, a.err, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + buf * KA_H;
-            const uint64_t dk = smem_desc_sw128(ring_u + kp.slot * ENTRY + (w & 1) * (KA_H * 128));
+            const uint64_t dk = smem_desc_sw128(ring_u + kp.slot * ENTRY + (UPT == 2 ? (w & 1) * (KA_H * 128) : 0));
 #pragma unroll
             for (int j = 0; j < HD / 16; ++j) {
-              const uint32_t ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
-              tc_mma_bf16(d, dq + ko, dk + ko, id1, j > 0 ? 1u : 0u);
+              const uint32_t qo = ((j >> 2) * Q_HALF + (j & 3) * 32) >> 4, ko = ((j >> 2) * HALF + (j & 3) * 32) >> 4;
+              tc_mma_bf16(d, dq + qo, dk + ko, id1, j > 0 ? 1u : 0u);
             }
             tc_commit(bar_sf + 8 * buf);
-            if ((w & 1) || w == W - 1) {
+            if (UPT == 1 || (w & 1) || w == W - 1) {
               tc_commit(bar_kve + 8 * kp.slot);
               if (both) tc_commit(bar_kve + 8 * kp.slot);
               kp.step(2, NS);
@@ -381,16 +398,16 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           if (w > 0) {   // O += P V of unit x
             const int x = w - 1;
             const uint32_t u = n + x, buf = 2 * g + (u & 1);
-            if (!(x & 1)) ok = kx_wait(bar_kvf + 8 * vp.slot, vp.turn, a.err, abort_flag);
+            if (UPT == 1 || !(x & 1)) ok = kx_wait(bar_kvf + 8 * vp.slot, vp.turn, a.err, abort_flag);
             ok = ok && kx_wait(bar_pf + 8 * buf, (u >> 1) & 1, a.err, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dv = smem_desc_sw128_mn(ring_u + vp.slot * ENTRY + (x & 1) * (KA_H * 128), HALF, 1024);
+            const uint64_t dv = smem_desc_sw128_mn(ring_u + vp.slot * ENTRY + (UPT == 2 ? (x & 1) * (KA_H * 128) : 0), HALF, 1024);
             const uint32_t tp = tmem + buf * KA_H;
 #pragma unroll
             for (int j = 0; j < KA_H / 16; ++j) tc_mma_bf16_ta(tO, tp + 8 * j, dv + j * 128, id2, x > 0 || j > 0 ? 1u : 0u);
             tc_commit(bar_pe + 8 * buf);
-            if ((x & 1) || x == W - 1) {
+            if (UPT == 1 || (x & 1) || x == W - 1) {
               tc_commit(bar_kve + 8 * vp.slot);
               if (both) tc_commit(bar_kve + 8 * vp.slot);
               vp.step(2, NS);
@@ -415,22 +432,26 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   } else if (warp >= CONV_WARP) {
     if constexpr (F4) {
       set_regs_down<KX_REG_CONV>();
-      // ------------------------------ raw tiles -> fp16 tiles, as in kv_attention_tc
-      constexpr int GR = HD / 16, IT = KA_CH * GR / CONV, RSTEP = CONV / GR;
+      // ------------------------------ raw tiles -> fp16 tiles: 16 dims per thread and step
+      // Teams of two warps take an entry each in turn: an entry's chain of waits, loads, stores and the
+      // proxy fence takes 1000 cycles however many warps share it.
+      constexpr int TEAM = 64, TEAMS = CONV / TEAM, GR = HD / 16, IT = KEYS * GR / TEAM, RSTEP = TEAM / GR;
       static_assert(RSTEP % 8 == 0, "the swizzle repeats every 8 rows");
-      const int ct = tid - 32 * CONV_WARP, gidx = ct % GR, r0 = ct / GR, sw = gidx >> 2;
+      const int team = (warp - CONV_WARP) >> 1, ct = (tid - 32 * CONV_WARP) % TEAM, gidx = ct % GR, r0 = ct / GR, sw = gidx >> 2;
       RingPos rp{0, 0}, wp{0, 0};
-      int done = 0;
+      const int box_log = min(a.pool.ps_log, 6);
+      int done = 0;                          // entries so far
       for (;; dp.step(1, KX_DESCS)) {
         const Seg s = segment(dp);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || !s.valid) break;
 #pragma unroll 1
-        for (int e = 0; e < 2 * s.T; ++e, rp.step(1, NS), wp.step(1, NR)) {
+        for (int e = 0; e < 2 * s.T; ++e, ++done, rp.step(1, NS), wp.step(1, NR)) {
+          if (done % TEAMS != team) continue;
           ok = kx_wait<true>(bar_rf + 8 * wp.slot, wp.turn, a.err, abort_flag);
           const uint8_t* src = raw + wp.slot * RAW;
           const uint32_t have = raw_pages[wp.slot];
-          const int k0 = (s.t0 + (e >> 1)) * KA_CH;
+          const int k0 = (s.t0 + (e >> 1)) * KEYS;
           uint2 code[IT];
           uint32_t scale[IT];
 #pragma unroll
@@ -439,11 +460,11 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
             code[i] = reinterpret_cast<const uint2*>(src + r * (HD / 2))[gidx];
             scale[i] = src[RAW_SCALES + r * GR + gidx];
           }
-          if (k0 + KA_CH > s.len || have != (1u << (KA_CH >> a.pool.ps_log)) - 1u) {
+          if (k0 + KEYS > s.len || have != (1u << (KEYS >> box_log)) - 1u) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) {     // rows behind the last key, and of pages that are not there: zeros
               const int r = r0 + i * RSTEP;
-              if (k0 + r >= s.len || !((have >> (r >> a.pool.ps_log)) & 1u)) {
+              if (k0 + r >= s.len || !((have >> (r >> box_log)) & 1u)) {
                 code[i] = make_uint2(0u, 0u);
                 scale[i] = 0u;
               }
@@ -452,7 +473,6 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_re + 8 * wp.slot);
           if (done >= NS) ok = kx_wait<true>(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag) && ok;
-          else ++done;
           ok = !__any_sync(0xffffffffu, !ok);
           if (!ok) break;
           const uint32_t dst = ring_u + rp.slot * ENTRY + sw * HALF, c = 2 * (gidx & 3);
@@ -514,7 +534,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           if (lane / ROWS == k) mine = theirs;
         }
         const int r = 32 * quad + ROWS * k + lane / LR;
-        st_smem16(q_u + g * ENTRY + (c >> 3) * HALF + ka_sw(r, c & 7), w);
+        st_smem16(q_u + g * Q_TILE + (c >> 3) * Q_HALF + ka_sw(r, c & 7), w);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -684,7 +704,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       rs = rs2;
       idle = 32 * quad >= s.qv - (both ? 0 : KA_QV * g);   // a warp without vectors
       const int end_page = s.len >> a.pool.ps_log, end_rows = F4 ? 0 : s.len & (ps - 1);
-      const int W = s.units_of(g, last_units(s));
+      const int W = s.units_of<UPT>(g, last_units(s));
       m_run = -INFINITY;
       l_run = 0.f;
 #pragma unroll 1
@@ -695,14 +715,14 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         if (!idle) {
           // The scores become p with the maximum so far, which mostly stays, while this unit's is found;
           // where that rose too far they are read again.
-          const int kt = (s.t0 + (both ? g + (w & ~1) : w >> 1)) * KA_CH;   // the tile's first key
+          const int own_tile = UPT == 2 ? w >> 1 : w, kt = (s.t0 + (both ? g + 2 * own_tile : own_tile)) * KEYS;   // the tile's first key
           float x[KA_H], p8[8], pk[32];
 #pragma unroll 1
           for (bool again = false;;) {
             tmem_ld32(ts, x);
             tmem_ld32(ts + 32, x + 32);
             tmem_wait_ld();
-            if (kt + KA_CH > s.len) {        // columns without a key
+            if (kt + KEYS > s.len) {         // columns without a key
               const int at = (end_page << a.pool.ps_log) - kt;
               Bits vis = bits_below(end_rows ? at + ps : s.len - kt);
               if (end_rows) {
@@ -710,7 +730,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
                 vis.lo &= lo.lo | ~hi.lo;
                 vis.hi &= lo.hi | ~hi.hi;
               }
-              const unsigned long long bits = w & 1 ? vis.hi : vis.lo;
+              const unsigned long long bits = UPT == 2 && (w & 1) ? vis.hi : vis.lo;
 #pragma unroll
               for (int e = 0; e < KA_H; ++e) x[e] = (bits >> e) & 1ull ? x[e] : -INFINITY;
             }
@@ -834,13 +854,13 @@ cudaError_t launch_wide(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
     }
     if (dev < 64) granted[dev].store(cap);
   }
-  const size_t fixed = 2 * ka_entry(HD) + KX_MISC;
-  const int ns = CACHE == EAGLE_CACHE_F4 ? (HD == 64 ? 6 : 4) : std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / ka_entry(HD)));
-  const size_t left = cap - fixed - static_cast<size_t>(ns) * ka_entry(HD);
-  const int nr = CACHE == EAGLE_CACHE_F4 ? std::min<int>(KX_MAX_RAW, static_cast<int>(left / ka_raw_bytes(HD))) : 0;
-  if (cap < fixed + 4 * ka_entry(HD) || ns < 4 ||   // (a shared item needs 4: its next keys come before its last values are free)
-       (CACHE == EAGLE_CACHE_F4 && nr < 2)) return cudaErrorInvalidConfiguration;
-  e = launch_after(OWN, dim3(ctas), kx_threads(CACHE), fixed + static_cast<size_t>(ns) * ka_entry(HD) + static_cast<size_t>(nr) * ka_raw_bytes(HD), st, kv_cross_wide<HD, CACHE, OWN>,
+  constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
+  constexpr size_t fixed = 2 * ka_entry(HD) + KX_MISC, entry = kx_entry(HD, CACHE), raw = kx_raw_bytes(HD);
+  const int ns = F4 ? (HD == 64 ? 12 : 8) : std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / entry));
+  if (cap < fixed + 4 * entry || ns < 4 || cap < fixed + ns * entry) return cudaErrorInvalidConfiguration;   // (a shared item's groups are 4 entries apart)
+  const int nr = F4 ? std::min<int>(KX_MAX_RAW, static_cast<int>((cap - fixed - ns * entry) / raw)) : 0;
+  if (F4 && nr < 2) return cudaErrorInvalidConfiguration;
+  e = launch_after(OWN, dim3(ctas), kx_threads(CACHE), fixed + ns * entry + nr * raw, st, kv_cross_wide<HD, CACHE, OWN>,
                    tmk, tmv, a, own, parts, ns, nr);
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_after(true, dim3(ctas, KX_QV / KX_JOIN_V), 32 * KX_JOIN_WARPS, 0, st, kv_cross_wide_join<HD>, a, own, OWN ? 1 : 0,
@@ -858,12 +878,13 @@ cudaError_t launch_kind(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
 
 }  // namespace
 
-KxPlan eagle::kx_plan(int Hkv, int hd, int G, int B, int max_rows, int max_len) {
-  const long long blocks = (static_cast<long long>(max_rows) * G + KX_QV - 1) / KX_QV, tiles = (static_cast<long long>(max_len) + KA_CH - 1) / KA_CH;
+KxPlan eagle::kx_plan(int kind, int Hkv, int hd, int G, int B, int max_rows, int max_len) {
+  const long long blocks = (static_cast<long long>(max_rows) * G + KX_QV - 1) / KX_QV, tiles = (static_cast<long long>(max_len) + kx_keys(kind) - 1) / kx_keys(kind);
   const double units = static_cast<double>(B) * Hkv * blocks * tiles;
   const int sms = num_sms() > 0 ? num_sms() : 152;   // (152: without a device, a GB300's)
   KxPlan p;
-  p.ctas = units / KX_MIN_UNITS < sms ? static_cast<int>(units / KX_MIN_UNITS) + 1 : sms;
+  const double ctas = units / (KX_MIN_KEYS / kx_keys(kind));
+  p.ctas = ctas < sms ? static_cast<int>(ctas) + 1 : sms;
   p.bytes = p.ctas * (static_cast<int64_t>(sizeof(Cut)) + (p.ctas == 1 ? 0 : 8ll * kx_slot(hd)));
   return p;
 }

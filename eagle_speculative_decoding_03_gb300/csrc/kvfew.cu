@@ -161,15 +161,21 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
         const bool data = t.keys > 0;
         push(t, (data ? kf_kv(HD) : 0u) + (x == 0 ? static_cast<uint32_t>(qv) * HD * 2 : 0u));
         if (!ok) break;
-        const uint32_t bar = bar_full + 8 * rp.slot, at = ring + rp.slot * kf_kv(HD);
-        if (data && lane < boxes) {          // (a page that is not there reads as zeros: a block outside the map)
-          const int blk = page >= 0 ? page * a.pool.Hkv + kvh : a.pool.num_pages * a.pool.Hkv;
-          const int row = (k0 + lane * rows) & ((1 << a.pool.ps_log) - 1);
-          const uint32_t dst = at + lane * (rows * 128);
+        const uint32_t slot = uniform(rp.slot), bar = bar_full + 8 * slot, at = ring + slot * kf_kv(HD);
+        // One lane copies box after box, all that the copies take being the same for the whole warp: a lane a
+        // box, each with values of its own, took 200 cycles a copy.
+#pragma unroll 1
+        for (int i = 0; i < boxes && data; ++i) {   // (a page that is not there reads as zeros: a block outside the map)
+          const int pg = __shfl_sync(0xffffffffu, page, i);
+          const int blk = pg >= 0 ? pg * a.pool.Hkv + kvh : a.pool.num_pages * a.pool.Hkv;
+          const int row = (k0 + i * rows) & ((1 << a.pool.ps_log) - 1);
+          const uint32_t dst = at + i * (rows * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < HD / 64; ++h) {
-            tma_load_3d(dst + h * HALF, &tmk, 64 * h, row, blk, bar, pol);
-            tma_load_3d(dst + V_AT + h * HALF, &tmv, 64 * h, row, blk, bar, pol);
+            for (int h = 0; h < HD / 64; ++h) {
+              tma_load_3d(dst + h * HALF, &tmk, 64 * h, row, blk, bar, pol);
+              tma_load_3d(dst + V_AT + h * HALF, &tmv, 64 * h, row, blk, bar, pol);
+            }
           }
         }
         if (x == 0 && lane >= 16 && lane - 16 < qv) {
@@ -399,11 +405,17 @@ cudaError_t launch_few(const CUtensorMap& tmk, const CUtensorMap& tmv, const KaA
 
 }  // namespace
 
+static double kf_units(int Hkv, int B, int max_len) {
+  return static_cast<double>(B) * Hkv * ((static_cast<long long>(max_len) + KF_KEYS - 1) / KF_KEYS);
+}
+static int kf_sms() { return num_sms() > 0 ? num_sms() : 152; }   // (152: without a device, a GB300's)
+
+bool eagle::kf_worth(int Hkv, int B, int max_len) { return kf_units(Hkv, B, max_len) >= 8. * kf_sms(); }
+
 KxPlan eagle::kf_plan(int Hkv, int hd, int B, int max_len) {
-  const double units = static_cast<double>(B) * Hkv * ((static_cast<long long>(max_len) + KF_KEYS - 1) / KF_KEYS);
-  const int sms = num_sms() > 0 ? num_sms() : 152;   // (152: without a device, a GB300's)
+  const double ctas = kf_units(Hkv, B, max_len) / KF_MIN_UNITS;
   KxPlan p;
-  p.ctas = units / KF_MIN_UNITS < sms ? static_cast<int>(units / KF_MIN_UNITS) + 1 : sms;
+  p.ctas = ctas < kf_sms() ? static_cast<int>(ctas) + 1 : kf_sms();
   p.bytes = p.ctas * (static_cast<int64_t>(sizeof(Cut)) + (p.ctas == 1 ? 0 : 8ll * kf_slot(hd)));
   return p;
 }

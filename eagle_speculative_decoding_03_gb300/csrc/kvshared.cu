@@ -238,9 +238,10 @@ CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int 
   const long long qv = static_cast<long long>(max_rows) * G;
   p.by = qv >= KX_FROM ? Cutting::WIDE : c->kind == EAGLE_CACHE_BF16 ? Cutting::FEW : Cutting::RANGES;
   if (p.by != Cutting::WIDE) p.ranges = ka_plan(c->kind, c->n_kv_heads, G, B, max_rows, max_len, may_join);
-  // (a step's few ranges in one cluster each: no second launch.  cross_step_b1 10 us, in line 16)
-  if (p.by == Cutting::FEW && p.ranges.joined) p.by = Cutting::RANGES;
-  if (p.by == Cutting::WIDE) p.line = kx_plan(c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
+  // (a step's few ranges in one cluster each take no second launch: cross_step_b1 10 us, in line 16; and
+  // with little to read its start counts for more than even shares: shared_step_b2 23 us, in line 30)
+  if (p.by == Cutting::FEW && (p.ranges.joined || !kf_worth(c->n_kv_heads, B, max_len))) p.by = Cutting::RANGES;
+  if (p.by == Cutting::WIDE) p.line = kx_plan(c->kind, c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
   if (p.by == Cutting::FEW) p.line = kf_plan(c->n_kv_heads, c->head_dim, B, max_len);
   return p;
 }
