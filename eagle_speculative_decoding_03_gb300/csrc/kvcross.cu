@@ -31,13 +31,14 @@ constexpr int KX_QV = 256;                 // query vectors of a block
 constexpr int KX_DESCS = 4;                // segments in flight between the scheduler and the roles
 constexpr int KX_MIN_KEYS = 384;           // keys of an item that are worth a CTA
 constexpr int KX_MAX_RAW = 12;             // raw tiles of a 4-bit pool in flight
-constexpr uint32_t KX_MISC = 3072;         // barriers (0), segments (704), states of an item that both groups take (1024)
+constexpr uint32_t KX_MISC = 3 << 10;         // barriers (0), segments (736), states of an item that both groups take (1024)
 constexpr int KX_SOFTMAX = 256;            // softmax threads: one per query vector
-// registers per thread of the 4-bit kernel's roles (the launch checks their sum)
-constexpr int KX_REG_CTRL = 48, KX_REG_SOFTMAX = 152, KX_REG_CONV = 64;
+constexpr int KX_COPIERS = 4;              // loader warps
+constexpr int KX_THREADS = 128 + KX_SOFTMAX + 32 * KX_COPIERS;   // control, softmax, loaders
+// registers per thread of the roles (the launch checks their sum)
+constexpr int KX_REG_CTRL = 48, KX_REG_SOFTMAX = 176, KX_REG_LOAD = 80;
 constexpr int KX_JOIN_V = 32, KX_JOIN_WARPS = 8;
 
-__host__ __device__ constexpr int kx_threads(int cache) { return 128 + KX_SOFTMAX + (cache == EAGLE_CACHE_F4 ? 256 : 0); }
 // floats of a partial result: [hd / 4][256] float4 outputs, [256] (maximum, sum)
 __host__ __device__ constexpr size_t kx_slot(int hd) { return static_cast<size_t>(KX_QV) * (hd + 2); }
 
@@ -48,6 +49,15 @@ __host__ __device__ constexpr uint32_t kx_entry(int hd, int cache) { return stat
 __host__ __device__ constexpr uint32_t kx_raw_bytes(int hd) { return static_cast<uint32_t>(hd) / 2 * KA_H + hd / 16 * KA_H; }
 template <int CACHE>
 using KxLine = Line<8, kx_keys(CACHE)>;    // (blocks of KX_QV vectors)
+
+EAGLE_DEV uint32_t ld_acquire_smem(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+EAGLE_DEV void st_release_smem(uint32_t addr, uint32_t x) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
 
 // Part of an item: tiles [t0, t0 + T) of query vectors [v0, v0 + qv) of sequence b.
 struct Seg {
@@ -133,12 +143,12 @@ EAGLE_DEV float powers64(float* x, float rs, float mb, float* p8, float* pk) {
 }
 
 template <int HD, int CACHE, bool OWN>
-__global__ void __launch_bounds__(kx_threads(CACHE), 1)
+__global__ void __launch_bounds__(KX_THREADS, 1)
 kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const KaArgs a, const KaArgs own,
               float* parts, const int NS, const int NR) {
   constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
   constexpr float LIFT = F4 ? 7.f : 0.f;     // fp16 p is held times 2^7 (as in kv_attention_tc)
-  constexpr int THREADS = kx_threads(CACHE), CONV_WARP = 4 + KX_SOFTMAX / 32, CONV = THREADS - 32 * CONV_WARP;
+  constexpr int LOAD_WARP = 4 + KX_SOFTMAX / 32;
   constexpr int KEYS = kx_keys(CACHE), UPT = KEYS / KA_H;
   constexpr uint32_t ENTRY = kx_entry(HD, CACHE), HALF = KEYS * 128, RAW = kx_raw_bytes(HD), RAW_SCALES = HD / 2 * KEYS;
   constexpr uint32_t Q_TILE = ka_entry(HD), Q_HALF = KA_QV * 128;
@@ -153,14 +163,15 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   const uint32_t misc_u = smem_u32(misc);
   // ring full / free; per score buffer (group, 64 columns): scores there, p there, P V done; per group:
   // queries there, segment done; raw tiles full / free, segments full / free; an item of both groups:
-  // states there / read
+  // states there / read; a loader's turn
   const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 256, bar_pe = misc_u + 288,
                  bar_q = misc_u + 320, bar_fin = misc_u + 336, bar_df = misc_u + 352, bar_de = misc_u + 384, bar_x = misc_u + 416,
-                 bar_rf = misc_u + 432, bar_re = misc_u + 528;
+                 bar_rf = misc_u + 432, bar_re = misc_u + 528, bar_next = misc_u + 680;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 624);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 628);
   volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(misc + 632);
-  Seg* segs = reinterpret_cast<Seg*>(misc + 704);
+  const uint32_t placed_u = misc_u + 716;    // ring entries whose place the loaders have taken
+  Seg* segs = reinterpret_cast<Seg*>(misc + 736);
 
   pdl_trigger();
   if (ring_u & 1023u) {                      // (the swizzled tiles' alignment)
@@ -169,7 +180,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   }
   if (tid == 0) {
     for (int s = 0; s < KA_MAX_SLOTS; ++s) {
-      mbar_init(bar_kvf + 8 * s, F4 ? 2 : 1);
+      mbar_init(bar_kvf + 8 * s, 1);
       mbar_init(bar_kve + 8 * s, 2);
     }
     for (int b = 0; b < 4; ++b) {
@@ -184,13 +195,15 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     }
     for (int s = 0; F4 && s < KX_MAX_RAW; ++s) {
       mbar_init(bar_rf + 8 * s, 1);
-      mbar_init(bar_re + 8 * s, 2);
+      mbar_init(bar_re + 8 * s, 1);
     }
+    for (int t = 0; t < KX_COPIERS; ++t) mbar_init(bar_next + 8 * t, 1);
     for (int s = 0; s < KX_DESCS; ++s) {
       mbar_init(bar_df + 8 * s, 1);
-      mbar_init(bar_de + 8 * s, 3 + KX_SOFTMAX / 32 + (F4 ? CONV / 32 : 0));
+      mbar_init(bar_de + 8 * s, 2 + KX_SOFTMAX / 32 + KX_COPIERS);
     }
     *abort_flag = 0;
+    st_release_smem(placed_u, 0);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -221,75 +234,8 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   };
 
   if (warp < 4) {
-    if constexpr (F4) set_regs_down<KX_REG_CTRL>();
-    if (warp == 0) {
-      // ------------------------------------------------------------ producer: lane = page of the tile
-      const uint64_t pol = policy_evict_normal();   // (the other blocks of the sequence read the keys too)
-      const int ps = 1 << a.pool.ps_log, box = min(ps, KEYS), per = KEYS / box, slots = F4 ? NR : NS;
-      RingPos rp{0, 0};
-      int e = 0;
-      for (;; dp.step(1, KX_DESCS)) {
-        const Seg s = segment(dp);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || !s.valid) break;
-        const int end_page = s.len >> a.pool.ps_log, end_rows = F4 ? 0 : s.len & (ps - 1);
-        int page = -1;
-        Pages pages;
-        pages.open(a, s.b, s.t0 * KEYS, s.len, box, lane);
-#pragma unroll 1
-        for (int x = 0; x < 2 * s.T && ok; ++x, rp.step(1, slots)) {
-          const int slot = uniform(rp.slot), tile = s.t0 + (x >> 1);
-          if (!(x & 1)) page = pages.get(a, s.b, s.t0 * KEYS, s.len, box, lane, (x >> 1) * per);   // (the values are in the keys' pages)
-          const uint32_t bar = (F4 ? bar_rf : bar_kvf) + 8 * slot;
-          if (e >= slots) ok = kx_wait((F4 ? bar_re : bar_kve) + 8 * slot, rp.turn ^ 1, a.err, abort_flag);
-          else ++e;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          // One lane copies box after box, all that the copies take being the same for the whole warp: a lane a
-          // box, each with values of its own, took 200 cycles a copy.
-          if (F4) {
-            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0 && lane < per);
-            const uint32_t codes = static_cast<uint32_t>(box) * (HD / 2), scales = static_cast<uint32_t>(box) * (HD / 16);
-            if (elect_one()) {
-              raw_pages[slot] = have;
-              mbar_arrive_expect_tx(bar, __popc(have) * (codes + scales));
-            }
-            __syncwarp();
-#pragma unroll 1
-            for (int i = 0; i < per; ++i) {
-              const int pg = __shfl_sync(0xffffffffu, page, i);
-              const size_t row = kv_row(a.pool, pg, s.kvh, tile * KEYS + i * box);
-              const uint32_t dst = smem_u32(raw) + slot * RAW;
-              if (pg >= 0 && elect_one()) {
-                bulk_load(dst + i * codes, static_cast<const uint8_t*>(x & 1 ? a.pool.v : a.pool.k) + row * (HD / 2), codes, bar);
-                bulk_load(dst + RAW_SCALES + i * scales, static_cast<const uint8_t*>(x & 1 ? a.pool.vs : a.pool.ks) + row * (HD / 16), scales, bar);
-              }
-            }
-          } else {
-            if (elect_one()) mbar_arrive_expect_tx(bar, ENTRY);
-            __syncwarp();
-#pragma unroll 1
-            for (int i = 0; i < per; ++i) {    // (a page that is not there reads as zeros: a block outside the map)
-              const int pg = __shfl_sync(0xffffffffu, page, i), pi = tile * per + i;
-              const int blk = pg >= 0 ? pg * a.pool.Hkv + s.kvh : a.pool.num_pages * a.pool.Hkv;
-              const int row = pi == end_page && end_rows ? end_rows - ps : 0;
-              const uint32_t dst = ring_u + slot * ENTRY + i * (ps * 128);
-              if (elect_one()) {
-#pragma unroll
-                for (int h = 0; h < HD / 64; ++h) tma_load_3d(dst + h * HALF, x & 1 ? &tmv : &tmk, 64 * h, row, blk, bar, pol);
-              }
-            }
-          }
-        }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(bar_de + 8 * dp.slot);
-      }
-      if (!ok) {   // let copies already issued land before the CTA releases its shared memory
-        const long long t0 = clock64();
-        while (clock64() - t0 < 4000000) {
-        }
-      }
-    } else if (warp == 1) {
+    set_regs_down<KX_REG_CTRL>();
+    if (warp == 1) {
       // ------------------------------------------------------------ scheduler
       const long long all = all_units<KxLine<CACHE>>(a, lane), per = units_per_cta(all, gridDim.x, KX_MIN_KEYS / KEYS);
       const long long begin = min(per * blockIdx.x, all), end = min(begin + per, all);
@@ -347,7 +293,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       }
       if (lane == 0) reinterpret_cast<Cut*>(parts)[blockIdx.x] = cut;
       if (OWN) pdl_wait();                   // (this kernel ends after the one before it)
-    } else if (elect_one()) {
+    } else if (warp >= 2 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer of group g
       // One thread walks the group's units and issues; nothing in the loop divides or votes.
       const int g = warp - 2;
@@ -357,6 +303,22 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       const uint32_t tO = tmem + T_O + 128 * g;
       RingPos base{0, 0};                    // the segment's first entry
       uint32_t n = 0, turn = 0;              // units of this group so far; segments with a tile
+      uint32_t first = 0, placed = 0;        // the segment's first entry, counted from the start; entries known to be under way
+      // Waits for entry e.  Its barrier is looked at only once the entry before it in the same place is
+      // through: of a shared item this group waits for every other tile only, and a place whose last entry,
+      // the other group's, was still being copied would look like the one that is waited for.
+      auto there = [&](const RingPos& p, uint32_t e) {
+#pragma unroll 1
+        for (uint32_t i = 0; static_cast<int>(placed - e) <= 0; ++i) {
+          placed = ld_acquire_smem(placed_u);
+          if ((i & 255u) == 255u && (*abort_flag || i > (1u << 24))) {
+            if (!*abort_flag) atomicOr(a.err, DEVERR_TIMEOUT);
+            *abort_flag = 1;
+            return false;
+          }
+        }
+        return kx_wait(bar_kvf + 8 * p.slot, p.turn, a.err, abort_flag);
+      };
       for (;; dp.step(1, KX_DESCS)) {
         const Seg s = segment(dp);
         if (!ok || !s.valid) break;
@@ -368,15 +330,17 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         tc_fence_after();
         const int W = s.units_of<UPT>(g, last_units(s));
         RingPos kp = base;
-        if (both && g) kp.step(2, NS);
+        uint32_t ke = first, ve;
+        if (both && g) kp.step(2, NS), ke += 2;
         RingPos vp = kp;
         vp.step(1, NS);
+        ve = ke + 1;
 #pragma unroll 1
         for (int w = 0; w <= W && ok; ++w) {
           if (w < W) {
             // S = Q K^T of unit w, once P V of the unit before the last (same buffer) is done
             const uint32_t u = n + w, buf = 2 * g + (u & 1);
-            if (UPT == 1 || !(w & 1)) ok = kx_wait(bar_kvf + 8 * kp.slot, kp.turn, a.err, abort_flag);
+            if (UPT == 1 || !(w & 1)) ok = there(kp, ke);
             ok = ok && kx_wait(bar_pe + 8 * buf, ((u >> 1) & 1) ^ 1, a.err, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -393,12 +357,13 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
               if (both) tc_commit(bar_kve + 8 * kp.slot);
               kp.step(2, NS);
               if (both) kp.step(2, NS);
+              ke += both ? 4 : 2;
             }
           }
           if (w > 0) {   // O += P V of unit x
             const int x = w - 1;
             const uint32_t u = n + x, buf = 2 * g + (u & 1);
-            if (UPT == 1 || !(x & 1)) ok = kx_wait(bar_kvf + 8 * vp.slot, vp.turn, a.err, abort_flag);
+            if (UPT == 1 || !(x & 1)) ok = there(vp, ve);
             ok = ok && kx_wait(bar_pf + 8 * buf, (u >> 1) & 1, a.err, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -412,6 +377,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
               if (both) tc_commit(bar_kve + 8 * vp.slot);
               vp.step(2, NS);
               if (both) vp.step(2, NS);
+              ve += both ? 4 : 2;
             }
           }
         }
@@ -421,6 +387,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         const uint32_t at = base.slot + 2u * s.T;
         base.turn ^= (at / NS) & 1;
         base.slot = at % NS;
+        first += 2u * s.T;
         mbar_arrive(bar_de + 8 * dp.slot);
       }
       if (!ok) {   // let MMAs already issued finish before TMEM is released
@@ -429,73 +396,169 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         }
       }
     }
-  } else if (warp >= CONV_WARP) {
-    if constexpr (F4) {
-      set_regs_down<KX_REG_CONV>();
-      // ------------------------------ raw tiles -> fp16 tiles: 16 dims per thread and step
-      // Teams of two warps take an entry each in turn: an entry's chain of waits, loads, stores and the
-      // proxy fence takes 1000 cycles however many warps share it.
-      constexpr int TEAM = 64, TEAMS = CONV / TEAM, GR = HD / 16, IT = KEYS * GR / TEAM, RSTEP = TEAM / GR;
-      static_assert(RSTEP % 8 == 0, "the swizzle repeats every 8 rows");
-      const int team = (warp - CONV_WARP) >> 1, ct = (tid - 32 * CONV_WARP) % TEAM, gidx = ct % GR, r0 = ct / GR, sw = gidx >> 2;
-      RingPos rp{0, 0}, wp{0, 0};
-      const int box_log = min(a.pool.ps_log, 6);
-      int done = 0;                          // entries so far
-      for (;; dp.step(1, KX_DESCS)) {
-        const Seg s = segment(dp);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || !s.valid) break;
-#pragma unroll 1
-        for (int e = 0; e < 2 * s.T; ++e, ++done, rp.step(1, NS), wp.step(1, NR)) {
-          if (done % TEAMS != team) continue;
-          ok = kx_wait<true>(bar_rf + 8 * wp.slot, wp.turn, a.err, abort_flag);
-          const uint8_t* src = raw + wp.slot * RAW;
-          const uint32_t have = raw_pages[wp.slot];
-          const int k0 = (s.t0 + (e >> 1)) * KEYS;
-          uint2 code[IT];
-          uint32_t scale[IT];
-#pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            const int r = r0 + i * RSTEP;
-            code[i] = reinterpret_cast<const uint2*>(src + r * (HD / 2))[gidx];
-            scale[i] = src[RAW_SCALES + r * GR + gidx];
+  } else if (warp >= LOAD_WARP) {
+    // ------------------------------------------------------------ loaders
+    // Four warps take the entries, keys and values of the tiles, in turn: one thread issues a copy in 200
+    // cycles, and 128 keys take 8 to 32 of them.  4 bits: they convert what they copied; an entry's chain of
+    // waits, loads, stores and the proxy fence takes 1000 cycles however many warps share it.
+    set_regs_down<KX_REG_LOAD>();
+    const int team = warp - LOAD_WARP;
+    const int ps = 1 << a.pool.ps_log, box = min(ps, KEYS), per = KEYS / box, NT = F4 ? NR / KX_COPIERS : 1;   // raw tiles of a warp
+    RingPos rp{0, 0}, cp{0, 0}, wp{0, 0};              // the warp's entry in the ring, its raw tile to copy into, to convert
+    rp.step(team, NS);
+    uint32_t entries = 0, taken = 0;                   // of the segments before; by this warp
+    for (;; dp.step(1, KX_DESCS)) {
+      const Seg s = segment(dp);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || !s.valid) break;
+      const int end_page = s.len >> a.pool.ps_log, end_rows = F4 ? 0 : s.len & (ps - 1);
+      const int first = (team - static_cast<int>(entries)) & (KX_COPIERS - 1), E = 2 * s.T;
+      entries += E;
+      // box `lane` of the tile of entry e, one entry ahead
+      auto lookup = [&](int e) {
+        const int k = (s.t0 + (e >> 1)) * KEYS + lane * box;
+        return e < E && lane < per && k < s.len ? kv_page(a.pool, s.b, k, a.err) : -1;
+      };
+      int page = lookup(first);
+      // All that a copy takes is the same for the whole warp.
+      auto copy = [&](int e, uint32_t bar, int slot) {
+        const int now = page, tile = s.t0 + (e >> 1), v = e & 1;
+        page = lookup(e + KX_COPIERS);
+        if constexpr (F4) {
+          const uint32_t have = __ballot_sync(0xffffffffu, now >= 0);
+          const uint32_t codes = static_cast<uint32_t>(box) * (HD / 2), scales = static_cast<uint32_t>(box) * (HD / 16);
+          if (elect_one()) {
+            raw_pages[slot] = have;
+            mbar_arrive_expect_tx(bar, __popc(have) * (codes + scales));
           }
-          if (k0 + KEYS > s.len || have != (1u << (KEYS >> box_log)) - 1u) {
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < per; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, now, i);
+            const size_t row = kv_row(a.pool, pg, s.kvh, tile * KEYS + i * box);
+            const uint32_t dst = smem_u32(raw) + slot * RAW;
+            if (pg >= 0 && elect_one()) {
+              bulk_load(dst + i * codes, static_cast<const uint8_t*>(v ? a.pool.v : a.pool.k) + row * (HD / 2), codes, bar);
+              bulk_load(dst + RAW_SCALES + i * scales, static_cast<const uint8_t*>(v ? a.pool.vs : a.pool.ks) + row * (HD / 16), scales, bar);
+            }
+          }
+        } else {
+          const uint64_t pol = policy_evict_normal();  // (the other blocks of the sequence read the keys too)
+          if (elect_one()) mbar_arrive_expect_tx(bar, ENTRY);
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < per; ++i) {              // (a page that is not there reads as zeros: a block outside the map)
+            const int pg = __shfl_sync(0xffffffffu, now, i), pi = tile * per + i;
+            const int blk = pg >= 0 ? pg * a.pool.Hkv + s.kvh : a.pool.num_pages * a.pool.Hkv;
+            const int row = pi == end_page && end_rows ? end_rows - ps : 0;
+            const uint32_t dst = ring_u + slot * ENTRY + i * (ps * 128);
+            if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {     // rows behind the last key, and of pages that are not there: zeros
-              const int r = r0 + i * RSTEP;
-              if (k0 + r >= s.len || !((have >> (r >> box_log)) & 1u)) {
-                code[i] = make_uint2(0u, 0u);
-                scale[i] = 0u;
+              for (int h = 0; h < HD / 64; ++h) tma_load_3d(dst + h * HALF, v ? &tmv : &tmk, 64 * h, row, blk, bar, pol);
+            }
+          }
+        }
+      };
+      // Waits until the entry's place in the ring is free.  The loaders take their places in the entries'
+      // order: one that was a whole turn of the ring ahead would take a barrier's turn before the last for
+      // the last (the groups of a shared item free theirs in no order).
+      auto place = [&]() {
+        const uint32_t n = taken * KX_COPIERS + team;
+        if (n) ok = kx_wait(bar_next + 8 * team, (team ? taken : taken - 1) & 1, a.err, abort_flag) && ok;
+        if (n >= static_cast<uint32_t>(NS)) ok = ok && kx_wait(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) {
+          if (ok) st_release_smem(placed_u, n + 1);
+          mbar_arrive(bar_next + 8 * ((team + 1) % KX_COPIERS));
+        }
+      };
+      if constexpr (!F4) {
+#pragma unroll 1
+        for (int e = first; e < E; e += KX_COPIERS, ++taken, rp.step(KX_COPIERS, NS)) {
+          const int slot = uniform(rp.slot);
+          place();
+          if (!ok) break;
+          copy(e, bar_kvf + 8 * slot, slot);
+        }
+      } else {
+        // raw tiles are copied NT entries ahead of their conversion: 16 dims per thread and step, 8 steps at once
+        constexpr int GR = HD / 16, IT = KEYS * GR / 32, RSTEP = 32 / GR;
+        static_assert(IT % 8 == 0 && (RSTEP == 8 || RSTEP == 4), "");
+        const int gidx = lane % GR, r0 = lane / GR, sw = gidx >> 2, c = 2 * (gidx & 3), box_log = min(a.pool.ps_log, 6);
+        int ahead = first;
+        uint32_t copied = taken;
+        auto fill = [&]() {
+          const int slot = uniform(team * NT + cp.slot);
+          if (copied >= static_cast<uint32_t>(NT)) ok = kx_wait(bar_re + 8 * slot, cp.turn ^ 1, a.err, abort_flag) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) copy(ahead, bar_rf + 8 * slot, slot);
+          ahead += KX_COPIERS;
+          ++copied;
+          cp.step(1, NT);
+        };
+        for (int i = 1; i < NT && ahead < E; ++i) fill();
+#pragma unroll 1
+        for (int e = first; e < E; e += KX_COPIERS, ++taken, rp.step(KX_COPIERS, NS), wp.step(1, NT)) {
+          if (ahead < E) fill();
+          const int rslot = team * NT + wp.slot;
+          ok = kx_wait(bar_rf + 8 * rslot, wp.turn, a.err, abort_flag) && ok;
+          const uint8_t* src = raw + rslot * RAW;
+          const uint32_t have = raw_pages[rslot];
+          const int k0 = (s.t0 + (e >> 1)) * KEYS;
+          const bool whole = k0 + KEYS <= s.len && have == (1u << per) - 1u;
+          place();
+          if (!ok) break;
+          const uint32_t dst = ring_u + rp.slot * ENTRY + sw * HALF;
+#pragma unroll 1
+          for (int i0 = 0; i0 < IT; i0 += 8) {
+            uint2 code[8];
+            uint32_t scale[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + (i0 + i) * RSTEP;
+              code[i] = reinterpret_cast<const uint2*>(src + r * (HD / 2))[gidx];
+              scale[i] = src[RAW_SCALES + r * GR + gidx];
+            }
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {    // rows behind the last key, and of pages that are not there: zeros
+                const int r = r0 + (i0 + i) * RSTEP;
+                if (k0 + r >= s.len || !((have >> (r >> box_log)) & 1u)) {
+                  code[i] = make_uint2(0u, 0u);
+                  scale[i] = 0u;
+                }
               }
+            }
+            // (the two 64-dim halves share banks: the upper one stores its chunks in the other order)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + (i0 + i) * RSTEP;
+              const uint32_t f = scale_pair(scale[i]);
+              uint32_t h[4];
+              dequant8(sw ? code[i].y : code[i].x, f, h);
+              st_smem16(dst + ka_sw(r, c + sw), h);
+              dequant8(sw ? code[i].x : code[i].y, f, h);
+              st_smem16(dst + ka_sw(r, c + (sw ^ 1)), h);
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_re + 8 * wp.slot);
-          if (done >= NS) ok = kx_wait<true>(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag) && ok;
-          ok = !__any_sync(0xffffffffu, !ok);
-          if (!ok) break;
-          const uint32_t dst = ring_u + rp.slot * ENTRY + sw * HALF, c = 2 * (gidx & 3);
-          const uint32_t d0 = dst + ka_sw(r0, c + sw), d1 = dst + ka_sw(r0, c + (sw ^ 1));
-#pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            const uint32_t f = scale_pair(scale[i]);
-            uint32_t h[4];
-            dequant8(sw ? code[i].y : code[i].x, f, h);
-            st_smem16(d0 + i * (RSTEP * 128), h);
-            dequant8(sw ? code[i].x : code[i].y, f, h);
-            st_smem16(d1 + i * (RSTEP * 128), h);
-          }
+          if (lane == 0) mbar_arrive(bar_re + 8 * rslot);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_kvf + 8 * rp.slot);
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(bar_de + 8 * dp.slot);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_de + 8 * dp.slot);
+    }
+    if (!ok) {   // let copies already issued land before the CTA releases its shared memory
+      const long long t0 = clock64();
+      while (clock64() - t0 < 4000000) {
       }
     }
   } else {
-    if constexpr (F4) set_regs_up<KX_REG_SOFTMAX>();
+    set_regs_up<KX_REG_SOFTMAX>();
     // ------------------------------------------------------------ softmax of group g
     const int g = (warp - 4) >> 2, quad = warp & 3, lv = 32 * quad + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
@@ -845,22 +908,20 @@ cudaError_t launch_wide(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
   if (!cap) {
     e = allow_max_smem(reinterpret_cast<const void*>(kv_cross_wide<HD, CACHE, OWN>), &cap);
     if (e != cudaSuccess) return e;
-    if (CACHE == EAGLE_CACHE_F4) {   // the roles' registers must fit what the launch gives, or they would wait for ever
-      cudaFuncAttributes fa;
-      e = cudaFuncGetAttributes(&fa, kv_cross_wide<HD, CACHE, OWN>);
-      if (e != cudaSuccess) return e;
-      const int need = 128 * KX_REG_CTRL + KX_SOFTMAX * KX_REG_SOFTMAX + 256 * KX_REG_CONV;
-      if (fa.numRegs / 8 * 8 * kx_threads(CACHE) < need || fa.numRegs < KX_REG_CONV) return cudaErrorInvalidConfiguration;
-    }
+    cudaFuncAttributes fa;                   // the roles' registers must fit what the launch gives, or they would wait for ever
+    e = cudaFuncGetAttributes(&fa, kv_cross_wide<HD, CACHE, OWN>);
+    if (e != cudaSuccess) return e;
+    const int need = 128 * KX_REG_CTRL + KX_SOFTMAX * KX_REG_SOFTMAX + 32 * KX_COPIERS * KX_REG_LOAD;
+    if (fa.numRegs / 8 * 8 * KX_THREADS < need || fa.numRegs < KX_REG_LOAD) return cudaErrorInvalidConfiguration;
     if (dev < 64) granted[dev].store(cap);
   }
   constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
   constexpr size_t fixed = 2 * ka_entry(HD) + KX_MISC, entry = kx_entry(HD, CACHE), raw = kx_raw_bytes(HD);
-  const int ns = F4 ? (HD == 64 ? 12 : 8) : std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / entry));
+  const int ns = F4 ? (HD == 64 ? 12 : 7) : std::min<int>(KA_MAX_SLOTS, static_cast<int>((cap - fixed) / entry));
   if (cap < fixed + 4 * entry || ns < 4 || cap < fixed + ns * entry) return cudaErrorInvalidConfiguration;   // (a shared item's groups are 4 entries apart)
   const int nr = F4 ? std::min<int>(KX_MAX_RAW, static_cast<int>((cap - fixed - ns * entry) / raw)) : 0;
-  if (F4 && nr < 2) return cudaErrorInvalidConfiguration;
-  e = launch_after(OWN, dim3(ctas), kx_threads(CACHE), fixed + ns * entry + nr * raw, st, kv_cross_wide<HD, CACHE, OWN>,
+  if (F4 && nr < KX_COPIERS) return cudaErrorInvalidConfiguration;
+  e = launch_after(OWN, dim3(ctas), KX_THREADS, fixed + ns * entry + nr * raw, st, kv_cross_wide<HD, CACHE, OWN>,
                    tmk, tmv, a, own, parts, ns, nr);
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_after(true, dim3(ctas, KX_QV / KX_JOIN_V), 32 * KX_JOIN_WARPS, 0, st, kv_cross_wide_join<HD>, a, own, OWN ? 1 : 0,

@@ -3,7 +3,7 @@
 // prefix.  Bound by the keys' bytes.  See kvattn.cu for the notation and kvline.cuh for how the work
 // is dealt out.
 //
-// One CTA per SM.  One warp walks the CTA's tiles of 64 keys, across items, and brings keys, values
+// One CTA per SM.  Four warps walk the CTA's tiles of 64 keys, across items, and bring keys, values
 // and (ahead of an item's first tile) its queries into a ring, so that the copies of the next item run
 // while the last is finished.  Eight warps, two teams that take every other tile, 16 keys of it each:
 //   S^T [16 keys x 8 vectors] = K Q^T        A = keys (ldmatrix), B = queries
@@ -24,7 +24,9 @@ namespace {
 
 constexpr int KF_KEYS = 64;                // keys of a tile
 constexpr int KF_WARPS = 8;                // computing warps: two teams of four
-constexpr int KF_THREADS = 32 * KF_WARPS + 32;
+constexpr int KF_LOADERS = 4;              // warps that bring the tiles: one thread issues a copy in 200 cycles (57 us of
+                                           // cross_step_b32_hd64, of 4 KB boxes, with one warp)
+constexpr int KF_THREADS = 32 * (KF_WARPS + KF_LOADERS);
 constexpr int KF_MAX_STAGES = 12;
 constexpr int KF_MIN_UNITS = 4;            // tiles that are worth a CTA
 constexpr uint32_t KF_MISC = 1152;         // barriers (0), tiles' descriptors (256), maxima (640) and sums (896)
@@ -102,7 +104,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
   }
   if (tid == 0) {
     for (int s = 0; s < KF_MAX_STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, KF_LOADERS);
       mbar_init(bar_free + 8 * s, KF_WARPS);
     }
     mbar_init(bar_states, KF_WARPS);
@@ -113,8 +115,9 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
   __syncthreads();
   bool ok = true;
   RingPos rp{0, 0};
-  if (warp == KF_WARPS) {
-    // ------------------------------------------------------------ the tiles: lane = box of rows
+  if (warp >= KF_WARPS) {
+    // ------------------------------------------------------------ the tiles
+    const int part = warp - KF_WARPS;        // of every tile's copies
     const uint64_t pol = policy_evict_first();
     const long long all = all_units<KfLine>(a, lane), per = units_per_cta(all, gridDim.x, KF_MIN_UNITS);
     const long long begin = min(per * blockIdx.x, all), end = min(begin + per, all);
@@ -123,14 +126,16 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
     Cut cut;
     cut.last = 0;
     const int rows = min(1 << a.pool.ps_log, KF_KEYS), boxes = KF_KEYS / rows;
-    // waits for the stage at rp and describes its tile
+    const int copies = 2 * (HD / 64) * boxes;          // 2, 4, ... 16
+    const uint32_t box_bytes = static_cast<uint32_t>(rows) * 128, mine = static_cast<uint32_t>((copies - part + KF_LOADERS - 1) / KF_LOADERS) * box_bytes;
+    // waits for the stage at rp and announces its tile, of which this warp copies `bytes`
     auto push = [&](const Tile& t, uint32_t bytes) {
       if (pushed >= NS) ok = kx_wait(bar_free + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag);
       else ++pushed;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       if (lane == 0) {
-        tiles[rp.slot] = t;
+        if (part == 0) tiles[rp.slot] = t;
         if (bytes) mbar_arrive_expect_tx(bar_full + 8 * rp.slot, bytes);
         else mbar_arrive(bar_full + 8 * rp.slot);
       }
@@ -159,26 +164,18 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
         t.keys = max(min(l.rq.len - k0, KF_KEYS), 0);
         t.flags = (x == 0 ? KF_FIRST : 0) | (x == n - 1 ? KF_LAST : 0);
         const bool data = t.keys > 0;
-        push(t, (data ? kf_kv(HD) : 0u) + (x == 0 ? static_cast<uint32_t>(qv) * HD * 2 : 0u));
+        push(t, (data ? mine : 0u) + (x == 0 && part == 0 ? static_cast<uint32_t>(qv) * HD * 2 : 0u));
         if (!ok) break;
         const uint32_t slot = uniform(rp.slot), bar = bar_full + 8 * slot, at = ring + slot * kf_kv(HD);
-        // One lane copies box after box, all that the copies take being the same for the whole warp: a lane a
-        // box, each with values of its own, took 200 cycles a copy.
+        // (all that a copy takes is the same for the whole warp)
 #pragma unroll 1
-        for (int i = 0; i < boxes && data; ++i) {   // (a page that is not there reads as zeros: a block outside the map)
-          const int pg = __shfl_sync(0xffffffffu, page, i);
+        for (int i = part; i < copies && data; i += KF_LOADERS) {   // (a page that is not there reads as zeros: a block outside the map)
+          const int v = i & 1, h = (i >> 1) & (HD / 64 - 1), bx = i / (2 * (HD / 64)), pg = __shfl_sync(0xffffffffu, page, bx);
           const int blk = pg >= 0 ? pg * a.pool.Hkv + kvh : a.pool.num_pages * a.pool.Hkv;
-          const int row = (k0 + i * rows) & ((1 << a.pool.ps_log) - 1);
-          const uint32_t dst = at + i * (rows * 128);
-          if (elect_one()) {
-#pragma unroll
-            for (int h = 0; h < HD / 64; ++h) {
-              tma_load_3d(dst + h * HALF, &tmk, 64 * h, row, blk, bar, pol);
-              tma_load_3d(dst + V_AT + h * HALF, &tmv, 64 * h, row, blk, bar, pol);
-            }
-          }
+          const int row = (k0 + bx * rows) & ((1 << a.pool.ps_log) - 1);
+          if (elect_one()) tma_load_3d(at + v * V_AT + h * HALF + bx * box_bytes, v ? &tmv : &tmk, 64 * h, row, blk, bar, pol);
         }
-        if (x == 0 && lane >= 16 && lane - 16 < qv) {
+        if (x == 0 && part == 0 && lane >= 16 && lane - 16 < qv) {
           const int v = lane - 16, i = row_of(a, v);
           bulk_load(queries + (rp.slot * KF_QV + v) * HD * 2, a.q + (t.row0 + i) * a.q_ld + static_cast<long long>(kvh * a.G + v - i * a.G) * HD, HD * 2, bar);
         }
@@ -192,7 +189,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
       t.flags = KF_END;
       push(t, 0);
     }
-    if (lane == 0) reinterpret_cast<Cut*>(parts)[blockIdx.x] = cut;
+    if (part == 0 && lane == 0) reinterpret_cast<Cut*>(parts)[blockIdx.x] = cut;
     if (!ok) {   // let copies already issued land before the CTA releases its shared memory
       const long long t0 = clock64();
       while (clock64() - t0 < 4000000) {
