@@ -419,6 +419,9 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
           }
         }
       }
+      // (the next copy into the raw tile is another proxy's write: without the fence it was seen to land
+      // ahead of these loads, in one of 10^7 CTAs)
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_re + 8 * wp.slot);
       if (e >= NS) ok = mbar_wait_sleepy(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag) && ok;
@@ -903,6 +906,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
           }
       }
     }
+    fence_proxy_async_smem();                // (the next copy into the stage is another proxy's write)
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(s_free + rp.slot));
     // ---- scores of 32 keys: s[gr] = {key g: vectors 2c, 2c + 1; key g + 8: the same}

@@ -541,11 +541,12 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
               st_smem16(dst + ka_sw(r, c + (sw ^ 1)), h);
             }
           }
+          fence_proxy_async_smem();            // (raw tile and entry change hands between the proxies)
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_re + 8 * rslot);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_kvf + 8 * rp.slot);
+          if (lane == 0) {
+            mbar_arrive(bar_re + 8 * rslot);
+            mbar_arrive(bar_kvf + 8 * rp.slot);
+          }
         }
       }
       if (!ok) break;
