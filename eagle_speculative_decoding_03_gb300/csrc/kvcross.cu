@@ -31,7 +31,8 @@ constexpr int KX_QV = 256;                 // query vectors of a block
 constexpr int KX_DESCS = 4;                // segments in flight between the scheduler and the roles
 constexpr int KX_MIN_KEYS = 384;           // keys of an item that are worth a CTA
 constexpr int KX_MAX_RAW = 12;             // raw tiles of a 4-bit pool in flight
-constexpr uint32_t KX_MISC = 3 << 10;         // barriers (0), segments (736), states of an item that both groups take (1024)
+constexpr uint32_t KX_MISC = 3 << 10;         // barriers (0, 896), segments (736), states of an item that both groups take (1024)
+constexpr uint32_t KX_FULL2 = 896;         // from a place's barrier for even turns of the ring to that for odd ones
 constexpr int KX_SOFTMAX = 256;            // softmax threads: one per query vector
 constexpr int KX_COPIERS = 4;              // loader warps
 constexpr int KX_THREADS = 128 + KX_SOFTMAX + 32 * KX_COPIERS;   // control, softmax, loaders
@@ -58,6 +59,22 @@ EAGLE_DEV uint32_t ld_acquire_smem(uint32_t addr) {
 EAGLE_DEV void st_release_smem(uint32_t addr, uint32_t x) {
   asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
+
+// A place in the ring of keys and values, and how often the ring has turned (mod 4).  Its places have two
+// barriers each, for the odd and the even turns: a group that skips the other's tiles may come to a place
+// while what is ahead of its entry is still being copied, and one barrier's parity would then read as done.
+struct RingAt {
+  int slot, turn;
+  EAGLE_DEV void step(int n, int NS) {
+    slot += n;
+    if (slot >= NS) {
+      slot -= NS;
+      turn = (turn + 1) & 3;
+    }
+  }
+  EAGLE_DEV uint32_t full(uint32_t bar) const { return bar + 8 * slot + (turn & 1) * KX_FULL2; }
+  EAGLE_DEV uint32_t parity() const { return static_cast<uint32_t>(turn) >> 1; }
+};
 
 // Part of an item: tiles [t0, t0 + T) of query vectors [v0, v0 + qv) of sequence b.
 struct Seg {
@@ -153,6 +170,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   constexpr uint32_t ENTRY = kx_entry(HD, CACHE), HALF = KEYS * 128, RAW = kx_raw_bytes(HD), RAW_SCALES = HD / 2 * KEYS;
   constexpr uint32_t Q_TILE = ka_entry(HD), Q_HALF = KA_QV * 128;
   constexpr uint32_t T_O = 256;
+  static_assert(736 + KX_DESCS * sizeof(Seg) <= KX_FULL2 && KX_FULL2 + 8 * KA_MAX_SLOTS <= 1024, "");
   extern __shared__ __align__(1024) uint8_t kx_sm[];   // (no byte is left to align it by hand: ring, queries, misc take all)
   uint8_t* sm = kx_sm;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -161,7 +179,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   uint8_t* raw = sm + static_cast<uint32_t>(NS) * ENTRY + 2 * Q_TILE;
   uint8_t* misc = raw + (F4 ? NR * RAW : 0);
   const uint32_t misc_u = smem_u32(misc);
-  // ring full / free; per score buffer (group, 64 columns): scores there, p there, P V done; per group:
+  // ring full (even turns; odd ones at KX_FULL2) / free; per score buffer (group, 64 columns): scores there, p there, P V done; per group:
   // queries there, segment done; raw tiles full / free, segments full / free; an item of both groups:
   // states there / read; a loader's turn
   const uint32_t bar_kvf = misc_u, bar_kve = misc_u + 112, bar_sf = misc_u + 224, bar_pf = misc_u + 256, bar_pe = misc_u + 288,
@@ -181,6 +199,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   if (tid == 0) {
     for (int s = 0; s < KA_MAX_SLOTS; ++s) {
       mbar_init(bar_kvf + 8 * s, 1);
+      mbar_init(bar_kvf + 8 * s + KX_FULL2, 1);
       mbar_init(bar_kve + 8 * s, 2);
     }
     for (int b = 0; b < 4; ++b) {
@@ -301,24 +320,9 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       const uint32_t id2 = (F4 ? idesc_f16_f32(128, HD) : idesc_bf16_f32(128, HD)) | (1u << 16);   // B (values) MN-major
       const uint64_t dq = smem_desc_sw128(q_u + g * Q_TILE);
       const uint32_t tO = tmem + T_O + 128 * g;
-      RingPos base{0, 0};                    // the segment's first entry
+      RingAt base{0, 0};                     // the segment's first entry
       uint32_t n = 0, turn = 0;              // units of this group so far; segments with a tile
-      uint32_t first = 0, placed = 0;        // the segment's first entry, counted from the start; entries known to be under way
-      // Waits for entry e.  Its barrier is looked at only once the entry before it in the same place is
-      // through: of a shared item this group waits for every other tile only, and a place whose last entry,
-      // the other group's, was still being copied would look like the one that is waited for.
-      auto there = [&](const RingPos& p, uint32_t e) {
-#pragma unroll 1
-        for (uint32_t i = 0; static_cast<int>(placed - e) <= 0; ++i) {
-          placed = ld_acquire_smem(placed_u);
-          if ((i & 255u) == 255u && (*abort_flag || i > (1u << 24))) {
-            if (!*abort_flag) atomicOr(a.err, DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            return false;
-          }
-        }
-        return kx_wait(bar_kvf + 8 * p.slot, p.turn, a.err, abort_flag);
-      };
+      uint32_t first = 0;                    // the segment's first entry, counted from the start
       for (;; dp.step(1, KX_DESCS)) {
         const Seg s = segment(dp);
         if (!ok || !s.valid) break;
@@ -329,18 +333,29 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         }
         tc_fence_after();
         const int W = s.units_of<UPT>(g, last_units(s));
-        RingPos kp = base;
-        uint32_t ke = first, ve;
-        if (both && g) kp.step(2, NS), ke += 2;
-        RingPos vp = kp;
+        RingAt kp = base;
+        if (both && g) kp.step(2, NS);
+        // The group's first entry is under way, so what was ahead of it in its place is through (in a run of
+        // short items this group may have skipped any number).  From there on it waits for one of any NS
+        // entries, which leaves its place's barriers two turns apart.
+        const uint32_t e0 = first + (both ? 2 * g : 0);
+#pragma unroll 1
+        for (uint32_t i = 1; work && static_cast<int>(ld_acquire_smem(placed_u) - e0) <= 0; ++i) {
+          if ((i & 255u) == 0 && (*abort_flag || i > (1u << 24))) {
+            if (!*abort_flag) atomicOr(a.err, DEVERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+        }
+        RingAt vp = kp;
         vp.step(1, NS);
-        ve = ke + 1;
 #pragma unroll 1
         for (int w = 0; w <= W && ok; ++w) {
           if (w < W) {
             // S = Q K^T of unit w, once P V of the unit before the last (same buffer) is done
             const uint32_t u = n + w, buf = 2 * g + (u & 1);
-            if (UPT == 1 || !(w & 1)) ok = there(kp, ke);
+            if (UPT == 1 || !(w & 1)) ok = kx_wait(kp.full(bar_kvf), kp.parity(), a.err, abort_flag);
             ok = ok && kx_wait(bar_pe + 8 * buf, ((u >> 1) & 1) ^ 1, a.err, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -357,13 +372,12 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
               if (both) tc_commit(bar_kve + 8 * kp.slot);
               kp.step(2, NS);
               if (both) kp.step(2, NS);
-              ke += both ? 4 : 2;
             }
           }
           if (w > 0) {   // O += P V of unit x
             const int x = w - 1;
             const uint32_t u = n + x, buf = 2 * g + (u & 1);
-            if (UPT == 1 || !(x & 1)) ok = there(vp, ve);
+            if (UPT == 1 || !(x & 1)) ok = kx_wait(vp.full(bar_kvf), vp.parity(), a.err, abort_flag);
             ok = ok && kx_wait(bar_pf + 8 * buf, (u >> 1) & 1, a.err, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -377,7 +391,6 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
               if (both) tc_commit(bar_kve + 8 * vp.slot);
               vp.step(2, NS);
               if (both) vp.step(2, NS);
-              ve += both ? 4 : 2;
             }
           }
         }
@@ -385,7 +398,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         n += W;
         if (work) tc_commit(bar_fin + 8 * g);
         const uint32_t at = base.slot + 2u * s.T;
-        base.turn ^= (at / NS) & 1;
+        base.turn = (base.turn + at / NS) & 3;
         base.slot = at % NS;
         first += 2u * s.T;
         mbar_arrive(bar_de + 8 * dp.slot);
@@ -404,7 +417,8 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
     set_regs_down<KX_REG_LOAD>();
     const int team = warp - LOAD_WARP;
     const int ps = 1 << a.pool.ps_log, box = min(ps, KEYS), per = KEYS / box, NT = F4 ? NR / KX_COPIERS : 1;   // raw tiles of a warp
-    RingPos rp{0, 0}, cp{0, 0}, wp{0, 0};              // the warp's entry in the ring, its raw tile to copy into, to convert
+    RingAt rp{0, 0};                                   // the warp's entry in the ring
+    RingPos cp{0, 0}, wp{0, 0};                        // its raw tile to copy into, to convert
     rp.step(team, NS);
     uint32_t entries = 0, taken = 0;                   // of the segments before; by this warp
     for (;; dp.step(1, KX_DESCS)) {
@@ -465,7 +479,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
       auto place = [&]() {
         const uint32_t n = taken * KX_COPIERS + team;
         if (n) ok = kx_wait(bar_next + 8 * team, (team ? taken : taken - 1) & 1, a.err, abort_flag) && ok;
-        if (n >= static_cast<uint32_t>(NS)) ok = ok && kx_wait(bar_kve + 8 * rp.slot, rp.turn ^ 1, a.err, abort_flag);
+        if (n >= static_cast<uint32_t>(NS)) ok = ok && kx_wait(bar_kve + 8 * rp.slot, (rp.turn & 1) ^ 1, a.err, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (lane == 0) {
           if (ok) st_release_smem(placed_u, n + 1);
@@ -478,7 +492,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           const int slot = uniform(rp.slot);
           place();
           if (!ok) break;
-          copy(e, bar_kvf + 8 * slot, slot);
+          copy(e, uniform(rp.full(bar_kvf)), slot);
         }
       } else {
         // raw tiles are copied NT entries ahead of their conversion: 16 dims per thread and step, 8 steps at once
@@ -545,7 +559,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar_re + 8 * rslot);
-            mbar_arrive(bar_kvf + 8 * rp.slot);
+            mbar_arrive(rp.full(bar_kvf));
           }
         }
       }
