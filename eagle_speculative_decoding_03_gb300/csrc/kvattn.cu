@@ -144,7 +144,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   rq.len = uniform(rq.len);
   const int v0 = blk0 * KA_QV * NB;
   const int qv = min(rq.R * a.G - v0, KA_QV * NB);
-  if (qv <= 0) return;
+  if (qv <= 0) {
+    if (a.behind) pdl_wait();
+    return;
+  }
   const int i_first = v0 / a.G, i_last = (v0 + qv - 1) / a.G;
   // keys this block can see, and this CTA's tiles of them
   const int seen = a.mask ? rq.len : min(rq.len, rq.ctx + i_last + 1);
@@ -153,7 +156,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   const bool joined = NB == 1 && a.joined;
   const int per_cta = joined ? (all_tiles + a.splits - 1) / a.splits : a.tiles_per_cta;
   const int t_begin = split * per_cta;
-  if (!joined && split > 0 && t_begin * KA_CH >= rq.len) return;  // (not a range of this request at all)
+  if (!joined && split > 0 && t_begin * KA_CH >= rq.len) {        // (not a range of this request at all)
+    if (a.behind) pdl_wait();
+    return;
+  }
   const int T = max(0, min(all_tiles - t_begin, per_cta));
   const int nb = uniform(NB == 2 && qv > KA_QV ? 2 : 1);
   const int nq0 = min(4, (min(qv, KA_QV) + 31) / 32), nq1 = nb == 2 ? (qv - KA_QV + 31) / 32 : nq0;
@@ -659,6 +665,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (a.behind) pdl_wait();
   if (joined) {   // the cluster's ranges, in rank order
     cluster_sync();
     for (int x = split * THREADS + tid; x < qv * (HD / 4); x += a.splits * THREADS) {
@@ -765,7 +772,10 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   const int qv = rq.R * a.G;
   const int per_cta = a.joined ? ((rq.len + KA_CH - 1) / KA_CH + a.splits - 1) / a.splits : a.tiles_per_cta;
   const int kb = split * per_cta * KA_CH;
-  if (qv <= 0 || (!a.joined && split > 0 && kb >= rq.len)) return;
+  if (qv <= 0 || (!a.joined && split > 0 && kb >= rq.len)) {
+    if (a.behind) pdl_wait();
+    return;
+  }
   const int ke = min(rq.len, kb + per_cta * KA_CH);
   const int tiles = max(0, (ke - kb + KA_CH - 1) / KA_CH);
   if (tid == 0) {
@@ -1066,6 +1076,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
       if (d == 0 && a.lse) a.lse[at] = none ? -INFINITY : (m2 + log2f(L)) * 0.6931471805599453f;
     }
   }
+  if (a.behind) pdl_wait();
   if (a.joined) {   // the cluster's ranges, in rank order
     __syncthreads();
     cluster_sync();

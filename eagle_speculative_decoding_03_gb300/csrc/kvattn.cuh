@@ -58,6 +58,7 @@ struct KaArgs {
   int tiles_per_cta, splits;
   int joined;                              // the ranges of a request are one cluster and join in it
   int parts;                               // results go to part_o / part_ml: of several ranges, or to be joined with others
+  int behind;                              // starts before the kernel ahead of it has ended, and ends after it
   int cross;                               // the rows are no keys of the cache: each sees lens[b] keys, all of them
   const int* groups;                       // [B + 1] or null: item b's rows are those of requests groups[b] .. groups[b + 1] - 1
   int requests;                            // (of this many)
@@ -269,13 +270,18 @@ cudaError_t kf_launch(KaArgs* a, const eagle_kv_cache_t* cache, const KxPlan& p,
 template <typename... P, typename... A>
 cudaError_t launch_ranges(const KaArgs& a, dim3 grid, int threads, size_t smem, cudaStream_t st, void (*kernel)(P...), const A&... args) {
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.joined ? a.splits : 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  if (a.behind) {                          // (never joined: its results go to another join)
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.joined ? a.splits : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.attrs = attr;
-  cfg.numAttrs = a.joined ? 1 : 0;
+  cfg.numAttrs = a.behind || a.joined ? 1 : 0;
   cfg.stream = st;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);

@@ -1,23 +1,29 @@
 // The products of cross attention: many query vectors over all cached keys of a sequence (bf16 or
-// 4-bit pages), the keys' tiles dealt out evenly to the SMs.  See kvattn.cu for the notation.
+// 4-bit pages), the keys' tiles dealt out evenly to the SMs.  See kvattn.cu for the notation and
+// kvline.cuh for how the work is dealt out.
 //
-// An item is a block of query vectors (row * G + head) of one sequence and KV head, a unit of work
-// one tile of 128 keys of an item.  The units of all items lie in one line, which is cut evenly:
-// CTA c takes units [c per, (c + 1) per), whatever the sequences' lengths.  An item that a cut
-// divides leaves partial results, which a second kernel joins in the CTAs' order.
+//   S = Q K^T, p = 2^(rs S - m), O += P V, l += sum p      over tiles of 128 keys (4 bits: 64)
 //
-// One CTA per SM: 256 query vectors as two TMEM tiles of 128, each with a softmax warpgroup and an
-// MMA thread of its own.  S = Q K^T of 128 keys takes 128 columns, P replaces its first half, O
-// takes hd columns.  While one tile's scores are in the softmax the tensor cores work for the other
-// tile.  128 keys an instruction, because Q and K both come from shared memory: 128 x 128 x 16 reads
-// 8 KB in the 64 cycles that it computes, which is all that shared memory gives (with 64 keys
-// kv_attention_tc needs 48 cycles for 32 of work).  P V starts when the first half of P is there.
+// An item is a block of up to 256 query vectors (row * G + head) of one sequence and KV head, one CTA
+// per SM.  Two TMEM tiles of 128 vectors, each with a softmax warpgroup (a thread per vector) and an
+// MMA thread of its own, so that the tensor cores work for one while the other's scores are in the
+// softmax.  Units of 64 keys, two score buffers a tile; P replaces S in place, O takes hd columns.
 // An item of at most 128 vectors is taken by both groups, every other tile each, and the two states
-// are joined in TMEM: one group alone would leave the tensor cores idle during its softmax.
+// are joined in TMEM: one group alone would leave the tensor cores idle during its softmax (the tree
+// of 8 requests 40 us, 53 with one group).  The next item's queries are staged while the last unit
+// of this one runs, and results are written while the copies and products of the next are under way.
 //
-// bf16 p (8 bits) against bf16 values, fp16 p (11 bits) against 4-bit ones; l sums the unrounded p.
-// No key that a row does not see enters a product (rows behind the last key are loaded as zeros), so
-// values that are not finite reach the rows that see them, and need no second pass.
+// Bound by the tensor cores: a unit's Q K^T takes 48 cycles an instruction for 32 of work, because
+// both operands come from shared memory; with P V that is 2560 cycles for 128 keys and 256 vectors,
+// and 3050 are measured (16 sequences of 1,500 keys and 512 rows of 32 heads, hd 128: 214 us with the
+// join, 1,290 TFLOP/s).  128 keys an instruction would run at the full rate, but its scores leave room
+// for one buffer a tile: 229 us.  Two threads per vector: 231.  4 bits: four warps convert what they
+// copied, 64 keys an entry (a chunk of 1,688 rows over 16,001 keys 415 us).
+//
+// bf16 p (8 bits) against bf16 values, fp16 p (11 bits) against 4-bit ones: the second product takes
+// one type on both sides, and p in two parts cost 25 of 160 us in kv_attention_tc; l sums the
+// unrounded p.  Every row sees every key and rows behind the last key are loaded as zeros, so nothing
+// that is not finite reaches a row that does not see it, and there is no second pass.
 #include "kvline.cuh"
 
 #include <algorithm>

@@ -6,7 +6,7 @@
 //
 // Partial results over disjoint keys (key ranges, the prefix and a request's own keys) are joined
 // by that rule, in a fixed order.  The kernels over the keys are in kvattn.cu.
-#include "kvattn.cuh"
+#include "kvline.cuh"
 
 #include <algorithm>
 
@@ -24,6 +24,7 @@ template <int HD, int WARPS>
 __global__ void __launch_bounds__(128) kv_shared_join(const KaArgs a, const KaArgs pre) {
   constexpr int E = HD / 32;
   __shared__ float s_o[4][2][HD], s_l[4];
+  pdl_wait();                                // the ranges' results
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
   const long long w = static_cast<long long>(blockIdx.x) * (4 / WARPS) + warp / WARPS;
   const int n = static_cast<int>(w / a.Hq), h = static_cast<int>(w - static_cast<long long>(n) * a.Hq);
@@ -92,9 +93,8 @@ __global__ void __launch_bounds__(128) kv_shared_join(const KaArgs a, const KaAr
 template <int HD>
 cudaError_t launch_join(const KaArgs& a, const KaArgs& pre, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.N) * a.Hq;
-  if (a.splits + pre.splits > 8) kv_shared_join<HD, 4><<<static_cast<unsigned>(rows), 128, 0, st>>>(a, pre);
-  else kv_shared_join<HD, 1><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(a, pre);
-  return cudaGetLastError();
+  return a.splits + pre.splits > 8 ? launch_after(true, dim3(static_cast<unsigned>(rows)), 128, 0, st, kv_shared_join<HD, 4>, a, pre)
+                                   : launch_after(true, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, st, kv_shared_join<HD, 1>, a, pre);
 }
 
 // ------------------------------------------------------------------ merge
@@ -409,6 +409,7 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   x.max_rows = g->max_rows;
   x.max_len = g->max_len;
   x.cross = 1;
+  x.behind = 1;
   x.groups = g->cu_groups;
   x.requests = w->B;
   x.lens = g->lens;

@@ -386,3 +386,28 @@ def test_merge_refusals_of_the_binding():
         with pytest.raises(eb.EagleError):
             eb.attention_merge(*args, **kw)
     assert eb.attention_merge([o[:0]], [l[:0]]).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("kinds", [("bf16", "bf16"), ("f4", "f4")])
+@pytest.mark.parametrize("rows,plen,clen", [([1] * 32, 4096, 500), ([300, 150, 260, 390], 2000, 0), ([9, 60, 33, 1, 64, 20], 700, 130)])
+def test_calls_behind_each_other_repeat(kinds, rows, plen, clen):
+    """Many calls in flight, each beginning while the one before ends, so that copies take their time
+    and land in any order: the same bits as the first call that ran alone."""
+    rng = np.random.default_rng(17)
+    B, hd, Hkv, G = len(rows), 128, 4, 4
+    ctx = [(97 * i) % (clen + 1) for i in range(B)]
+    prefix, _ = make_cache(rng, kinds[0], hd, 64, Hkv, [plen])
+    cache, _ = make_cache(rng, kinds[1], hd, 128, Hkv, [c + r for c, r in zip(ctx, rows)])
+    args = (prefix, dev(np.array([0, B], np.int32)), dev(np.array([plen], np.int32)), cache)
+    lens, at = dev(np.array(ctx, np.int32)), dev(cu(rows))
+    sizes = dict(max_group_rows=sum(rows), max_prefix=plen, max_rows=max(rows), max_len=max(c + r for c, r in zip(ctx, rows)), lse=True)
+    qs = [torch.randn(sum(rows), Hkv * G, hd, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    first = []
+    for q in qs:
+        first.append(eb.kv_shared_attention(*args, q, at, lens, **sizes))
+        torch.cuda.synchronize()
+    for _ in range(40):
+        outs = [eb.kv_shared_attention(*args, qs[i & 1], at, lens, **sizes) for i in range(10)]
+        for i, (o, l) in enumerate(outs):
+            assert torch.equal(o, first[i & 1][0]) and torch.equal(l, first[i & 1][1])
+    assert cache.check() == 0 and prefix.check() == 0
