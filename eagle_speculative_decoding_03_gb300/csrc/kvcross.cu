@@ -9,20 +9,20 @@
 // MMA thread of its own, so that the tensor cores work for one while the other's scores are in the
 // softmax.  Units of 64 keys, two score buffers a tile; P replaces S in place, O takes hd columns.
 // An item of at most 128 vectors is taken by both groups, every other tile each, and the two states
-// are joined in TMEM: one group alone would leave the tensor cores idle during its softmax (the tree
-// of 8 requests 40 us, 53 with one group).  The next item's queries are staged while the last unit
-// of this one runs, and results are written while the copies and products of the next are under way.
+// are joined in TMEM: one group alone would leave the tensor cores idle during its softmax.  The next
+// item's queries are staged while the last unit of this one runs, and results are written while the
+// copies and products of the next are under way.
 //
 // Bound by the tensor cores: a unit's Q K^T takes 48 cycles an instruction for 32 of work, because
 // both operands come from shared memory; with P V that is 2560 cycles for 128 keys and 256 vectors,
-// and 3050 are measured (16 sequences of 1,500 keys and 512 rows of 32 heads, hd 128: 214 us with the
-// join, 1,290 TFLOP/s).  128 keys an instruction would run at the full rate, but its scores leave room
-// for one buffer a tile: 229 us.  Two threads per vector: 231.  4 bits: four warps convert what they
-// copied, 64 keys an entry (a chunk of 1,688 rows over 16,001 keys 415 us).
+// and 3050 are measured (2 prompts of 2,047 rows and 32 heads of 128 over 4,099 keys: 214 us with the
+// join, 1,285 TFLOP/s, 68% of the measured rate).  128 keys an instruction would run at the full rate, but its scores leave room
+// for one buffer a tile: 250 us.  4 bits: four warps convert what they copied, 64 keys an entry (a
+// chunk of 1,688 rows of 32 heads over 16,001 keys 418 us, 1,070 TFLOP/s).
 //
 // bf16 p (8 bits) against bf16 values, fp16 p (11 bits) against 4-bit ones: the second product takes
-// one type on both sides, and p in two parts cost 25 of 160 us in kv_attention_tc; l sums the
-// unrounded p.  Every row sees every key and rows behind the last key are loaded as zeros, so nothing
+// one type on both sides, and p in two parts takes kv_attention_tc 75 us of a tree where one takes 60;
+// l sums the unrounded p.  Every row sees every key and rows behind the last key are loaded as zeros, so nothing
 // that is not finite reaches a row that does not see it, and there is no second pass.
 #include "kvline.cuh"
 

@@ -11,6 +11,11 @@
 // with a running maximum and sum a warp; their states meet in shared memory at the item's end, in warp
 // order.  (kv_attention_tc spends 128 rows of MMA and a CTA's start and end on such an item.)
 //
+// 32 sequences of 300 to 3,000 keys, 16 heads of 64 (217 MB): 48.7 us with the join, 4.5 TB/s, 66% of
+// the measured copy rate; the ranges of kv_attention_tc take 75.  What is over is the start (a CTA finds
+// its place among the sequences, 3 us), the copies' first latency and the join's launch.  With little
+// to read those count for more than even shares (2 requests: 30 us, by ranges 23), see kf_worth.
+//
 // Rows behind the last key are cleared in the fragments (they may hold NaN).  p is rounded to bf16 for
 // the second product, as in kvcross.cu; l sums the unrounded p.
 #include "kvline.cuh"
@@ -25,7 +30,7 @@ namespace {
 constexpr int KF_KEYS = 64;                // keys of a tile
 constexpr int KF_WARPS = 8;                // computing warps: two teams of four
 constexpr int KF_LOADERS = 4;              // warps that bring the tiles: one thread issues a copy in 200 cycles (57 us of
-                                           // cross_step_b32_hd64, of 4 KB boxes, with one warp)
+                                           // the case above, of 8 KB boxes, with one warp)
 constexpr int KF_THREADS = 32 * (KF_WARPS + KF_LOADERS);
 constexpr int KF_MAX_STAGES = 12;
 constexpr int KF_MIN_UNITS = 4;            // tiles that are worth a CTA

@@ -18,7 +18,9 @@ constexpr int MG_THREADS = 256;
 
 // ------------------------------------------------------------------ prefix and own keys
 // WARPS warps per (row, query head), each a share of the ranges: the own keys' first, then the
-// prefix's (`pre`, whose buffers lie behind them).  The two caches' value factors are applied after
+// prefix's (`pre`, whose buffers lie behind them).  For prefixes cut by ranges: kvcross.cu joins in its
+// own epilogue.  Starts while the ranges run and waits for them; the prefix's ranges run beside the own
+// keys' (2 requests behind 700 keys: 16.5 us, 22 one after the other).  The two caches' value factors are applied after
 // the division (as in kvattn.cu), so the sums of the two are kept apart.
 template <int HD, int WARPS>
 __global__ void __launch_bounds__(128) kv_shared_join(const KaArgs a, const KaArgs pre) {
@@ -127,7 +129,9 @@ EAGLE_DEV void load8(const void* base, long long at, float* x) {
   }
 }
 
-// A thread per 8 dims of a row and head.
+// A thread per 8 dims of a row and head: each value is read once, the parts' weights again by each of a
+// head's threads (from L1).  Bound by the bytes: 4 fp32 parts of 8,191 rows and 32 heads of 128 take
+// 92 us, 98% of the measured copy rate; one row is one launch, 3.4 us.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(MG_THREADS) attention_merge(const MgArgs a) {
   const long long x = static_cast<long long>(blockIdx.x) * MG_THREADS + threadIdx.x;
@@ -239,7 +243,7 @@ CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int 
   p.by = qv >= KX_FROM ? Cutting::WIDE : c->kind == EAGLE_CACHE_BF16 ? Cutting::FEW : Cutting::RANGES;
   if (p.by != Cutting::WIDE) p.ranges = ka_plan(c->kind, c->n_kv_heads, G, B, max_rows, max_len, may_join);
   // (a step's few ranges in one cluster each take no second launch: cross_step_b1 10 us, in line 16; and
-  // with little to read its start counts for more than even shares: shared_step_b2 23 us, in line 30)
+  // with little to read its start counts for more than even shares: shared_step_b2 16.5 us, in line 30)
   if (p.by == Cutting::FEW && (p.ranges.joined || !kf_worth(c->n_kv_heads, B, max_len))) p.by = Cutting::RANGES;
   if (p.by == Cutting::WIDE) p.line = kx_plan(c->kind, c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
   if (p.by == Cutting::FEW) p.line = kf_plan(c->n_kv_heads, c->head_dim, B, max_len);
