@@ -57,6 +57,11 @@ __host__ __device__ constexpr uint32_t kx_raw_bytes(int hd) { return static_cast
 template <int CACHE>
 using KxLine = Line<8, kx_keys(CACHE)>;    // (blocks of KX_QV vectors)
 
+EAGLE_DEV uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 EAGLE_DEV uint32_t ld_acquire_smem(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
