@@ -42,8 +42,10 @@ constexpr uint32_t KX_FULL2 = 896;         // from a place's barrier for even tu
 constexpr int KX_SOFTMAX = 256;            // softmax threads: one per query vector
 constexpr int KX_COPIERS = 4;              // loader warps
 constexpr int KX_THREADS = 128 + KX_SOFTMAX + 32 * KX_COPIERS;   // control, softmax, loaders
-// registers per thread of the roles (the launch checks their sum)
-constexpr int KX_REG_CTRL = 48, KX_REG_SOFTMAX = 176, KX_REG_LOAD = 80;
+// registers per thread: at the launch, and of the roles (the launch checks their sum).  What is left of an
+// SM's holds a CTA of kv_few_join, which waits there when own keys go ahead of this kernel: at 128 a thread
+// this one could only start where that had ended.
+constexpr int KX_REGS = 112, KX_REG_CTRL = 48, KX_REG_SOFTMAX = 160, KX_REG_LOAD = 72;
 constexpr int KX_JOIN_V = 32, KX_JOIN_WARPS = 8;
 
 // floats of a partial result: [hd / 4][256] float4 outputs, [256] (maximum, sum)
@@ -171,7 +173,7 @@ EAGLE_DEV float powers64(float* x, float rs, float mb, float* p8, float* pk) {
 }
 
 template <int HD, int CACHE, bool OWN>
-__global__ void __launch_bounds__(KX_THREADS, 1)
+__global__ void __maxnreg__(KX_REGS)
 kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const KaArgs a, const KaArgs own,
               float* parts, const int NS, const int NR) {
   constexpr bool F4 = CACHE == EAGLE_CACHE_F4;
