@@ -299,6 +299,9 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
         mma_bf16(o[j], v, p[0], p[1]);
       }
     }
+    // (the stage's next copy is another proxy's write; keys and values went through products, queries may
+    // still be on their way to the registers of the team whose turn it is not)
+    if (t.flags & KF_FIRST) fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_free + 8 * rp.slot);
     if (t.flags & KF_LAST) {
