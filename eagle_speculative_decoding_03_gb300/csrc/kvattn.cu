@@ -684,10 +684,10 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const float f = M == INFINITY ? (m[r] == INFINITY ? 1.f : 0.f) : exp2f(m[r] - M);
         const float4 y = remote4(state + v * ST_LD + d, r);
         L = fmaf(f, remote(lcta + v, r), L);
-        o.x = fmaf(f, y.x, o.x);
-        o.y = fmaf(f, y.y, o.y);
-        o.z = fmaf(f, y.z, o.z);
-        o.w = fmaf(f, y.w, o.w);
+        o.x = add_weighted(o.x, f, y.x);
+        o.y = add_weighted(o.y, f, y.y);
+        o.z = add_weighted(o.z, f, y.z);
+        o.w = add_weighted(o.w, f, y.w);
       }
       const bool none = L == 0.f;
       const float inv = none ? 0.f : a.vg / L;
@@ -1139,7 +1139,7 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
     L = fmaf(f, ml.y, L);
     const float* p = a.part_o + (s * step + at) * HD + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e], o[e]);
+    for (int e = 0; e < E; ++e) o[e] = add_weighted(o[e], f, p[e]);
   }
   if constexpr (WARPS > 1) {                 // (the CTA is one row's: it is here whole)
 #pragma unroll

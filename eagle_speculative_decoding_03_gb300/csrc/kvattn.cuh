@@ -204,6 +204,11 @@ EAGLE_DEV void dequant8(uint32_t code, uint32_t s, uint32_t* h) {
 // a masked score (-inf * 0), one that overflowed of a score of 0.
 EAGLE_DEV float finite_scale(float x) { return fminf(fmaxf(x, FLT_MIN), FLT_MAX); }
 
+// f y, x + f y of a part with a weight.  In 32 bits f may have fallen to 0: what is not finite in y stays
+// all the same, so that no infinity or NaN depends on how the keys were cut into parts.
+EAGLE_DEV float weighted(float f, float y) { return f != 0.f ? f * y : fabsf(y) < INFINITY ? 0.f : y; }
+EAGLE_DEV float add_weighted(float x, float f, float y) { return f != 0.f ? fmaf(f, y, x) : fabsf(y) < INFINITY ? x : x + y; }
+
 // a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
 // registers (the operands of tcgen05.mma)
 EAGLE_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }

@@ -121,13 +121,11 @@ struct Own {
   EAGLE_DEV size_t place(int s) const { return s * (static_cast<size_t>(a.N) * a.Hq) + at; }
   EAGLE_DEV float2 ml(int s) const { return a.part_ml[place(s)]; }
 };
-// x[0 .. 3] += f y, nothing of a part without weight (whatever it holds)
 EAGLE_DEV void add_part(float* x, float f, float4 y) {
-  if (f == 0.f) return;
-  x[0] = fmaf(f, y.x, x[0]);
-  x[1] = fmaf(f, y.y, x[1]);
-  x[2] = fmaf(f, y.z, x[2]);
-  x[3] = fmaf(f, y.w, x[3]);
+  x[0] = add_weighted(x[0], f, y.x);
+  x[1] = add_weighted(x[1], f, y.y);
+  x[2] = add_weighted(x[2], f, y.z);
+  x[3] = add_weighted(x[3], f, y.w);
 }
 
 // 64 scores x -> p = 2^(x rs - mb), packed two to a word (fp16 or bf16), their sum into p8, and the
@@ -683,8 +681,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
 #pragma unroll 1
         for (int k = 0; OWN && k < mine.used; ++k) {
           const float2 ml = mine.ml(k);
-          const float f = part_factor(ml.x, M);
-          if (f != 0.f) L = fmaf(f, ml.y, L);
+          if (ml.x != -INFINITY) L = fmaf(part_factor(ml.x, M), ml.y, L);
         }
         const bool none = L == 0.f, writes = live && (!join || mine.used > 0);
         const float inv = s.slot >= 0 ? 1.f : none ? 0.f : a.vg / L, own_inv = !OWN || none ? 0.f : own.vg / L;
@@ -695,8 +692,8 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         const long long at = row * a.out_ld + static_cast<long long>(h) * HD;
         const int ranges = OWN && join ? __reduce_max_sync(0xffffffffu, mine.used) : 0;
         const float w0 = f0 * inv, w1 = f1 * inv;
-        // (a state without weight may be of no tile: its O was never written)
-        const bool gone0 = __any_sync(0xffffffffu, f0 == 0.f), gone1 = __any_sync(0xffffffffu, f1 == 0.f);
+        // (a state of no tile: its O was never written; one whose weight fell to 0 leaves what is not finite)
+        const bool gone0 = __any_sync(0xffffffffu, w0 == 0.f), gone1 = __any_sync(0xffffffffu, w1 == 0.f);
 #pragma unroll 1
         for (int c0 = c_lo; c0 < c_hi; c0 += CW) {
           float x[CW];
@@ -705,20 +702,22 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
           tmem_wait_ld();
           if (gone0) {
 #pragma unroll
-            for (int e = 0; e < CW; ++e) x[e] = f0 == 0.f ? 0.f : x[e];
-          }
+            for (int e = 0; e < CW; ++e) x[e] = st[0].x == -INFINITY ? 0.f : weighted(w0, x[e]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < CW; ++e) x[e] *= w0;
+            for (int e = 0; e < CW; ++e) x[e] *= w0;
+          }
           if (both) {
             float y[CW];
             tmem_ld32(o1 + c0, y);
             tmem_wait_ld();
             if (gone1) {
 #pragma unroll
-              for (int e = 0; e < CW; ++e) y[e] = f1 == 0.f ? 0.f : y[e];
-            }
+              for (int e = 0; e < CW; ++e) x[e] = st[1].x == -INFINITY ? x[e] : add_weighted(x[e], w1, y[e]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < CW; ++e) x[e] = fmaf(w1, y[e], x[e]);
+              for (int e = 0; e < CW; ++e) x[e] = fmaf(w1, y[e], x[e]);
+            }
           }
           if (s.slot >= 0) {
             float4* dst = reinterpret_cast<float4*>(part) + static_cast<size_t>(c0 / 4) * KX_QV + pv;
@@ -756,11 +755,16 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
 #pragma unroll 1
             for (int k = 0; OWN && k < ranges; ++k) {
               float f = 0.f;
-              if (k < mine.used) f = part_factor(mine.ml(k).x, M) * own_inv;
+              unsigned long long place = ~0ull;
+              if (k < mine.used) {
+                const float m = mine.ml(k).x;
+                f = part_factor(m, M) * own_inv;
+                if (m != -INFINITY) place = mine.place(k);
+              }
               f = __shfl_sync(0xffffffffu, f, from);
-              const size_t place = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(mine.place(k)), from);
+              place = __shfl_sync(0xffffffffu, place, from);
               const float4* src = reinterpret_cast<const float4*>(own.part_o + place * HD + d0);
-              if (f != 0.f) {
+              if (place != ~0ull) {
 #pragma unroll
                 for (int e = 0; e < WORDS / 4; ++e) add_part(y + 4 * e, f, src[e]);
               }
@@ -894,8 +898,8 @@ __global__ void __launch_bounds__(32 * KX_JOIN_WARPS) kv_cross_wide_join(const K
 #pragma unroll 4
   for (int k = c; k <= last; ++k) {
     const float2 ml = state(k);
+    if (ml.x == -INFINITY) continue;
     const float f = part_factor(ml.x, M);
-    if (f == 0.f) continue;
     L = fmaf(f, ml.y, L);
     const float4* src = reinterpret_cast<const float4*>(part(k)) + static_cast<size_t>(warp * E) * KX_QV + pv;
 #pragma unroll
@@ -905,8 +909,8 @@ __global__ void __launch_bounds__(32 * KX_JOIN_WARPS) kv_cross_wide_join(const K
 #pragma unroll 1
   for (int k = 0; k < mine.used; ++k) {
     const float2 ml = mine.ml(k);
+    if (ml.x == -INFINITY) continue;
     const float f = part_factor(ml.x, M);
-    if (f == 0.f) continue;
     L = fmaf(f, ml.y, L);
     const float4* src = reinterpret_cast<const float4*>(own.part_o + mine.place(k) * HD) + warp * E;
 #pragma unroll

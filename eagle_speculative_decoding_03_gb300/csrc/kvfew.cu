@@ -341,8 +341,8 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
           const float f = part_factor(mw, M);
           const float2 y = *reinterpret_cast<const float2*>(s_o + (w * KF_QV + v) * LD + d);
           L = fmaf(f, s_l[w * KF_QV + v], L);
-          y0 = fmaf(f, y.x, y0);
-          y1 = fmaf(f, y.y, y1);
+          y0 = add_weighted(y0, f, y.x);
+          y1 = add_weighted(y1, f, y.y);
         }
         if (t.slot >= 0) {
           float* part = parts + static_cast<size_t>(t.slot) * kf_slot(HD);
@@ -378,11 +378,11 @@ __global__ void __launch_bounds__(256) kv_few_join(const KaArgs a, const float* 
 #pragma unroll 4
     for (int k = c; k <= s.last; ++k) {
       const float2 ml = state(k), y = *reinterpret_cast<const float2*>(part(k) + v * HD + d);
+      if (ml.x == -INFINITY) continue;
       const float f = part_factor(ml.x, M);
-      if (f == 0.f) continue;
       L = fmaf(f, ml.y, L);
-      y0 = fmaf(f, y.x, y0);
-      y1 = fmaf(f, y.y, y1);
+      y0 = add_weighted(y0, f, y.x);
+      y1 = add_weighted(y1, f, y.y);
     }
     emit(a, s.row0, s.kvh, v, d, HD, M, L, y0, y1);
   }

@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(128) kv_shared_join(const KaArgs a, const KaAr
     const float* p = a.part_o + place(s) * HD + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      if (s < own) o[0][e] = fmaf(f, p[e], o[0][e]);
-      else o[1][e] = fmaf(f, p[e], o[1][e]);
+      if (s < own) o[0][e] = add_weighted(o[0][e], f, p[e]);
+      else o[1][e] = add_weighted(o[1][e], f, p[e]);
     }
   }
   if constexpr (WARPS > 1) {                 // (the CTA is one row's: it is here whole)
@@ -148,12 +148,11 @@ __global__ void __launch_bounds__(MG_THREADS) attention_merge(const MgArgs a) {
     const float l = a.lses[i][nh];
     if (l == -INFINITY) continue;
     const float f = M == INFINITY ? (l == INFINITY ? 1.f : 0.f) : expf(l - M);
-    if (f == 0.f) continue;
     L += f;
     float y[8];
     load8<TI>(a.outs[i], n * a.ld[i] + at, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = fmaf(f, y[e], o[e]);
+    for (int e = 0; e < 8; ++e) o[e] = add_weighted(o[e], f, y[e]);
   }
   const bool none = M == -INFINITY;
   const float inv = none ? 0.f : 1.f / L;

@@ -692,9 +692,10 @@ typedef struct {
 
 /* out = sum_i w_i outs_i / sum_i w_i and lse = log sum_i w_i, w_i = exp(lses_i), in fp32 and rounded
  * once.  A part whose lse is -infinity adds nothing, whatever its output holds; where all are, out is
- * 0 and lse -infinity.  Parts of lse +infinity share the result evenly; a NaN lse makes the row of
- * that head NaN.  out may be one of the parts (same dtype and stride), and overlaps them in no other
- * way; lse may overlap no other buffer. */
+ * 0 and lse -infinity.  An infinity or NaN in any other part's output reaches the result, however far
+ * its lse lies below the largest.  Parts of lse +infinity share the result evenly; a NaN lse makes the
+ * row of that head NaN.  out may be one of the parts (same dtype and stride), and overlaps them in no
+ * other way; lse may overlap no other buffer. */
 EAGLE_API eagle_status_t eagle_attention_merge(const eagle_attention_parts_t* args, void* stream);
 
 /* Thread-local description of the last error (never NULL). */
