@@ -99,7 +99,7 @@ EAGLE_DEV void visible_sum(const VisibleKeys& keys, const __nv_bfloat16* qp, flo
       if (!keys.see(k + i)) continue;
       const float p = fast_exp2(fmaf(s[i], row_scale, -m * row_scale));
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(p, vv[i][e], o[e]);
+      for (int e = 0; e < E; ++e) o[e] = s[i] == -INFINITY ? fmaf(p, vv[i][e], o[e]) : add_weighted(o[e], p, vv[i][e]);
     }
   }
 }
@@ -576,10 +576,11 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
       const bool none = l_run == 0.f;
       const float inv = none ? 0.f : a.vg / l_run;
       // A non-finite V reaches vectors that have nothing of it: in a row that the step masks as 0 *
-      // NaN, and with p in two parts the lower part (0 or negative) makes NaN of a visible infinity.
+      // NaN; and p that fell to 0, or its lower part (0 or negative), makes NaN of a visible infinity.
       // Such sums are formed again from the visible keys alone, a vector at a time by the whole warp
-      // (unless the vector's own sum of p is NaN: then so is its output), and written once more.
-      const bool recheck = !F4 && T > 0 && (HILO || (t_begin + T) * KA_CH > rq.ctx);
+      // (unless the vector's own sum of p is NaN: then so is its output), and written once more.  Where
+      // every vector sees all of the range, its NaN alone are looked up, for 32 dims of all vectors at once.
+      const bool recheck = !F4 && T > 0, all_seen = a.cross || (t_begin + T) * KA_CH <= rq.ctx;
       for (bool again = false;; again = true) {
         float2 z0 = make_float2(0.f, 0.f), z1 = z0;
 #pragma unroll 1
@@ -627,10 +628,33 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const bool bad = !((z0.x + z0.y) + (z1.x + z1.y) == 0.f);
         unsigned todo = __ballot_sync(0xffffffffu, bad && live && !none && l_run < INFINITY);
         if (!todo) break;
+        if (all_seen) {
+          const bool mine = (todo >> lane) & 1u;
+#pragma unroll 1
+          for (int c0 = 0; c0 < HD; c0 += 32) {
+            float x[32], inf;
+            __syncwarp();
+            tmem_ld32(tO + c0, x);
+            tmem_wait_ld();
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) odd |= isnan(x[e]);
+            if (!__any_sync(0xffffffffu, mine && odd)) continue;
+            infinities<HD, 1>(a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), c0 + lane, &inf, lane, a.err);
+            uint32_t y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float z = __shfl_sync(0xffffffffu, inf, e);
+              y[e] = __float_as_uint(mine && isnan(x[e]) && z != 0.f ? z : x[e]);
+            }
+            tmem_st32(tO + c0, y);
+          }
+          tmem_wait_st();
+          todo = 0;
+        }
         for (; todo; todo &= todo - 1) {
           const int u = __ffs(todo) - 1, ui = __shfl_sync(0xffffffffu, irow, u);
-          const VisibleKeys keys{a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), rq.ctx,
-                                 a.cross ? -1 : ui,
+          const VisibleKeys keys{a.pool, b, kvh, t_begin * KA_CH, min(rq.len, (t_begin + T) * KA_CH), rq.ctx, ui,
                                  a.mask != nullptr, __shfl_sync(0xffffffffu, tree_bits, u)};
           const __nv_bfloat16* qp = a.q + (rq.row0 + ui) * a.q_ld + static_cast<long long>(kvh * a.G + v - lane + u - ui * a.G) * HD;
           float o[HD / 32];

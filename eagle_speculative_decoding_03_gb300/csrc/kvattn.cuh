@@ -209,6 +209,47 @@ EAGLE_DEV float finite_scale(float x) { return fminf(fmaxf(x, FLT_MIN), FLT_MAX)
 EAGLE_DEV float weighted(float f, float y) { return f != 0.f ? f * y : fabsf(y) < INFINITY ? 0.f : y; }
 EAGLE_DEV float add_weighted(float x, float f, float y) { return f != 0.f ? fmaf(f, y, x) : fabsf(y) < INFINITY ? x : x + y; }
 
+// The sum of what is not finite among the values of keys [begin, end), all of which the row sees: lane by
+// lane of E dims from d on, bf16 pages: 0, an infinity, or NaN.  For sums p v that came out as NaN where no p is: a p
+// that fell to 0, or the lower part of one in two parts, makes NaN of an infinity that the formula keeps.  A key
+// that is not finite itself has a weight of 0 there (its score is -infinity; any other would have made
+// the row's sum of p NaN), and 0 times infinity is NaN.  By a whole warp; begin a multiple of 16.  The rare
+// path, bound by the latency of its loads: 0.05 us a key.
+template <int HD, int E>
+EAGLE_DEV void infinities(const KvPool& pool, int b, int kvh, int begin, int end, int d, float* r, int lane, unsigned* err) {
+  constexpr int KB = 16;                   // keys in flight (of one page)
+  const auto* kp = static_cast<const __nv_bfloat16*>(pool.k);
+  const auto* vp = static_cast<const __nv_bfloat16*>(pool.v);
+  auto value = [&](size_t row, int e) { return static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(vp + row * HD + d) + e)); };
+#pragma unroll
+  for (int e = 0; e < E; ++e) r[e] = 0.f;
+#pragma unroll 1
+  for (int k = begin; k < end; k += KB) {
+    const int page = kv_page(pool, b, k, err);
+    if (page < 0) continue;                // (reads as zeros)
+    const size_t row = kv_row(pool, page, kvh, k);
+    uint32_t top = 0;                      // (the page is there whole: rows behind `end` are read and dropped)
+#pragma unroll
+    for (int i = 0; i < KB; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) top = max(top, value(row + i, e) & 0x7fffu);
+    if (!__any_sync(0xffffffffu, top >= 0x7f80u)) continue;
+#pragma unroll 1
+    for (int i = 0; i < KB && k + i < end; ++i) {
+      bool odd = false;                    // the key's own dims
+#pragma unroll
+      for (int x = 0; x < HD / 32; ++x)
+        odd |= (__ldg(reinterpret_cast<const unsigned short*>(kp + (row + i) * HD) + x * 32 + lane) & 0x7f80u) == 0x7f80u;
+      odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t v = value(row + i, e);
+        if ((v & 0x7f80u) == 0x7f80u) r[e] += odd ? __uint_as_float(0x7fc00000u) : __uint_as_float(v << 16);
+      }
+    }
+  }
+}
+
 // a warp-uniform value, in a form that lets the compiler keep what follows from it in uniform
 // registers (the operands of tcgen05.mma)
 EAGLE_DEV int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }

@@ -22,8 +22,10 @@
 //
 // bf16 p (8 bits) against bf16 values, fp16 p (11 bits) against 4-bit ones: the second product takes
 // one type on both sides, and p in two parts takes kv_attention_tc 75 us of a tree where one takes 60;
-// l sums the unrounded p.  Every row sees every key and rows behind the last key are loaded as zeros, so nothing
-// that is not finite reaches a row that does not see it, and there is no second pass.
+// l sums the unrounded p.  Every row sees every key and rows behind the last key are loaded as zeros, so
+// nothing that is not finite reaches a row that does not see it.  An infinite value times a p that fell to 0
+// is NaN where the formula has infinity: sums that are NaN are looked up among the values (`infinities`;
+// cross_prompt's sizes with one infinite dim 517 us where 204 without, with all of them 1,490).
 #include "kvline.cuh"
 
 #include <algorithm>
@@ -717,6 +719,21 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
             } else {
 #pragma unroll
               for (int e = 0; e < CW; ++e) x[e] = fmaf(w1, y[e], x[e]);
+            }
+          }
+          if constexpr (!F4) {                 // (of 4-bit values none is infinite)
+            float2 z = make_float2(0.f, 0.f);  // (0 unless some sum is not finite)
+#pragma unroll
+            for (int e = 0; e < CW; e += 2) z = __ffma2_rn(make_float2(x[e], x[e + 1]), make_float2(0.f, 0.f), z);
+            const bool bad = live && isnan(z.x + z.y) && fabsf(L) < INFINITY;
+            if (__any_sync(0xffffffffu, bad)) {
+              float inf;
+              infinities<HD, 1>(a.pool, s.b, s.kvh, s.t0 * KEYS, min((s.t0 + s.T) * KEYS, s.len), c0 + lane, &inf, lane, a.err);
+#pragma unroll
+              for (int e = 0; e < CW; ++e) {
+                const float y = __shfl_sync(0xffffffffu, inf, e);
+                if (bad && isnan(x[e]) && y != 0.f) x[e] = y;
+              }
             }
           }
           if (s.slot >= 0) {

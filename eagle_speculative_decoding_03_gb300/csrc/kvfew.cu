@@ -48,7 +48,7 @@ __host__ __device__ constexpr size_t kf_slot(int hd) { return static_cast<size_t
 // A tile in the ring, and its place in the CTA's part of an item.
 enum : int { KF_FIRST = 1, KF_LAST = 2, KF_END = 4 };
 struct Tile {
-  int flags, keys, row0, kvh, qv, slot, pad[2];   // keys: of the tile (0 .. 64); slot: partial result, -1: the item is whole
+  int flags, keys, row0, kvh, qv, slot, b, k0;   // keys: of the tile (0 .. 64), from k0 on; slot: partial result, -1: the item is whole
 };
 
 EAGLE_DEV void ldmatrix4(uint32_t* r, uint32_t addr) {
@@ -156,6 +156,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
       const int kvh = static_cast<int>(quotient(rest_u, l.tiles)), t0 = static_cast<int>(rest_u - static_cast<long long>(kvh) * l.tiles);
       const int n = static_cast<int>(min(static_cast<long long>(l.tiles - t0), end - u)), qv = l.rq.R * a.G;
       Tile t;
+      t.b = b;
       t.row0 = l.rq.row0;
       t.kvh = kvh;
       t.qv = qv;
@@ -166,6 +167,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
 #pragma unroll 1
       for (int x = 0; x < n && ok; ++x) {
         const int k0 = (t0 + x) * KF_KEYS, page = pages.get(a, b, t0 * KF_KEYS, l.rq.len, rows, lane, x * boxes);
+        t.k0 = k0;
         t.keys = max(min(l.rq.len - k0, KF_KEYS), 0);
         t.flags = (x == 0 ? KF_FIRST : 0) | (x == n - 1 ? KF_LAST : 0);
         const bool data = t.keys > 0;
@@ -210,6 +212,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
   uint32_t q[KS][2];
   float o[KS][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;   // log2 units; sums over this lane's keys
   uint32_t items = 0;
+  int begin = 0;                             // the item's first key here
   for (uint32_t n = 0;; ++n, rp.step(1, NS)) {
     ok = kx_wait(bar_full + 8 * rp.slot, rp.turn, a.err, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
@@ -231,6 +234,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
         for (int e = 0; e < 4; ++e) o[s][e] = 0.f;
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
+      begin = t.k0;
     }
     const int left = t.keys - sub;           // keys of this warp's 16
     if ((n & 1) == team && left > 0) {
@@ -329,9 +333,10 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_states);
       ok = kx_wait(bar_states, items & 1, a.err, abort_flag) && ok;
-      for (int x = tid; x < t.qv * (HD / 2); x += 32 * KF_WARPS) {
-        const int v = x / (HD / 2), d = 2 * (x - v * (HD / 2));
-        float M = -INFINITY, L = 0.f, y0 = 0.f, y1 = 0.f;
+      // one (vector, pair of dims): the warps' states joined, and written
+      auto join = [&](int v, int d, float& M, float& L, float& y0, float& y1) {
+        M = -INFINITY;
+        L = y0 = y1 = 0.f;
 #pragma unroll
         for (int w = 0; w < KF_WARPS; ++w) M = max_nan(M, s_m[w * KF_QV + v]);
 #pragma unroll
@@ -344,12 +349,36 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
           y0 = add_weighted(y0, f, y.x);
           y1 = add_weighted(y1, f, y.y);
         }
+      };
+      auto write = [&](int v, int d, float M, float L, float y0, float y1) {
         if (t.slot >= 0) {
           float* part = parts + static_cast<size_t>(t.slot) * kf_slot(HD);
           *reinterpret_cast<float2*>(part + v * HD + d) = make_float2(y0, y1);
           if (d == 0) reinterpret_cast<float2*>(part + KF_QV * HD)[v] = make_float2(L == 0.f ? -INFINITY : M, L);
         } else {
           emit(a, t.row0, t.kvh, v, d, HD, M, L, y0, y1);
+        }
+      };
+      bool odd = false;                      // some sum is NaN where no p is
+      for (int x = tid; x < t.qv * (HD / 2); x += 32 * KF_WARPS) {
+        const int v = x / (HD / 2), d = 2 * (x - v * (HD / 2));
+        float M, L, y0, y1;
+        join(v, d, M, L, y0, y1);
+        odd |= (isnan(y0) || isnan(y1)) && fabsf(L) < INFINITY;
+        write(v, d, M, L, y0, y1);
+      }
+      // A p or a factor that fell to 0 makes NaN of an infinite value: such sums are written once more.  (No loop
+      // over x around the lookup: with one the case above took 54.4 us, whether a lookup ran or not.)
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+        for (int i = 0; i < KF_QV * HD / 2 / (32 * KF_WARPS); ++i) {
+          const int x = tid + 32 * KF_WARPS * i, v = x / (HD / 2), d = 2 * (x - v * (HD / 2));
+          float M, L, y0, y1, z[2];
+          infinities<HD, 2>(a.pool, t.b, t.kvh, begin, t.k0 + t.keys, d, z, lane, a.err);
+          join(v, d, M, L, y0, y1);
+          if (isnan(y0) && z[0] != 0.f) y0 = z[0];
+          if (isnan(y1) && z[1] != 0.f) y1 = z[1];
+          if (v < t.qv && fabsf(L) < INFINITY) write(v, d, M, L, y0, y1);
         }
       }
       __syncwarp();

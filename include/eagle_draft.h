@@ -643,9 +643,11 @@ typedef struct {
  * product with the values: to 11 bits with 4-bit pages; with bf16 pages to 8 bits (2.3e-3 of the
  * output in all, where its own rounding has 1.7e-3), but for calls of at most 8 query vectors a KV
  * head with little to read, which keep 16.  Which it is depends on the sizes in args alone.
- * Infinities and NaN in a key or value reach every row of its sequence as the formula has it.
- * A row of a sequence without keys, or whose scores are all -infinity, gets zeros and lse -infinity.  Rows past max_rows, and keys past max_len, are left out and flagged
- * (EAGLE_DEVERR_PREFIX). */
+ * Infinities and NaN in a key or value reach every row of its sequence as the formula has it, however
+ * small the key's weight (an infinite value gives that infinity in its dim, NaN beside the other one
+ * or at a key of score -infinity); calls that meet infinities take longer.
+ * A row of a sequence without keys, or whose scores are all -infinity, gets zeros and lse -infinity.
+ * Rows past max_rows, and keys past max_len, are left out and flagged (EAGLE_DEVERR_PREFIX). */
 EAGLE_API int64_t eagle_kv_cross_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* args);
 EAGLE_API eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* args,
                                                   uint32_t* err_word, void* stream);

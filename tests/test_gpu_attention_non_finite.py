@@ -85,14 +85,16 @@ CROSS = [
 
 
 def cross_case(hd, ps, Hkv, G, lens, rows, first):
-    """first: the side of the first keys (the other side's are the last)."""
+    """first: the side of the first keys (the other side's are the last); 0: of either side in turn."""
     rng = np.random.default_rng(hd + sum(lens))
     cache, held = make_cache(rng, "bf16", hd, ps, Hkv, lens)
-    sides = [np.where(np.arange(n) < n // 2, first, -first) for n in lens]
+    sides = [np.where(np.arange(n) < n // 2, first, -first) if first else np.where(rng.random(n) < 0.5, 1, -1) for n in lens]
     steep(rng, cache, held, sides)
     for b, n in enumerate(lens):
         at = [n // 9, n - 1 - n // 7]
-        odd_values(cache, held, b, *(at if first > 0 else at[::-1]))
+        if first == 0:
+            at = [int(rng.choice(np.flatnonzero(sides[b] == s))) for s in (1, -1)]
+        odd_values(cache, held, b, *(at if first >= 0 else at[::-1]))
     q = queries(rng, sum(rows), Hkv * G, hd)
     out, lse = eb.kv_cross_attention(cache, dev(q, torch.bfloat16), dev(cu(rows)), dev(np.array(lens, np.int32)), max_rows=max(rows),
                                      max_len=max(lens), scale=1.0, lse=True)
@@ -108,6 +110,14 @@ def cross_case(hd, ps, Hkv, G, lens, rows, first):
 def test_far_values_reach_every_row(hd, ps, Hkv, G, lens, rows, first):
     for out, lse, q, keys, see in cross_case(hd, ps, Hkv, G, lens, rows, first):
         compare(out, lse, q, keys, see, hd, exact=False)
+
+
+@pytest.mark.parametrize("first", [1, -1, 0])
+@pytest.mark.parametrize("hd,ps,Hkv,G,lens,rows", CROSS)
+def test_far_infinities_are_the_formulas(hd, ps, Hkv, G, lens, rows, first):
+    """The sum's infinity, or NaN where it meets the other or a NaN: also where p is 0 in 32 bits."""
+    for out, lse, q, keys, see in cross_case(hd, ps, Hkv, G, lens, rows, first):
+        compare(out, lse, q, keys, see, hd)
 
 
 def shared_case(hd, Hkv, G, plens, groups, ctx, rows, side):
@@ -153,6 +163,59 @@ SHARED = [
 def test_far_values_of_prefix_or_own_keys_reach_every_row(hd, Hkv, G, plens, groups, ctx, rows, side):
     for out, lse, q, keys, see in shared_case(hd, Hkv, G, plens, groups, ctx, rows, side):
         compare(out, lse, q, keys, see, hd, exact=False)
+
+
+@pytest.mark.parametrize("side", [1, -1])
+@pytest.mark.parametrize("hd,Hkv,G,plens,groups,ctx,rows", SHARED)
+def test_far_infinities_of_prefix_or_own_keys_are_the_formulas(hd, Hkv, G, plens, groups, ctx, rows, side):
+    for out, lse, q, keys, see in shared_case(hd, Hkv, G, plens, groups, ctx, rows, side):
+        compare(out, lse, q, keys, see, hd)
+
+
+@pytest.mark.parametrize("first", [1, -1, 0])
+@pytest.mark.parametrize("hd,G,ctx,rows", [(128, 4, [900, 130], [1, 2]), (64, 2, [40000], [1]), (128, 8, [700, 60], [30, 64]), (64, 4, [0, 3000], [200, 10])])
+def test_the_steps_own_attention_too(hd, G, ctx, rows, first):
+    """eagle_kv_attention, whose rows are keys of the sequence: an infinity in keys that a row does not see
+    leaves nothing, in the others the sum's."""
+    rng = np.random.default_rng(hd + G)
+    lens = [c + r for c, r in zip(ctx, rows)]
+    cache, held = make_cache(rng, "bf16", hd, 64, 1, lens)
+    sides = [np.where(np.arange(n) < n // 2, first, -first) if first else np.where(rng.random(n) < 0.5, 1, -1) for n in lens]
+    steep(rng, cache, held, sides)
+    for b, n in enumerate(lens):
+        for key in (n // 3, n - 1):                  # (the last: the last row's alone)
+            for dim, h, lo in ODD:
+                put(cache, held, b, key, dim, h if sides[b][key] > 0 else lo)
+    q = queries(rng, sum(rows), G, hd)
+    out, lse = eb.kv_attention(cache, dev(q, torch.bfloat16), dev(cu(rows)), dev(np.array(ctx, np.int32)), max_rows=max(rows), max_len=max(lens),
+                               scale=1.0, lse=True)
+    assert cache.check() == 0
+    at = cu(rows)
+    for b, r in enumerate(rows):
+        s = slice(at[b], at[b + 1])
+        compare(out[s], lse[s], q[s], held[b], see_matrix(ctx[b], r), hd)
+
+
+@pytest.mark.parametrize("rows", [[1] * 20, [40] * 20])
+def test_an_infinity_at_a_key_of_no_weight(rows):
+    """A key of score -infinity has a weight of 0, and 0 times an infinite value is NaN; the other dims
+    are as without that key."""
+    rng = np.random.default_rng(4)
+    lens, hd, Hkv, G = [300 + 41 * i for i in range(len(rows))], 128, 8, 1
+    cache, held = make_cache(rng, "bf16", hd, 64, Hkv, lens)
+    q = K.bf16(np.abs(K.bf16(rng.standard_normal((sum(rows), Hkv * G, hd)))) + 0.5)
+    for b in range(len(lens)):
+        cache.k[int(cache.page_table[b, 1]), :, 7, 11] = -INF
+        cache.v[int(cache.page_table[b, 1]), :, 7, 20] = INF
+    out, lse = eb.kv_cross_attention(cache, dev(q, torch.bfloat16), dev(cu(rows)), dev(np.array(lens, np.int32)), max_rows=max(rows),
+                                     max_len=max(lens), lse=True)
+    o, l, at = out.double().cpu().numpy(), lse.double().cpu().numpy(), cu(rows)
+    assert np.isnan(o[..., 20]).all()
+    for b, r in enumerate(rows):
+        s, keep = slice(at[b], at[b + 1]), np.delete(np.arange(lens[b]), 64 + 7)
+        ref = K.attention(q[s], held[b][0][keep], held[b][1][keep], np.ones((r, len(keep)), bool), hd ** -0.5)
+        rest = np.delete(np.arange(hd), 20)
+        check(o[s][..., rest], l[s], (ref[0][..., rest], ref[1], ref[2][..., rest], ref[3], ref[4][..., rest]), hd)
 
 
 def test_a_nan_key_reaches_every_row_from_any_part():
