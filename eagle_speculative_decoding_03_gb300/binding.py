@@ -1005,13 +1005,16 @@ def kv_shared_attention(prefix: KVCache, cu_groups, prefix_lens, cache: KVCache,
 
 def kv_shared_attention_workspace(prefix: KVCache, cache: KVCache, n_heads: int, N: int, n_groups: int, B: int,
                                   max_group_rows: int, max_prefix: int, max_rows: int, max_len: int) -> int:
-    """Bytes of workspace that kv_shared_attention needs for these sizes."""
+    """Bytes of workspace that kv_shared_attention needs for these sizes, with a mask or without."""
     g = KVGroups(n_groups=n_groups, max_rows=max_group_rows, max_len=max_prefix)
-    a = KVAttention(B=B, N=N, n_heads=n_heads, max_rows=max_rows, max_len=max_len)
-    need = load().eagle_kv_shared_attention_workspace(C.byref(prefix.c), C.byref(g), C.byref(cache.c), C.byref(a))
-    if need < 0:
-        _bad(load().eagle_draft_last_error().decode())
-    return need
+    most = 0
+    for slots in (0, max_rows) if 1 <= max_rows <= 64 else (0,):   # (a masked step is cut another way; the pointer is only told from null)
+        a = KVAttention(B=B, N=N, n_heads=n_heads, max_rows=max_rows, max_len=max_len, mask=slots or None, mask_slots=slots)
+        need = load().eagle_kv_shared_attention_workspace(C.byref(prefix.c), C.byref(g), C.byref(cache.c), C.byref(a))
+        if need < 0:
+            _bad(load().eagle_draft_last_error().decode())
+        most = max(most, need)
+    return most
 
 
 def attention_merge(outs, lses, dtype=None, out=None, lse=False, stream=None):
