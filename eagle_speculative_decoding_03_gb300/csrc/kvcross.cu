@@ -66,14 +66,6 @@ EAGLE_DEV uint64_t policy_evict_normal() {
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-EAGLE_DEV uint32_t ld_acquire_smem(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-  return r;
-}
-EAGLE_DEV void st_release_smem(uint32_t addr, uint32_t x) {
-  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
 
 // A place in the ring of keys and values, and how often the ring has turned (mod 4).  Its places have two
 // barriers each, for the odd and the even turns: a group that skips the other's tiles may come to a place
@@ -351,16 +343,7 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
         // The group's first entry is under way, so what was ahead of it in its place is through (in a run of
         // short items this group may have skipped any number).  From there on it waits for one of any NS
         // entries, which leaves its place's barriers two turns apart.
-        const uint32_t e0 = first + (both ? 2 * g : 0);
-#pragma unroll 1
-        for (uint32_t i = 1; work && static_cast<int>(ld_acquire_smem(placed_u) - e0) <= 0; ++i) {
-          if ((i & 255u) == 0 && (*abort_flag || i > (1u << 24))) {
-            if (!*abort_flag) atomicOr(a.err, DEVERR_TIMEOUT);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-        }
+        if (work) ok = ok && kx_wait_past(placed_u, first + (both ? 2 * g : 0), a.err, abort_flag);
         RingAt vp = kp;
         vp.step(1, NS);
 #pragma unroll 1

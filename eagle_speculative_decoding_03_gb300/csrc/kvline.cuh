@@ -7,14 +7,45 @@
 
 namespace eagle {
 
-// Waits of these kernels, bounded by a count of polls (a quarter of a second and more), in few
-// instructions.  SLEEP: for roles that may wake up late.
+// Waits of these kernels, bounded by the clock as mbar_wait's are (a poll may suspend the thread for as
+// long as the hardware likes, so their number bounds nothing).  32 bits of it, read at every 256th poll: with
+// 64, or with a loop of its own behind the first 256, cross_prompt's sizes took 239 and 255 us where 218.
+// SLEEP: for roles that may wake up late.
+static_assert(WAIT_LIMIT_CYCLES < 1ll << 32, "");
 template <bool SLEEP = false>
-EAGLE_DEV bool kx_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile int* abort_flag) {
+EAGLE_DEV bool kx_wait(uint32_t bar, uint32_t parity, unsigned* err, volatile int* abort_flag, uint32_t limit = WAIT_LIMIT_CYCLES) {
+  uint32_t since = 0;
 #pragma unroll 1
   for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
     if (SLEEP) __nanosleep(32);
-    if ((i & 255u) == 255u && (*abort_flag || i > (SLEEP ? 1u << 22 : 1u << 24))) {
+    if ((i & 255u) != 255u) continue;
+    const uint32_t now = static_cast<uint32_t>(clock64());
+    if (i == 255u) since = now;
+    if (*abort_flag || now - since > limit) {
+      if (!*abort_flag) atomicOr(err, DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+EAGLE_DEV uint32_t ld_acquire_smem(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+EAGLE_DEV void st_release_smem(uint32_t addr, uint32_t x) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+// the same until the count at `addr` has passed n (counts wrap)
+EAGLE_DEV bool kx_wait_past(uint32_t addr, uint32_t n, unsigned* err, volatile int* abort_flag, uint32_t limit = WAIT_LIMIT_CYCLES) {
+  uint32_t since = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; static_cast<int>(ld_acquire_smem(addr) - n) <= 0; ++i) {
+    if ((i & 255u) != 255u) continue;
+    const uint32_t now = static_cast<uint32_t>(clock64());
+    if (i == 255u) since = now;
+    if (*abort_flag || now - since > limit) {
       if (!*abort_flag) atomicOr(err, DEVERR_TIMEOUT);
       *abort_flag = 1;
       return false;
