@@ -197,8 +197,8 @@ kv_cross_wide(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
   Seg* segs = reinterpret_cast<Seg*>(misc + 736);
 
   pdl_trigger();
-  if (ring_u & 1023u) {                      // (the swizzled tiles' alignment)
-    if (tid == 0) atomicOr(a.err, DEVERR_TIMEOUT);
+  if (misplaced(ring_u, parts, a.err)) {
+    if (OWN) pdl_wait();                     // (this kernel ends after the one before it)
     return;
   }
   if (tid == 0) {

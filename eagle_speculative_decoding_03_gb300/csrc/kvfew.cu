@@ -103,10 +103,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
   float* s_m = reinterpret_cast<float*>(misc + 640);                 // [warp][8]
   float* s_l = reinterpret_cast<float*>(misc + 896);
   pdl_trigger();
-  if (ring & 1023u) {                        // (the swizzled tiles' alignment)
-    if (tid == 0) atomicOr(a.err, DEVERR_TIMEOUT);
-    return;
-  }
+  if (misplaced(ring, parts, a.err)) return;
   if (tid == 0) {
     for (int s = 0; s < KF_MAX_STAGES; ++s) {
       mbar_init(bar_full + 8 * s, KF_LOADERS);

@@ -73,6 +73,14 @@ struct Line {
 struct Cut {
   int last, kvh, row0, v0, qv, slot, pad[2];
 };
+// Whether the swizzled tiles cannot lie at shared address `ring`.  The call is flagged, and this CTA's cut
+// left empty: the join, which follows all the same, takes its places from there.
+EAGLE_DEV bool misplaced(uint32_t ring, float* parts, unsigned* err) {
+  if ((ring & 1023u) == 0) return false;
+  atomicOr(err, DEVERR_TIMEOUT);
+  reinterpret_cast<Cut*>(parts)[blockIdx.x].last = 0;
+  return true;
+}
 // x / y (x >= 0, y > 0), by 32 bits where they do
 static __device__ __noinline__ long long quotient64(long long x, long long y) { return x / y; }
 EAGLE_DEV long long quotient(long long x, long long y) {
