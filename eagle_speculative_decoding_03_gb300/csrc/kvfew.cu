@@ -11,13 +11,15 @@
 // with a running maximum and sum a warp; their states meet in shared memory at the item's end, in warp
 // order.  (kv_attention_tc spends 128 rows of MMA and a CTA's start and end on such an item.)
 //
-// 32 sequences of 300 to 3,000 keys, 16 heads of 64 (217 MB): 48.7 us with the join, 4.5 TB/s, 66% of
+// 32 sequences of 300 to 3,000 keys, 16 heads of 64 (217 MB): 51 us with the join, 4.3 TB/s, 63% of
 // the measured copy rate; the ranges of kv_attention_tc take 75.  What is over is the start (a CTA finds
 // its place among the sequences, 3 us), the copies' first latency and the join's launch.  With little
 // to read those count for more than even shares (2 requests: 30 us, by ranges 23), see kf_worth.
 //
-// Rows behind the last key are cleared in the fragments (they may hold NaN).  p is rounded to bf16 for
-// the second product, as in kvcross.cu; l sums the unrounded p.
+// Rows behind the last key are cleared in the fragments (they may hold NaN).  For the second product p is
+// held in two bf16 parts, 16 bits, as in kv_attention_tc's ranges, so that a request's result does not get
+// coarser with the batch that it is in: 1.7e-3 of the output's norm from 64 bits, its own rounding, for
+// 1.2 us of the 51 (one part: 2.2e-3).  l sums the unrounded p.
 #include "kvline.cuh"
 
 #include <algorithm>
@@ -275,13 +277,15 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
         }
       }
       const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;   // (nothing seen yet: every p is 0)
-      uint32_t p[2];
+      uint32_t p[2], r[2];                   // rounded to bf16, and what that leaves
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float p0 = fast_exp2(s[2 * h] - b0), p1 = fast_exp2(s[2 * h + 1] - b1);
         l0 += p0;
         l1 += p1;
-        p[h] = transpose8x8(pack_bf16(p0, p1));   // keys 2c, 2c + 1 (+ 8 h) of vector g
+        const uint32_t hi = pack_bf16(p0, p1);
+        p[h] = transpose8x8(hi);             // keys 2c, 2c + 1 (+ 8 h) of vector g
+        r[h] = transpose8x8(pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
       }
       // masks of the pairs of keys 2c, 2c + 1 and 8 + those that are there
       const uint32_t lo = (2 * c < left ? 0xFFFFu : 0u) | (2 * c + 1 < left ? 0xFFFF0000u : 0u);
@@ -298,6 +302,7 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
           v[3] &= hi;
         }
         mma_bf16(o[j], v, p[0], p[1]);
+        mma_bf16(o[j], v, r[0], r[1]);
       }
     }
     // (the stage's next copy is another proxy's write; keys and values went through products, queries may
