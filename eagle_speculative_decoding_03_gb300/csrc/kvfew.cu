@@ -220,12 +220,13 @@ kv_few(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensor
     if (t.flags & KF_END) break;
     const uint32_t at = ring + rp.slot * kf_kv(HD);
     if (t.flags & KF_FIRST) {
-      // vector g's dims 16 s + 2 c, + 1, + 8, + 9 (of vectors that are not there: anything, in columns of their own)
+      // vector g's dims 16 s + 2 c, + 1, + 8, + 9 (of vectors that are not there: zeros)
       const uint32_t src = queries + (rp.slot * KF_QV + g) * HD * 2 + 4 * c;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[s][0]) : "r"(src + 32 * s) : "memory");
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[s][1]) : "r"(src + 32 * s + 16) : "memory");
+        if (g >= t.qv) q[s][0] = q[s][1] = 0u;
       }
 #pragma unroll
       for (int s = 0; s < KS; ++s)
