@@ -1244,6 +1244,38 @@ cudaError_t launch_step(const KaArgs& a, cudaStream_t st) {
   return launch_ranges(a, dim3(a.splits, a.pool.Hkv, a.B), 32 * KS_WARPS + 32, smem, st, kv_attention_step_f4<HD>, a);
 }
 
+// How many clusters of `ranges` CTAs of the kernel the device holds at once.  (SMs come in groups of unequal
+// sizes, so this is asked for: one GB300 holds 15 clusters of 7 or 8 CTAs, not two in each of 8 groups of 19;
+// one row of 16 heads of 64 over 1,000, 20,000 keys in 16 clusters of 8: two waves, 15.4, 55.9 us; now 9.3, 28.7.)
+int active_clusters(bool step, int ranges) {
+  static std::atomic<int> known[64][2][KA_MAX_JOIN + 1];
+  const int gb300[2][KA_MAX_JOIN + 1] = {{0, 152, 76, 46, 36, 28, 23, 15, 15}, {0, 456, 228, 148, 110, 87, 74, 59, 51}};   // (without a device)
+  int dev = 0;
+  if (num_sms() <= 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return gb300[step][ranges];
+  int n = known[dev][step][ranges].load();
+  if (n > 0) return n;
+  const void* kernel = step ? reinterpret_cast<const void*>(kv_attention_step_f4<128>) : reinterpret_cast<const void*>(kv_attention_tc<128, EAGLE_CACHE_BF16, 1>);
+  size_t smem = static_cast<size_t>(KS_STAGES) * ks_stage(128);
+  const cudaError_t e = step ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) : allow_max_smem(kernel, &smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranges;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(ranges);
+  cfg.blockDim = dim3(step ? 32 * KS_WARPS + 32 : ka_threads(EAGLE_CACHE_BF16, 1));
+  cfg.dynamicSmemBytes = smem;
+  if (e != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = gb300[step][ranges];
+  }
+  known[dev][step][ranges].store(n);
+  return n;
+}
+
 }  // namespace
 
 KaPlan eagle::ka_plan(int kind, int Hkv, int G, int B, int max_rows, int max_len, bool may_join) {
@@ -1256,7 +1288,7 @@ KaPlan eagle::ka_plan(int kind, int Hkv, int G, int B, int max_rows, int max_len
   const long long tiles = (static_cast<long long>(max_len) + KA_CH - 1) / KA_CH;
   // Key ranges: the split that takes least, a CTA costing its tiles and `fixed` more
   // for its start and its result.  Up to 8 ranges join in a cluster where the device holds all
-  // clusters at once (each within one of its groups of about 19 SMs); in several waves the ranges of
+  // clusters at once; in several waves the ranges of
   // requests of different lengths keep each other waiting (150 us of attention_step_b32_f4 where
   // separate ranges take 131).  Others join in a second kernel, which costs `second` tiles and
   // another for every four ranges (attention_step_b1: 13.2 us, joined 12.2, and 8 us less host time).
@@ -1270,7 +1302,7 @@ KaPlan eagle::ka_plan(int kind, int Hkv, int G, int B, int max_rows, int max_len
   for (long long n = 1, t = 0; n <= most; n = t > 1 ? (tiles + t - 2) / (t - 1) : most + 1) {
     t = (tiles + n - 1) / n;
     const long long ranges = (tiles + t - 1) / t;
-    const bool join = may_join && ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= sms / 19 * (19 * per_sm / ranges);
+    const bool join = may_join && ranges > 1 && ranges <= KA_MAX_JOIN && p.nb == 1 && base <= active_clusters(p.step, static_cast<int>(ranges));
     // the requests all as long as the bound, and (of several requests) of lengths spread below it:
     // then the longest CTA, or the work of the average request on all slots
     const double even = static_cast<double>((base * ranges + slots - 1) / slots * (t + fixed));
