@@ -299,17 +299,18 @@ struct KxPlan {
   int ctas;
   int64_t bytes;
 };
-constexpr int KX_FROM = 9;                 // query vectors per KV head of a request from which it is taken
 KxPlan kx_plan(int kind, int Hkv, int hd, int G, int B, int max_rows, int max_len);
 cudaError_t kx_launch(const KaArgs& a, const KaArgs* own, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, const KxPlan& p,
                       float* parts, cudaStream_t st);
+// Whether it takes less time than ranges, for qv query vectors a KV head and sequence.
+bool kx_worth(int kind, int Hkv, long long qv, int B, int max_len);
 
 // The same for few query vectors (kvfew.cu: at most KF_QV a KV head and request, bf16 pages, every row
 // sees all its keys).  Writes out and lse, or with a.parts the one partial result of every row; the
 // plan's members of `a` are filled in here.
 constexpr int KF_QV = 8;
 KxPlan kf_plan(int Hkv, int hd, int B, int max_len);
-bool kf_worth(int Hkv, int B, int max_len);   // whether the SMs have several tiles each
+bool kf_worth(int Hkv, int hd, int qv, int B, int max_len, bool alone);   // alone: no other keys are joined to them
 cudaError_t kf_launch(KaArgs* a, const eagle_kv_cache_t* cache, const KxPlan& p, float* parts, cudaStream_t st);
 
 // The ranges of a request (grid x) as one cluster where they join in it.

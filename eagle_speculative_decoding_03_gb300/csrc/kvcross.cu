@@ -971,6 +971,29 @@ cudaError_t launch_kind(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
 
 }  // namespace
 
+// Ranges (kv_attention_tc, kv_attention_step_f4) start sooner and need one launch where they join in a cluster;
+// this kernel's shares are even whatever the lengths, but it starts and joins for 16 us and every short
+// item costs it a queue's drain.  Measured over 700 sizes (both kinds, 64 and 128 dims, 12 to 4,096
+// vectors, 1 to 128 sequences of 250 to 80,000 keys, equal and spread): of long items (2,432 keys and more)
+//   bf16, up to 128 vectors: ranges, which keep 16 bits of p where this kernel keeps 8 (and are slower where
+//     few long sequences differ: 4 of 5,000 to 35,000 keys and 8 heads, 128 vectors: 96 us, here 82)
+//   bf16, more: here where a few sequences leave the SMs under one item each (4 of 1,500 to 10,500 keys, 8
+//     heads, 512 vectors: 64 us, by ranges 81), or where a hundred tiles an SM outweigh the start
+//     (prompts: 219, by ranges 229)
+//   4 bits, up to 128: several sequences, under one item and at least 30 tiles an SM (76, by ranges 103)
+//   4 bits, more: 10 tiles an SM and more (1 of 16,000 keys, 1,024 vectors: 74, by ranges 85)
+// and ranges elsewhere (1 of 8,000 bf16 keys, 12 vectors: 18 us, here 31; 32 of 125 to 870: 25, here 60;
+// 512 vectors: 63, here 117).  The mean loss to the faster of the two is 5.3, 0.5, 1.7 and 0.9% of the four.
+bool eagle::kx_worth(int kind, int Hkv, long long qv, int B, int max_len) {
+  const int sms = num_sms() > 0 ? num_sms() : 152;   // (152: without a device, a GB300's)
+  const double tiles = static_cast<double>((static_cast<long long>(max_len) + KA_CH - 1) / KA_CH);
+  const double items = static_cast<double>(B) * Hkv * static_cast<double>((qv + KX_QV - 1) / KX_QV) / sms, work = items * tiles;
+  if (tiles < 20) return false;
+  const bool few = B > 1 && items <= 1;      // (of several sequences, whose lengths may differ)
+  if (kind == EAGLE_CACHE_F4) return qv <= KA_QV ? few && work >= 30 : work >= 10;
+  return qv > KA_QV && ((few && work >= 10) || work >= 100);
+}
+
 KxPlan eagle::kx_plan(int kind, int Hkv, int hd, int G, int B, int max_rows, int max_len) {
   const long long blocks = (static_cast<long long>(max_rows) * G + KX_QV - 1) / KX_QV, tiles = (static_cast<long long>(max_len) + kx_keys(kind) - 1) / kx_keys(kind);
   const double units = static_cast<double>(B) * Hkv * blocks * tiles;

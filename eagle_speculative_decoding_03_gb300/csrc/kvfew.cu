@@ -14,7 +14,7 @@
 // 32 sequences of 300 to 3,000 keys, 16 heads of 64 (217 MB): 51 us with the join, 4.3 TB/s, 63% of
 // the measured copy rate; the ranges of kv_attention_tc take 75.  What is over is the start (a CTA finds
 // its place among the sequences, 3 us), the copies' first latency and the join's launch.  With little
-// to read those count for more than even shares (2 requests: 30 us, by ranges 23), see kf_worth.
+// to read those count for more than even shares, see kf_worth.
 //
 // Rows behind the last key are cleared in the fragments (they may hold NaN).  For the second product p is
 // held in two bf16 parts, 16 bits, as in kv_attention_tc's ranges, so that a request's result does not get
@@ -447,7 +447,16 @@ static double kf_units(int Hkv, int B, int max_len) {
 }
 static int kf_sms() { return num_sms() > 0 ? num_sms() : 152; }   // (152: without a device, a GB300's)
 
-bool eagle::kf_worth(int Hkv, int B, int max_len) { return kf_units(Hkv, B, max_len) >= 8. * kf_sms(); }
+// Where the SMs have so many tiles each that even shares count for more than an earlier start.  Measured for 1 to
+// 128 sequences of 250 to 80,000 keys: 8 heads of 64, 16 of 2,000 keys a head: 16.8 us, by ranges 20.5 (23 tiles an SM), 32 of
+// 300: 16.4, 17.2 (15), 8 of 500: 10.9, 11.0 (6); heads of 128, 4 vectors: 16 of 1,000: 21.5, 23.0 (24), 32 of
+// 300: 20.8, 19.4 (15); 8 vectors, whose eight columns are all at work: 32 of 2,000: 55, 60 (93), 128 of 300: 68, 60
+// (61).  A step's own keys behind a prefix go by ranges side by side with the prefix's otherwise: 64
+// of 500: 69 us, here 75 (50), 256 of 1,000: 317, here 296 (404).
+bool eagle::kf_worth(int Hkv, int hd, int qv, int B, int max_len, bool alone) {
+  const double least = !alone ? 80. : hd == 64 ? 12. : qv <= 4 ? 20. : 90.;
+  return kf_units(Hkv, B, max_len) >= least * kf_sms();
+}
 
 KxPlan eagle::kf_plan(int Hkv, int hd, int B, int max_len) {
   const double ctas = kf_units(Hkv, B, max_len) / KF_MIN_UNITS;

@@ -5,7 +5,8 @@
 //   M = max m_i,  L = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) o_i / L,  lse = ln 2 (M + log2 L)
 //
 // Partial results over disjoint keys (key ranges, the prefix and a request's own keys) are joined
-// by that rule, in a fixed order.  The kernels over the keys are in kvattn.cu.
+// by that rule, in a fixed order.  The kernels over the keys are in kvattn.cu (by ranges), kvcross.cu and
+// kvfew.cu (dealt out in line).
 #include "kvline.cuh"
 
 #include <algorithm>
@@ -20,8 +21,9 @@ constexpr int MG_THREADS = 256;
 // WARPS warps per (row, query head), each a share of the ranges: the own keys' first, then the
 // prefix's (`pre`, whose buffers lie behind them).  For prefixes cut by ranges: kvcross.cu joins in its
 // own epilogue.  Starts while the ranges run and waits for them; the prefix's ranges run beside the own
-// keys' (2 requests behind 700 keys: 16.5 us, 22 one after the other).  The two caches' value factors are applied after
-// the division (as in kvattn.cu), so the sums of the two are kept apart.
+// keys' (2 requests behind 700 keys: 17 us, 22 one after the other; 32 behind 8,192: 44, with the own keys dealt out
+// in line ahead of the prefix in the wide kernel 58).  The two caches' value factors are applied after the division
+// (as in kvattn.cu), so the sums of the two are kept apart.
 template <int HD, int WARPS>
 __global__ void __launch_bounds__(128) kv_shared_join(const KaArgs a, const KaArgs pre) {
   constexpr int E = HD / 32;
@@ -225,9 +227,9 @@ float log2_scale(float scale, int hd) {
   return std::min((scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(hd))) * 1.4426950408889634f, FLT_MAX);
 }
 
-// How a call over keys that all rows see is cut: in line over the SMs, or (4-bit pages with few query
-// vectors, and steps whose ranges join in a cluster) by ranges.  FEW also takes a step's own keys, of one
-// row a request, which sees them all.
+// How a call over keys that all rows see is cut: by ranges, or dealt out in line over the SMs (WIDE, or FEW for
+// at most KF_QV query vectors over bf16 pages; FEW also takes a step's own keys, of one row a request, which
+// sees them all).
 enum class Cutting { RANGES, WIDE, FEW };
 struct CrossPlan {
   Cutting by;
@@ -236,16 +238,30 @@ struct CrossPlan {
   bool separate() const { return by == Cutting::RANGES && ranges.splits > 1 && !ranges.joined; }
   int64_t line_bytes() const { return by == Cutting::RANGES ? 0 : line.bytes; }
 };
-CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int max_len, bool may_join) {
+// alone: a cross call; else the prefix of a shared one.
+CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int max_len, bool alone) {
   CrossPlan p;
+  const int Hkv = c->n_kv_heads, hd = c->head_dim;
   const long long qv = static_cast<long long>(max_rows) * G;
-  p.by = qv >= KX_FROM ? Cutting::WIDE : c->kind == EAGLE_CACHE_BF16 ? Cutting::FEW : Cutting::RANGES;
-  if (p.by != Cutting::WIDE) p.ranges = ka_plan(c->kind, c->n_kv_heads, G, B, max_rows, max_len, may_join);
-  // (a step's few ranges in one cluster each take no second launch: cross_step_b1 10 us, in line 16; and
-  // with little to read its start counts for more than even shares: shared_step_b2 16.5 us, in line 30)
-  if (p.by == Cutting::FEW && (p.ranges.joined || !kf_worth(c->n_kv_heads, B, max_len))) p.by = Cutting::RANGES;
-  if (p.by == Cutting::WIDE) p.line = kx_plan(c->kind, c->n_kv_heads, c->head_dim, G, B, max_rows, max_len);
-  if (p.by == Cutting::FEW) p.line = kf_plan(c->n_kv_heads, c->head_dim, B, max_len);
+  p.by = Cutting::RANGES;
+  p.ranges = ka_plan(c->kind, Hkv, G, B, max_rows, max_len, alone);
+  if (qv > KF_QV) {                          // (and where a launch by ranges has no room for all blocks)
+    if (kx_worth(c->kind, Hkv, qv, B, max_len) || static_cast<long long>(B) * p.ranges.blocks > 65535) p.by = Cutting::WIDE;
+  } else if (alone && c->kind == EAGLE_CACHE_BF16 && kf_worth(Hkv, hd, static_cast<int>(qv), B, max_len, true)) {
+    p.by = Cutting::FEW;
+  }
+  if (p.by == Cutting::WIDE) p.line = kx_plan(c->kind, Hkv, hd, G, B, max_rows, max_len);
+  if (p.by == Cutting::FEW) p.line = kf_plan(Hkv, hd, B, max_len);
+  return p;
+}
+// The own keys of a shared call.
+CrossPlan own_plan(const eagle_kv_cache_t* c, int G, const eagle_kv_attention_t* w) {
+  CrossPlan p;
+  const int Hkv = c->n_kv_heads, hd = c->head_dim;
+  p.by = w->max_rows == 1 && !w->mask && c->kind == EAGLE_CACHE_BF16 && G <= KF_QV && kf_worth(Hkv, hd, G, w->B, w->max_len, false)
+             ? Cutting::FEW : Cutting::RANGES;
+  p.ranges = ka_plan(c->kind, Hkv, G, w->B, w->max_rows, w->max_len, false);
+  if (p.by == Cutting::FEW) p.line = kf_plan(Hkv, hd, w->B, w->max_len);
   return p;
 }
 
@@ -266,7 +282,7 @@ int64_t cross_bytes(const eagle_kv_cross_t* w, int hd, const CrossPlan& p) {
 
 // Ranges of partial results of a shared call: the own keys', then the prefix's.
 int own_ranges(const CrossPlan& own) { return own.by == Cutting::RANGES ? own.ranges.splits : 1; }
-int pre_ranges(const CrossPlan& pre) { return pre.by == Cutting::WIDE ? 0 : own_ranges(pre); }
+int pre_ranges(const CrossPlan& pre) { return pre.by == Cutting::WIDE ? 0 : pre.ranges.splits; }
 int64_t shared_bytes(const eagle_kv_attention_t* w, int hd, const CrossPlan& pre, const CrossPlan& own) {
   return pre.line_bytes() + own.line_bytes() + (own_ranges(own) + pre_ranges(pre)) * ka_part_bytes(w->N, w->n_heads, hd);
 }
@@ -288,12 +304,7 @@ eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, con
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: a mask needs max_rows <= mask_slots <= 64", who);
   const int G = w->n_heads / cache->n_kv_heads;
   *pp = cross_plan(prefix, G, g->n_groups, g->max_rows, g->max_len, false);
-  if (w->max_rows == 1 && !w->mask && cache->kind == EAGLE_CACHE_BF16 && G <= KF_QV) {
-    *po = cross_plan(cache, G, w->B, 1, w->max_len, false);
-  } else {
-    po->by = Cutting::RANGES;
-    po->ranges = ka_plan(cache->kind, cache->n_kv_heads, G, w->B, w->max_rows, w->max_len, false);
-  }
+  *po = own_plan(cache, G, w);
   if (pp->by == Cutting::RANGES) r = check_plan(who, g->n_groups, pp->ranges);
   return r != EAGLE_OK || po->by != Cutting::RANGES ? r : check_plan(who, w->B, po->ranges);
 }
@@ -431,7 +442,7 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   if (e == cudaSuccess && pp.by == Cutting::WIDE) {
     e = kx_launch(x, &a, pf4, pmk, pmv, pp.line, pre_parts, st);
   } else if (e == cudaSuccess) {
-    e = pp.by == Cutting::FEW ? kf_launch(&x, prefix, pp.line, pre_parts, st) : ka_launch(&x, pp.ranges, pf4, pmk, pmv, st);
+    e = ka_launch(&x, pp.ranges, pf4, pmk, pmv, st);
     if (e == cudaSuccess) e = hd == 64 ? launch_join<64>(a, x, st) : launch_join<128>(a, x, st);
   }
   return e == cudaSuccess ? EAGLE_OK : kv_fail(EAGLE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));

@@ -641,8 +641,8 @@ typedef struct {
 /* out = softmax(scale q k) v over all keys of the sequence, in the types of eagle_kv_attention:
  * scores, maxima, sums and lse in fp32, out rounded once.  The probabilities are rounded for the
  * product with the values: to 11 bits with 4-bit pages; with bf16 pages to 16 bits in calls of at
- * most 8 query vectors a KV head (max_rows * n_heads / n_kv_heads), else to 8 (2.3e-3 of the output in
- * all, where its own rounding has 1.7e-3).
+ * most 128 query vectors a KV head (max_rows * n_heads / n_kv_heads) and 65,535 sequences, else to 8
+ * (2.3e-3 of the output in all, where its own rounding has 1.7e-3).
  * Infinities and NaN in a key or value reach every row of its sequence as the formula has it, however
  * small the key's weight (an infinite value gives that infinity in its dim, NaN beside the other one
  * or at a key of score -infinity); calls that meet infinities take longer.
@@ -667,8 +667,9 @@ typedef struct {
  * before) what args->mask says, or j <= i: args is as in eagle_kv_attention, but for the workspace
  * (eagle_kv_shared_attention_workspace bytes).  Positions are the caller's: append the own keys
  * with positions behind the prefix.  The two caches have the same heads and head_dim; their kinds,
- * page sizes and pools are their own.  Rounding: the prefix as eagle_kv_cross_attention, the own keys
- * as eagle_kv_attention; joined in fp32 and rounded once.  Rows of a request outside every group, and rows past
+ * page sizes and pools are their own.  Rounding: the prefix as eagle_kv_cross_attention (with
+ * groups->max_rows and the groups as sequences), the own keys as eagle_kv_attention; joined in fp32
+ * and rounded once.  Rows of a request outside every group, and rows past
  * groups->max_rows, are left as they were; groups that descend, leave [0, B] or leave requests out
  * are flagged (EAGLE_DEVERR_PREFIX). */
 EAGLE_API int64_t eagle_kv_shared_attention_workspace(const eagle_kv_cache_t* prefix, const eagle_kv_groups_t* groups,

@@ -63,27 +63,30 @@ def close(out, keys, Hq, hd, rows):
     assert len(keys[0]) < 700 or (np.abs(o) < 2.0 ** -3 * mag).all()
 
 
+@pytest.mark.parametrize("bound", [0, 1 << 20])      # (by a bound so far above the lengths the keys are dealt out in line)
 @pytest.mark.parametrize("hd,ps,Hkv,G,lens,rows", [
-    (128, 64, 2, 4, [1500], 1), (64, 32, 1, 1, [20000], 1),                              # by ranges
-    (128, 64, 8, 4, [1000 + 37 * i for i in range(16)], 2), (64, 16, 16, 1, [700] * 16, 1),   # in line
+    (128, 64, 2, 4, [1500], 1), (64, 32, 1, 1, [20000], 1),
+    (128, 64, 8, 4, [1000 + 37 * i for i in range(16)], 2), (64, 16, 16, 1, [700] * 16, 1),
     (128, 128, 8, 1, [9000, 5, 1200], 8),
 ])
-def test_cross_attention_of_few_vectors(hd, ps, Hkv, G, lens, rows):
+def test_cross_attention_of_few_vectors(hd, ps, Hkv, G, lens, rows, bound):
     rng = np.random.default_rng(1)
     cache, held = make_cache(rng, "bf16", hd, ps, Hkv, lens)
     fill(rng, cache, held)
     B = len(lens)
     q = torch.zeros(B * rows, Hkv * G, hd, dtype=torch.bfloat16, device="cuda")
     q[..., 0] = 1.0
-    out = eb.kv_cross_attention(cache, q, dev(cu([rows] * B)), dev(np.array(lens, np.int32)), max_rows=rows, max_len=max(lens), scale=1.0)
+    out = eb.kv_cross_attention(cache, q, dev(cu([rows] * B)), dev(np.array(lens, np.int32)), max_rows=rows,
+                                max_len=max(max(lens), bound), scale=1.0)
     assert cache.check() == 0
     for b in range(B):
         close(out[b * rows:(b + 1) * rows], held[b], Hkv * G, hd, rows)
 
 
+@pytest.mark.parametrize("bound", [0, 1 << 20])
 @pytest.mark.parametrize("hd,Hkv,G,plens,ctx", [(128, 8, 4, [700] * 40, [300 + i for i in range(40)]), (64, 2, 4, [500, 90], [30, 9]),
                                                 (64, 8, 8, [0] * 30, [400 + 9 * i for i in range(30)])])
-def test_steps_behind_a_prefix_each(hd, Hkv, G, plens, ctx):
+def test_steps_behind_a_prefix_each(hd, Hkv, G, plens, ctx, bound):
     """One request a group: prefix and own keys both as few vectors."""
     rng = np.random.default_rng(2)
     B = len(ctx)
@@ -95,7 +98,27 @@ def test_steps_behind_a_prefix_each(hd, Hkv, G, plens, ctx):
     q[..., 0] = 1.0
     ints = lambda x: dev(np.array(x, np.int32))  # noqa: E731
     out = eb.kv_shared_attention(prefix, ints(list(range(B + 1))), ints(plens), cache, q, ints(list(range(B + 1))), ints(ctx), max_group_rows=1,
-                                 max_prefix=max(max(plens), 1), max_rows=1, max_len=max(ctx) + 1, scale=1.0)
+                                 max_prefix=max(max(plens), 1), max_rows=1, max_len=max(max(ctx) + 1, bound), scale=1.0)
     assert cache.check() == 0 and prefix.check() == 0
     for b in range(B):
         close(out[b:b + 1], tuple(np.concatenate(x) for x in zip(pre[b], own[b])), Hkv * G, hd, 1)
+
+
+@pytest.mark.parametrize("hd,Hkv,G,plens,groups,ctx", [(128, 8, 4, [3000], [0, 32], [200 + i for i in range(32)]), (64, 2, 8, [900, 1200], [0, 7, 15], [9 * i for i in range(15)]),
+                                                       (128, 1, 16, [1500], [0, 8], [90] * 8)])
+def test_steps_of_up_to_128_vectors_behind_a_prefix(hd, Hkv, G, plens, groups, ctx):
+    rng = np.random.default_rng(3)
+    B = len(ctx)
+    prefix, pre = make_cache(rng, "bf16", hd, 64, Hkv, plens)
+    cache, own = make_cache(rng, "bf16", hd, 32, Hkv, [c + 1 for c in ctx])
+    fill(rng, prefix, pre)
+    fill(rng, cache, own)
+    q = torch.zeros(B, Hkv * G, hd, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    ints = lambda x: dev(np.array(x, np.int32))  # noqa: E731
+    out = eb.kv_shared_attention(prefix, ints(groups), ints(plens), cache, q, ints(list(range(B + 1))), ints(ctx),
+                                 max_group_rows=max(np.diff(groups)), max_prefix=max(plens), max_rows=1, max_len=max(ctx) + 1, scale=1.0)
+    assert cache.check() == 0 and prefix.check() == 0
+    for b in range(B):
+        g = next(i for i in range(len(plens)) if groups[i] <= b < groups[i + 1])
+        close(out[b:b + 1], tuple(np.concatenate(x) for x in zip(pre[g], own[b])), Hkv * G, hd, 1)
