@@ -245,11 +245,10 @@ CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int 
   const long long qv = static_cast<long long>(max_rows) * G;
   p.by = Cutting::RANGES;
   p.ranges = ka_plan(c->kind, Hkv, G, B, max_rows, max_len, alone);
-  if (qv > KF_QV) {                          // (and where a launch by ranges has no room for all blocks)
-    if (kx_worth(c->kind, Hkv, qv, B, max_len) || static_cast<long long>(B) * p.ranges.blocks > 65535) p.by = Cutting::WIDE;
-  } else if (alone && c->kind == EAGLE_CACHE_BF16 && kf_worth(Hkv, hd, static_cast<int>(qv), B, max_len, true)) {
-    p.by = Cutting::FEW;
-  }
+  if (qv > KF_QV && kx_worth(c->kind, Hkv, qv, B, max_len)) p.by = Cutting::WIDE;
+  if (alone && qv <= KF_QV && c->kind == EAGLE_CACHE_BF16 && kf_worth(Hkv, hd, static_cast<int>(qv), B, max_len, true)) p.by = Cutting::FEW;
+  // (a launch by ranges has no room for more blocks)
+  if (p.by == Cutting::RANGES && (qv > KF_QV || !alone) && static_cast<long long>(B) * p.ranges.blocks > 65535) p.by = Cutting::WIDE;
   if (p.by == Cutting::WIDE) p.line = kx_plan(c->kind, Hkv, hd, G, B, max_rows, max_len);
   if (p.by == Cutting::FEW) p.line = kf_plan(Hkv, hd, B, max_len);
   return p;

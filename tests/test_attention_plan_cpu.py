@@ -74,3 +74,11 @@ def test_up_to_128_vectors_over_bf16_pages_never_lose_bits(lib, B, max_len, rows
 
 def test_calls_of_more_blocks_than_a_launch_has_are_taken(lib):  # noqa: F811
     assert cross(lib, bf16(n_kv_heads=1, head_dim=128), 16, 70000, 1, 100) == wide(128)
+    for G in (1, 16):                                # a prefix for each of 70,000 requests
+        c = bf16(n_kv_heads=1, head_dim=128)
+        g = eb.KVGroups(n_groups=70000, max_rows=1, max_len=100)
+        a = eb.KVAttention(B=70000, N=70000, n_heads=G, max_rows=1, max_len=100)
+        if G == 1:                                   # (their own keys are cut by ranges with 16 heads, which refuses them)
+            assert lib.eagle_kv_shared_attention_workspace(C.byref(c), C.byref(g), C.byref(c), C.byref(a)) > wide(128)
+        a = eb.KVAttention(B=60000, N=60000, n_heads=G, max_rows=1, max_len=100)
+        assert lib.eagle_kv_shared_attention_workspace(C.byref(c), C.byref(g), C.byref(c), C.byref(a)) > wide(128)
