@@ -15,9 +15,9 @@
 //
 // Bound by the tensor cores: a unit's Q K^T takes 48 cycles an instruction for 32 of work, because
 // both operands come from shared memory; with P V that is 2560 cycles for 128 keys and 256 vectors,
-// and 3050 are measured (2 prompts of 2,047 rows and 32 heads of 128 over 4,099 keys: 215 us with the
-// join, 1,280 TFLOP/s, 68% of the measured rate).  128 keys an instruction would run at the full rate, but its scores leave room
-// for one buffer a tile: 250 us.  4 bits: four warps convert what they copied, 64 keys an entry (a
+// and 3050 are measured (2 prompts of 2,047 rows and 32 heads of 128 over 4,099 keys: 219 us with the
+// join, 1,255 TFLOP/s, 67% of the measured rate).  128 keys an instruction would run at the full rate, but
+// its scores leave room for one buffer a tile: 250 us.  4 bits: four warps convert what they copied, 64 keys an entry (a
 // chunk of 1,688 rows of 32 heads over 16,001 keys 420 us, 1,070 TFLOP/s).
 //
 // bf16 p (8 bits) against bf16 values, fp16 p (11 bits) against 4-bit ones: the second product takes
