@@ -302,8 +302,8 @@ struct KxPlan {
 KxPlan kx_plan(int kind, int Hkv, int hd, int G, int B, int max_rows, int max_len);
 cudaError_t kx_launch(const KaArgs& a, const KaArgs* own, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, const KxPlan& p,
                       float* parts, cudaStream_t st);
-// Whether it takes less time than ranges, for qv query vectors a KV head and sequence.
-bool kx_worth(int kind, int Hkv, long long qv, int B, int max_len);
+// Whether it takes less time than ranges, for up to max_rows rows of G heads a KV head and sequence, N in all.
+bool kx_worth(int kind, int Hkv, int G, int B, long long N, int max_rows, int max_len);
 
 // The same for few query vectors (kvfew.cu: at most KF_QV a KV head and request, bf16 pages, every row
 // sees all its keys).  Writes out and lse, or with a.parts the one partial result of every row; the

@@ -984,10 +984,15 @@ cudaError_t launch_kind(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
 //   4 bits, more: 10 tiles an SM and more (1 of 16,000 keys, 1,024 vectors: 74, by ranges 85)
 // and ranges elsewhere (1 of 8,000 bf16 keys, 12 vectors: 18 us, here 31; 32 of 125 to 870: 25, here 60;
 // 512 vectors: 63, here 117).  The mean loss to the faster of the two is 5.3, 0.5, 1.7 and 0.9% of the four.
-bool eagle::kx_worth(int kind, int Hkv, long long qv, int B, int max_len) {
+// A range's CTAs are launched for every block that the bounds allow; where the rows can fill one in 8 of
+// them at most, as a prompt of 4,096 rows among 63 single tokens does, the empty ones cost more than the
+// rest (1,000 keys, 8 heads: 285 us, here 143; 1,024 rows: 109, here 96; one in 5: 56, here 63).
+bool eagle::kx_worth(int kind, int Hkv, int G, int B, long long N, int max_rows, int max_len) {
   const int sms = num_sms() > 0 ? num_sms() : 152;   // (152: without a device, a GB300's)
+  const long long qv = static_cast<long long>(max_rows) * G, blocks = (qv + KX_QV - 1) / KX_QV;
+  if (blocks > 1 && static_cast<double>(B) * static_cast<double>(blocks) > 8. * (static_cast<double>(N) * G / KX_QV + B)) return true;
   const double tiles = static_cast<double>((static_cast<long long>(max_len) + KA_CH - 1) / KA_CH);
-  const double items = static_cast<double>(B) * Hkv * static_cast<double>((qv + KX_QV - 1) / KX_QV) / sms, work = items * tiles;
+  const double items = static_cast<double>(B) * Hkv * static_cast<double>(blocks) / sms, work = items * tiles;
   if (tiles < 20) return false;
   const bool few = B > 1 && items <= 1;      // (of several sequences, whose lengths may differ)
   if (kind == EAGLE_CACHE_F4) return qv <= KA_QV ? few && work >= 30 : work >= 10;

@@ -239,13 +239,13 @@ struct CrossPlan {
   int64_t line_bytes() const { return by == Cutting::RANGES ? 0 : line.bytes; }
 };
 // alone: a cross call; else the prefix of a shared one.
-CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int max_rows, int max_len, bool alone) {
+CrossPlan cross_plan(const eagle_kv_cache_t* c, int G, int B, int N, int max_rows, int max_len, bool alone) {
   CrossPlan p;
   const int Hkv = c->n_kv_heads, hd = c->head_dim;
   const long long qv = static_cast<long long>(max_rows) * G;
   p.by = Cutting::RANGES;
   p.ranges = ka_plan(c->kind, Hkv, G, B, max_rows, max_len, alone);
-  if (qv > KF_QV && kx_worth(c->kind, Hkv, qv, B, max_len)) p.by = Cutting::WIDE;
+  if (qv > KF_QV && kx_worth(c->kind, Hkv, G, B, N, max_rows, max_len)) p.by = Cutting::WIDE;
   if (alone && qv <= KF_QV && c->kind == EAGLE_CACHE_BF16 && kf_worth(Hkv, hd, static_cast<int>(qv), B, max_len, true)) p.by = Cutting::FEW;
   // (a launch by ranges has no room for more blocks)
   if (p.by == Cutting::RANGES && (qv > KF_QV || !alone) && static_cast<long long>(B) * p.ranges.blocks > 65535) p.by = Cutting::WIDE;
@@ -271,7 +271,7 @@ eagle_status_t check_cross(const char* who, const eagle_kv_cache_t* cache, const
   r = check_extent(who, w->max_rows, w->max_len);
   if (r == EAGLE_OK) r = check_rows(who, cache->n_kv_heads, cache->head_dim, w->B, w->N, w->n_heads, w->q, w->q_stride, w->out, w->out_stride, w->scale);
   if (r != EAGLE_OK) return r;
-  *p = cross_plan(cache, w->n_heads / cache->n_kv_heads, w->B, w->max_rows, w->max_len, true);
+  *p = cross_plan(cache, w->n_heads / cache->n_kv_heads, w->B, w->N, w->max_rows, w->max_len, true);
   return p->by != Cutting::RANGES ? EAGLE_OK : check_plan(who, w->B, p->ranges);
 }
 
@@ -302,7 +302,7 @@ eagle_status_t check_shared(const char* who, const eagle_kv_cache_t* prefix, con
   if (w->mask && (w->mask_slots < 1 || w->mask_slots > 64 || w->max_rows > w->mask_slots))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: a mask needs max_rows <= mask_slots <= 64", who);
   const int G = w->n_heads / cache->n_kv_heads;
-  *pp = cross_plan(prefix, G, g->n_groups, g->max_rows, g->max_len, false);
+  *pp = cross_plan(prefix, G, g->n_groups, w->N, g->max_rows, g->max_len, false);
   *po = own_plan(cache, G, w);
   if (pp->by == Cutting::RANGES) r = check_plan(who, g->n_groups, pp->ranges);
   return r != EAGLE_OK || po->by != Cutting::RANGES ? r : check_plan(who, w->B, po->ranges);

@@ -82,3 +82,19 @@ def test_calls_of_more_blocks_than_a_launch_has_are_taken(lib):  # noqa: F811
             assert lib.eagle_kv_shared_attention_workspace(C.byref(c), C.byref(g), C.byref(c), C.byref(a)) > wide(128)
         a = eb.KVAttention(B=60000, N=60000, n_heads=G, max_rows=1, max_len=100)
         assert lib.eagle_kv_shared_attention_workspace(C.byref(c), C.byref(g), C.byref(c), C.byref(a)) > wide(128)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f4"])
+def test_bounds_far_above_the_rows_do_not_launch_empty_blocks(lib, kind):  # noqa: F811
+    """A prompt among single tokens: 64 requests of up to 4,096 rows, 4,159 in all."""
+    c = bf16() if kind == "bf16" else cache()
+
+    def need(N, rows):
+        return lib.eagle_kv_cross_attention_workspace(C.byref(c), C.byref(eb.KVCross(B=64, N=N, n_heads=32, max_rows=rows, max_len=1000)))
+    assert need(4159, 4096) == wide(128)               # 285 us by ranges, 143 in line (bf16)
+    assert need(64 * 128, 128) != wide(128)
+    g = eb.KVGroups(n_groups=64, max_rows=4096, max_len=1000)
+    a = eb.KVAttention(B=64, N=4159, n_heads=32, max_rows=1, max_len=40)
+    few_rows = eb.KVAttention(B=64, N=64, n_heads=32, max_rows=1, max_len=40)
+    for w in (a, few_rows):
+        assert lib.eagle_kv_shared_attention_workspace(C.byref(c), C.byref(g), C.byref(c), C.byref(w)) > wide(128)
