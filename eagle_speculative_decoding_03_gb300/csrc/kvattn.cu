@@ -154,7 +154,7 @@ kv_attention_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
   const int all_tiles = (seen + KA_CH - 1) / KA_CH;
   // (a cluster shares the tiles there are; separate ranges are cut by the call's bounds)
   const bool joined = NB == 1 && a.joined;
-  const int per_cta = joined ? (all_tiles + a.splits - 1) / a.splits : a.tiles_per_cta;
+  const int per_cta = joined ? (all_tiles + a.splits - 1) / a.splits : range_tiles(a, rq.len);
   const int t_begin = split * per_cta;
   if (!joined && split > 0 && t_begin * KA_CH >= rq.len) {        // (not a range of this request at all)
     if (a.behind) pdl_wait();
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(32 * KS_WARPS + 32, KS_CTAS) kv_attention_step
   pdl_trigger();
   const Req rq = request(a, b);
   const int qv = rq.R * a.G;
-  const int per_cta = a.joined ? ((rq.len + KA_CH - 1) / KA_CH + a.splits - 1) / a.splits : a.tiles_per_cta;
+  const int per_cta = a.joined ? ((rq.len + KA_CH - 1) / KA_CH + a.splits - 1) / a.splits : range_tiles(a, rq.len);
   const int kb = split * per_cta * KA_CH;
   if (qv <= 0 || (!a.joined && split > 0 && kb >= rq.len)) {
     if (a.behind) pdl_wait();
@@ -1147,7 +1147,7 @@ __global__ void __launch_bounds__(128) kv_attention_combine(const KaArgs a) {
   if (b < 0) return;
   const Req rq = request(a, b);
   if (n - rq.row0 >= rq.R || n < rq.row0) return;
-  const int used = min(a.splits, (rq.len + a.tiles_per_cta * KA_CH - 1) / (a.tiles_per_cta * KA_CH));
+  const int used = ranges_of(a, rq.len);
   const size_t at = static_cast<size_t>(n) * a.Hq + h, step = static_cast<size_t>(a.N) * a.Hq;
   float M = -INFINITY;
   for (int s = lane; s < used; s += 32) M = fmaxf(M, a.part_ml[s * step + at].x);
@@ -1315,6 +1315,9 @@ KaPlan eagle::ka_plan(int kind, int Hkv, int G, int B, int max_rows, int max_len
     }
   }
   p.tiles_per_cta = static_cast<int>(per);
+  // (several waves: shorter ranges than these cost more CTAs and results than they even out; 32 4-bit requests of
+  // 2,048 to 16,384 keys: 130 us, with at least 16 tiles 135, with 4 144)
+  p.least = base * ((tiles + per - 1) / per) <= slots ? 1 : p.step ? 24 : p.nb == 2 ? 16 : 8;
   p.splits = static_cast<int>((tiles + per - 1) / per);
   return p;
 }
@@ -1330,6 +1333,7 @@ static cudaError_t launch_kind(const CUtensorMap& tmk, const CUtensorMap& tmv, c
 cudaError_t eagle::ka_launch(KaArgs* a, const KaPlan& p, bool f4, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t st) {
   a->blocks = p.blocks;
   a->tiles_per_cta = p.tiles_per_cta;
+  a->least = p.least;
   a->splits = p.splits;
   a->joined = p.joined;
   return a->pool.hd == 64 ? launch_kind<64>(tmk, tmv, *a, f4, p, st) : launch_kind<128>(tmk, tmv, *a, f4, p, st);

@@ -110,7 +110,7 @@ struct Own {
     if (b < 0) return;
     const Req rq = request(o, b);
     if (n < rq.row0 || n - rq.row0 >= rq.R) return;
-    used = min(o.splits, (rq.len + o.tiles_per_cta * KA_CH - 1) / (o.tiles_per_cta * KA_CH));
+    used = ranges_of(o, rq.len);
   }
   EAGLE_DEV size_t place(int s) const { return s * (static_cast<size_t>(a.N) * a.Hq) + at; }
   EAGLE_DEV float2 ml(int s) const { return a.part_ml[place(s)]; }
@@ -974,16 +974,16 @@ cudaError_t launch_kind(const CUtensorMap& tmk, const CUtensorMap& tmv, const Ka
 // Ranges (kv_attention_tc, kv_attention_step_f4) start sooner and need one launch where they join in a cluster;
 // this kernel's shares are even whatever the lengths, but it starts and joins for 16 us and every short
 // item costs it a queue's drain.  Measured over 700 sizes (both kinds, 64 and 128 dims, 12 to 4,096
-// vectors, 1 to 128 sequences of 250 to 80,000 keys, equal and spread): of long items (2,432 keys and more)
-//   bf16, up to 128 vectors: ranges, which keep 16 bits of p where this kernel keeps 8 (and are slower where
-//     few long sequences differ: 4 of 5,000 to 35,000 keys and 8 heads, 128 vectors: 96 us, here 82)
-//   bf16, more: here where a few sequences leave the SMs under one item each (4 of 1,500 to 10,500 keys, 8
-//     heads, 512 vectors: 64 us, by ranges 81), or where a hundred tiles an SM outweigh the start
+// vectors, 1 to 128 sequences of 250 to 80,000 keys, equal and spread), of items of 2,432 keys and more:
+//   up to 128 vectors: ranges, which over bf16 pages keep 16 bits of p where this kernel keeps 8 (and are
+//     slower where few sequences meet 16 KV heads of 64 dims: 8 of 8,000 keys, 128 vectors 94 us, here 60)
+//   bf16, more: here where a few sequences leave the SMs under one item each (4 of 5,000 to 35,000 keys, 8
+//     heads, 256 vectors: 86 us, by ranges 98), or where a hundred tiles an SM outweigh the start
 //     (prompts: 219, by ranges 229)
-//   4 bits, up to 128: several sequences, under one item and at least 30 tiles an SM (76, by ranges 103)
-//   4 bits, more: 10 tiles an SM and more (1 of 16,000 keys, 1,024 vectors: 74, by ranges 85)
-// and ranges elsewhere (1 of 8,000 bf16 keys, 12 vectors: 18 us, here 31; 32 of 125 to 870: 25, here 60;
-// 512 vectors: 63, here 117).  The mean loss to the faster of the two is 5.3, 0.5, 1.7 and 0.9% of the four.
+//   4 bits, more: 10 tiles an SM and more (the same 4 sequences: 90, by ranges 119)
+// and ranges elsewhere (1 of 8,000 bf16 keys, 12 vectors: 18 us, here 31; 32 of 125 to 870: 25, here 61;
+// 256 vectors: 38, here 72).  The mean loss to the faster of the two: up to 128 vectors 4.2% (bf16) and 3.3%,
+// more 0.6% and 1.2%.
 // A range's CTAs are launched for every block that the bounds allow; where the rows can fill one in 8 of
 // them at most, as a prompt of 4,096 rows among 63 single tokens does, the empty ones cost more than the
 // rest (1,000 keys, 8 heads: 285 us, here 143; 1,024 rows: 109, here 96; one in 5: 56, here 63).
@@ -993,10 +993,10 @@ bool eagle::kx_worth(int kind, int Hkv, int G, int B, long long N, int max_rows,
   if (blocks > 1 && static_cast<double>(B) * static_cast<double>(blocks) > 8. * (static_cast<double>(N) * G / KX_QV + B)) return true;
   const double tiles = static_cast<double>((static_cast<long long>(max_len) + KA_CH - 1) / KA_CH);
   const double items = static_cast<double>(B) * Hkv * static_cast<double>(blocks) / sms, work = items * tiles;
-  if (tiles < 20) return false;
+  if (qv <= KA_QV || tiles < 20) return false;
   const bool few = B > 1 && items <= 1;      // (of several sequences, whose lengths may differ)
-  if (kind == EAGLE_CACHE_F4) return qv <= KA_QV ? few && work >= 30 : work >= 10;
-  return qv > KA_QV && ((few && work >= 10) || work >= 100);
+  if (kind == EAGLE_CACHE_F4) return work >= 10;
+  return (few && work >= 10) || work >= 100;
 }
 
 KxPlan eagle::kx_plan(int kind, int Hkv, int hd, int G, int B, int max_rows, int max_len) {

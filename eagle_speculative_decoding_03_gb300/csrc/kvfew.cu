@@ -475,5 +475,6 @@ cudaError_t eagle::kf_launch(KaArgs* a, const eagle_kv_cache_t* cache, const KxP
     return cudaErrorInvalidValue;
   a->splits = 1;                             // (whoever joins the results further finds one range)
   a->tiles_per_cta = 1 << 20;
+  a->least = 1;
   return a->pool.hd == 64 ? launch_few<64>(tmk, tmv, *a, parts, p.ctas, st) : launch_few<128>(tmk, tmv, *a, parts, p.ctas, st);
 }

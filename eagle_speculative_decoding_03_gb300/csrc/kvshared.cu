@@ -42,8 +42,7 @@ __global__ void __launch_bounds__(128) kv_shared_join(const KaArgs a, const KaAr
   }
   const Req rq = request(a, b), rp = request(pre, g);
   if (n < rq.row0 || n - rq.row0 >= rq.R || n < rp.row0 || n - rp.row0 >= rp.R) return;
-  auto ranges = [](const KaArgs& x, int len) { return min(x.splits, (len + x.tiles_per_cta * KA_CH - 1) / (x.tiles_per_cta * KA_CH)); };
-  const int own = ranges(a, rq.len), used = own + ranges(pre, rp.len);
+  const int own = ranges_of(a, rq.len), used = own + ranges_of(pre, rp.len);
   const size_t at = static_cast<size_t>(n) * a.Hq + h, step = static_cast<size_t>(a.N) * a.Hq;
   auto place = [&](int s) { return (s < own ? s : a.splits + s - own) * step + at; };
   float M = -INFINITY;

@@ -47,7 +47,10 @@ MEASURED = [
     ("bf16", 8, 128, 4, 4, 128, 10500, "wide"),      # 81.4, 64.2
     ("bf16", 8, 128, 4, 2, 2047, 4099, "wide"),      # 229, 219
     ("f4", 8, 128, 4, 1, 16, 32000, "ranges"),       # 32.9, 52.5
-    ("f4", 8, 128, 4, 4, 16, 35000, "wide"),         # 95.6, 75.9
+    ("f4", 8, 128, 4, 4, 4, 35000, "ranges"),        # 73.9, 74.5
+    ("f4", 8, 128, 4, 4, 64, 35000, "wide"),         # 119.4, 90.3
+    ("bf16", 8, 128, 4, 4, 32, 35000, "ranges"),     # 81.1, 83.2
+    ("bf16", 8, 128, 4, 4, 64, 35000, "wide"),       # 97.6, 86.2
     ("f4", 8, 128, 4, 1, 256, 16000, "wide"),        # 84.5, 74.4
     ("f4", 8, 128, 4, 32, 64, 870, "ranges"),        # 46.4, 66.1
     ("bf16", 16, 64, 1, 32, 1, 3000, "few"),         # 86.5, 56.7
