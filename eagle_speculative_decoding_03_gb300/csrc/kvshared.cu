@@ -199,6 +199,18 @@ eagle_status_t check_rows(const char* who, int Hkv, int hd, int B, int N, int Hq
   return EAGLE_OK;
 }
 
+// What a call writes beside out: lse and the workspace are its own.
+eagle_status_t check_own(const char* who, int N, int Hq, int hd, const void* q, long long q_ld, const void* out, long long out_ld,
+                         const float* lse, const void* workspace, int64_t need) {
+  const long long width = 2ll * Hq * hd, q_bytes = (N - 1) * 2 * q_ld + width, out_bytes = (N - 1) * 2 * out_ld + width, lse_bytes = 4ll * N * Hq;
+  auto meet = [](const void* a, long long na, const void* b, long long nb) { return rows_meet(a, na, na, b, nb, nb, 1); };
+  if (lse && (meet(lse, lse_bytes, q, q_bytes) || meet(lse, lse_bytes, out, out_bytes)))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: lse overlaps q or out", who);
+  if (need > 0 && (meet(workspace, need, q, q_bytes) || meet(workspace, need, out, out_bytes) || (lse && meet(workspace, need, lse, lse_bytes))))
+    return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: the workspace overlaps q, out or lse", who);
+  return EAGLE_OK;
+}
+
 eagle_status_t check_extent(const char* who, int max_rows, int max_len) {
   if (max_rows < 1 || max_len < 1) return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: need max_rows and max_len >= 1", who);
   if (max_len > 1 << 30) return kv_fail(EAGLE_ERR_UNSUPPORTED, "%s: max_len must be at most 2^30", who);
@@ -330,6 +342,8 @@ extern "C" eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || !aligned(w->workspace)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
+  r = check_own(who, w->N, w->n_heads, cache->head_dim, w->q, w->q_stride, w->out, w->out_stride, w->lse, w->workspace, need);
+  if (r != EAGLE_OK) return r;
   a.B = w->B;
   a.N = w->N;
   a.Hq = w->n_heads;
@@ -389,6 +403,8 @@ extern "C" eagle_status_t eagle_kv_shared_attention(const eagle_kv_cache_t* pref
   if (need > 0 && (!w->workspace || w->workspace_bytes < need || !aligned(w->workspace)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: needs %lld bytes of workspace, 16-byte aligned", who, static_cast<long long>(need));
   if (w->N == 0) return EAGLE_OK;
+  r = check_own(who, w->N, w->n_heads, hd, w->q, w->q_stride, w->out, w->out_stride, w->lse, w->workspace, need);
+  if (r != EAGLE_OK) return r;
   const size_t outs = static_cast<size_t>(w->N) * w->n_heads;
   a.B = w->B;
   a.N = w->N;

@@ -633,8 +633,9 @@ typedef struct {
   float   scale;              /* 0: 1 / sqrt(hd) */
   void*   out;                /* bf16 [N][Hq][hd], rows out_stride apart; may not overlap q */
   int64_t out_stride;
-  float*  lse;                /* [N][Hq] log-sum-exp of the scaled scores, or NULL */
-  void*   workspace;          /* eagle_kv_cross_attention_workspace bytes, 16-byte aligned (NULL if 0) */
+  float*  lse;                /* [N][Hq] log-sum-exp of the scaled scores, or NULL; may not overlap q, out */
+  void*   workspace;          /* eagle_kv_cross_attention_workspace bytes, 16-byte aligned (NULL if 0),
+                               * which overlap none of the above */
   int64_t workspace_bytes;
 } eagle_kv_cross_t;
 
@@ -647,6 +648,7 @@ typedef struct {
  * small the key's weight (an infinite value gives that infinity in its dim, NaN beside the other one
  * or at a key of score -infinity); calls that meet infinities take longer.
  * A row of a sequence without keys, or whose scores are all -infinity, gets zeros and lse -infinity.
+ * The sums before the division are fp32: values of 1e30 and more may overflow them.
  * Rows past max_rows, and keys past max_len, are left out and flagged (EAGLE_DEVERR_PREFIX). */
 EAGLE_API int64_t eagle_kv_cross_attention_workspace(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* args);
 EAGLE_API eagle_status_t eagle_kv_cross_attention(const eagle_kv_cache_t* cache, const eagle_kv_cross_t* args,
@@ -665,7 +667,8 @@ typedef struct {
 /* Row i of request b of group g sees the lens[g] keys of row g of `prefix`'s page table, the
  * args->lens[b] keys of `cache` before the step and of the step's own rows (appended to `cache`
  * before) what args->mask says, or j <= i: args is as in eagle_kv_attention, but for the workspace
- * (eagle_kv_shared_attention_workspace bytes).  Positions are the caller's: append the own keys
+ * (eagle_kv_shared_attention_workspace bytes); lse and the workspace overlap nothing else of the call.
+ * Positions are the caller's: append the own keys
  * with positions behind the prefix.  The two caches have the same heads and head_dim; their kinds,
  * page sizes and pools are their own.  Rounding: the prefix as eagle_kv_cross_attention (with
  * groups->max_rows and the groups as sequences), the own keys as eagle_kv_attention; joined in fp32
