@@ -202,7 +202,7 @@ eagle_status_t check_rows(const char* who, int Hkv, int hd, int B, int N, int Hq
 // What a call writes beside out: lse and the workspace are its own.
 eagle_status_t check_own(const char* who, int N, int Hq, int hd, const void* q, long long q_ld, const void* out, long long out_ld,
                          const float* lse, const void* workspace, int64_t need) {
-  const long long width = 2ll * Hq * hd, q_bytes = (N - 1) * 2 * q_ld + width, out_bytes = (N - 1) * 2 * out_ld + width, lse_bytes = 4ll * N * Hq;
+  const long long width = 2ll * Hq * hd, q_bytes = 2ll * (N - 1) * q_ld + width, out_bytes = 2ll * (N - 1) * out_ld + width, lse_bytes = 4ll * N * Hq;
   auto meet = [](const void* a, long long na, const void* b, long long nb) { return rows_meet(a, na, na, b, nb, nb, 1); };
   if (lse && (meet(lse, lse_bytes, q, q_bytes) || meet(lse, lse_bytes, out, out_bytes)))
     return kv_fail(EAGLE_ERR_INVALID_ARG, "%s: lse overlaps q or out", who);
